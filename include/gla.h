@@ -383,6 +383,63 @@ gla_status gla_conv1d_step(const void *x, const float *w, const float *b, float 
                            gla_dtype dtype, void *y, void *stream);
 
 /*
+ * The selective state-space scan: the mixer with a decay per channel and
+ * state that depends on the token (the selective form of a diagonal state
+ * space model), per sequence, channel d of D and state n of N:
+ *     delta_t = softplus(dt_t[d] + dt_bias[d])   (softplus = 0: dt + dt_bias as it is)
+ *     h_t     = exp(delta_t A[d][n]) h_{t-1} + delta_t B_t[n] u_t[d]       (fp32)
+ *     y_t     = (sum_n C_t[n] h_t + skip[d] u_t[d]) * SiLU(z_t[d])
+ * u is x, or (gla_ssm_varlen and gla_ssm_step, with conv_w) the causal
+ * depthwise Conv1d with SiLU of x (the formula and the windows of
+ * gla_conv1d_fwd; u is not rounded in between).
+ *   x, dt, z: rows of D channels of `dtype`, Bm, Cm: rows of N of `dtype`;
+ *     ld_*: elements from one token's row to the next (a column range of a
+ *     wider projection output can be passed as it is). Rows of x, dt and z
+ *     start 16-byte aligned; Bm and Cm need only their element's alignment.
+ *   A [D, N] fp32 (negative for a decay; not its logarithm), skip [D] fp32 or
+ *     NULL (0), dt_bias [D] fp32 or NULL (0), z or NULL (no gate).
+ *   y: contiguous rows of D. States [*, D, N] fp32, N fastest.
+ *   D a multiple of 8; N = 8, 16 or 32. y may not be x, dt or z.
+ *
+ * gla_ssm_fwd: B sequences of T tokens, x, dt, z, y [B, T, D], Bm, Cm
+ *   [B, T, N] (token rows ld_* apart throughout, b-th sequence's first row at
+ *   b*T); h0 [B, D, N] or NULL (zero), hT [B, D, N] or NULL (not wanted; may
+ *   be h0). T = 0 copies h0 to hT.
+ * gla_ssm_varlen: packed sequences, as gla_chunk_fwd_varlen: tokens
+ *   [cu_seqlens[n], cu_seqlens[n+1]), state in state_pool [n_slots, D, N] and
+ *   (with conv_w [D, 4], conv_b [D] or NULL) window in win_pool
+ *   [n_slots, 4, D], both fp32, at slots[n] (NULL: n), read and overwritten.
+ *   Slots of one call are distinct. An empty sequence leaves its slot
+ *   untouched; rows past the last sequence are left as they were. A bad entry
+ *   (decreasing offset, offset past total_T, slot outside the pool) skips its
+ *   sequence and the next gla_check() reports GLA_ERR_INVALID_ARG; where
+ *   offsets decrease, other sequences may be skipped with it.
+ * gla_ssm_step: one token per sequence, rows [nseq, *], on the same pools;
+ *   a bad slot skips its sequence likewise.
+ * gla_ssm_fwd and gla_ssm_varlen cut sequences into segments that run in
+ *   parallel when workspace_bytes is at least the *_workspace_size query
+ *   (0: nothing to gain); with less they run one chain per sequence and
+ *   channel: the same result up to rounding, never a failure.
+ */
+gla_status gla_ssm_fwd(const void *x, int64_t ld_x, const void *dt, int64_t ld_dt, const float *A, const void *Bm,
+                       int64_t ld_B, const void *Cm, int64_t ld_C, const float *skip, const void *z, int64_t ld_z,
+                       const float *dt_bias, int softplus, const float *h0, int B, int T, int D, int N,
+                       gla_dtype dtype, void *y, float *hT, void *workspace, size_t workspace_bytes, void *stream);
+size_t gla_ssm_fwd_workspace_size(int B, int T, int D, int N, gla_dtype dtype);
+gla_status gla_ssm_varlen(const void *x, int64_t ld_x, const void *dt, int64_t ld_dt, const float *A, const void *Bm,
+                          int64_t ld_B, const void *Cm, int64_t ld_C, const float *skip, const void *z, int64_t ld_z,
+                          const float *dt_bias, int softplus, const float *conv_w, const float *conv_b,
+                          const int *cu_seqlens, const int *slots, float *state_pool, float *win_pool, int n_slots,
+                          int nseq, int total_T, int D, int N, gla_dtype dtype, void *y, void *workspace,
+                          size_t workspace_bytes, void *stream);
+size_t gla_ssm_varlen_workspace_size(int nseq, int total_T, int D, int N, gla_dtype dtype);
+gla_status gla_ssm_step(const void *x, int64_t ld_x, const void *dt, int64_t ld_dt, const float *A, const void *Bm,
+                        int64_t ld_B, const void *Cm, int64_t ld_C, const float *skip, const void *z, int64_t ld_z,
+                        const float *dt_bias, int softplus, const float *conv_w, const float *conv_b, const int *slots,
+                        float *state_pool, float *win_pool, int n_slots, int nseq, int D, int N, gla_dtype dtype,
+                        void *y, void *stream);
+
+/*
  * gla_selftest_wait_timeout -- diagnostic of the device-side failure
  * detection, with no fault and no hang: one kernel waits on two mbarriers
  * that nothing completes. The first wait gives up after limit_us (1 to

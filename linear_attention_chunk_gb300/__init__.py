@@ -38,6 +38,11 @@ from .binding import (  # noqa: F401
     gla_last_launch_count,
     gla_mixer_epilogue,
     gla_selftest_wait_timeout,
+    gla_ssm_fwd,
+    gla_ssm_fwd_workspace_size,
+    gla_ssm_step,
+    gla_ssm_varlen,
+    gla_ssm_varlen_workspace_size,
     gla_status_string,
     gla_version,
     lib,

@@ -22,6 +22,9 @@ Functions:
   gla_conv1d_fwd(x, w, b=None, win_in=None, ...)                          -> (y, win_out)
   gla_conv1d_varlen(x, w, b, cu_seqlens, win_pool, slots=None)            -> y  (pool updated)
   gla_conv1d_step(x, w, b, win)                                           -> y  (window updated)
+  gla_ssm_fwd(x, dt, A, Bm, Cm, skip=None, z=None, dt_bias=None, h0=None) -> (y, hT)  selective scan
+  gla_ssm_varlen(x, dt, A, Bm, Cm, cu_seqlens, state_pool, ...)           -> y  (pools updated)
+  gla_ssm_step(x, dt, A, Bm, Cm, state_pool, ...)                         -> y  (pools updated)
   gla_check(stream=None), gla_status_string(code), gla_version()
   gla_chunk_fwd_workspace_size(...), gla_chunk_bwd_workspace_size(...)
 `lib()` returns the loaded ctypes library for callers that hold raw pointers.
@@ -43,7 +46,8 @@ GLA_BF16, GLA_FP32 = 0, 1
 ABI_FUNCTIONS = ("gla_chunk_fwd", "gla_chunk_fwd_workspace_size", "gla_chunk_fwd_noalloc", "gla_chunk_fwd_varlen", "gla_chunk_fwd_varlen_gated",
                  "gla_chunk_fwd_mixer", "gla_chunk_fwd_gated", "gla_chunk_fwd_gated_workspace_size", "gla_decode_step_gated", "gla_chunk_bwd",
                  "gla_chunk_bwd_workspace_size", "gla_chunk_bwd_gated", "gla_chunk_bwd_gated_workspace_size", "gla_decode_step", "gla_decode_step_mixer", "gla_mixer_epilogue",
-                 "gla_conv1d_fwd", "gla_conv1d_varlen", "gla_conv1d_step", "gla_selftest_wait_timeout", "gla_check",
+                 "gla_conv1d_fwd", "gla_conv1d_varlen", "gla_conv1d_step", "gla_ssm_fwd", "gla_ssm_fwd_workspace_size",
+                 "gla_ssm_varlen", "gla_ssm_varlen_workspace_size", "gla_ssm_step", "gla_selftest_wait_timeout", "gla_check",
                  "gla_status_string", "gla_last_error", "gla_last_launch_count", "gla_version")
 
 
@@ -60,6 +64,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
+_ll = ctypes.c_int64
 
 
 def lib():
@@ -118,6 +123,18 @@ def lib():
             L.gla_conv1d_varlen.restype = _i
             L.gla_conv1d_step.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp]
             L.gla_conv1d_step.restype = _i
+            rows = [_vp, _ll, _vp, _ll, _vp, _vp, _ll, _vp, _ll, _vp, _vp, _ll, _vp, _i]   # x .. softplus
+            L.gla_ssm_fwd.argtypes = rows + [_vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]
+            L.gla_ssm_fwd.restype = _i
+            L.gla_ssm_fwd_workspace_size.argtypes = [_i, _i, _i, _i, _i]
+            L.gla_ssm_fwd_workspace_size.restype = _sz
+            L.gla_ssm_varlen.argtypes = rows + [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _sz,
+                                                _vp]
+            L.gla_ssm_varlen.restype = _i
+            L.gla_ssm_varlen_workspace_size.argtypes = [_i, _i, _i, _i, _i]
+            L.gla_ssm_varlen_workspace_size.restype = _sz
+            L.gla_ssm_step.argtypes = rows + [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp]
+            L.gla_ssm_step.restype = _i
             L.gla_selftest_wait_timeout.argtypes = [ctypes.c_uint, _vp, _vp]
             L.gla_selftest_wait_timeout.restype = _i
             L.gla_check.argtypes = [_vp]
@@ -519,6 +536,180 @@ def gla_conv1d_step(x, w, b, win, *, y=None, stream=None):
         y = torch.empty_like(x)
     st = lib().gla_conv1d_step(_ptr(x), _ptr(w), _ptr(b), _ptr(win), N, D, _dtype_code(x), _ptr(y), _stream(stream))
     _raise_on(st, "gla_conv1d_step")
+    return y
+
+
+class _Call:
+    """The tensors of one call: all on the device of the first, each checked
+    for type and shape before its address is taken. The call runs with that
+    device current, on `stream` or the device's current stream; what it
+    allocates (outputs, workspace) belongs to the stream it runs on."""
+
+    def __init__(self, x, stream):
+        if not x.is_cuda:
+            raise GlaError(GLA_ERR_INVALID_ARG, "argument", "tensors must live on a CUDA device")
+        self.torch = _torch()
+        self.dev = x.device
+        self.dtype = x.dtype
+        self.code = _dtype_code(x)
+        cuda = self.torch.cuda
+        current = cuda.current_stream(self.dev)
+        self.stream = current.cuda_stream if stream is None else _stream(stream)
+        self.other = None
+        if self.stream != current.cuda_stream:
+            if hasattr(stream, "cuda_stream"):
+                self.other = stream
+            else:
+                self.other = cuda.ExternalStream(self.stream, self.dev) if self.stream else cuda.default_stream(self.dev)
+
+    def _check(self, t, shape, dtype, name):
+        if t.device != self.dev:
+            raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} is on {t.device}, the call's tensors on {self.dev}")
+        if t.dtype != dtype:
+            raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+    def whole(self, t, shape, name, dtype=None):
+        """Address of a contiguous tensor (None passes); dtype None: the call's element type."""
+        if t is None:
+            return None
+        self._check(t, shape, self.dtype if dtype is None else dtype, name)
+        if not t.is_contiguous():
+            raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def f32(self, t, shape, name):
+        return self.whole(t, shape, name, self.torch.float32) if t is not None else None
+
+    def i32(self, t, shape, name):
+        return self.whole(t, shape, name, self.torch.int32) if t is not None else None
+
+    def rows(self, t, shape, name):
+        """Address and row step of [..., C] rows an equal distance apart with
+        contiguous columns (a column range of a wider tensor passes)."""
+        if t is None:
+            return None, 0
+        self._check(t, shape, self.dtype, name)
+        if t.numel() == 0 or t.is_contiguous():
+            return t.data_ptr(), shape[-1]
+        lead = [(n, st) for n, st in zip(shape[:-1], t.stride()[:-1]) if n > 1]
+        step = lead[-1][1] if lead else shape[-1]
+        if t.stride(-1) != 1 and shape[-1] > 1 or len(lead) == 2 and lead[0][1] != lead[1][0] * step or step < shape[-1]:
+            raise GlaError(GLA_ERR_INVALID_ARG, "argument",
+                           f"{name} must have contiguous columns and token rows an equal distance apart")
+        return t.data_ptr(), step
+
+    def empty(self, shape, dtype=None):
+        dtype = self.dtype if dtype is None else dtype
+        if self.other is None:
+            return self.torch.empty(shape, dtype=dtype, device=self.dev)
+        with self.torch.cuda.stream(self.other):
+            return self.torch.empty(shape, dtype=dtype, device=self.dev)
+
+    def scratch(self, workspace, need):
+        """Address and bytes of the caller's workspace, or of a new one of `need` bytes."""
+        if workspace is None:
+            if need == 0:
+                return None, 0
+            workspace = self.kept = self.empty(need, self.torch.uint8)
+        elif workspace.device != self.dev or not workspace.is_contiguous():
+            raise GlaError(GLA_ERR_INVALID_ARG, "argument", "the workspace must be contiguous and on the call's device")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+    def run(self, name, *args):
+        torch = self.torch
+        if self.dev.index == torch.cuda.current_device():
+            st = getattr(lib(), name)(*args, self.stream)
+        else:
+            with torch.cuda.device(self.dev):
+                st = getattr(lib(), name)(*args, self.stream)
+        _raise_on(st, name)
+
+
+def _lead(t, n, name):
+    if t.dim() != n:
+        raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} has {t.dim()} dimensions, expected {n}")
+    return t.shape
+
+
+def _ssm_rows(c, x, dt, A, Bm, Cm, skip, z, dt_bias, softplus):
+    """The arguments every selective-scan entry point begins with."""
+    D, N = x.shape[-1], _lead(A, 2, "A")[1]
+    narrow = x.shape[:-1] + (N,)
+    return (*c.rows(x, x.shape, "x"), *c.rows(dt, x.shape, "dt"), c.f32(A, (D, N), "A"), *c.rows(Bm, narrow, "Bm"),
+            *c.rows(Cm, narrow, "Cm"), c.f32(skip, (D,), "skip"), *c.rows(z, x.shape, "z"),
+            c.f32(dt_bias, (D,), "dt_bias"), int(bool(softplus)))
+
+
+def gla_ssm_fwd_workspace_size(B, T, D, N, dtype=GLA_BF16) -> int:
+    return int(lib().gla_ssm_fwd_workspace_size(B, T, D, N, dtype))
+
+
+def gla_ssm_varlen_workspace_size(nseq, total_T, D, N, dtype=GLA_BF16) -> int:
+    return int(lib().gla_ssm_varlen_workspace_size(nseq, total_T, D, N, dtype))
+
+
+def gla_ssm_fwd(x, dt, A, Bm, Cm, skip=None, z=None, dt_bias=None, h0=None, *, softplus=True, y=None, hT=None,
+                want_hT=True, workspace=None, stream=None):
+    """The selective state-space scan: x, dt, z [B,T,D], Bm, Cm [B,T,N] (bf16
+    or fp32; column ranges of wider tensors pass), A [D,N], skip, dt_bias [D]
+    fp32, h0 [B,D,N] fp32 or None (zeros). With delta = softplus(dt + dt_bias),
+    h = exp(delta A) h + delta B x, y = (C.h + skip x) SiLU(z). Returns
+    (y [B,T,D], hT [B,D,N] fp32; hT may be h0)."""
+    B, T, D = _lead(x, 3, "x")
+    c = _Call(x, stream)
+    args = _ssm_rows(c, x, dt, A, Bm, Cm, skip, z, dt_bias, softplus)
+    N = A.shape[1]
+    if y is None:
+        y = c.empty((B, T, D))
+    if hT is None and want_hT:
+        hT = c.empty((B, D, N), c.torch.float32)
+    need = gla_ssm_fwd_workspace_size(B, T, D, N, c.code) if workspace is None else 0
+    c.run("gla_ssm_fwd", *args, c.f32(h0, (B, D, N), "h0"), B, T, D, N, c.code, c.whole(y, (B, T, D), "y"),
+          c.f32(hT, (B, D, N), "hT"), *c.scratch(workspace, need))
+    return y, hT
+
+
+def _pools(c, n, D, N, state_pool, slots, conv_w, conv_b, win_pool):
+    k = _lead(state_pool, 3, "state_pool")[0]
+    return (c.f32(conv_w, (D, 4), "conv_w"), c.f32(conv_b, (D,), "conv_b"), c.i32(slots, (n,), "slots"),
+            c.f32(state_pool, (k, D, N), "state_pool"), c.f32(win_pool, (k, 4, D), "win_pool"), k)
+
+
+def gla_ssm_varlen(x, dt, A, Bm, Cm, cu_seqlens, state_pool, skip=None, z=None, dt_bias=None, slots=None, *,
+                   conv_w=None, conv_b=None, win_pool=None, softplus=True, y=None, workspace=None, stream=None):
+    """The selective scan over packed sequences: x, dt, z [total_T,D], Bm, Cm
+    [total_T,N], sequence n = tokens [cu_seqlens[n], cu_seqlens[n+1]) (int32
+    CUDA tensor), state_pool [n_slots,D,N] fp32 updated in place at slots[n]
+    (int32 CUDA tensor, or None for slot n). With conv_w [D,4] (and conv_b [D],
+    win_pool [n_slots,4,D], fp32) x goes through the causal Conv1d with SiLU
+    first, its windows updated in place. Returns y [total_T,D]."""
+    total_T, D = _lead(x, 2, "x")
+    c = _Call(x, stream)
+    args = _ssm_rows(c, x, dt, A, Bm, Cm, skip, z, dt_bias, softplus)
+    N, nseq = A.shape[1], cu_seqlens.numel() - 1
+    w, b, sl, pool, win, k = _pools(c, nseq, D, N, state_pool, slots, conv_w, conv_b, win_pool)
+    if y is None:
+        y = c.empty((total_T, D))
+    need = gla_ssm_varlen_workspace_size(nseq, total_T, D, N, c.code) if workspace is None else 0
+    c.run("gla_ssm_varlen", *args, w, b, c.i32(cu_seqlens, (nseq + 1,), "cu_seqlens"), sl, pool, win, k, nseq,
+          total_T, D, N, c.code, c.whole(y, (total_T, D), "y"), *c.scratch(workspace, need))
+    return y
+
+
+def gla_ssm_step(x, dt, A, Bm, Cm, state_pool, skip=None, z=None, dt_bias=None, slots=None, *, conv_w=None,
+                 conv_b=None, win_pool=None, softplus=True, y=None, stream=None):
+    """One token per sequence of the selective scan: x, dt, z [N,D], Bm, Cm
+    [N,n]; pools, slots and the Conv1d as gla_ssm_varlen. Returns y [N,D]."""
+    n, D = _lead(x, 2, "x")
+    c = _Call(x, stream)
+    args = _ssm_rows(c, x, dt, A, Bm, Cm, skip, z, dt_bias, softplus)
+    N = A.shape[1]
+    w, b, sl, pool, win, k = _pools(c, n, D, N, state_pool, slots, conv_w, conv_b, win_pool)
+    if y is None:
+        y = c.empty((n, D))
+    c.run("gla_ssm_step", *args, w, b, sl, pool, win, k, n, D, N, c.code, c.whole(y, (n, D), "y"))
     return y
 
 

@@ -140,6 +140,70 @@ gla_status decode_common(const void *q, const void *k, const void *v, const floa
     return e == cudaSuccess ? GLA_OK : cuda_fail(e, "decode launch");
 }
 
+// A [rows, cols] array of a selective-scan call: pointer, row step, alignment.
+gla_status check_rows(const void *ptr, int64_t ld, int cols, int elem, bool vector, const char *name) {
+    if (!ptr) return fail(GLA_ERR_INVALID_ARG, "%s is NULL", name);
+    const uintptr_t align = vector ? 16 : (uintptr_t)elem;
+    if (reinterpret_cast<uintptr_t>(ptr) % align) return fail(GLA_ERR_INVALID_ARG, "%s is not %d-byte aligned", name, (int)align);
+    if (ld < cols) return fail(GLA_ERR_INVALID_ARG, "%s has rows of %d elements %lld apart", name, cols, (long long)ld);
+    if (vector && (ld * elem) % 16) return fail(GLA_ERR_INVALID_ARG, "%s has rows that are not 16-byte aligned", name);
+    if (ld > (1ll << 31)) return fail(GLA_ERR_INVALID_ARG, "%s has rows too far apart", name);
+    return GLA_OK;
+}
+
+gla_status check_ssm_shape(int64_t seqs, int64_t rows, int D, int N, gla_dtype dtype) {
+    if (dtype != GLA_BF16 && dtype != GLA_FP32) return fail(GLA_ERR_INVALID_ARG, "dtype %d is not GLA_BF16/GLA_FP32", (int)dtype);
+    if (seqs < 0 || rows < 0) return fail(GLA_ERR_INVALID_ARG, "negative size (sequences %lld, tokens %lld)", (long long)seqs, (long long)rows);
+    if (D <= 0 || D % 8 != 0) return fail(GLA_ERR_UNSUPPORTED, "D=%d must be a positive multiple of 8", D);
+    if (N != 8 && N != 16 && N != 32) return fail(GLA_ERR_UNSUPPORTED, "N=%d is not 8, 16 or 32", N);
+    // one CTA per 64 channels of a sequence or segment: well inside a 1-D grid
+    if ((long double)(seqs + rows) * ((D + 63) / 64) > 2147483647.0L || (long double)rows * D > (long double)(1ull << 40))
+        return fail(GLA_ERR_INVALID_ARG, "tensor too large");
+    return GLA_OK;
+}
+
+// The arrays every selective-scan call reads.
+gla_status check_ssm_inputs(const SsmParams &p, gla_dtype dtype) {
+    const int e = dtype == GLA_BF16 ? 2 : 4;
+    gla_status st;
+    if ((st = check_rows(p.x, p.ldx, p.D, e, true, "x")) != GLA_OK) return st;
+    if ((st = check_rows(p.dt, p.ldt, p.D, e, true, "dt")) != GLA_OK) return st;
+    if ((st = check_rows(p.Bm, p.ldb, p.N, e, false, "Bm")) != GLA_OK) return st;
+    if ((st = check_rows(p.Cm, p.ldc, p.N, e, false, "Cm")) != GLA_OK) return st;
+    if (p.z && (st = check_rows(p.z, p.ldz, p.D, e, true, "z")) != GLA_OK) return st;
+    REQUIRE_PTR(p.A, "A");
+    OPTIONAL_PTR(p.skip, "skip");
+    OPTIONAL_PTR(p.dt_bias, "dt_bias");
+    return GLA_OK;
+}
+
+// Pools, windows and filter of the packed and the single-token calls.
+gla_status check_ssm_pools(const SsmParams &p) {
+    if (p.n_slots < 0) return fail(GLA_ERR_INVALID_ARG, "negative n_slots=%d", p.n_slots);
+    if (!p.slots && p.n_slots < p.nseq)
+        return fail(GLA_ERR_INVALID_ARG, "without slots the pool needs nseq=%d slots, has %d", p.nseq, p.n_slots);
+    OPTIONAL_PTR(p.slots, "slots");
+    REQUIRE_PTR(p.h0, "state_pool");
+    OPTIONAL_PTR(p.conv_w, "conv_w");
+    OPTIONAL_PTR(p.conv_b, "conv_b");
+    OPTIONAL_PTR(p.win, "win_pool");
+    if ((p.conv_w != nullptr) != (p.win != nullptr))
+        return fail(GLA_ERR_INVALID_ARG, "conv_w and win_pool come together");
+    if (p.conv_b && !p.conv_w) return fail(GLA_ERR_INVALID_ARG, "conv_b without conv_w");
+    return GLA_OK;
+}
+
+// Splits the workspace of a segmented scan; without enough of it, one segment per sequence.
+void ssm_workspace(SsmParams &p, SsmPlan plan, void *workspace, size_t bytes, bool varlen) {
+    const size_t need = ssm_workspace_bytes(plan, p.nseq, p.D, p.N);
+    if (need == 0 || !workspace || bytes < need) plan = SsmPlan{varlen ? p.rows : p.T, p.nseq};
+    else {
+        p.seg_h = static_cast<float *>(workspace);
+        p.seg_sum = p.seg_h + (size_t)plan.slots * p.D * p.N;
+    }
+    p.L = plan.L;
+    p.nseg = varlen ? 0 : (int)((p.T + p.L - 1) / p.L);
+}
 
 }  // namespace
 
@@ -595,6 +659,101 @@ gla_status gla_conv1d_step(const void *x, const float *w, const float *b, float 
     const cudaError_t e = launch_conv_step(p, dtype == GLA_BF16, static_cast<cudaStream_t>(stream), &launches);
     t_launches = launches;
     return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_conv1d_step launch");
+}
+
+gla_status gla_ssm_fwd(const void *x, int64_t ld_x, const void *dt, int64_t ld_dt, const float *A, const void *Bm,
+                       int64_t ld_B, const void *Cm, int64_t ld_C, const float *skip, const void *z, int64_t ld_z,
+                       const float *dt_bias, int softplus, const float *h0, int B, int T, int D, int N,
+                       gla_dtype dtype, void *y, float *hT, void *workspace, size_t workspace_bytes, void *stream) {
+    t_err[0] = 0;
+    t_launches = 0;
+    gla_status st = check_ssm_shape(B, T < 0 ? -1 : (int64_t)B * T, D, N, dtype);
+    if (st != GLA_OK) return st;
+    OPTIONAL_PTR(h0, "h0");
+    OPTIONAL_PTR(hT, "hT");
+    OPTIONAL_PTR(workspace, "workspace");
+    if (B == 0) return GLA_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int launches = 0;
+    cudaError_t e;
+    if (T == 0) {
+        if (h0 == hT) return GLA_OK;
+        e = launch_copy_state(h0, hT, (size_t)B * D * N, s, &launches);
+        t_launches = launches;
+        return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_ssm_fwd(T=0)");
+    }
+    SsmParams p{x, dt, z, Bm, Cm, (long)ld_x, (long)ld_dt, (long)ld_z, (long)ld_B, (long)ld_C, A, skip, dt_bias,
+                nullptr, nullptr, h0, hT, nullptr, nullptr, nullptr, B, B, T, D, N, softplus, (long)B * T, y};
+    if ((st = check_ssm_inputs(p, dtype)) != GLA_OK) return st;
+    REQUIRE_PTR(y, "y");
+    if (y == x || y == dt || y == z) return fail(GLA_ERR_INVALID_ARG, "y may not alias an input");
+    ssm_workspace(p, plan_ssm(B, p.rows, D, false), workspace, workspace_bytes, false);
+    e = launch_ssm_scan(p, dtype == GLA_BF16, s, &launches);
+    t_launches = launches;
+    return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_ssm_fwd launch");
+}
+
+size_t gla_ssm_fwd_workspace_size(int B, int T, int D, int N, gla_dtype dtype) {
+    if (check_ssm_shape(B, T < 0 ? -1 : (int64_t)B * T, D, N, dtype) != GLA_OK || B == 0 || T == 0) return 0;
+    return ssm_workspace_bytes(plan_ssm(B, (long)B * T, D, false), B, D, N);
+}
+
+gla_status gla_ssm_varlen(const void *x, int64_t ld_x, const void *dt, int64_t ld_dt, const float *A, const void *Bm,
+                          int64_t ld_B, const void *Cm, int64_t ld_C, const float *skip, const void *z, int64_t ld_z,
+                          const float *dt_bias, int softplus, const float *conv_w, const float *conv_b,
+                          const int *cu_seqlens, const int *slots, float *state_pool, float *win_pool, int n_slots,
+                          int nseq, int total_T, int D, int N, gla_dtype dtype, void *y, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+    t_err[0] = 0;
+    t_launches = 0;
+    gla_status st = check_ssm_shape(nseq, total_T, D, N, dtype);
+    if (st != GLA_OK) return st;
+    OPTIONAL_PTR(workspace, "workspace");
+    if (nseq == 0) return GLA_OK;
+    SsmParams p{x, dt, z, Bm, Cm, (long)ld_x, (long)ld_dt, (long)ld_z, (long)ld_B, (long)ld_C, A, skip, dt_bias,
+                conv_w, conv_b, state_pool, state_pool, win_pool, cu_seqlens, slots, n_slots, nseq, 0, D, N, softplus,
+                (long)total_T, y};
+    REQUIRE_PTR(cu_seqlens, "cu_seqlens");
+    if ((st = check_ssm_pools(p)) != GLA_OK) return st;
+    if (total_T == 0) return GLA_OK;   // every sequence is empty: no state changes
+    if ((st = check_ssm_inputs(p, dtype)) != GLA_OK) return st;
+    REQUIRE_PTR(y, "y");
+    if (y == x || y == dt || y == z) return fail(GLA_ERR_INVALID_ARG, "y may not alias an input");
+    if ((st = status_word(&p.status)) != GLA_OK) return st;
+    ssm_workspace(p, plan_ssm(nseq, total_T, D, true), workspace, workspace_bytes, true);
+    int launches = 0;
+    const cudaError_t e = launch_ssm_scan(p, dtype == GLA_BF16, static_cast<cudaStream_t>(stream), &launches);
+    t_launches = launches;
+    return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_ssm_varlen launch");
+}
+
+size_t gla_ssm_varlen_workspace_size(int nseq, int total_T, int D, int N, gla_dtype dtype) {
+    if (check_ssm_shape(nseq, total_T, D, N, dtype) != GLA_OK || nseq == 0 || total_T == 0) return 0;
+    return ssm_workspace_bytes(plan_ssm(nseq, total_T, D, true), nseq, D, N);
+}
+
+gla_status gla_ssm_step(const void *x, int64_t ld_x, const void *dt, int64_t ld_dt, const float *A, const void *Bm,
+                        int64_t ld_B, const void *Cm, int64_t ld_C, const float *skip, const void *z, int64_t ld_z,
+                        const float *dt_bias, int softplus, const float *conv_w, const float *conv_b, const int *slots,
+                        float *state_pool, float *win_pool, int n_slots, int nseq, int D, int N, gla_dtype dtype,
+                        void *y, void *stream) {
+    t_err[0] = 0;
+    t_launches = 0;
+    gla_status st = check_ssm_shape(nseq, nseq, D, N, dtype);
+    if (st != GLA_OK) return st;
+    if (nseq == 0) return GLA_OK;
+    SsmParams p{x, dt, z, Bm, Cm, (long)ld_x, (long)ld_dt, (long)ld_z, (long)ld_B, (long)ld_C, A, skip, dt_bias,
+                conv_w, conv_b, state_pool, state_pool, win_pool, nullptr, slots, n_slots, nseq, 1, D, N, softplus,
+                (long)nseq, y};
+    if ((st = check_ssm_pools(p)) != GLA_OK) return st;
+    if ((st = check_ssm_inputs(p, dtype)) != GLA_OK) return st;
+    REQUIRE_PTR(y, "y");
+    if (y == x || y == dt || y == z) return fail(GLA_ERR_INVALID_ARG, "y may not alias an input");
+    if ((st = status_word(&p.status)) != GLA_OK) return st;
+    int launches = 0;
+    const cudaError_t e = launch_ssm_step(p, dtype == GLA_BF16, static_cast<cudaStream_t>(stream), &launches);
+    t_launches = launches;
+    return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_ssm_step launch");
 }
 
 gla_status gla_selftest_wait_timeout(unsigned int limit_us, int *result, void *stream) {

@@ -109,6 +109,37 @@ cudaError_t launch_selftest_wait(unsigned int *status, uint64_t limit_ns, int *r
 cudaError_t launch_conv_fwd(const ConvParams &p, bool varlen, bool bf16, cudaStream_t s, int *launches);
 cudaError_t launch_conv_step(const ConvParams &p, bool bf16, cudaStream_t s, int *launches);
 
+// The selective state-space scan (ssm.cu, ssm_step.cu). Rows are tokens of
+// [rows, D] (x, dt, z; ld* = elements from one row to the next) and [rows, N]
+// (Bm, Cm) arrays; y is contiguous. Batched: nseq sequences of T tokens with
+// states at h0 / hT + n*D*N (either may be NULL). Packed (cu_seqlens) and
+// step: states in a pool, h0 == hT, and conv windows in win, at slots[n]
+// (NULL: n). seg_h, seg_sum: the workspace of a segmented run, or NULL.
+struct SsmParams {
+    const void *x, *dt, *z, *Bm, *Cm;
+    long ldx, ldt, ldz, ldb, ldc;
+    const float *A, *skip, *dt_bias, *conv_w, *conv_b;
+    const float *h0;
+    float *hT, *win;
+    const int *cu_seqlens, *slots;
+    int n_slots, nseq, T, D, N, softplus;
+    long rows;                   // tokens in x
+    void *y;
+    float *seg_h, *seg_sum;      // [slots, D, N], [slots, D]
+    long L;                      // tokens per segment
+    int nseg;                    // segments per sequence (batched)
+    unsigned int *status;
+};
+// How a scan is cut: segments of L tokens, `slots` workspace slots (slots <=
+// nseq: not cut, no workspace).
+struct SsmPlan {
+    long L, slots;
+};
+SsmPlan plan_ssm(long nseq, long rows, int D, bool varlen);
+size_t ssm_workspace_bytes(const SsmPlan &plan, long nseq, int D, int N);
+cudaError_t launch_ssm_scan(const SsmParams &p, bool bf16, cudaStream_t s, int *launches);
+cudaError_t launch_ssm_step(const SsmParams &p, bool bf16, cudaStream_t s, int *launches);
+
 // SIMT kernels (any dk <= 128, dv <= 256; fp32 or bf16 elements).
 cudaError_t launch_fwd_simt(const FwdParams &p, bool bf16, cudaStream_t s, int *launches);
 cudaError_t launch_bwd_simt(const BwdParams &p, bool bf16, cudaStream_t s, int *launches);

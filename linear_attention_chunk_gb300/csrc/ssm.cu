@@ -1,0 +1,408 @@
+// ssm.cu -- the selective state-space scan over prompts and training
+// sequences, with the causal depthwise Conv1d fused in front when asked.
+//
+// Per sequence, channel d and state n, with delta = softplus(dt + bias):
+//     h_t = exp(delta_t A[d][n]) h_{t-1} + delta_t B_t[n] u_t[d]
+//     y_t = (sum_n C_t[n] h_t + skip[d] u_t[d]) SiLU(z_t[d])
+// The decay differs by channel and state, so a chunk has no matrix-product
+// form (the decays do not factor into one weight per token pair): the work is
+// one exponential and four fp32 operations per (token, channel, state).
+//
+// Layout: a CTA of W warps owns 8 W channels of one sequence (or of one
+// segment of it); a quad of lanes owns a channel, each lane N / 4 of its
+// states, in registers as fp32 pairs for the whole run. Tiles of 32 tokens:
+// every thread loads eight channels of one token (16-byte accesses; the next
+// tile's are in flight during the scan), forms the input u and the step
+// delta, and leaves (delta, delta, delta u, delta u) in shared memory, so the
+// scan's packed operands need no moves; then each warp walks the 32 tokens of
+// its eight channels; then the same thread that loaded a vector adds the
+// skip, applies the gate and stores it. Each elementwise value is computed
+// once, and the quad's sums over states are exchanged four tokens at a time.
+//
+// Sequences are cut into segments when they are too few to fill the GPU: one
+// launch runs every segment but a sequence's last (the first from the initial
+// state, the others from zero) and leaves its final state and the sum of its
+// steps; in the second launch each segment folds the ones before it,
+// h <- exp(A sum delta) h + h_local, and runs from there. No CTA waits on
+// another.
+#include "ssm_common.cuh"
+
+namespace gla {
+namespace {
+
+using namespace ssm;
+
+constexpr int kTile = 32;   // tokens per tile (one vector of 8 channels per thread)
+constexpr int kYPad = 8;    // floats: rows of y start 8 banks apart
+constexpr int kWarps = 8;
+constexpr int kMinBlocks = 2;
+
+template <int N, int W> constexpr int scan_smem_floats() {
+    return kTile * 8 * W * 4 + kTile * (8 * W + kYPad) + 2 * kTile * N;
+}
+
+// The unit's sequence, its segment and its tokens. False: nothing to do.
+struct Unit {
+    int seq, seg, slot;
+    long first;    // row of the sequence's first token
+    long len;      // tokens of the sequence
+    long base;     // first segment slot of the sequence in the workspace
+    int nseg;      // segments of the sequence
+};
+
+// Varlen: the segments of sequence n take the slots cu[n] / L + n, ... (as
+// many as ceil(length / L)): slots of different sequences cannot meet, and
+// no prefix sum is needed. Every thread returns the same answer.
+__device__ __forceinline__ bool find_unit(const SsmParams &p, long u, int *s_found, Unit &un) {
+    if (!p.cu_seqlens) {
+        un.seq = (int)(u / p.nseg);
+        un.seg = (int)(u % p.nseg);
+        un.slot = un.seq;
+        un.first = (long)un.seq * p.T;
+        un.len = p.T;
+        un.base = (long)un.seq * p.nseg;
+        un.nseg = p.nseg;
+        return true;
+    }
+    if (threadIdx.x == 0) *s_found = p.nseq;
+    __syncthreads();
+    for (int n = threadIdx.x; n < p.nseq; n += blockDim.x) {
+        const long s = p.cu_seqlens[n], e = p.cu_seqlens[n + 1];
+        const int slot = p.slots ? p.slots[n] : n;
+        if (s < 0 || e < s || e > p.rows || slot < 0 || slot >= p.n_slots) {
+            if (u == 0) atomicOr(p.status, kDevBadState);
+            continue;
+        }
+        const long b = s / p.L + n;
+        if (u >= b && u < b + (e - s + p.L - 1) / p.L) atomicMin(s_found, n);
+    }
+    __syncthreads();
+    const int n = *s_found;
+    if (n >= p.nseq) return false;
+    un.seq = n;
+    un.first = p.cu_seqlens[n];
+    un.len = p.cu_seqlens[n + 1] - un.first;
+    un.base = un.first / p.L + n;
+    un.seg = (int)(u - un.base);
+    un.nseg = (int)((un.len + p.L - 1) / p.L);
+    un.slot = p.slots ? p.slots[n] : n;
+    return true;
+}
+
+// u of one token for eight channels: SiLU of the width-4 filter over the
+// token's input and the three before it, from the window before the
+// sequence's first token (rows oldest first, the last four inputs).
+template <typename T>
+__device__ __forceinline__ void conv8(const SsmParams &p, const Unit &un, long row, int c, const Raw8<T> &now,
+                                      float (&u)[8]) {
+    float acc[8], w[kTaps][8];
+    param8(p.conv_b, c, 0.f, acc);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 f = __ldg(reinterpret_cast<const float4 *>(p.conv_w) + c + i);
+        w[0][i] = f.x; w[1][i] = f.y; w[2][i] = f.z; w[3][i] = f.w;
+    }
+#pragma unroll
+    for (int j = 0; j < kTaps; ++j) {
+        const long src = row - 3 + j;
+        float v[8];
+        if (j == 3) {
+            raw_unpack(now, v);
+        } else if (src >= un.first) {
+            raw_unpack(raw_load(static_cast<const T *>(p.x) + (size_t)src * p.ldx + c), v);
+        } else {
+            // plain loads: this launch rewrites the window later
+            const float4 *r = reinterpret_cast<const float4 *>(
+                p.win + ((size_t)un.slot * kTaps + (kTaps + src - un.first)) * p.D + c);
+            const float4 a = r[0], b = r[1];
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[j][i], v[i], acc[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = silu(acc[i]);
+}
+
+template <typename T, int N, int W, bool kFull, bool kConv>
+__global__ void __launch_bounds__(32 * W, kMinBlocks) ssm_scan_kernel(const SsmParams p, int tiles) {
+    constexpr int SP = N / 4, P = SP / 2, CH = 8 * W, YS = CH + kYPad, TH = 32 * W;
+    extern __shared__ __align__(16) float smem[];
+    float4 *sD = reinterpret_cast<float4 *>(smem);     // [kTile * W vectors][8], channels swizzled
+    float *sY = smem + kTile * CH * 4;                 // [kTile][YS]
+    float *sB = sY + kTile * YS;                       // [kTile][N]
+    float *sC = sB + kTile * N;
+    __shared__ int s_found;
+
+    const int c0 = (int)(blockIdx.x % (unsigned)tiles) * CH;
+    const long unit = blockIdx.x / (unsigned)tiles;
+    Unit un;
+    if (!find_unit(p, unit, &s_found, un)) return;
+    const long seg0 = (long)un.seg * p.L;
+    const long row0 = un.first + seg0;
+    const long ntok = min((long)p.L, un.len - seg0);
+    const bool last = seg0 + p.L >= un.len;
+    if (!kFull && last) return;
+
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, q = lane % 4;
+    // the vector this thread loads and stores: channels c .. c+7 of token vt of every tile
+    const int vt = tid / W, c = c0 + (tid % W) * kVec;
+    const bool vec_on = c < p.D;
+    // the channel and states this lane scans
+    const int ch = c0 + warp * 8 + lane / 4;
+    const bool ch_on = ch < p.D;
+
+    f2 a2[P], h[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        a2[i] = 0;
+        h[i] = 0;
+    }
+    const size_t cell = (size_t)ch * N + q * SP;       // of this lane's states in a [D, N] array
+    if (ch_on) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float2 a = __ldg(reinterpret_cast<const float2 *>(p.A + cell) + i);
+            a2[i] = f2_pack(a.x * kLog2e, a.y * kLog2e);
+        }
+        // The state entering the unit. The last segment of a sequence has no
+        // local pass, and its workspace slot keeps a copy of the initial state:
+        // the second launch overwrites the pool, and reads the copy instead.
+        const float *src = nullptr;
+        if (un.seg == 0 && (!kFull || un.nseg == 1)) {
+            src = p.h0 ? p.h0 + (size_t)un.slot * p.D * N + cell : nullptr;
+        } else if (kFull) {
+            src = p.seg_h + (size_t)(un.base + (un.seg == 0 ? un.nseg - 1 : 0)) * p.D * N + cell;
+        }
+        if (src) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float2 v = reinterpret_cast<const float2 *>(src)[i];
+                h[i] = f2_pack(v.x, v.y);
+            }
+        }
+        if (!kFull && un.seg == 0) {
+            float2 *dst = reinterpret_cast<float2 *>(p.seg_h + (size_t)(un.base + un.nseg - 1) * p.D * N + cell);
+#pragma unroll
+            for (int i = 0; i < P; ++i) dst[i] = f2_split(h[i]);
+        }
+        if (kFull) {                                   // the first segment's state is final; fold the others
+#pragma unroll 4
+            for (int s = 1; s < un.seg; ++s) {
+                const size_t k = (size_t)(un.base + s);
+                const float sum = p.seg_sum[k * p.D + ch];
+                const float2 *e = reinterpret_cast<const float2 *>(p.seg_h + k * p.D * N + cell);
+                const f2 ss = f2_pack(sum, sum);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const float2 v = e[i];
+                    h[i] = fma2(ex2_pair(mul2(ss, a2[i])), h[i], f2_pack(v.x, v.y));
+                }
+            }
+        }
+    }
+
+    float bias[8];
+    param8(vec_on ? p.dt_bias : nullptr, c, 0.f, bias);
+    float skip[8];
+    if (kFull) param8(vec_on ? p.skip : nullptr, c, 0.f, skip);
+
+    // one tile's inputs as they lie in memory
+    Raw8<T> rx, rd, rz;
+    constexpr int BN = (kTile * N + TH - 1) / TH;      // B (and C) elements per thread
+    T rb[BN], rc[BN];
+    auto fetch = [&](long t0) {
+        const long row = row0 + t0 + vt;
+        const bool on = vec_on && t0 + vt < ntok;
+        rx = on ? raw_load(static_cast<const T *>(p.x) + (size_t)row * p.ldx + c) : raw_zero<T>();
+        rd = on ? raw_load(static_cast<const T *>(p.dt) + (size_t)row * p.ldt + c) : raw_zero<T>();
+        if (kFull && p.z) rz = on ? raw_load(static_cast<const T *>(p.z) + (size_t)row * p.ldz + c) : raw_zero<T>();
+#pragma unroll
+        for (int i = 0; i < BN; ++i) {
+            const int e = tid + i * TH, t = e / N, n = e % N;
+            const bool in = e < kTile * N && t0 + t < ntok;
+            rb[i] = in ? static_cast<const T *>(p.Bm)[(size_t)(row0 + t0 + t) * p.ldb + n] : T(0.f);
+            if (kFull) rc[i] = in ? static_cast<const T *>(p.Cm)[(size_t)(row0 + t0 + t) * p.ldc + n] : T(0.f);
+        }
+    };
+    fetch(0);
+
+    float dsum = 0.f;
+    for (long t0 = 0; t0 < ntok; t0 += kTile) {
+        // ---- inputs of the tile: u, delta; zero steps past the end leave the state as it is
+        const bool on = vec_on && t0 + vt < ntok;
+        float u[8], dl[8];
+        raw_unpack(rd, dl);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            dl[i] += bias[i];
+            if (p.softplus) dl[i] = softplus(dl[i]);
+            if (!on) dl[i] = 0.f;
+        }
+        if (kConv) {
+            if (on) {
+                conv8(p, un, row0 + t0 + vt, c, rx, u);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = 0.f;
+            }
+        } else {
+            raw_unpack(rx, u);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float du = dl[i] * u[i];
+            sD[tid * 8 + (i ^ (tid & 7))] = make_float4(dl[i], dl[i], du, du);
+        }
+#pragma unroll
+        for (int i = 0; i < BN; ++i) {
+            const int e = tid + i * TH;
+            if (e < kTile * N) {
+                sB[e] = (float)rb[i];
+                if (kFull) sC[e] = (float)rc[i];
+            }
+        }
+        const Raw8<T> zc = rz;
+        __syncthreads();
+        if (t0 + kTile < ntok) fetch(t0 + kTile);
+
+        // ---- the scan: 32 tokens of this warp's eight channels
+#pragma unroll 2
+        for (int t = 0; t < kTile; t += 4) {
+            float part[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int v = (t + j) * W + warp;      // the vector that holds this token's channels
+                const ulonglong2 d = reinterpret_cast<const ulonglong2 *>(sD)[v * 8 + ((lane / 4) ^ (v & 7))];
+                const f2 *b = reinterpret_cast<const f2 *>(sB + (t + j) * N + q * SP);
+                const f2 *cc = reinterpret_cast<const f2 *>(sC + (t + j) * N + q * SP);
+                f2 y = 0;
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const f2 a = ex2_pair(mul2(d.x, a2[i]));
+                    h[i] = fma2(a, h[i], mul2(d.y, b[i]));
+                    if (kFull) y = i == 0 ? mul2(h[i], cc[i]) : fma2(h[i], cc[i], y);
+                }
+                if (kFull) {
+                    const float2 ys = f2_split(y);
+                    part[j] = ys.x + ys.y;
+                } else {
+                    dsum += f2_split(d.x).x;
+                }
+            }
+            if (kFull) sY[(t + q) * YS + warp * 8 + lane / 4] = quad_transpose_sum(part, lane);
+        }
+        __syncthreads();
+
+        // ---- skip, gate, store
+        if (kFull && on) {
+            const float *ys = sY + vt * YS + (tid % W) * kVec;
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = fmaf(skip[i], u[i], ys[i]);
+            if (p.z) {
+                float z[8];
+                raw_unpack(zc, z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] *= silu(z[i]);
+            }
+            store8(static_cast<T *>(p.y) + (size_t)(row0 + t0 + vt) * p.D + c, y);
+        }
+    }
+
+    // ---- the state after the unit
+    if (ch_on) {
+        float *dst = nullptr;
+        if (!kFull) dst = p.seg_h + (size_t)(un.base + un.seg) * p.D * N + cell;
+        else if (last && p.hT) dst = p.hT + (size_t)un.slot * p.D * N + cell;
+        if (dst) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) reinterpret_cast<float2 *>(dst)[i] = f2_split(h[i]);
+        }
+        if (!kFull && q == 0) p.seg_sum[(size_t)(un.base + un.seg) * p.D + ch] = dsum;
+    }
+    // ---- the window after the call: this CTA (the sequence's first tokens)
+    // is the only one that reads it, and has done so before the last barrier
+    if (kFull && kConv && un.seg == 0) {
+        for (int i = tid; i < CH; i += TH) {
+            const int cc = c0 + i;
+            if (cc >= p.D) break;
+            float *w = p.win + (size_t)un.slot * kTaps * p.D + cc;
+#pragma unroll
+            for (int k = 0; k < kTaps; ++k) {
+                const long src = un.len - kTaps + k;   // row k after the call; an old row has a larger index
+                w[(size_t)k * p.D] = src >= 0 ? Elem<T>::load(static_cast<const T *>(p.x) +
+                                                              (size_t)(un.first + src) * p.ldx + cc)
+                                              : w[(size_t)(kTaps + src) * p.D];
+            }
+        }
+    }
+}
+
+template <typename T, int N, bool kFull, bool kConv> cudaError_t launch(const SsmParams &p, long units, cudaStream_t s, int *launches) {
+    const int tiles = (p.D + 8 * kWarps - 1) / (8 * kWarps);
+    if ((long double)units * tiles > 2147483647.0L) return cudaErrorInvalidValue;
+    constexpr int bytes = scan_smem_floats<N, kWarps>() * (int)sizeof(float);
+    auto *kern = ssm_scan_kernel<T, N, kWarps, kFull, kConv>;
+    if (bytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+    }
+    kern<<<(unsigned)(units * tiles), 32 * kWarps, bytes, s>>>(p, tiles);
+    if (launches) ++*launches;
+    return cudaGetLastError();
+}
+
+template <typename T, int N, bool kConv> cudaError_t run(const SsmParams &p, cudaStream_t s, int *launches) {
+    const long units = p.cu_seqlens ? p.rows / p.L + p.nseq : (long)p.nseq * p.nseg;
+    if (p.seg_h) {
+        const cudaError_t e = launch<T, N, false, kConv>(p, units, s, launches);
+        if (e != cudaSuccess) return e;
+    }
+    return launch<T, N, true, kConv>(p, units, s, launches);
+}
+
+template <typename T, bool kConv> cudaError_t by_state(const SsmParams &p, cudaStream_t s, int *launches) {
+    switch (p.N) {
+    case 8: return run<T, 8, kConv>(p, s, launches);
+    case 16: return run<T, 16, kConv>(p, s, launches);
+    case 32: return run<T, 32, kConv>(p, s, launches);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_ssm_scan(const SsmParams &p, bool bf16, cudaStream_t s, int *launches) {
+    if (p.conv_w)
+        return bf16 ? by_state<__nv_bfloat16, true>(p, s, launches) : by_state<float, true>(p, s, launches);
+    return bf16 ? by_state<__nv_bfloat16, false>(p, s, launches) : by_state<float, false>(p, s, launches);
+}
+
+// The segment length: a multiple of the tile, long enough that the first
+// launch's work (about 0.9 of the second's) buys parallelism.
+SsmPlan plan_ssm(long nseq, long rows, int D, bool varlen) {
+    const long warps = nseq * ((D + 7) / 8);
+    const long want = (long)device_sm_count() * 12;
+    const long mean = nseq > 0 ? (rows + nseq - 1) / nseq : 0;
+    SsmPlan pl{rows > 0 ? rows : 1, 1};
+    if (rows <= 0 || nseq <= 0) return pl;
+    if (!varlen && warps >= want) return SsmPlan{mean, 1};
+    long nseg = (2 * want + warps - 1) / warps;
+    long L = (mean + nseg - 1) / nseg;
+    L = (L + 127) / 128 * 128;
+    if (varlen && L > 512) L = 512;
+    if (!varlen && L >= mean) return SsmPlan{mean, 1};
+    if (varlen && L >= rows) return SsmPlan{rows, nseq};
+    pl.L = L;
+    pl.slots = varlen ? rows / L + nseq : nseq * ((mean + L - 1) / L);
+    return pl;
+}
+
+// Segment states and sums of steps, [slots, D, N] and [slots, D] fp32.
+size_t ssm_workspace_bytes(const SsmPlan &plan, long nseq, int D, int N) {
+    return plan.slots <= nseq ? 0 : (size_t)plan.slots * D * (N + 1) * sizeof(float);
+}
+
+}  // namespace gla

@@ -1,0 +1,147 @@
+// ssm_common.cuh -- device helpers of the selective state-space kernels
+// (ssm.cu, ssm_step.cu, ssm_bwd.cu): fp32 pairs, the step's softplus and the
+// SiLU gate, and vectors of eight channels in either element type.
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace gla {
+namespace ssm {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTaps = 4;
+constexpr int kVec = 8;   // channels a thread loads and stores at once
+
+// Two fp32 numbers in a 64-bit register pair: the packed instructions do two
+// multiply-adds an issue slot (at the same rate per lane as the scalar ones).
+using f2 = uint64_t;
+
+__device__ __forceinline__ f2 f2_pack(float lo, float hi) {
+    f2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 f2_split(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {   // 2^x, relative error below 1.5e-7 (measured on [-4, 0])
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ f2 ex2_pair(f2 x) {
+    const float2 v = f2_split(x);
+    return f2_pack(ex2(v.x), ex2(v.y));
+}
+
+// log(1 + e^v) = max(v, 0) + log1p(w), w = e^-|v| in (0, 1], by the series
+// log1p(w) = 2 atanh(s) = 2 (s + s^3/3 + s^5/5 + ...), s = w / (2 + w) <= 1/3:
+// eight terms leave 2 s^17 / 17 < 1e-9. Relative to the result, not to 1: a
+// step of 1e-3 keeps fp32's precision, which log(1 + w) would lose.
+__device__ __forceinline__ float softplus(float v) {
+    const float w = ex2(-fabsf(v) * kLog2e);
+    const float s = w * rcp(2.f + w);
+    const float q = s * s;
+    float r = 1.f / 15.f;
+    r = fmaf(r, q, 1.f / 13.f);
+    r = fmaf(r, q, 1.f / 11.f);
+    r = fmaf(r, q, 1.f / 9.f);
+    r = fmaf(r, q, 1.f / 7.f);
+    r = fmaf(r, q, 1.f / 5.f);
+    r = fmaf(r, q, 1.f / 3.f);
+    r = fmaf(r * q, s, s);
+    return fmaf(2.f, r, fmaxf(v, 0.f));
+}
+__device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(-v * kLog2e)); }
+__device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
+
+// Eight consecutive channels as they lie in memory.
+template <typename T> struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+};
+
+template <typename T> __device__ __forceinline__ Raw8<T> raw_zero() {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = make_uint4(0, 0, 0, 0);
+    return r;
+}
+template <typename T> __device__ __forceinline__ Raw8<T> raw_load(const T *p) {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    return r;
+}
+__device__ __forceinline__ void raw_unpack(const Raw8<__nv_bfloat16> &r, float (&v)[8]) {
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void raw_unpack(const Raw8<float> &r, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        v[4 * i] = __uint_as_float(r.w[i].x);
+        v[4 * i + 1] = __uint_as_float(r.w[i].y);
+        v[4 * i + 2] = __uint_as_float(r.w[i].z);
+        v[4 * i + 3] = __uint_as_float(r.w[i].w);
+    }
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+// Eight fp32 parameters of consecutive channels, or `fill` without an array.
+__device__ __forceinline__ void param8(const float *p, int c, float fill, float (&v)[8]) {
+    if (p) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(p + c));
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(p + c) + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fill;
+    }
+}
+
+// Four numbers, one per token, each spread over the four lanes of a quad:
+// returns the sum of number (lane % 4), in three exchanges.
+__device__ __forceinline__ float quad_transpose_sum(const float (&v)[4], int lane) {
+    const bool hi = lane & 2, lo = lane & 1;
+    float k0 = hi ? v[2] : v[0], k1 = hi ? v[3] : v[1];
+    k0 += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 2);
+    k1 += __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 2);
+    const float k = lo ? k1 : k0;
+    return k + __shfl_xor_sync(0xffffffffu, lo ? k0 : k1, 1);
+}
+__device__ __forceinline__ float quad_sum(float v) {
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+}  // namespace ssm
+}  // namespace gla
