@@ -399,7 +399,7 @@ gla_status gla_conv1d_step(const void *x, const float *w, const float *b, float 
  *   A [D, N] fp32 (negative for a decay; not its logarithm), skip [D] fp32 or
  *     NULL (0), dt_bias [D] fp32 or NULL (0), z or NULL (no gate).
  *   y: contiguous rows of D. States [*, D, N] fp32, N fastest.
- *   D a multiple of 8; N = 8, 16 or 32. y may not be x, dt or z.
+ *   D a multiple of 8 (bf16) or 4 (fp32); N = 8, 16 or 32. y may not be x, dt or z.
  *
  * gla_ssm_fwd: B sequences of T tokens, x, dt, z, y [B, T, D], Bm, Cm
  *   [B, T, N] (token rows ld_* apart throughout, b-th sequence's first row at
@@ -438,6 +438,47 @@ gla_status gla_ssm_step(const void *x, int64_t ld_x, const void *dt, int64_t ld_
                         const float *dt_bias, int softplus, const float *conv_w, const float *conv_b, const int *slots,
                         float *state_pool, float *win_pool, int n_slots, int nseq, int D, int N, gla_dtype dtype,
                         void *y, void *stream);
+
+/*
+ * gla_conv1d_bwd -- gradients of L = sum_t <dy_t, y_t> through gla_conv1d_fwd
+ * (the same x, w, b and win_in): dx [B, T, D] of `dtype`, dw [D, 4] and db [D]
+ * fp32 (db or NULL: not wanted). The window is a constant: it gets no
+ * gradient, and none comes from a later call through win_out. dx may not be
+ * x or dy. workspace: at least gla_conv1d_bwd_workspace_size() bytes (partial
+ * sums of dw and db; required when B*T > 0). Sums run in a fixed order: the
+ * same call gives the same bits. B*T = 0 zeroes dw and db.
+ */
+gla_status gla_conv1d_bwd(const void *x, const float *w, const float *b, const void *dy, const float *win_in, int B,
+                          int T, int D, gla_dtype dtype, void *dx, float *dw, float *db, void *workspace,
+                          size_t workspace_bytes, void *stream);
+size_t gla_conv1d_bwd_workspace_size(int B, int T, int D, gla_dtype dtype);
+
+/*
+ * The norm in front of a mixer layer, over rows of D channels:
+ *     s = x + res,   y = s w / sqrt(mean(s^2) + eps)
+ * gla_rmsnorm_fwd: x, res [rows, D] of `dtype` (res NULL: s = x), w [D] fp32
+ *   or NULL (one), eps >= 0. Any of: s_out [rows, D] (s rounded to `dtype`; may
+ *   be res or x), y [rows, D] of `dtype`, and y8 [rows, D] e4m3 with its scales,
+ *   y = y8 * scale: group 32, 64 or 128 channels a scale (scale
+ *   [rows, ceil(D / group)] fp32, the last block shorter) or 0 for one a row
+ *   (scale [rows]). scale = max|y| / 448 over the block, at least 2^-126, and 1
+ *   where every y is 0; a NaN in a block makes its scale NaN. y and y8 are each
+ *   rounded once, from fp32. y and y8 may not overlap an input.
+ * gla_rmsnorm_bwd: gradients of L = <dy, y> + <ds, s> with s given: with
+ *   xn = s / sqrt(mean(s^2) + eps) and g = dy w,
+ *     dx = ds + (g - xn mean(g xn)) / sqrt(mean(s^2) + eps)   (x's and res's alike)
+ *     dw = sum over rows of dy xn
+ *   s, dy, ds (or NULL: zero), dx [rows, D] of `dtype` (dx may be dy or ds),
+ *   dw [D] fp32 or NULL (not wanted); workspace: at least
+ *   gla_rmsnorm_bwd_workspace_size() bytes when dw is wanted and rows > 0.
+ *   rows = 0 zeroes dw. Sums run in a fixed order.
+ * D a multiple of 8 (bf16) or 4 (fp32), at most 8192.
+ */
+gla_status gla_rmsnorm_fwd(const void *x, const void *res, const float *w, float eps, int64_t rows, int D, int group,
+                           gla_dtype dtype, void *s_out, void *y, void *y8, float *scale, void *stream);
+gla_status gla_rmsnorm_bwd(const void *s, const float *w, const void *dy, const void *ds, float eps, int64_t rows, int D,
+                           gla_dtype dtype, void *dx, float *dw, void *workspace, size_t workspace_bytes, void *stream);
+size_t gla_rmsnorm_bwd_workspace_size(int64_t rows, int D, gla_dtype dtype);
 
 /*
  * gla_selftest_wait_timeout -- diagnostic of the device-side failure

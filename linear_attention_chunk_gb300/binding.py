@@ -25,6 +25,10 @@ Functions:
   gla_ssm_fwd(x, dt, A, Bm, Cm, skip=None, z=None, dt_bias=None, h0=None) -> (y, hT)  selective scan
   gla_ssm_varlen(x, dt, A, Bm, Cm, cu_seqlens, state_pool, ...)           -> y  (pools updated)
   gla_ssm_step(x, dt, A, Bm, Cm, state_pool, ...)                         -> y  (pools updated)
+  gla_conv1d_bwd(x, w, b, dy, win_in=None)                                -> (dx, dw, db)
+  gla_rmsnorm(x, w=None, res=None, eps=1e-6)                              -> (y, s)  s = x + res
+  gla_rmsnorm_q8(x, w=None, res=None, eps=1e-6, group=128)                -> (y8 e4m3, scale, s)
+  gla_rmsnorm_bwd(s, w, dy, ds=None, eps=1e-6)                            -> (dx, dw)
   gla_check(stream=None), gla_status_string(code), gla_version()
   gla_chunk_fwd_workspace_size(...), gla_chunk_bwd_workspace_size(...)
 `lib()` returns the loaded ctypes library for callers that hold raw pointers.
@@ -47,7 +51,9 @@ ABI_FUNCTIONS = ("gla_chunk_fwd", "gla_chunk_fwd_workspace_size", "gla_chunk_fwd
                  "gla_chunk_fwd_mixer", "gla_chunk_fwd_gated", "gla_chunk_fwd_gated_workspace_size", "gla_decode_step_gated", "gla_chunk_bwd",
                  "gla_chunk_bwd_workspace_size", "gla_chunk_bwd_gated", "gla_chunk_bwd_gated_workspace_size", "gla_decode_step", "gla_decode_step_mixer", "gla_mixer_epilogue",
                  "gla_conv1d_fwd", "gla_conv1d_varlen", "gla_conv1d_step", "gla_ssm_fwd", "gla_ssm_fwd_workspace_size",
-                 "gla_ssm_varlen", "gla_ssm_varlen_workspace_size", "gla_ssm_step", "gla_selftest_wait_timeout", "gla_check",
+                 "gla_ssm_varlen", "gla_ssm_varlen_workspace_size", "gla_ssm_step",
+                 "gla_conv1d_bwd", "gla_conv1d_bwd_workspace_size", "gla_rmsnorm_fwd", "gla_rmsnorm_bwd",
+                 "gla_rmsnorm_bwd_workspace_size", "gla_selftest_wait_timeout", "gla_check",
                  "gla_status_string", "gla_last_error", "gla_last_launch_count", "gla_version")
 
 
@@ -135,6 +141,16 @@ def lib():
             L.gla_ssm_varlen_workspace_size.restype = _sz
             L.gla_ssm_step.argtypes = rows + [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp]
             L.gla_ssm_step.restype = _i
+            L.gla_conv1d_bwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]
+            L.gla_conv1d_bwd.restype = _i
+            L.gla_conv1d_bwd_workspace_size.argtypes = [_i, _i, _i, _i]
+            L.gla_conv1d_bwd_workspace_size.restype = _sz
+            L.gla_rmsnorm_fwd.argtypes = [_vp, _vp, _vp, _f, _ll, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]
+            L.gla_rmsnorm_fwd.restype = _i
+            L.gla_rmsnorm_bwd.argtypes = [_vp, _vp, _vp, _vp, _f, _ll, _i, _i, _vp, _vp, _vp, _sz, _vp]
+            L.gla_rmsnorm_bwd.restype = _i
+            L.gla_rmsnorm_bwd_workspace_size.argtypes = [_ll, _i, _i]
+            L.gla_rmsnorm_bwd_workspace_size.restype = _sz
             L.gla_selftest_wait_timeout.argtypes = [ctypes.c_uint, _vp, _vp]
             L.gla_selftest_wait_timeout.restype = _i
             L.gla_check.argtypes = [_vp]
@@ -711,6 +727,87 @@ def gla_ssm_step(x, dt, A, Bm, Cm, state_pool, skip=None, z=None, dt_bias=None, 
         y = c.empty((n, D))
     c.run("gla_ssm_step", *args, w, b, sl, pool, win, k, n, D, N, c.code, c.whole(y, (n, D), "y"))
     return y
+
+
+def gla_conv1d_bwd_workspace_size(B, T, D, dtype=GLA_BF16) -> int:
+    return int(lib().gla_conv1d_bwd_workspace_size(B, T, D, dtype))
+
+
+def gla_conv1d_bwd(x, w, b, dy, win_in=None, *, dx=None, dw=None, db=None, want_db=True, workspace=None, stream=None):
+    """Gradients of gla_conv1d_fwd (its y without the window it leaves): x, dy
+    [B,T,D], w [D,4], b [D] or None, win_in [B,4,D] or None (a constant).
+    Returns (dx, dw, db); db None with want_db=False."""
+    B, T, D = _lead(x, 3, "x")
+    c = _Call(x, stream)
+    f32 = c.torch.float32
+    args = (c.whole(x, x.shape, "x"), c.f32(w, (D, 4), "w"), c.f32(b, (D,), "b"), c.whole(dy, x.shape, "dy"),
+            c.f32(win_in, (B, 4, D), "win_in"))
+    dx = c.empty((B, T, D)) if dx is None else dx
+    dw = c.empty((D, 4), f32) if dw is None else dw
+    if db is None and want_db:
+        db = c.empty((D,), f32)
+    need = gla_conv1d_bwd_workspace_size(B, T, D, c.code) if workspace is None else 0
+    c.run("gla_conv1d_bwd", *args, B, T, D, c.code, c.whole(dx, x.shape, "dx"), c.f32(dw, (D, 4), "dw"),
+          c.f32(db, (D,), "db"), *c.scratch(workspace, need))
+    return dx, dw, db
+
+
+def _norm_rows(x):
+    if x.dim() < 1:
+        raise GlaError(GLA_ERR_INVALID_ARG, "argument", "x has no channels")
+    D = x.shape[-1]
+    return (x.numel() // D if D else 0), D
+
+
+def gla_rmsnorm(x, w=None, res=None, eps=1e-6, *, y=None, s=None, stream=None):
+    """Residual addition and RMSNorm over the last dimension: x, res [..., D],
+    w [D] fp32 or None. Returns (y, s): s = x + res (may be given as res, in
+    place), or None without res; y = s w / sqrt(mean(s^2) + eps)."""
+    rows, D = _norm_rows(x)
+    c = _Call(x, stream)
+    y = c.empty(x.shape) if y is None else y
+    if s is None and res is not None:
+        s = c.empty(x.shape)
+    c.run("gla_rmsnorm_fwd", c.whole(x, x.shape, "x"), c.whole(res, x.shape, "res"), c.f32(w, (D,), "w"), float(eps),
+          rows, D, 0, c.code, c.whole(s, x.shape, "s"), c.whole(y, x.shape, "y"), None, None)
+    return y, s
+
+
+def gla_rmsnorm_q8(x, w=None, res=None, eps=1e-6, group=128, *, y8=None, scale=None, s=None, stream=None):
+    """gla_rmsnorm with its output in 8 bits: y8 [..., D] float8_e4m3fn and
+    scale fp32, y = y8 * scale: [..., ceil(D / group)] for group 32, 64 or 128
+    channels a scale, [..., 1] for group 0 (one a row). Returns (y8, scale, s)."""
+    rows, D = _norm_rows(x)
+    c = _Call(x, stream)
+    shape = x.shape[:-1] + (-(-D // group) if group > 0 else 1,)
+    y8 = c.empty(x.shape, c.torch.float8_e4m3fn) if y8 is None else y8
+    scale = c.empty(shape, c.torch.float32) if scale is None else scale
+    if s is None and res is not None:
+        s = c.empty(x.shape)
+    c.run("gla_rmsnorm_fwd", c.whole(x, x.shape, "x"), c.whole(res, x.shape, "res"), c.f32(w, (D,), "w"), float(eps),
+          rows, D, int(group), c.code, c.whole(s, x.shape, "s"), None,
+          c.whole(y8, x.shape, "y8", c.torch.float8_e4m3fn), c.f32(scale, shape, "scale"))
+    return y8, scale, s
+
+
+def gla_rmsnorm_bwd_workspace_size(rows, D, dtype=GLA_BF16) -> int:
+    return int(lib().gla_rmsnorm_bwd_workspace_size(rows, D, dtype))
+
+
+def gla_rmsnorm_bwd(s, w, dy, ds=None, eps=1e-6, *, dx=None, dw=None, want_dw=True, workspace=None, stream=None):
+    """Gradients of gla_rmsnorm: s (x + res, or x), dy, ds (the gradient that
+    reaches s itself, or None) [..., D], w [D] or None. Returns (dx, dw): dx is
+    x's and res's alike, dw [D] fp32 (None with want_dw=False)."""
+    rows, D = _norm_rows(s)
+    c = _Call(s, stream)
+    args = (c.whole(s, s.shape, "s"), c.f32(w, (D,), "w"), c.whole(dy, s.shape, "dy"), c.whole(ds, s.shape, "ds"))
+    dx = c.empty(s.shape) if dx is None else dx
+    if dw is None and want_dw:
+        dw = c.empty((D,), c.torch.float32)
+    need = gla_rmsnorm_bwd_workspace_size(rows, D, c.code) if workspace is None and dw is not None else 0
+    c.run("gla_rmsnorm_bwd", *args, float(eps), rows, D, c.code, c.whole(dx, s.shape, "dx"), c.f32(dw, (D,), "dw"),
+          *c.scratch(workspace, need))
+    return dx, dw
 
 
 def gla_selftest_wait_timeout(limit_us=20000, *, stream=None):

@@ -1,0 +1,184 @@
+// conv_bwd.cu -- the gradients of the causal depthwise Conv1d (width 4) with
+// SiLU, per channel, with a_t = sum_j w_j x_{t-3+j} + b and sg = sigmoid(a):
+//     dp_t = dy_t sg_t (1 + a_t (1 - sg_t))
+//     dx_t = sum_j w_j dp_{t+3-j},   dw_j = sum_t dp_t x_{t-3+j},   db = sum_t dp_t
+// (dp past the sequence's end is 0; x before its first token is the window,
+// a constant).
+//
+// A stream: 6 bytes an element at bf16 (x, dy in, dx out). A thread owns four
+// channels over a tile of tokens and walks it forward with the last three x
+// and dp in registers, so dx lags three tokens behind, and reads three tokens
+// past the tile's end for it (the tile's own sums leave those out). Eight
+// tokens' loads are issued at once. dw and db stay in registers and leave once
+// per tile as partial sums, added in a second launch (reduce.cu).
+#include "ssm_common.cuh"
+
+namespace gla {
+namespace {
+
+using namespace ssm;
+
+constexpr int kThreads = 128;   // 512 channels a CTA
+constexpr int kStep = 8;        // tokens loaded at once
+
+template <typename T> struct Raw4 {
+    uint2 w[sizeof(T) / 2];
+};
+template <typename T> __device__ __forceinline__ Raw4<T> load4(const T *p) {
+    Raw4<T> r;
+    if constexpr (sizeof(T) == 2) {
+        r.w[0] = __ldg(reinterpret_cast<const uint2 *>(p));
+    } else {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+        r.w[0] = make_uint2(u.x, u.y);
+        r.w[1] = make_uint2(u.z, u.w);
+    }
+    return r;
+}
+template <typename T> __device__ __forceinline__ Raw4<T> zero4() {
+    Raw4<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = make_uint2(0, 0);
+    return r;
+}
+__device__ __forceinline__ void unpack4(const Raw4<__nv_bfloat16> &r, f2 (&v)[2]) {
+    v[0] = f2_pack(__uint_as_float(r.w[0].x << 16), __uint_as_float(r.w[0].x & 0xffff0000u));
+    v[1] = f2_pack(__uint_as_float(r.w[0].y << 16), __uint_as_float(r.w[0].y & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack4(const Raw4<float> &r, f2 (&v)[2]) {
+    v[0] = f2_pack(__uint_as_float(r.w[0].x), __uint_as_float(r.w[0].y));
+    v[1] = f2_pack(__uint_as_float(r.w[1].x), __uint_as_float(r.w[1].y));
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, f2 a, f2 b) {
+    const float2 u = f2_split(a), v = f2_split(b);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(u.x, u.y), pack_bf16x2(v.x, v.y));
+}
+__device__ __forceinline__ void store4(float *p, f2 a, f2 b) {
+    const float2 u = f2_split(a), v = f2_split(b);
+    *reinterpret_cast<float4 *>(p) = make_float4(u.x, u.y, v.x, v.y);
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvBwdParams p, int blocks, int tiles) {
+    const int c = ((int)(blockIdx.x % (unsigned)blocks) * kThreads + threadIdx.x) * 4;
+    const long unit = blockIdx.x / (unsigned)blocks;
+    if (c >= p.D) return;
+    const long b = unit / tiles, t0 = unit % tiles * p.tile, t1 = min(t0 + p.tile, (long)p.T);
+    const size_t D = (size_t)p.D;
+    const T *x = static_cast<const T *>(p.x) + (size_t)b * p.T * D + c;
+    const T *dy = static_cast<const T *>(p.dy) + (size_t)b * p.T * D + c;
+    T *dx = static_cast<T *>(p.dx) + (size_t)b * p.T * D + c;
+
+    f2 w[kTaps][2], bias[2] = {0, 0}, dw[kTaps][2], db[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const float4 u = __ldg(reinterpret_cast<const float4 *>(p.w) + c + 2 * e);
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(p.w) + c + 2 * e + 1);
+        w[0][e] = f2_pack(u.x, v.x);
+        w[1][e] = f2_pack(u.y, v.y);
+        w[2][e] = f2_pack(u.z, v.z);
+        w[3][e] = f2_pack(u.w, v.w);
+        if (p.b) bias[e] = f2_pack(p.b[c + 2 * e], p.b[c + 2 * e + 1]);
+#pragma unroll
+        for (int j = 0; j < kTaps; ++j) dw[j][e] = 0;
+    }
+    f2 h[3][2], dp[3][2];           // x and dp of the three tokens before
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        const long t = t0 - 3 + j;
+        if (t >= 0) {
+            unpack4(load4(x + (size_t)t * D), h[j]);
+        } else if (p.win) {
+            const float *r = p.win + ((size_t)b * kTaps + kTaps + t) * D + c;
+            h[j][0] = f2_pack(r[0], r[1]);
+            h[j][1] = f2_pack(r[2], r[3]);
+        } else {
+            h[j][0] = h[j][1] = 0;
+        }
+        dp[j][0] = dp[j][1] = 0;
+    }
+    const f2 one = f2_pack(1.f, 1.f), neg = f2_pack(-kLog2e, -kLog2e), minus = f2_pack(-1.f, -1.f);
+    for (long t = t0; t < t1 + 3; t += kStep) {
+        Raw4<T> rx[kStep], ry[kStep];
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) {
+            const bool in = t + i < min(t1 + 3, (long)p.T);
+            rx[i] = in ? load4(x + (size_t)(t + i) * D) : zero4<T>();
+            ry[i] = in ? load4(dy + (size_t)(t + i) * D) : zero4<T>();
+        }
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) {
+            const bool own = t + i < t1, past = t + i >= p.T;
+            f2 xv[2], g[2], o[2];
+            unpack4(rx[i], xv);
+            unpack4(ry[i], g);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                f2 a = fma2(w[0][e], h[0][e], bias[e]);
+                a = fma2(w[1][e], h[1][e], a);
+                a = fma2(w[2][e], h[2][e], a);
+                a = fma2(w[3][e], xv[e], a);
+                const float2 n = f2_split(mul2(a, neg));
+                const f2 sg = f2_pack(rcp(1.f + ex2(n.x)), rcp(1.f + ex2(n.y)));
+                // sg (1 + a (1 - sg)); where a overflows the exponential, sg = 0 and a (1 - sg) is finite
+                f2 d = mul2(g[e], mul2(sg, fma2(a, fma2(sg, minus, one), one)));
+                if (past) d = 0;
+                if (own) {
+                    dw[0][e] = fma2(d, h[0][e], dw[0][e]);
+                    dw[1][e] = fma2(d, h[1][e], dw[1][e]);
+                    dw[2][e] = fma2(d, h[2][e], dw[2][e]);
+                    dw[3][e] = fma2(d, xv[e], dw[3][e]);
+                    db[e] = fma2(d, one, db[e]);
+                }
+                o[e] = mul2(w[0][e], d);
+                o[e] = fma2(w[1][e], dp[2][e], o[e]);
+                o[e] = fma2(w[2][e], dp[1][e], o[e]);
+                o[e] = fma2(w[3][e], dp[0][e], o[e]);
+                h[0][e] = h[1][e];
+                h[1][e] = h[2][e];
+                h[2][e] = xv[e];
+                dp[0][e] = dp[1][e];
+                dp[1][e] = dp[2][e];
+                dp[2][e] = d;
+            }
+            const long to = t + i - 3;
+            if (to >= t0 && to < t1) store4(dx + (size_t)to * D, o[0], o[1]);
+        }
+    }
+    // partials: [D, 4] of dw, then [D] of db
+    float *part = p.part + (size_t)unit * 5 * D;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const float2 a = f2_split(dw[0][e]), bb = f2_split(dw[1][e]), cc = f2_split(dw[2][e]), d = f2_split(dw[3][e]);
+        reinterpret_cast<float4 *>(part)[c + 2 * e] = make_float4(a.x, bb.x, cc.x, d.x);
+        reinterpret_cast<float4 *>(part)[c + 2 * e + 1] = make_float4(a.y, bb.y, cc.y, d.y);
+        *reinterpret_cast<float2 *>(part + 4 * D + c + 2 * e) = f2_split(db[e]);
+    }
+}
+
+}  // namespace
+
+// Tokens per tile: long enough that the three extra tokens and the partial
+// sums (20 bytes a channel and tile) stay small, short enough to give every
+// SM four CTAs.
+int conv_bwd_tile(int B, int T, int D) {
+    const long blocks = (D + 4 * kThreads - 1) / (4 * kThreads), want = 4L * device_sm_count();
+    int tile = 128;
+    while (tile > 16 && (long)B * ((T + tile - 1) / tile) * blocks < want) tile /= 2;
+    return tile;
+}
+
+cudaError_t launch_conv_bwd(const ConvBwdParams &p, bool bf16, cudaStream_t s, int *launches) {
+    const int blocks = (p.D + 4 * kThreads - 1) / (4 * kThreads), tiles = (p.T + p.tile - 1) / p.tile;
+    const long units = (long)p.B * tiles;
+    if ((long double)units * blocks > 2147483647.0L) return cudaErrorInvalidValue;
+    if (bf16) conv_bwd_kernel<__nv_bfloat16><<<(unsigned)(units * blocks), kThreads, 0, s>>>(p, blocks, tiles);
+    else conv_bwd_kernel<float><<<(unsigned)(units * blocks), kThreads, 0, s>>>(p, blocks, tiles);
+    if (launches) ++*launches;
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = launch_sum_rows(p.part, units, 4L * p.D, 5L * p.D, p.dw, s, launches);
+    if (e != cudaSuccess) return e;
+    return launch_sum_rows(p.part + 4L * p.D, units, p.D, 5L * p.D, p.db, s, launches);
+}
+
+}  // namespace gla

@@ -140,6 +140,16 @@ gla_status decode_common(const void *q, const void *k, const void *v, const floa
     return e == cudaSuccess ? GLA_OK : cuda_fail(e, "decode launch");
 }
 
+gla_status check_norm_shape(int64_t rows, int D, gla_dtype dtype) {
+    if (dtype != GLA_BF16 && dtype != GLA_FP32) return fail(GLA_ERR_INVALID_ARG, "dtype %d is not GLA_BF16/GLA_FP32", (int)dtype);
+    if (rows < 0 || rows > 2147483647ll) return fail(GLA_ERR_INVALID_ARG, "rows=%lld out of range", (long long)rows);
+    const int vec = dtype == GLA_BF16 ? 8 : 4;
+    if (D <= 0 || D % vec != 0 || D > 8192)
+        return fail(GLA_ERR_UNSUPPORTED, "D=%d must be a positive multiple of %d, at most 8192", D, vec);
+    if ((long double)rows * D > (long double)(1ull << 40)) return fail(GLA_ERR_INVALID_ARG, "tensor too large");
+    return GLA_OK;
+}
+
 // A [rows, cols] array of a selective-scan call: pointer, row step, alignment.
 gla_status check_rows(const void *ptr, int64_t ld, int cols, int elem, bool vector, const char *name) {
     if (!ptr) return fail(GLA_ERR_INVALID_ARG, "%s is NULL", name);
@@ -154,7 +164,8 @@ gla_status check_rows(const void *ptr, int64_t ld, int cols, int elem, bool vect
 gla_status check_ssm_shape(int64_t seqs, int64_t rows, int D, int N, gla_dtype dtype) {
     if (dtype != GLA_BF16 && dtype != GLA_FP32) return fail(GLA_ERR_INVALID_ARG, "dtype %d is not GLA_BF16/GLA_FP32", (int)dtype);
     if (seqs < 0 || rows < 0) return fail(GLA_ERR_INVALID_ARG, "negative size (sequences %lld, tokens %lld)", (long long)seqs, (long long)rows);
-    if (D <= 0 || D % 8 != 0) return fail(GLA_ERR_UNSUPPORTED, "D=%d must be a positive multiple of 8", D);
+    const int vec = dtype == GLA_BF16 ? 8 : 4;
+    if (D <= 0 || D % vec != 0) return fail(GLA_ERR_UNSUPPORTED, "D=%d must be a positive multiple of %d", D, vec);
     if (N != 8 && N != 16 && N != 32) return fail(GLA_ERR_UNSUPPORTED, "N=%d is not 8, 16 or 32", N);
     // one CTA per 64 channels of a sequence or segment: well inside a 1-D grid
     if ((long double)(seqs + rows) * ((D + 63) / 64) > 2147483647.0L || (long double)rows * D > (long double)(1ull << 40))
@@ -754,6 +765,112 @@ gla_status gla_ssm_step(const void *x, int64_t ld_x, const void *dt, int64_t ld_
     const cudaError_t e = launch_ssm_step(p, dtype == GLA_BF16, static_cast<cudaStream_t>(stream), &launches);
     t_launches = launches;
     return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_ssm_step launch");
+}
+
+size_t gla_conv1d_bwd_workspace_size(int B, int T, int D, gla_dtype dtype) {
+    if (check_conv_shape(B, T, D, dtype) != GLA_OK || B == 0 || T == 0) return 0;
+    const int tile = conv_bwd_tile(B, T, D);
+    return (size_t)B * ((T + tile - 1) / tile) * 5 * D * sizeof(float);
+}
+
+gla_status gla_conv1d_bwd(const void *x, const float *w, const float *b, const void *dy, const float *win_in, int B,
+                          int T, int D, gla_dtype dtype, void *dx, float *dw, float *db, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+    t_err[0] = 0;
+    t_launches = 0;
+    gla_status st = check_conv_shape(B, T, D, dtype);
+    if (st != GLA_OK) return st;
+    OPTIONAL_PTR(b, "b");
+    OPTIONAL_PTR(win_in, "win_in");
+    OPTIONAL_PTR(db, "db");
+    REQUIRE_PTR(dw, "dw");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int launches = 0;
+    if (B == 0 || T == 0) {   // no tokens: the sums are empty
+        cudaError_t e = cudaMemsetAsync(dw, 0, (size_t)D * 4 * sizeof(float), s);
+        if (e == cudaSuccess && db) e = cudaMemsetAsync(db, 0, (size_t)D * sizeof(float), s);
+        return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_conv1d_bwd(no tokens)");
+    }
+    REQUIRE_PTR(w, "w");
+    REQUIRE_PTR(x, "x");
+    REQUIRE_PTR(dy, "dy");
+    REQUIRE_PTR(dx, "dx");
+    if (dx == x || dx == dy) return fail(GLA_ERR_INVALID_ARG, "dx may not alias x or dy");
+    REQUIRE_PTR(workspace, "workspace");
+    const size_t need = gla_conv1d_bwd_workspace_size(B, T, D, dtype);
+    if (workspace_bytes < need)
+        return fail(GLA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+    ConvBwdParams p{x, dy, w, b, win_in, B, T, D, conv_bwd_tile(B, T, D), dx, dw, db, static_cast<float *>(workspace)};
+    const cudaError_t e = launch_conv_bwd(p, dtype == GLA_BF16, s, &launches);
+    t_launches = launches;
+    return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_conv1d_bwd launch");
+}
+
+gla_status gla_rmsnorm_fwd(const void *x, const void *res, const float *w, float eps, int64_t rows, int D, int group,
+                           gla_dtype dtype, void *s_out, void *y, void *y8, float *scale, void *stream) {
+    t_err[0] = 0;
+    t_launches = 0;
+    gla_status st = check_norm_shape(rows, D, dtype);
+    if (st != GLA_OK) return st;
+    if (!(eps >= 0.f)) return fail(GLA_ERR_INVALID_ARG, "eps must be >= 0");
+    if (group != 0 && group != 32 && group != 64 && group != 128)
+        return fail(GLA_ERR_UNSUPPORTED, "group %d is not 0, 32, 64 or 128", group);
+    OPTIONAL_PTR(res, "res");
+    OPTIONAL_PTR(w, "w");
+    OPTIONAL_PTR(s_out, "s_out");
+    OPTIONAL_PTR(y, "y");
+    OPTIONAL_PTR(y8, "y8");
+    OPTIONAL_PTR(scale, "scale");
+    if ((y8 != nullptr) != (scale != nullptr)) return fail(GLA_ERR_INVALID_ARG, "y8 and scale come together");
+    if (rows == 0 || (!s_out && !y && !y8)) return GLA_OK;
+    REQUIRE_PTR(x, "x");
+    for (const void *out : {(const void *)y, (const void *)y8})
+        if (out && (out == x || out == res || out == s_out)) return fail(GLA_ERR_INVALID_ARG, "y and y8 may not alias x, res or s_out");
+    if (y && y == y8) return fail(GLA_ERR_INVALID_ARG, "y8 may not alias y");
+    NormParams p{x, res, w, eps, (long)rows, D, group, s_out, y, static_cast<unsigned char *>(y8), scale};
+    int launches = 0;
+    const cudaError_t e = launch_rmsnorm_fwd(p, dtype == GLA_BF16, static_cast<cudaStream_t>(stream), &launches);
+    t_launches = launches;
+    return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_rmsnorm_fwd launch");
+}
+
+size_t gla_rmsnorm_bwd_workspace_size(int64_t rows, int D, gla_dtype dtype) {
+    if (check_norm_shape(rows, D, dtype) != GLA_OK || rows == 0) return 0;
+    return (size_t)norm_bwd_grid((long)rows, D) * D * sizeof(float);
+}
+
+gla_status gla_rmsnorm_bwd(const void *s_in, const float *w, const void *dy, const void *ds, float eps, int64_t rows,
+                           int D, gla_dtype dtype, void *dx, float *dw, void *workspace, size_t workspace_bytes,
+                           void *stream) {
+    t_err[0] = 0;
+    t_launches = 0;
+    gla_status st = check_norm_shape(rows, D, dtype);
+    if (st != GLA_OK) return st;
+    if (!(eps >= 0.f)) return fail(GLA_ERR_INVALID_ARG, "eps must be >= 0");
+    OPTIONAL_PTR(w, "w");
+    OPTIONAL_PTR(ds, "ds");
+    OPTIONAL_PTR(dw, "dw");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int launches = 0;
+    if (rows == 0) {
+        const cudaError_t e = dw ? cudaMemsetAsync(dw, 0, (size_t)D * sizeof(float), s) : cudaSuccess;
+        return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_rmsnorm_bwd(rows=0)");
+    }
+    REQUIRE_PTR(s_in, "s");
+    REQUIRE_PTR(dy, "dy");
+    REQUIRE_PTR(dx, "dx");
+    if (dx == s_in) return fail(GLA_ERR_INVALID_ARG, "dx may not alias s");
+    if (dw) {
+        REQUIRE_PTR(workspace, "workspace");
+        const size_t need = gla_rmsnorm_bwd_workspace_size(rows, D, dtype);
+        if (workspace_bytes < need)
+            return fail(GLA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+    }
+    NormParams p{s_in, nullptr, w, eps, (long)rows, D, 0, nullptr, nullptr, nullptr, nullptr, dy, ds, dx, dw,
+                 dw ? static_cast<float *>(workspace) : nullptr};
+    const cudaError_t e = launch_rmsnorm_bwd(p, dtype == GLA_BF16, s, &launches);
+    t_launches = launches;
+    return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_rmsnorm_bwd launch");
 }
 
 gla_status gla_selftest_wait_timeout(unsigned int limit_us, int *result, void *stream) {

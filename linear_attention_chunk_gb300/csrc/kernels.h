@@ -140,6 +140,40 @@ size_t ssm_workspace_bytes(const SsmPlan &plan, long nseq, int D, int N);
 cudaError_t launch_ssm_scan(const SsmParams &p, bool bf16, cudaStream_t s, int *launches);
 cudaError_t launch_ssm_step(const SsmParams &p, bool bf16, cudaStream_t s, int *launches);
 
+// Gradients of the Conv1d (conv_bwd.cu): x, dy, dx [B, T, D]; win [B, 4, D] or
+// NULL; part: [B * ceil(T / tile), 5 D] partial sums; dw [D, 4], db [D] or NULL.
+struct ConvBwdParams {
+    const void *x, *dy;
+    const float *w, *b, *win;
+    int B, T, D, tile;
+    void *dx;
+    float *dw, *db, *part;
+};
+int conv_bwd_tile(int B, int T, int D);
+cudaError_t launch_conv_bwd(const ConvBwdParams &p, bool bf16, cudaStream_t s, int *launches);
+
+// Residual addition, RMSNorm, 8-bit output, and the gradients (rmsnorm.cu).
+struct NormParams {
+    const void *x, *res;         // forward: s = x + res (res or NULL); backward: x is s
+    const float *w;              // [D] or NULL (one)
+    float eps;
+    long rows;
+    int D, group;                // group: channels per scale, 0: the row
+    void *s_out, *y;             // s and y, or NULL
+    unsigned char *y8;           // e4m3 [rows, D], or NULL
+    float *scale;                // [rows, ceil(D / group)] or [rows]
+    const void *dy, *ds;         // backward: ds or NULL
+    void *dx;
+    float *dw, *part;            // part [norm_bwd_grid, D], or NULL (dw not wanted)
+};
+long norm_bwd_grid(long rows, int D);
+cudaError_t launch_rmsnorm_fwd(const NormParams &p, bool bf16, cudaStream_t s, int *launches);
+cudaError_t launch_rmsnorm_bwd(const NormParams &p, bool bf16, cudaStream_t s, int *launches);
+
+// out[c] = sum over rows of part[r * pitch + c], in a fixed order (reduce.cu).
+cudaError_t launch_sum_rows(const float *part, long rows, long cols, long pitch, float *out, cudaStream_t s,
+                            int *launches);
+
 // SIMT kernels (any dk <= 128, dv <= 256; fp32 or bf16 elements).
 cudaError_t launch_fwd_simt(const FwdParams &p, bool bf16, cudaStream_t s, int *launches);
 cudaError_t launch_bwd_simt(const BwdParams &p, bool bf16, cudaStream_t s, int *launches);

@@ -1,0 +1,280 @@
+// rmsnorm.cu -- the norm in front of a mixer layer, with the residual's
+// addition before it and an 8-bit output behind it, and its gradients:
+//     s = x + res,   y = s w / sqrt(mean(s^2) + eps)       per row of D channels
+//     scale = max |y| / 448 over the row or a block of channels,  y8 = e4m3(y / scale)
+// and, with xn = s / sqrt(mean(s^2) + eps) and g = dy w,
+//     dx = ds + (g - xn mean(g xn)) / sqrt(mean(s^2) + eps),  dw = sum over rows of dy xn.
+//
+// Streams over HBM: forward 7 bytes an element (bf16 x and res in, s and e4m3
+// out), backward 8. A CTA holds a row in registers, each thread VPT vectors of
+// eight channels, all its loads issued up front; the row's sums go through
+// shuffles and one shared-memory exchange. A block of 128, 64 or 32 channels
+// is 16, 8 or 4 neighbouring lanes, so its maximum needs shuffles only. The
+// backward's CTAs walk every G-th row, load the next while the present one is
+// summed, and keep dw of their channels in registers; the partial sums of the
+// CTAs are added in a second launch (reduce.cu).
+// y is rounded once from fp32; y8 from the unrounded y.
+#include "ssm_common.cuh"
+
+namespace gla {
+namespace {
+
+using ssm::Raw8;
+using ssm::param8;
+using ssm::raw_load;
+using ssm::raw_unpack;
+using ssm::raw_zero;
+using ssm::store8;
+
+constexpr float kTop = 448.f;   // the largest e4m3 value
+constexpr int kMost = 512;      // threads of a CTA, two vectors a thread: D <= 8192
+
+__device__ __forceinline__ float max_nan(float a, float b) {   // a NaN wins
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+__device__ __forceinline__ float lanes_max(float v, int lanes) {
+    for (int off = lanes / 2; off > 0; off >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
+template <typename T, int VPT> __global__ void __launch_bounds__(kMost) rmsnorm_fwd_kernel(const NormParams p) {
+    __shared__ float s_sum[32], s_max[32];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, nw = blockDim.x / 32;
+    const long row = blockIdx.x;
+    const T *x = static_cast<const T *>(p.x) + (size_t)row * p.D;
+    const T *res = p.res ? static_cast<const T *>(p.res) + (size_t)row * p.D : nullptr;
+
+    Raw8<T> rx[VPT], rr[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = (i * (int)blockDim.x + tid) * 8;
+        rx[i] = c < p.D ? raw_load(x + c, c + 8 <= p.D) : raw_zero<T>();
+        rr[i] = res && c < p.D ? raw_load(res + c, c + 8 <= p.D) : raw_zero<T>();
+    }
+    float v[VPT][8], ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        float r[8];
+        raw_unpack(rx[i], v[i]);
+        raw_unpack(rr[i], r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (res) v[i][j] += r[j];
+            ss = fmaf(v[i][j], v[i][j], ss);
+        }
+    }
+    ss = warp_sum(ss);
+    if (nw > 1) {
+        if (lane == 0) s_sum[warp] = ss;
+        __syncthreads();
+        ss = warp_sum(lane < nw ? s_sum[lane] : 0.f);
+    }
+    const float rinv = rsqrtf(ss / (float)p.D + p.eps);
+
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = (i * (int)blockDim.x + tid) * 8;
+        const bool on = c < p.D, whole = c + 8 <= p.D;
+        if (p.s_out && on) store8(static_cast<T *>(p.s_out) + (size_t)row * p.D + c, v[i], whole);
+        float w[8];
+        param8(on ? p.w : nullptr, c, whole, w);
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[i][j] *= rinv;
+            if (p.w) v[i][j] *= w[j];
+            if (!on) v[i][j] = 0.f;
+            m = max_nan(m, fabsf(v[i][j]));
+        }
+        if (p.y && on) store8(static_cast<T *>(p.y) + (size_t)row * p.D + c, v[i], whole);
+        if (p.y8 && p.group) {
+            m = lanes_max(m, p.group / 8);
+            const float scale = m == 0.f ? 1.f : max_nan(m / kTop, 1.17549435e-38f);
+            const float inv = 1.f / scale;
+            const int per = p.group / 8;             // lanes of a block
+            if (on && lane % per == 0)
+                p.scale[(size_t)row * ((p.D + p.group - 1) / p.group) + c / p.group] = scale;
+            if (on) {
+                uint32_t *o = reinterpret_cast<uint32_t *>(p.y8 + (size_t)row * p.D + c);
+                const uint32_t a = e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+                const uint32_t b = e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
+                if (sizeof(T) == 2) {
+                    *reinterpret_cast<uint2 *>(o) = make_uint2(a, b);
+                } else {
+                    o[0] = a;
+                    if (whole) o[1] = b;
+                }
+            }
+        }
+        top = max_nan(top, m);
+    }
+    if (!p.y8 || p.group) return;
+    top = lanes_max(top, 32);
+    if (nw > 1) {
+        if (lane == 0) s_max[warp] = top;
+        __syncthreads();
+        top = lanes_max(lane < nw ? s_max[lane] : 0.f, 32);
+    }
+    const float scale = top == 0.f ? 1.f : max_nan(top / kTop, 1.17549435e-38f);
+    const float inv = 1.f / scale;
+    if (tid == 0) p.scale[row] = scale;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = (i * (int)blockDim.x + tid) * 8;
+        if (c >= p.D) break;
+        uint32_t *o = reinterpret_cast<uint32_t *>(p.y8 + (size_t)row * p.D + c);
+        const uint32_t a = e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+        const uint32_t b = e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
+        if (sizeof(T) == 2) {
+            *reinterpret_cast<uint2 *>(o) = make_uint2(a, b);
+        } else {
+            o[0] = a;
+            if (c + 8 <= p.D) o[1] = b;
+        }
+    }
+}
+
+// p.x: s; rows blockIdx.x, + gridDim.x, ...; partial dw of the CTA at p.part.
+template <typename T, int VPT> __global__ void __launch_bounds__(kMost) rmsnorm_bwd_kernel(const NormParams p) {
+    __shared__ float2 s_red[2][32];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, nw = blockDim.x / 32;
+    Raw8<T> nx[VPT], ny[VPT], ns[VPT];
+    auto fetch = [&](long row) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (i * (int)blockDim.x + tid) * 8;
+            const bool on = c < p.D, whole = c + 8 <= p.D;
+            const size_t at = (size_t)row * p.D + c;
+            nx[i] = on ? raw_load(static_cast<const T *>(p.x) + at, whole) : raw_zero<T>();
+            ny[i] = on ? raw_load(static_cast<const T *>(p.dy) + at, whole) : raw_zero<T>();
+            ns[i] = on && p.ds ? raw_load(static_cast<const T *>(p.ds) + at, whole) : raw_zero<T>();
+        }
+    };
+    float w[VPT][8], dw[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = (i * (int)blockDim.x + tid) * 8;
+        param8(p.w && c < p.D ? p.w : nullptr, c, c + 8 <= p.D, w[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (!p.w) w[i][j] = 1.f;
+            dw[i][j] = 0.f;
+        }
+    }
+    int par = 0;
+    long row = blockIdx.x;
+    if (row < p.rows) fetch(row);
+    for (; row < p.rows; row += gridDim.x, par ^= 1) {
+        Raw8<T> cx[VPT], cy[VPT], cs[VPT];
+        float ss = 0.f, sg = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            cx[i] = nx[i];
+            cy[i] = ny[i];
+            cs[i] = ns[i];
+            float x[8], g[8];
+            raw_unpack(cx[i], x);
+            raw_unpack(cy[i], g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                ss = fmaf(x[j], x[j], ss);
+                sg = fmaf(g[j] * w[i][j], x[j], sg);
+            }
+        }
+        if (row + gridDim.x < p.rows) fetch(row + gridDim.x);
+        ss = warp_sum(ss);
+        sg = warp_sum(sg);
+        if (nw > 1) {                                // two buffers in turn: one barrier a row
+            if (lane == 0) s_red[par][warp] = make_float2(ss, sg);
+            __syncthreads();
+            const float2 r = lane < nw ? s_red[par][lane] : make_float2(0.f, 0.f);
+            ss = warp_sum(r.x);
+            sg = warp_sum(r.y);
+        }
+        const float rinv = rsqrtf(ss / (float)p.D + p.eps);
+        const float k = rinv * rinv * (sg / (float)p.D);   // xn mean(g xn) = x k
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (i * (int)blockDim.x + tid) * 8;
+            float x[8], g[8], s[8];
+            raw_unpack(cx[i], x);
+            raw_unpack(cy[i], g);
+            raw_unpack(cs[i], s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dw[i][j] = fmaf(g[j], x[j] * rinv, dw[i][j]);
+                s[j] = fmaf(rinv, fmaf(-k, x[j], g[j] * w[i][j]), s[j]);
+            }
+            if (c < p.D) store8(static_cast<T *>(p.dx) + (size_t)row * p.D + c, s, c + 8 <= p.D);
+        }
+    }
+    if (!p.part) return;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = (i * (int)blockDim.x + tid) * 8;
+        if (c < p.D) store8(p.part + (size_t)blockIdx.x * p.D + c, dw[i], c + 8 <= p.D);
+    }
+}
+
+int round32(int v) { return (v + 31) / 32 * 32; }
+
+template <typename T> cudaError_t fwd(const NormParams &p, cudaStream_t s, int *launches) {
+    const int vecs = (p.D + 7) / 8;
+    // Few rows: one vector a thread, the shortest chain. Many: two, so that a
+    // thread has four loads in flight and a row half the warps to exchange with.
+    const int vpt = vecs > kMost || (p.rows > 2L * device_sm_count() && vecs > 32) ? 2 : 1;
+    const int th = round32((vecs + vpt - 1) / vpt);
+    if (vpt == 1) rmsnorm_fwd_kernel<T, 1><<<(unsigned)p.rows, th, 0, s>>>(p);
+    else rmsnorm_fwd_kernel<T, 2><<<(unsigned)p.rows, th, 0, s>>>(p);
+    if (launches) ++*launches;
+    return cudaGetLastError();
+}
+
+// The backward's shape by D alone: one vector a thread up to 4,096 channels.
+int bwd_vpt(int vecs) { return vecs > kMost ? 2 : 1; }
+int bwd_threads(int vecs) { return round32((vecs + bwd_vpt(vecs) - 1) / bwd_vpt(vecs)); }
+
+template <typename T> cudaError_t bwd(const NormParams &p, cudaStream_t s, int *launches) {
+    const int vecs = (p.D + 7) / 8, vpt = bwd_vpt(vecs), th = bwd_threads(vecs);
+    const unsigned grid = (unsigned)norm_bwd_grid(p.rows, p.D);
+    if (vpt == 1) rmsnorm_bwd_kernel<T, 1><<<grid, th, 0, s>>>(p);
+    else rmsnorm_bwd_kernel<T, 2><<<grid, th, 0, s>>>(p);
+    if (launches) ++*launches;
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !p.part) return e;
+    return launch_sum_rows(p.part, grid, p.D, p.D, p.dw, s, launches);
+}
+
+}  // namespace
+
+// CTAs of the backward: 1,024 threads an SM, each CTA walking its share of the rows.
+long norm_bwd_grid(long rows, int D) {
+    const int th = bwd_threads((D + 7) / 8);
+    const long per_sm = 1024 / th > 8 ? 8 : 1024 / th;
+    const long most = per_sm * device_sm_count();
+    return rows < most ? rows : most;
+}
+
+cudaError_t launch_rmsnorm_fwd(const NormParams &p, bool bf16, cudaStream_t s, int *launches) {
+    return bf16 ? fwd<__nv_bfloat16>(p, s, launches) : fwd<float>(p, s, launches);
+}
+cudaError_t launch_rmsnorm_bwd(const NormParams &p, bool bf16, cudaStream_t s, int *launches) {
+    return bf16 ? bwd<__nv_bfloat16>(p, s, launches) : bwd<float>(p, s, launches);
+}
+
+}  // namespace gla

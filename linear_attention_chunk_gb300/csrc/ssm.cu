@@ -8,16 +8,18 @@
 // form (the decays do not factor into one weight per token pair): the work is
 // one exponential and four fp32 operations per (token, channel, state).
 //
-// Layout: a CTA of W warps owns 8 W channels of one sequence (or of one
-// segment of it); a quad of lanes owns a channel, each lane N / 4 of its
-// states, in registers as fp32 pairs for the whole run. Tiles of 32 tokens:
-// every thread loads eight channels of one token (16-byte accesses; the next
-// tile's are in flight during the scan), forms the input u and the step
-// delta, and leaves (delta, delta, delta u, delta u) in shared memory, so the
-// scan's packed operands need no moves; then each warp walks the 32 tokens of
-// its eight channels; then the same thread that loaded a vector adds the
-// skip, applies the gate and stores it. Each elementwise value is computed
-// once, and the quad's sums over states are exchanged four tokens at a time.
+// Layout: a CTA of W warps owns 16 W channels of one sequence (or of one
+// segment of it); a quad of lanes owns two channels, each lane N / 4 of their
+// states, in registers as fp32 pairs for the whole run. Two channels a lane
+// halve the loads of B and C: shared memory fills registers at 128 bytes a
+// clock per SM, and one channel a lane was bound by that (282 us against
+// 8 x 2048 x 2048, N = 16). Tiles of 16 tokens: every thread loads eight
+// channels of one token (16-byte accesses; the next tile's are in flight
+// during the scan), forms the input u and the step delta, and leaves
+// (delta, delta u) in shared memory; then each warp walks the tile's tokens of
+// its sixteen channels; then the thread that loaded a vector adds the skip,
+// applies the gate and stores it. Each elementwise value is computed once,
+// and the quad's sums over states are exchanged four tokens at a time.
 //
 // Sequences are cut into segments when they are too few to fill the GPU: one
 // launch runs every segment but a sequence's last (the first from the initial
@@ -32,13 +34,11 @@ namespace {
 
 using namespace ssm;
 
-constexpr int kTile = 32;   // tokens per tile (one vector of 8 channels per thread)
+constexpr int kTile = 16;   // tokens per tile (one vector of 8 channels per thread)
 constexpr int kYPad = 8;    // floats: rows of y start 8 banks apart
-constexpr int kWarps = 8;
-constexpr int kMinBlocks = 2;
 
 template <int N, int W> constexpr int scan_smem_floats() {
-    return kTile * 8 * W * 4 + kTile * (8 * W + kYPad) + 2 * kTile * N;
+    return kTile * 16 * W * 2 + kTile * (16 * W + kYPad) + 2 * kTile * N;
 }
 
 // The unit's sequence, its segment and its tokens. False: nothing to do.
@@ -93,12 +93,16 @@ __device__ __forceinline__ bool find_unit(const SsmParams &p, long u, int *s_fou
 // token's input and the three before it, from the window before the
 // sequence's first token (rows oldest first, the last four inputs).
 template <typename T>
-__device__ __forceinline__ void conv8(const SsmParams &p, const Unit &un, long row, int c, const Raw8<T> &now,
-                                      float (&u)[8]) {
+__device__ __forceinline__ void conv8(const SsmParams &p, const Unit &un, long row, int c, bool whole,
+                                      const Raw8<T> &now, float (&u)[8]) {
     float acc[8], w[kTaps][8];
-    param8(p.conv_b, c, 0.f, acc);
+    param8(p.conv_b, c, whole, acc);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+        if (sizeof(T) == 4 && i >= 4 && !whole) {
+            w[0][i] = w[1][i] = w[2][i] = w[3][i] = 0.f;
+            continue;
+        }
         const float4 f = __ldg(reinterpret_cast<const float4 *>(p.conv_w) + c + i);
         w[0][i] = f.x; w[1][i] = f.y; w[2][i] = f.z; w[3][i] = f.w;
     }
@@ -109,12 +113,12 @@ __device__ __forceinline__ void conv8(const SsmParams &p, const Unit &un, long r
         if (j == 3) {
             raw_unpack(now, v);
         } else if (src >= un.first) {
-            raw_unpack(raw_load(static_cast<const T *>(p.x) + (size_t)src * p.ldx + c), v);
+            raw_unpack(raw_load(static_cast<const T *>(p.x) + (size_t)src * p.ldx + c, whole), v);
         } else {
             // plain loads: this launch rewrites the window later
             const float4 *r = reinterpret_cast<const float4 *>(
                 p.win + ((size_t)un.slot * kTaps + (kTaps + src - un.first)) * p.D + c);
-            const float4 a = r[0], b = r[1];
+            const float4 a = r[0], b = whole ? r[1] : make_float4(0.f, 0.f, 0.f, 0.f);
             v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
             v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         }
@@ -126,11 +130,11 @@ __device__ __forceinline__ void conv8(const SsmParams &p, const Unit &un, long r
 }
 
 template <typename T, int N, int W, bool kFull, bool kConv>
-__global__ void __launch_bounds__(32 * W, kMinBlocks) ssm_scan_kernel(const SsmParams p, int tiles) {
-    constexpr int SP = N / 4, P = SP / 2, CH = 8 * W, YS = CH + kYPad, TH = 32 * W;
+__global__ void __launch_bounds__(32 * W, 16 / W) ssm_scan_kernel(const SsmParams p, int tiles) {
+    constexpr int SP = N / 4, P = SP / 2, CH = 16 * W, VW = 2 * W, YS = CH + kYPad, TH = 32 * W;
     extern __shared__ __align__(16) float smem[];
-    float4 *sD = reinterpret_cast<float4 *>(smem);     // [kTile * W vectors][8], channels swizzled
-    float *sY = smem + kTile * CH * 4;                 // [kTile][YS]
+    float4 *sD = reinterpret_cast<float4 *>(smem);     // [kTile * VW vectors][4 channel pairs, swizzled]
+    float *sY = smem + kTile * CH * 2;                 // [kTile][YS]
     float *sB = sY + kTile * YS;                       // [kTile][N]
     float *sC = sB + kTile * N;
     __shared__ int s_found;
@@ -147,25 +151,19 @@ __global__ void __launch_bounds__(32 * W, kMinBlocks) ssm_scan_kernel(const SsmP
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, q = lane % 4;
     // the vector this thread loads and stores: channels c .. c+7 of token vt of every tile
-    const int vt = tid / W, c = c0 + (tid % W) * kVec;
-    const bool vec_on = c < p.D;
-    // the channel and states this lane scans
-    const int ch = c0 + warp * 8 + lane / 4;
-    const bool ch_on = ch < p.D;
+    const int vt = tid / VW, c = c0 + (tid % VW) * kVec;
+    const bool vec_on = c < p.D, whole = c + kVec <= p.D;
+    // the two channels and the states this lane scans
+    const int ch = c0 + warp * 16 + lane / 4 * 2;
+    const bool ch_on = ch < p.D;                       // D is even
 
-    f2 a2[P], h[P];
+    f2 a2[2][P], h[2][P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        a2[i] = 0;
-        h[i] = 0;
-    }
-    const size_t cell = (size_t)ch * N + q * SP;       // of this lane's states in a [D, N] array
-    if (ch_on) {
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const float2 a = __ldg(reinterpret_cast<const float2 *>(p.A + cell) + i);
-            a2[i] = f2_pack(a.x * kLog2e, a.y * kLog2e);
-        }
+        for (int i = 0; i < P; ++i) a2[k][i] = h[k][i] = 0;
+    const size_t cell = (size_t)ch * N + q * SP;       // of this lane's states in a [D, N] array; the second channel's
+    if (ch_on) {                                       // are N further
         // The state entering the unit. The last segment of a sequence has no
         // local pass, and its workspace slot keeps a copy of the initial state:
         // the second launch overwrites the pool, and reads the copy instead.
@@ -175,38 +173,47 @@ __global__ void __launch_bounds__(32 * W, kMinBlocks) ssm_scan_kernel(const SsmP
         } else if (kFull) {
             src = p.seg_h + (size_t)(un.base + (un.seg == 0 ? un.nseg - 1 : 0)) * p.D * N + cell;
         }
-        if (src) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const float2 v = reinterpret_cast<const float2 *>(src)[i];
-                h[i] = f2_pack(v.x, v.y);
+                const float2 a = __ldg(reinterpret_cast<const float2 *>(p.A + cell + k * N) + i);
+                a2[k][i] = f2_pack(a.x * kLog2e, a.y * kLog2e);
+                if (src) {
+                    const float2 v = reinterpret_cast<const float2 *>(src + k * N)[i];
+                    h[k][i] = f2_pack(v.x, v.y);
+                }
             }
-        }
         if (!kFull && un.seg == 0) {
-            float2 *dst = reinterpret_cast<float2 *>(p.seg_h + (size_t)(un.base + un.nseg - 1) * p.D * N + cell);
+            float *dst = p.seg_h + (size_t)(un.base + un.nseg - 1) * p.D * N + cell;
 #pragma unroll
-            for (int i = 0; i < P; ++i) dst[i] = f2_split(h[i]);
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < P; ++i) reinterpret_cast<float2 *>(dst + k * N)[i] = f2_split(h[k][i]);
         }
         if (kFull) {                                   // the first segment's state is final; fold the others
-#pragma unroll 4
+#pragma unroll 2
             for (int s = 1; s < un.seg; ++s) {
-                const size_t k = (size_t)(un.base + s);
-                const float sum = p.seg_sum[k * p.D + ch];
-                const float2 *e = reinterpret_cast<const float2 *>(p.seg_h + k * p.D * N + cell);
-                const f2 ss = f2_pack(sum, sum);
+                const size_t slot = (size_t)(un.base + s);
+                const float2 sum = *reinterpret_cast<const float2 *>(p.seg_sum + slot * p.D + ch);
+                const float *e = p.seg_h + slot * p.D * N + cell;
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const float2 v = e[i];
-                    h[i] = fma2(ex2_pair(mul2(ss, a2[i])), h[i], f2_pack(v.x, v.y));
+                for (int k = 0; k < 2; ++k) {
+                    const f2 ss = k ? f2_pack(sum.y, sum.y) : f2_pack(sum.x, sum.x);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        const float2 v = reinterpret_cast<const float2 *>(e + k * N)[i];
+                        h[k][i] = fma2(ex2_pair(mul2(ss, a2[k][i])), h[k][i], f2_pack(v.x, v.y));
+                    }
                 }
             }
         }
     }
 
     float bias[8];
-    param8(vec_on ? p.dt_bias : nullptr, c, 0.f, bias);
+    param8(vec_on ? p.dt_bias : nullptr, c, whole, bias);
     float skip[8];
-    if (kFull) param8(vec_on ? p.skip : nullptr, c, 0.f, skip);
+    if (kFull) param8(vec_on ? p.skip : nullptr, c, whole, skip);
 
     // one tile's inputs as they lie in memory
     Raw8<T> rx, rd, rz;
@@ -215,9 +222,9 @@ __global__ void __launch_bounds__(32 * W, kMinBlocks) ssm_scan_kernel(const SsmP
     auto fetch = [&](long t0) {
         const long row = row0 + t0 + vt;
         const bool on = vec_on && t0 + vt < ntok;
-        rx = on ? raw_load(static_cast<const T *>(p.x) + (size_t)row * p.ldx + c) : raw_zero<T>();
-        rd = on ? raw_load(static_cast<const T *>(p.dt) + (size_t)row * p.ldt + c) : raw_zero<T>();
-        if (kFull && p.z) rz = on ? raw_load(static_cast<const T *>(p.z) + (size_t)row * p.ldz + c) : raw_zero<T>();
+        rx = on ? raw_load(static_cast<const T *>(p.x) + (size_t)row * p.ldx + c, whole) : raw_zero<T>();
+        rd = on ? raw_load(static_cast<const T *>(p.dt) + (size_t)row * p.ldt + c, whole) : raw_zero<T>();
+        if (kFull && p.z) rz = on ? raw_load(static_cast<const T *>(p.z) + (size_t)row * p.ldz + c, whole) : raw_zero<T>();
 #pragma unroll
         for (int i = 0; i < BN; ++i) {
             const int e = tid + i * TH, t = e / N, n = e % N;
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(32 * W, kMinBlocks) ssm_scan_kernel(const SsmP
     };
     fetch(0);
 
-    float dsum = 0.f;
+    float dsum[2] = {0.f, 0.f};
     for (long t0 = 0; t0 < ntok; t0 += kTile) {
         // ---- inputs of the tile: u, delta; zero steps past the end leave the state as it is
         const bool on = vec_on && t0 + vt < ntok;
@@ -242,7 +249,7 @@ __global__ void __launch_bounds__(32 * W, kMinBlocks) ssm_scan_kernel(const SsmP
         }
         if (kConv) {
             if (on) {
-                conv8(p, un, row0 + t0 + vt, c, rx, u);
+                conv8(p, un, row0 + t0 + vt, c, whole, rx, u);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) u[i] = 0.f;
@@ -251,10 +258,9 @@ __global__ void __launch_bounds__(32 * W, kMinBlocks) ssm_scan_kernel(const SsmP
             raw_unpack(rx, u);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float du = dl[i] * u[i];
-            sD[tid * 8 + (i ^ (tid & 7))] = make_float4(dl[i], dl[i], du, du);
-        }
+        for (int i = 0; i < 4; ++i)                    // eight lanes' 64-byte vectors over all the banks
+            sD[tid * 4 + (i ^ ((tid >> 1) & 3))] =
+                make_float4(dl[2 * i], dl[2 * i] * u[2 * i], dl[2 * i + 1], dl[2 * i + 1] * u[2 * i + 1]);
 #pragma unroll
         for (int i = 0; i < BN; ++i) {
             const int e = tid + i * TH;
@@ -267,37 +273,43 @@ __global__ void __launch_bounds__(32 * W, kMinBlocks) ssm_scan_kernel(const SsmP
         __syncthreads();
         if (t0 + kTile < ntok) fetch(t0 + kTile);
 
-        // ---- the scan: 32 tokens of this warp's eight channels
+        // ---- the scan: the tile's tokens of this warp's sixteen channels
 #pragma unroll 2
         for (int t = 0; t < kTile; t += 4) {
-            float part[4];
+            float part[2][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int v = (t + j) * W + warp;      // the vector that holds this token's channels
-                const ulonglong2 d = reinterpret_cast<const ulonglong2 *>(sD)[v * 8 + ((lane / 4) ^ (v & 7))];
+                const int v = (t + j) * VW + warp * 2 + lane / 16;   // the vector that holds this token's channels
+                const float4 d = sD[v * 4 + ((lane / 4 % 4) ^ ((v >> 1) & 3))];
                 const f2 *b = reinterpret_cast<const f2 *>(sB + (t + j) * N + q * SP);
                 const f2 *cc = reinterpret_cast<const f2 *>(sC + (t + j) * N + q * SP);
-                f2 y = 0;
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const f2 a = ex2_pair(mul2(d.x, a2[i]));
-                    h[i] = fma2(a, h[i], mul2(d.y, b[i]));
-                    if (kFull) y = i == 0 ? mul2(h[i], cc[i]) : fma2(h[i], cc[i], y);
-                }
-                if (kFull) {
-                    const float2 ys = f2_split(y);
-                    part[j] = ys.x + ys.y;
-                } else {
-                    dsum += f2_split(d.x).x;
+                for (int k = 0; k < 2; ++k) {
+                    const f2 dd = k ? f2_pack(d.z, d.z) : f2_pack(d.x, d.x);
+                    const f2 du = k ? f2_pack(d.w, d.w) : f2_pack(d.y, d.y);
+                    f2 y = 0;
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        h[k][i] = fma2(ex2_pair(mul2(dd, a2[k][i])), h[k][i], mul2(du, b[i]));
+                        if (kFull) y = i == 0 ? mul2(h[k][i], cc[i]) : fma2(h[k][i], cc[i], y);
+                    }
+                    if (kFull) {
+                        const float2 ys = f2_split(y);
+                        part[k][j] = ys.x + ys.y;
+                    } else {
+                        dsum[k] += k ? d.z : d.x;
+                    }
                 }
             }
-            if (kFull) sY[(t + q) * YS + warp * 8 + lane / 4] = quad_transpose_sum(part, lane);
+            if (kFull)
+                *reinterpret_cast<float2 *>(sY + (t + q) * YS + warp * 16 + lane / 4 * 2) =
+                    make_float2(quad_transpose_sum(part[0], lane), quad_transpose_sum(part[1], lane));
         }
         __syncthreads();
 
         // ---- skip, gate, store
         if (kFull && on) {
-            const float *ys = sY + vt * YS + (tid % W) * kVec;
+            const float *ys = sY + vt * YS + (tid % VW) * kVec;
             float y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = fmaf(skip[i], u[i], ys[i]);
@@ -307,7 +319,7 @@ __global__ void __launch_bounds__(32 * W, kMinBlocks) ssm_scan_kernel(const SsmP
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] *= silu(z[i]);
             }
-            store8(static_cast<T *>(p.y) + (size_t)(row0 + t0 + vt) * p.D + c, y);
+            store8(static_cast<T *>(p.y) + (size_t)(row0 + t0 + vt) * p.D + c, y, whole);
         }
     }
 
@@ -318,9 +330,12 @@ __global__ void __launch_bounds__(32 * W, kMinBlocks) ssm_scan_kernel(const SsmP
         else if (last && p.hT) dst = p.hT + (size_t)un.slot * p.D * N + cell;
         if (dst) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) reinterpret_cast<float2 *>(dst)[i] = f2_split(h[i]);
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < P; ++i) reinterpret_cast<float2 *>(dst + k * N)[i] = f2_split(h[k][i]);
         }
-        if (!kFull && q == 0) p.seg_sum[(size_t)(un.base + un.seg) * p.D + ch] = dsum;
+        if (!kFull && q == 0)
+            *reinterpret_cast<float2 *>(p.seg_sum + (size_t)(un.base + un.seg) * p.D + ch) = make_float2(dsum[0], dsum[1]);
     }
     // ---- the window after the call: this CTA (the sequence's first tokens)
     // is the only one that reads it, and has done so before the last barrier
@@ -340,15 +355,14 @@ __global__ void __launch_bounds__(32 * W, kMinBlocks) ssm_scan_kernel(const SsmP
     }
 }
 
-template <typename T, int N, bool kFull, bool kConv> cudaError_t launch(const SsmParams &p, long units, cudaStream_t s, int *launches) {
-    const int tiles = (p.D + 8 * kWarps - 1) / (8 * kWarps);
+constexpr int kWarps = 8;   // 64 channels a CTA
+
+template <typename T, int N, bool kFull, bool kConv>
+cudaError_t launch(const SsmParams &p, long units, cudaStream_t s, int *launches) {
+    const int tiles = (p.D + 16 * kWarps - 1) / (16 * kWarps);
     if ((long double)units * tiles > 2147483647.0L) return cudaErrorInvalidValue;
     constexpr int bytes = scan_smem_floats<N, kWarps>() * (int)sizeof(float);
     auto *kern = ssm_scan_kernel<T, N, kWarps, kFull, kConv>;
-    if (bytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-    }
     kern<<<(unsigned)(units * tiles), 32 * kWarps, bytes, s>>>(p, tiles);
     if (launches) ++*launches;
     return cudaGetLastError();

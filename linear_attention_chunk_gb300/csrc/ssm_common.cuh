@@ -54,14 +54,13 @@ __device__ __forceinline__ f2 ex2_pair(f2 x) {
 
 // log(1 + e^v) = max(v, 0) + log1p(w), w = e^-|v| in (0, 1], by the series
 // log1p(w) = 2 atanh(s) = 2 (s + s^3/3 + s^5/5 + ...), s = w / (2 + w) <= 1/3:
-// eight terms leave 2 s^17 / 17 < 1e-9. Relative to the result, not to 1: a
+// seven terms leave 2 s^15 / 15 < 1e-8. Relative to the result, not to 1: a
 // step of 1e-3 keeps fp32's precision, which log(1 + w) would lose.
 __device__ __forceinline__ float softplus(float v) {
     const float w = ex2(-fabsf(v) * kLog2e);
     const float s = w * rcp(2.f + w);
     const float q = s * s;
-    float r = 1.f / 15.f;
-    r = fmaf(r, q, 1.f / 13.f);
+    float r = 1.f / 13.f;
     r = fmaf(r, q, 1.f / 11.f);
     r = fmaf(r, q, 1.f / 9.f);
     r = fmaf(r, q, 1.f / 7.f);
@@ -84,10 +83,12 @@ template <typename T> __device__ __forceinline__ Raw8<T> raw_zero() {
     for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = make_uint4(0, 0, 0, 0);
     return r;
 }
-template <typename T> __device__ __forceinline__ Raw8<T> raw_load(const T *p) {
+// `whole`: all eight channels exist. D is a multiple of 8 at bf16; at fp32 it
+// may be a multiple of 4 only, and the last vector of a row half there.
+template <typename T> __device__ __forceinline__ Raw8<T> raw_load(const T *p, bool whole) {
     Raw8<T> r;
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    r.w[0] = __ldg(reinterpret_cast<const uint4 *>(p));
+    if constexpr (sizeof(T) == 4) r.w[1] = whole ? __ldg(reinterpret_cast<const uint4 *>(p) + 1) : make_uint4(0, 0, 0, 0);
     return r;
 }
 __device__ __forceinline__ void raw_unpack(const Raw8<__nv_bfloat16> &r, float (&v)[8]) {
@@ -107,24 +108,24 @@ __device__ __forceinline__ void raw_unpack(const Raw8<float> &r, float (&v)[8]) 
         v[4 * i + 3] = __uint_as_float(r.w[i].w);
     }
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8], bool) {
     *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+__device__ __forceinline__ void store8(float *p, const float (&v)[8], bool whole) {
     reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    if (whole) reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
-// Eight fp32 parameters of consecutive channels, or `fill` without an array.
-__device__ __forceinline__ void param8(const float *p, int c, float fill, float (&v)[8]) {
+// Eight fp32 parameters of consecutive channels (zeros without an array).
+__device__ __forceinline__ void param8(const float *p, int c, bool whole, float (&v)[8]) {
     if (p) {
         const float4 a = __ldg(reinterpret_cast<const float4 *>(p + c));
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(p + c) + 1);
+        const float4 b = whole ? __ldg(reinterpret_cast<const float4 *>(p + c) + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fill;
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
     }
 }
 

@@ -51,7 +51,8 @@ def call_fwd(gla, s, h0=None, **kw):
     (BF, 3, 31, 64, 8, False, True, True, True), (FP, 1, 64, 200, 32, True, False, False, False),
     (BF, 2, 129, 136, 16, True, True, False, True), (FP, 1, 7, 1032, 8, False, False, True, True),
     (BF, 1, 700, 24, 16, True, True, True, True), (FP, 2, 1025, 40, 16, True, True, True, False),
-    (BF, 1, 300, 16, 32, True, True, True, True)])
+    (BF, 1, 300, 16, 32, True, True, True, True), (FP, 2, 70, 4, 8, True, True, True, True),
+    (FP, 1, 45, 516, 16, True, True, True, True)])
 def test_fwd_matches_the_definition(gla, dtype, B, T, D, N, gate, bias, skip, state):
     s = inputs((B, T), D, N, dtype, 100 + T, gate, bias, skip)
     h0 = torch.randn(B, D, N, generator=torch.Generator().manual_seed(T)).cuda() if state else None
@@ -175,7 +176,7 @@ def i32(v):
 @pytest.mark.parametrize("dtype,lens,D,N,filt", [
     (BF, [5, 0, 1, 64, 3, 0], 72, 16, True), (FP, [1], 8, 8, True), (FP, [2, 1, 3, 1], 64, 16, True),
     (BF, [1300, 2, 513, 0, 40], 40, 16, True), (FP, [700, 1, 600], 24, 32, True), (BF, [33, 200, 7], 136, 16, False),
-    (FP, [0, 0, 9], 16, 16, False)])
+    (FP, [0, 0, 9], 16, 16, False), (FP, [2, 90, 1], 68, 8, True)])
 def test_varlen_matches_the_definition(gla, dtype, lens, D, N, filt):
     cu = [0]
     for v in lens:
@@ -241,7 +242,7 @@ def call_step(gla, s, pool, slots=None, w=None, b=None, win=None, **kw):
 
 @pytest.mark.parametrize("dtype,n,D,N,filt,gate", [
     (BF, 1, 8, 16, True, True), (FP, 5, 72, 16, True, True), (BF, 7, 136, 8, True, False), (FP, 3, 40, 32, False, True),
-    (BF, 33, 1032, 16, True, True), (FP, 2, 64, 16, False, False)])
+    (BF, 33, 1032, 16, True, True), (FP, 2, 64, 16, False, False), (FP, 3, 12, 8, True, True)])
 def test_step_matches_the_definition(gla, dtype, n, D, N, filt, gate):
     s = inputs((n,), D, N, dtype, 60 + n, gate=gate)
     pool, win, w, b = pools(n + 1, D, N, 4)

@@ -1,4 +1,4 @@
-"""Refusals of the selective state-space entry points, all on the host: bad
+"""Refusals of the selective state-space, Conv1d-gradient and norm entry points, all on the host: bad
 arguments get the documented status before anything is launched. The fake
 addresses are never dereferenced."""
 import pytest
@@ -45,7 +45,7 @@ def test_selective_scan_rejects_bad_arguments(L):
                    dict(y=None), dict(y=FAKE), dict(y=ODD), dict(dtype=2), dict(skip=ODD), dict(bias=ODD)):
             assert f(**kw) == binding.GLA_ERR_INVALID_ARG, (f.__name__, kw)
             assert L.gla_last_launch_count() == 0
-        for kw in (dict(D=60), dict(D=0), dict(N=12), dict(N=64)):
+        for kw in (dict(D=60), dict(D=62, dtype=1), dict(D=0), dict(N=12), dict(N=64)):
             assert f(**kw) == binding.GLA_ERR_UNSUPPORTED, (f.__name__, kw)
     assert fwd(B=-1) == fwd(T=-1) == fwd(h0=ODD) == fwd(hT=ODD) == binding.GLA_ERR_INVALID_ARG
     assert fwd(B=1 << 20, T=1 << 20) == binding.GLA_ERR_INVALID_ARG       # too large
@@ -63,3 +63,51 @@ def test_selective_scan_rejects_bad_arguments(L):
     assert binding.gla_ssm_fwd_workspace_size(64, 2048, 4096, 16) == 0    # enough chains
     assert binding.gla_ssm_varlen_workspace_size(2, 5000, 64, 16) > 0
     assert binding.gla_ssm_varlen_workspace_size(2, 5000, 64, 12) == 0    # invalid
+
+
+def test_conv_backward_rejects_bad_arguments(L):
+    def bwd(**kw):
+        a = dict(x=FAKE, w=FAKE, b=None, dy=FAKE + 0x100, win=None, B=2, T=50, D=64, dt=0, dx=FAKE + 0x200, dw=FAKE,
+                 db=None, ws=FAKE, n=1 << 30)
+        a.update(kw)
+        return L.gla_conv1d_bwd(a["x"], a["w"], a["b"], a["dy"], a["win"], a["B"], a["T"], a["D"], a["dt"], a["dx"],
+                                a["dw"], a["db"], a["ws"], a["n"], None)
+    for kw in (dict(x=None), dict(x=ODD), dict(w=None), dict(b=ODD), dict(dy=None), dict(win=ODD), dict(dx=None),
+               dict(dx=FAKE), dict(dx=FAKE + 0x100), dict(dw=None), dict(dw=ODD), dict(db=ODD), dict(dt=4), dict(B=-1),
+               dict(T=-1), dict(ws=None), dict(ws=ODD)):
+        assert bwd(**kw) == binding.GLA_ERR_INVALID_ARG, kw
+    assert bwd(D=12) == bwd(D=0) == binding.GLA_ERR_UNSUPPORTED
+    need = binding.gla_conv1d_bwd_workspace_size(2, 50, 64)
+    assert need >= 2 * 5 * 64 * 4 and bwd(n=need - 1) == binding.GLA_ERR_WORKSPACE
+    assert binding.gla_conv1d_bwd_workspace_size(0, 50, 64) == 0
+
+
+def test_norm_rejects_bad_arguments(L):
+    def fwd(**kw):
+        a = dict(x=FAKE, res=None, w=None, eps=1e-6, rows=4, D=256, group=0, dt=0, s=None, y=FAKE + 0x100, y8=None,
+                 scale=None)
+        a.update(kw)
+        return L.gla_rmsnorm_fwd(a["x"], a["res"], a["w"], a["eps"], a["rows"], a["D"], a["group"], a["dt"], a["s"],
+                                 a["y"], a["y8"], a["scale"], None)
+    for kw in (dict(x=None), dict(x=ODD), dict(res=ODD), dict(w=ODD), dict(eps=-1.0), dict(eps=float("nan")),
+               dict(rows=-1), dict(rows=1 << 31), dict(dt=3), dict(s=ODD), dict(y=ODD), dict(y=FAKE),
+               dict(y8=FAKE + 0x200), dict(scale=FAKE), dict(y8=FAKE + 0x100, scale=FAKE),
+               dict(y8=FAKE, scale=FAKE), dict(s=FAKE + 0x100)):
+        assert fwd(**kw) == binding.GLA_ERR_INVALID_ARG, kw
+    for kw in (dict(D=12), dict(D=0), dict(D=8200), dict(D=6, dt=1), dict(group=16), dict(group=-1), dict(group=256)):
+        assert fwd(**kw) == binding.GLA_ERR_UNSUPPORTED, kw
+    assert fwd(rows=0) == fwd(y=None) == binding.GLA_OK
+
+    def bwd(**kw):
+        a = dict(s=FAKE, w=None, dy=FAKE + 0x100, ds=None, eps=1e-6, rows=4, D=256, dt=0, dx=FAKE + 0x200, dw=FAKE,
+                 ws=FAKE, n=1 << 30)
+        a.update(kw)
+        return L.gla_rmsnorm_bwd(a["s"], a["w"], a["dy"], a["ds"], a["eps"], a["rows"], a["D"], a["dt"], a["dx"],
+                                 a["dw"], a["ws"], a["n"], None)
+    for kw in (dict(s=None), dict(dy=None), dict(dy=ODD), dict(ds=ODD), dict(dx=None), dict(dx=FAKE), dict(dw=ODD),
+               dict(w=ODD), dict(eps=-1.0), dict(rows=-2), dict(ws=None)):
+        assert bwd(**kw) == binding.GLA_ERR_INVALID_ARG, kw
+    assert bwd(D=8200) == bwd(D=4) == binding.GLA_ERR_UNSUPPORTED
+    need = binding.gla_rmsnorm_bwd_workspace_size(4, 256)
+    assert need == 4 * 256 * 4 and bwd(n=need - 1) == binding.GLA_ERR_WORKSPACE
+    assert bwd(rows=0, dw=None) == binding.GLA_OK
