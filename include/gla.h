@@ -440,6 +440,33 @@ gla_status gla_ssm_step(const void *x, int64_t ld_x, const void *dt, int64_t ld_
                         void *y, void *stream);
 
 /*
+ * gla_ssm_bwd -- gradients of L = sum_t <dy_t, y_t> + <dhT, hT> through
+ * gla_ssm_fwd (the same inputs; the states are recomputed, nothing is kept
+ * from the forward call), with dy' = dy SiLU(z) and G_t = dL/dh_t:
+ *     G_t = C_t dy'_t + exp(delta_{t+1} A) G_{t+1}   (G_{T-1} = C dy' + dhT)
+ *     dB_t = sum_d delta u G_t,   dC_t = sum_d dy' h_t,   gb = sum_n G B
+ *     dx = delta gb + skip dy',   dA = sum delta P with P = G h_{t-1} exp(delta A)
+ *     ddt = (sum_n P A + u gb) softplus'(dt + dt_bias),   ddt_bias = sum ddt
+ *     dz = dy (C.h + skip u) SiLU'(z),   dskip = sum dy' u,   dh0 = exp(delta_0 A) G_0
+ *   dy rows of D (ld_dy apart), dhT [B, D, N] fp32 or NULL (zero). Outputs,
+ *   contiguous: dx, ddt, dz [B, T, D] and dB, dC [B, T, N] of `dtype`, dA
+ *   [D, N], dskip, ddt_bias [D] and dh0 [B, D, N] fp32. dz goes with z (both
+ *   or neither); dskip, ddt_bias, dh0 may be NULL (not wanted). Outputs may
+ *   not alias inputs.
+ *   workspace: at least gla_ssm_bwd_workspace_size() bytes (required when
+ *   B*T > 0): a state per 16 tokens and partial sums. Sums run in a fixed
+ *   order: the same call gives the same bits. B*T = 0 zeroes the sums, and
+ *   dh0 = dhT.
+ */
+gla_status gla_ssm_bwd(const void *x, int64_t ld_x, const void *dt, int64_t ld_dt, const float *A, const void *Bm,
+                       int64_t ld_B, const void *Cm, int64_t ld_C, const float *skip, const void *z, int64_t ld_z,
+                       const float *dt_bias, int softplus, const float *h0, const void *dy, int64_t ld_dy,
+                       const float *dhT, int B, int T, int D, int N, gla_dtype dtype, void *dx, void *ddt, float *dA,
+                       void *dB, void *dC, float *dskip, void *dz, float *ddt_bias, float *dh0, void *workspace,
+                       size_t workspace_bytes, void *stream);
+size_t gla_ssm_bwd_workspace_size(int B, int T, int D, int N, gla_dtype dtype);
+
+/*
  * gla_conv1d_bwd -- gradients of L = sum_t <dy_t, y_t> through gla_conv1d_fwd
  * (the same x, w, b and win_in): dx [B, T, D] of `dtype`, dw [D, 4] and db [D]
  * fp32 (db or NULL: not wanted). The window is a constant: it gets no

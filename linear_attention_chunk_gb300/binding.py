@@ -25,6 +25,7 @@ Functions:
   gla_ssm_fwd(x, dt, A, Bm, Cm, skip=None, z=None, dt_bias=None, h0=None) -> (y, hT)  selective scan
   gla_ssm_varlen(x, dt, A, Bm, Cm, cu_seqlens, state_pool, ...)           -> y  (pools updated)
   gla_ssm_step(x, dt, A, Bm, Cm, state_pool, ...)                         -> y  (pools updated)
+  gla_ssm_bwd(x, dt, A, Bm, Cm, dy, skip=None, z=None, ...)               -> (dx, ddt, dA, dB, dC, dskip, dz, ddt_bias, dh0)
   gla_conv1d_bwd(x, w, b, dy, win_in=None)                                -> (dx, dw, db)
   gla_rmsnorm(x, w=None, res=None, eps=1e-6)                              -> (y, s)  s = x + res
   gla_rmsnorm_q8(x, w=None, res=None, eps=1e-6, group=128)                -> (y8 e4m3, scale, s)
@@ -52,6 +53,7 @@ ABI_FUNCTIONS = ("gla_chunk_fwd", "gla_chunk_fwd_workspace_size", "gla_chunk_fwd
                  "gla_chunk_bwd_workspace_size", "gla_chunk_bwd_gated", "gla_chunk_bwd_gated_workspace_size", "gla_decode_step", "gla_decode_step_mixer", "gla_mixer_epilogue",
                  "gla_conv1d_fwd", "gla_conv1d_varlen", "gla_conv1d_step", "gla_ssm_fwd", "gla_ssm_fwd_workspace_size",
                  "gla_ssm_varlen", "gla_ssm_varlen_workspace_size", "gla_ssm_step",
+                 "gla_ssm_bwd", "gla_ssm_bwd_workspace_size",
                  "gla_conv1d_bwd", "gla_conv1d_bwd_workspace_size", "gla_rmsnorm_fwd", "gla_rmsnorm_bwd",
                  "gla_rmsnorm_bwd_workspace_size", "gla_selftest_wait_timeout", "gla_check",
                  "gla_status_string", "gla_last_error", "gla_last_launch_count", "gla_version")
@@ -141,6 +143,10 @@ def lib():
             L.gla_ssm_varlen_workspace_size.restype = _sz
             L.gla_ssm_step.argtypes = rows + [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp]
             L.gla_ssm_step.restype = _i
+            L.gla_ssm_bwd.argtypes = rows + [_vp, _vp, _ll, _vp, _i, _i, _i, _i, _i] + [_vp] * 10 + [_sz, _vp]
+            L.gla_ssm_bwd.restype = _i
+            L.gla_ssm_bwd_workspace_size.argtypes = [_i, _i, _i, _i, _i]
+            L.gla_ssm_bwd_workspace_size.restype = _sz
             L.gla_conv1d_bwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]
             L.gla_conv1d_bwd.restype = _i
             L.gla_conv1d_bwd_workspace_size.argtypes = [_i, _i, _i, _i]
@@ -727,6 +733,43 @@ def gla_ssm_step(x, dt, A, Bm, Cm, state_pool, skip=None, z=None, dt_bias=None, 
         y = c.empty((n, D))
     c.run("gla_ssm_step", *args, w, b, sl, pool, win, k, n, D, N, c.code, c.whole(y, (n, D), "y"))
     return y
+
+
+def gla_ssm_bwd_workspace_size(B, T, D, N, dtype=GLA_BF16) -> int:
+    return int(lib().gla_ssm_bwd_workspace_size(B, T, D, N, dtype))
+
+
+def gla_ssm_bwd(x, dt, A, Bm, Cm, dy, skip=None, z=None, dt_bias=None, h0=None, dhT=None, *, softplus=True, dx=None,
+                ddt=None, dA=None, dB=None, dC=None, dskip=None, dz=None, ddt_bias=None, dh0=None, want_dh0=True,
+                workspace=None, stream=None):
+    """Gradients of gla_ssm_fwd (the same inputs; dy [B,T,D] for y, dhT
+    [B,D,N] fp32 or None for hT). Returns (dx, ddt, dA, dB, dC, dskip, dz,
+    ddt_bias, dh0): dskip, dz and ddt_bias are None where skip, z and dt_bias
+    are, dh0 with want_dh0=False."""
+    B, T, D = _lead(x, 3, "x")
+    c = _Call(x, stream)
+    args = _ssm_rows(c, x, dt, A, Bm, Cm, skip, z, dt_bias, softplus)
+    N = A.shape[1]
+    f32, wide, narrow, state = c.torch.float32, (B, T, D), (B, T, N), (B, D, N)
+    args += (c.f32(h0, state, "h0"), *c.rows(dy, wide, "dy"), c.f32(dhT, state, "dhT"), B, T, D, N, c.code)
+    dx = c.empty(wide) if dx is None else dx
+    ddt = c.empty(wide) if ddt is None else ddt
+    dA = c.empty((D, N), f32) if dA is None else dA
+    dB = c.empty(narrow) if dB is None else dB
+    dC = c.empty(narrow) if dC is None else dC
+    if dskip is None and skip is not None:
+        dskip = c.empty((D,), f32)
+    if dz is None and z is not None:
+        dz = c.empty(wide)
+    if ddt_bias is None and dt_bias is not None:
+        ddt_bias = c.empty((D,), f32)
+    if dh0 is None and want_dh0:
+        dh0 = c.empty(state, f32)
+    need = gla_ssm_bwd_workspace_size(B, T, D, N, c.code) if workspace is None else 0
+    c.run("gla_ssm_bwd", *args, c.whole(dx, wide, "dx"), c.whole(ddt, wide, "ddt"), c.f32(dA, (D, N), "dA"),
+          c.whole(dB, narrow, "dB"), c.whole(dC, narrow, "dC"), c.f32(dskip, (D,), "dskip"), c.whole(dz, wide, "dz"),
+          c.f32(ddt_bias, (D,), "ddt_bias"), c.f32(dh0, state, "dh0"), *c.scratch(workspace, need))
+    return dx, ddt, dA, dB, dC, dskip, dz, ddt_bias, dh0
 
 
 def gla_conv1d_bwd_workspace_size(B, T, D, dtype=GLA_BF16) -> int:

@@ -767,6 +767,69 @@ gla_status gla_ssm_step(const void *x, int64_t ld_x, const void *dt, int64_t ld_
     return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_ssm_step launch");
 }
 
+size_t gla_ssm_bwd_workspace_size(int B, int T, int D, int N, gla_dtype dtype) {
+    if (check_ssm_shape(B, T < 0 ? -1 : (int64_t)B * T, D, N, dtype) != GLA_OK || B == 0 || T == 0) return 0;
+    SsmBwdParams p{};
+    p.B = B;
+    p.T = T;
+    p.D = D;
+    p.N = N;
+    return plan_ssm_bwd(p, nullptr) * sizeof(float);
+}
+
+gla_status gla_ssm_bwd(const void *x, int64_t ld_x, const void *dt, int64_t ld_dt, const float *A, const void *Bm,
+                       int64_t ld_B, const void *Cm, int64_t ld_C, const float *skip, const void *z, int64_t ld_z,
+                       const float *dt_bias, int softplus, const float *h0, const void *dy, int64_t ld_dy,
+                       const float *dhT, int B, int T, int D, int N, gla_dtype dtype, void *dx, void *ddt, float *dA,
+                       void *dB, void *dC, float *dskip, void *dz, float *ddt_bias, float *dh0, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    t_err[0] = 0;
+    t_launches = 0;
+    gla_status st = check_ssm_shape(B, T < 0 ? -1 : (int64_t)B * T, D, N, dtype);
+    if (st != GLA_OK) return st;
+    OPTIONAL_PTR(h0, "h0");
+    OPTIONAL_PTR(dhT, "dhT");
+    OPTIONAL_PTR(dh0, "dh0");
+    OPTIONAL_PTR(dskip, "dskip");
+    OPTIONAL_PTR(ddt_bias, "ddt_bias");
+    REQUIRE_PTR(dA, "dA");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int launches = 0;
+    cudaError_t e;
+    if (B == 0 || T == 0) {   // no tokens: the sums are empty, the state passes through
+        e = cudaMemsetAsync(dA, 0, (size_t)D * N * sizeof(float), s);
+        if (e == cudaSuccess && dskip) e = cudaMemsetAsync(dskip, 0, (size_t)D * sizeof(float), s);
+        if (e == cudaSuccess && ddt_bias) e = cudaMemsetAsync(ddt_bias, 0, (size_t)D * sizeof(float), s);
+        if (e == cudaSuccess && B > 0 && dh0 != dhT) e = launch_copy_state(dhT, dh0, (size_t)B * D * N, s, &launches);
+        t_launches = launches;
+        return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_ssm_bwd(no tokens)");
+    }
+    SsmParams in{x, dt, z, Bm, Cm, (long)ld_x, (long)ld_dt, (long)ld_z, (long)ld_B, (long)ld_C, A, skip, dt_bias};
+    in.D = D;
+    in.N = N;
+    if ((st = check_ssm_inputs(in, dtype)) != GLA_OK) return st;
+    if ((st = check_rows(dy, ld_dy, D, dtype == GLA_BF16 ? 2 : 4, true, "dy")) != GLA_OK) return st;
+    REQUIRE_PTR(dx, "dx");
+    REQUIRE_PTR(ddt, "ddt");
+    REQUIRE_PTR(dB, "dB");
+    REQUIRE_PTR(dC, "dC");
+    if ((z != nullptr) != (dz != nullptr)) return fail(GLA_ERR_INVALID_ARG, "z and dz come together");
+    OPTIONAL_PTR(dz, "dz");
+    for (const void *out : {(const void *)dx, (const void *)ddt, (const void *)dz, (const void *)dB, (const void *)dC})
+        if (out && (out == x || out == dt || out == z || out == dy || out == Bm || out == Cm))
+            return fail(GLA_ERR_INVALID_ARG, "an output may not alias an input");
+    REQUIRE_PTR(workspace, "workspace");
+    const size_t need = gla_ssm_bwd_workspace_size(B, T, D, N, dtype);
+    if (workspace_bytes < need)
+        return fail(GLA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+    SsmBwdParams p{x, dt, z, Bm, Cm, dy, (long)ld_x, (long)ld_dt, (long)ld_z, (long)ld_B, (long)ld_C, (long)ld_dy, A, skip,
+                   dt_bias, h0, dhT, B, T, D, N, softplus, dx, ddt, dz, dB, dC, dA, dskip, ddt_bias, dh0};
+    plan_ssm_bwd(p, static_cast<float *>(workspace));
+    e = launch_ssm_bwd(p, dtype == GLA_BF16, s, &launches);
+    t_launches = launches;
+    return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_ssm_bwd launch");
+}
+
 size_t gla_conv1d_bwd_workspace_size(int B, int T, int D, gla_dtype dtype) {
     if (check_conv_shape(B, T, D, dtype) != GLA_OK || B == 0 || T == 0) return 0;
     const int tile = conv_bwd_tile(B, T, D);

@@ -140,6 +140,23 @@ size_t ssm_workspace_bytes(const SsmPlan &plan, long nseq, int D, int N);
 cudaError_t launch_ssm_scan(const SsmParams &p, bool bf16, cudaStream_t s, int *launches);
 cudaError_t launch_ssm_step(const SsmParams &p, bool bf16, cudaStream_t s, int *launches);
 
+// Gradients of the selective scan (ssm_bwd.cu), batched; names as in
+// SsmParams, dy's rows ldg apart; the outputs contiguous. L .. part_c: the cut
+// and the workspace, laid out by plan_ssm_bwd (its floats returned; ws NULL: sizes only).
+struct SsmBwdParams {
+    const void *x, *dt, *z, *Bm, *Cm, *dy;
+    long ldx, ldt, ldz, ldb, ldc, ldg;
+    const float *A, *skip, *dt_bias, *h0, *dhT;
+    int B, T, D, N, softplus;
+    void *dx, *ddt, *dz, *dB, *dC;
+    float *dA, *dskip, *ddt_bias, *dh0;
+    long L;
+    int nseg, tiles;
+    float *seg_h, *seg_g, *seg_sum, *tile_h, *part_a, *part_v, *part_b, *part_c;
+};
+size_t plan_ssm_bwd(SsmBwdParams &p, float *ws);
+cudaError_t launch_ssm_bwd(const SsmBwdParams &p, bool bf16, cudaStream_t s, int *launches);
+
 // Gradients of the Conv1d (conv_bwd.cu): x, dy, dx [B, T, D]; win [B, 4, D] or
 // NULL; part: [B * ceil(T / tile), 5 D] partial sums; dw [D, 4], db [D] or NULL.
 struct ConvBwdParams {

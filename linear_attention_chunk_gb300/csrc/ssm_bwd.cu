@@ -1,0 +1,609 @@
+// ssm_bwd.cu -- gradients of the selective state-space scan (ssm.cu). With
+// delta = softplus(dt + bias), a_t = exp(delta_t A), dy'_t = dy_t SiLU(z_t),
+// per channel and state:
+//     h_t = a_t h_{t-1} + delta_t B_t u_t             (recomputed)
+//     G_t = C_t dy'_t + c_t,   c_{t-1} = a_t G_t      (from the last token back, c_{T-1} = dhT)
+//     P_t = c_{t-1} h_{t-1}                           (dL / d(delta_t A))
+// and the sums
+//     over states n:   y0 = sum C h,  s1 = sum G B,  s2 = sum P A
+//         dx = delta s1 + skip dy',   ddt = (s2 + u s1) sigmoid(dt + bias),
+//         dz = dy (y0 + skip u) SiLU'(z)
+//     over channels:   dC_t = sum dy' h_t,  dB_t = sum delta u G_t
+//     over tokens:     dA = sum delta P,  dskip = sum dy' u,  ddt_bias = sum ddt;  dh0 = c_{-1}
+//
+// Two chains run against each other in time, so every state is needed once
+// more after the forward sweep has passed it. A CTA owns 32 W channels (a
+// quad of lanes four of them, each lane a quarter of their states) of one
+// segment of a sequence: it sweeps forward and leaves the state entering every
+// 16-token tile in the workspace (read back soon after, from L2), then takes
+// the tiles from the last to the first: forward through the tile, keeping the
+// state before every fourth token in shared memory, then for each four tokens,
+// last first, the four states again in registers (64 of them) with y0 and dC
+// on the way, and back through them with G. States are thus recomputed, never
+// stored per token (64 bytes a token and channel) nor divided back.
+// Sums over states are exchanged inside a quad, four tokens at a time; sums
+// over channels between the quads, eight numbers over eight quads, then added
+// over the warps of the CTA through shared memory and over CTAs in a second
+// launch, in a fixed order. The elementwise ends (loads, SiLU, softplus, the
+// products above) are vectors of eight channels a thread, as in the forward.
+//
+// Few sequences are cut into segments as in the forward: a first launch
+// leaves each segment's state from zero and its c from zero together, with one
+// exponential a state (c needs the running product of the decays), and the
+// second folds the segments before and behind its own.
+#include "ssm_common.cuh"
+
+namespace gla {
+namespace {
+
+using namespace ssm;
+
+constexpr int kTile = 16;          // tokens per tile
+constexpr int kWarps = 4;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int K> struct Lane;      // K channels' numbers as one shared-memory access
+template <> struct Lane<2> {
+    using type = float2;
+    static __device__ __forceinline__ void get(const float *p, float (&v)[2]) {
+        const float2 u = *reinterpret_cast<const float2 *>(p);
+        v[0] = u.x; v[1] = u.y;
+    }
+    static __device__ __forceinline__ void put(float *p, const float (&v)[2]) {
+        *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+    }
+};
+template <> struct Lane<4> {
+    static __device__ __forceinline__ void get(const float *p, float (&v)[4]) {
+        const float4 u = *reinterpret_cast<const float4 *>(p);
+        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+    }
+    static __device__ __forceinline__ void put(float *p, const float (&v)[4]) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+};
+
+// Eight numbers, each spread over the eight quads of a warp: the sum of
+// number (lane / 4), in seven exchanges.
+__device__ __forceinline__ float across_quads(const float (&v)[8], int lane) {
+    float a[4], b[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 16;
+        a[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 4], 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool up = lane & 8;
+        b[i] = (up ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 2], 8);
+    }
+    const bool up = lane & 4;
+    return (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4);
+}
+
+// Shapes of one instance: N states, K channels a lane.
+template <int N_> struct Shape {
+    static constexpr int N = N_, SP = N / 4, P = SP / 2;
+    static constexpr int K = N == 32 ? 2 : 4;         // 16 states a lane at most (8 at N = 8)
+    static constexpr int CW = 8 * K, CH = CW * kWarps, VW = CH / 8, TH = 32 * kWarps;
+    static constexpr int RS = CH + 8;                 // row step of the [token][channel] arrays
+    static constexpr int VPT = kTile * VW / TH;       // vectors a thread loads per tile
+    static constexpr int kRow = kTile * RS;           // floats of one such array
+    // delta, delta u (then s1), dy' (then y0), s2; B, C; states; dB, dC of every warp
+    static constexpr int kCkpt = 3 * K * P * 32 * 2 * kWarps;
+    static constexpr int kPart = kWarps * 2 * kTile * N;
+    static constexpr int kMain = 4 * kRow + 2 * kTile * N + kCkpt + kPart;
+    static constexpr int kLocal = 3 * kRow + 2 * kTile * N;
+};
+
+// A thread's vectors of a tile: rows and channels.
+template <class S> struct Where {
+    int c, vt;
+    bool on, whole;
+    __device__ __forceinline__ Where(int c0, int D)
+        : c(c0 + (int)(threadIdx.x % S::VW) * 8), vt((int)threadIdx.x / S::VW), on(c < D), whole(c + 8 <= D) {}
+};
+
+// One tile's delta, delta u and (kGrad) dy' into shared memory, B and C too.
+// Steps past the end are 0: they leave both chains as they are.
+template <typename T, class S, bool kGrad>
+__device__ __forceinline__ void load_tile(const SsmBwdParams &p, const Where<S> &w, long row0, int ntok, float *sD, float *sU,
+                                          float *sG, float *sB, float *sC, const float (&bias)[8]) {
+#pragma unroll
+    for (int k = 0; k < S::VPT; ++k) {
+        const int t = w.vt + k * (kTile / S::VPT);
+        const bool in = w.on && t < ntok;
+        const size_t row = (size_t)(row0 + t);
+        float x[8], d[8], g[8];
+        raw_unpack(in ? raw_load(static_cast<const T *>(p.x) + row * p.ldx + w.c, w.whole) : raw_zero<T>(), x);
+        raw_unpack(in ? raw_load(static_cast<const T *>(p.dt) + row * p.ldt + w.c, w.whole) : raw_zero<T>(), d);
+        if (kGrad) {
+            raw_unpack(in ? raw_load(static_cast<const T *>(p.dy) + row * p.ldg + w.c, w.whole) : raw_zero<T>(), g);
+            if (p.z && in) {
+                float z[8];
+                raw_unpack(raw_load(static_cast<const T *>(p.z) + row * p.ldz + w.c, w.whole), z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[i] *= silu(z[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            d[i] += bias[i];
+            if (p.softplus) d[i] = softplus(d[i]);
+            if (!in) d[i] = 0.f;
+            x[i] *= d[i];
+        }
+        const int at = t * S::RS + (int)(threadIdx.x % S::VW) * 8;
+        store8(sD + at, d, true);
+        store8(sU + at, x, true);
+        if (kGrad) store8(sG + at, g, true);
+    }
+    for (int e = threadIdx.x; e < kTile * S::N; e += S::TH) {
+        const int t = e / S::N, n = e % S::N;
+        const size_t row = (size_t)(row0 + t);
+        sB[e] = t < ntok ? Elem<T>::load(static_cast<const T *>(p.Bm) + row * p.ldb + n) : 0.f;
+        if (kGrad) sC[e] = t < ntok ? Elem<T>::load(static_cast<const T *>(p.Cm) + row * p.ldc + n) : 0.f;
+    }
+}
+
+template <class S> struct State {
+    f2 v[S::K][S::P];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int k = 0; k < S::K; ++k)
+#pragma unroll
+            for (int i = 0; i < S::P; ++i) v[k][i] = 0;
+    }
+    __device__ __forceinline__ void load(const float *src, float f = 1.f) {   // src: the first channel's, in [D, N]
+#pragma unroll
+        for (int k = 0; k < S::K; ++k)
+#pragma unroll
+            for (int i = 0; i < S::P; ++i) {
+                const float2 u = reinterpret_cast<const float2 *>(src + k * S::N)[i];
+                v[k][i] = f2_pack(u.x * f, u.y * f);
+            }
+    }
+    __device__ __forceinline__ void store(float *dst) const {
+#pragma unroll
+        for (int k = 0; k < S::K; ++k)
+#pragma unroll
+            for (int i = 0; i < S::P; ++i) reinterpret_cast<float2 *>(dst + k * S::N)[i] = f2_split(v[k][i]);
+    }
+};
+
+// h <- exp(delta A) h + (delta u) B for one token of the lane's channels.
+template <class S>
+__device__ __forceinline__ void advance(State<S> &h, const State<S> &a2, const float *sD, const float *sU, const float *sB) {
+    float d[S::K], u[S::K];
+    Lane<S::K>::get(sD, d);
+    Lane<S::K>::get(sU, u);
+    const f2 *b = reinterpret_cast<const f2 *>(sB);
+#pragma unroll
+    for (int k = 0; k < S::K; ++k) {
+        const f2 dd = f2_pack(d[k], d[k]), uu = f2_pack(u[k], u[k]);
+#pragma unroll
+        for (int i = 0; i < S::P; ++i) h.v[k][i] = fma2(ex2_pair(mul2(dd, a2.v[k][i])), h.v[k][i], mul2(uu, b[i]));
+    }
+}
+
+// ------------------------------------------------------------ first launch
+// Of every segment: the state it ends in from zero (seg_h), the c that leaves
+// its first token from zero (seg_g), and the sum of its steps.
+template <typename T, class S>
+__global__ void __launch_bounds__(S::TH, 2) ssm_bwd_local_kernel(const SsmBwdParams p, int tiles) {
+    extern __shared__ __align__(16) float smem[];
+    float *sD = smem, *sU = sD + S::kRow, *sG = sU + S::kRow, *sB = sG + S::kRow, *sC = sB + kTile * S::N;
+    const int c0 = (int)(blockIdx.x % (unsigned)tiles) * S::CH;
+    const long unit = blockIdx.x / (unsigned)tiles;
+    const int b = (int)(unit / p.nseg), seg = (int)(unit % p.nseg);
+    const long row0 = (long)b * p.T + (long)seg * p.L;
+    const int ntok = (int)min(p.L, (long)p.T - (long)seg * p.L);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, q = lane % 4;
+    const int lc = warp * S::CW + lane / 4 * S::K, ch = c0 + lc;
+    const size_t cell = (size_t)ch * S::N + q * S::SP;
+    const bool on = ch < p.D;
+    const Where<S> w(c0, p.D);
+    float bias[8];
+    param8(w.on ? p.dt_bias : nullptr, w.c, w.whole, bias);
+
+    State<S> a2, h, pr, c;
+    a2.zero();
+    if (on) a2.load(p.A + cell, kLog2e);
+    h.zero();
+    c.zero();
+#pragma unroll
+    for (int k = 0; k < S::K; ++k)
+#pragma unroll
+        for (int i = 0; i < S::P; ++i) pr.v[k][i] = f2_pack(1.f, 1.f);
+    float sum[S::K] = {};
+    for (int t0 = 0; t0 < ntok; t0 += kTile) {
+        load_tile<T, S, true>(p, w, row0 + t0, ntok - t0, sD, sU, sG, sB, sC, bias);
+        __syncthreads();
+#pragma unroll 2
+        for (int t = 0; t < kTile; ++t) {
+            float d[S::K], u[S::K], g[S::K];
+            Lane<S::K>::get(sD + t * S::RS + lc, d);
+            Lane<S::K>::get(sU + t * S::RS + lc, u);
+            Lane<S::K>::get(sG + t * S::RS + lc, g);
+            const f2 *bb = reinterpret_cast<const f2 *>(sB + t * S::N + q * S::SP);
+            const f2 *cc = reinterpret_cast<const f2 *>(sC + t * S::N + q * S::SP);
+#pragma unroll
+            for (int k = 0; k < S::K; ++k) {
+                const f2 dd = f2_pack(d[k], d[k]), uu = f2_pack(u[k], u[k]), gg = f2_pack(g[k], g[k]);
+                sum[k] += d[k];
+#pragma unroll
+                for (int i = 0; i < S::P; ++i) {
+                    const f2 a = ex2_pair(mul2(dd, a2.v[k][i]));
+                    h.v[k][i] = fma2(a, h.v[k][i], mul2(uu, bb[i]));
+                    pr.v[k][i] = mul2(pr.v[k][i], a);
+                    c.v[k][i] = fma2(pr.v[k][i], mul2(gg, cc[i]), c.v[k][i]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    if (on) {
+        h.store(p.seg_h + (size_t)unit * p.D * S::N + cell);
+        c.store(p.seg_g + (size_t)unit * p.D * S::N + cell);
+        if (q == 0)
+#pragma unroll
+            for (int k = 0; k < S::K; ++k) p.seg_sum[(size_t)unit * p.D + ch + k] = sum[k];
+    }
+}
+
+// ----------------------------------------------------------- second launch
+template <typename T, class S>
+__global__ void __launch_bounds__(S::TH, 3) ssm_bwd_kernel(const SsmBwdParams p, int tiles) {
+    extern __shared__ __align__(16) float smem[];
+    float *sD = smem, *sU = sD + S::kRow, *sG = sU + S::kRow, *sS = sG + S::kRow, *sB = sS + S::kRow;
+    float *sC = sB + kTile * S::N;
+    f2 *sH = reinterpret_cast<f2 *>(sC + kTile * S::N);        // [warp][3][K * P][lane]
+    float *sP = reinterpret_cast<float *>(sH) + S::kCkpt;      // [warp][B, C][token][N]
+    const int blk = (int)(blockIdx.x % (unsigned)tiles), c0 = blk * S::CH;
+    const long unit = blockIdx.x / (unsigned)tiles;
+    const int b = (int)(unit / p.nseg), seg = (int)(unit % p.nseg);
+    const long row0 = (long)b * p.T + (long)seg * p.L;
+    const int ntok = (int)min(p.L, (long)p.T - (long)seg * p.L), ntile = (ntok + kTile - 1) / kTile;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, q = lane % 4;
+    const int lc = warp * S::CW + lane / 4 * S::K, ch = c0 + lc;
+    const size_t cell = (size_t)ch * S::N + q * S::SP, plane = (size_t)p.D * S::N;
+    const bool on = ch < p.D;
+    const Where<S> w(c0, p.D);
+    float bias[8];
+    param8(w.on ? p.dt_bias : nullptr, w.c, w.whole, bias);
+
+    State<S> a2, h, c;
+    a2.zero();
+    h.zero();
+    c.zero();
+    if (on) {
+        a2.load(p.A + cell, kLog2e);
+        if (p.h0) h.load(p.h0 + (size_t)b * plane + cell);
+        if (p.dhT) c.load(p.dhT + (size_t)b * plane + cell);
+        auto fold = [&](State<S> &s, const float *seg_s, size_t u) {
+            State<S> e;
+            e.load(seg_s + u * plane + cell);
+#pragma unroll
+            for (int k = 0; k < S::K; ++k) {
+                const float d = p.seg_sum[u * p.D + ch + k];
+                const f2 dd = f2_pack(d, d);
+#pragma unroll
+                for (int i = 0; i < S::P; ++i) s.v[k][i] = fma2(ex2_pair(mul2(dd, a2.v[k][i])), s.v[k][i], e.v[k][i]);
+            }
+        };
+        for (int s = 0; s < seg; ++s) fold(h, p.seg_h, (size_t)(unit - seg + s));
+        for (int s = p.nseg - 1; s > seg; --s) fold(c, p.seg_g, (size_t)(unit - seg + s));
+    }
+
+    // ---- forward sweep: the state entering every tile
+    float *tile_h = p.tile_h + ((size_t)b * p.tiles + (size_t)seg * p.L / kTile) * plane + cell;
+    for (int i = 0; i + 1 < ntile; ++i) {
+        if (on) h.store(tile_h + (size_t)i * plane);
+        load_tile<T, S, false>(p, w, row0 + i * kTile, kTile, sD, sU, nullptr, sB, nullptr, bias);
+        __syncthreads();
+#pragma unroll 2
+        for (int t = 0; t < kTile; ++t) advance<S>(h, a2, sD + t * S::RS + lc, sU + t * S::RS + lc, sB + t * S::N + q * S::SP);
+        __syncthreads();
+    }
+
+    float skip[8], dskip[8] = {}, dbias[8] = {};
+    param8(w.on ? p.skip : nullptr, w.c, w.whole, skip);
+    State<S> dA;
+    dA.zero();
+    f2 *ck = sH + (size_t)warp * 3 * S::K * S::P * 32 + lane;
+    float *myP = sP + warp * 2 * kTile * S::N;
+
+    for (int i = ntile - 1; i >= 0; --i) {
+        const long tr = row0 + (long)i * kTile;
+        const int left = min(kTile, ntok - i * kTile);
+        load_tile<T, S, true>(p, w, tr, left, sD, sU, sG, sB, sC, bias);
+        if (i + 1 < ntile && on) h.load(tile_h + (size_t)i * plane);
+        __syncthreads();
+        // ---- forward through the tile's first twelve tokens
+        State<S> hs[4];
+        hs[0] = h;
+#pragma unroll
+        for (int s = 0; s < 3; ++s) {
+#pragma unroll
+            for (int k = 0; k < S::K; ++k)
+#pragma unroll
+                for (int j = 0; j < S::P; ++j) ck[(s * S::K * S::P + k * S::P + j) * 32] = hs[0].v[k][j];
+#pragma unroll
+            for (int t = 4 * s; t < 4 * s + 4; ++t)
+                advance<S>(hs[0], a2, sD + t * S::RS + lc, sU + t * S::RS + lc, sB + t * S::N + q * S::SP);
+        }
+        // ---- four tokens at a time, the last first
+#pragma unroll 1
+        for (int s = 3; s >= 0; --s) {
+            if (s < 3)
+#pragma unroll
+                for (int k = 0; k < S::K; ++k)
+#pragma unroll
+                    for (int j = 0; j < S::P; ++j) hs[0].v[k][j] = ck[(s * S::K * S::P + k * S::P + j) * 32];
+            const int t0 = 4 * s;
+            float pk[S::K][4];                          // a sum over states, per channel and token
+            float pn[8];                                // a sum over channels, per token and state
+            // the states again, with y0 and dC
+            State<S> cur = hs[0];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = t0 + j;
+                if (j) hs[j] = cur;
+                advance<S>(cur, a2, sD + t * S::RS + lc, sU + t * S::RS + lc, sB + t * S::N + q * S::SP);
+                float g[S::K];
+                Lane<S::K>::get(sG + t * S::RS + lc, g);
+                const f2 *cc = reinterpret_cast<const f2 *>(sC + t * S::N + q * S::SP);
+                f2 dc[S::P];
+#pragma unroll
+                for (int k = 0; k < S::K; ++k) {
+                    const f2 gg = f2_pack(g[k], g[k]);
+                    f2 y = 0;
+#pragma unroll
+                    for (int m = 0; m < S::P; ++m) {
+                        y = m ? fma2(cur.v[k][m], cc[m], y) : mul2(cur.v[k][m], cc[m]);
+                        dc[m] = k ? fma2(gg, cur.v[k][m], dc[m]) : mul2(gg, cur.v[k][m]);
+                    }
+                    const float2 ys = f2_split(y);
+                    pk[k][j] = ys.x + ys.y;
+                }
+                constexpr int per = 8 / S::SP;          // tokens whose sums fill eight numbers
+#pragma unroll
+                for (int m = 0; m < S::P; ++m) {
+                    const float2 v = f2_split(dc[m]);
+                    pn[j % per * S::SP + 2 * m] = v.x;
+                    pn[j % per * S::SP + 2 * m + 1] = v.y;
+                }
+                if (j % per == per - 1) {
+                    const int idx = lane / 4;
+                    myP[(kTile + t - per + 1 + idx / S::SP) * S::N + q * S::SP + idx % S::SP] = across_quads(pn, lane);
+                }
+            }
+            float y0[S::K];
+#pragma unroll
+            for (int k = 0; k < S::K; ++k) y0[k] = quad_transpose_sum(pk[k], lane);
+            // back through them
+            float pk2[S::K][4];
+#pragma unroll
+            for (int j = 3; j >= 0; --j) {
+                const int t = t0 + j;
+                float d[S::K], u[S::K], g[S::K];
+                Lane<S::K>::get(sD + t * S::RS + lc, d);
+                Lane<S::K>::get(sU + t * S::RS + lc, u);
+                Lane<S::K>::get(sG + t * S::RS + lc, g);
+                const f2 *bb = reinterpret_cast<const f2 *>(sB + t * S::N + q * S::SP);
+                const f2 *cc = reinterpret_cast<const f2 *>(sC + t * S::N + q * S::SP);
+                f2 db[S::P];
+#pragma unroll
+                for (int k = 0; k < S::K; ++k) {
+                    const f2 dd = f2_pack(d[k], d[k]), uu = f2_pack(u[k], u[k]), gg = f2_pack(g[k], g[k]);
+                    f2 s1 = 0, s2 = 0;
+#pragma unroll
+                    for (int m = 0; m < S::P; ++m) {
+                        const f2 G = fma2(gg, cc[m], c.v[k][m]);
+                        db[m] = k ? fma2(uu, G, db[m]) : mul2(uu, G);
+                        s1 = m ? fma2(G, bb[m], s1) : mul2(G, bb[m]);
+                        c.v[k][m] = mul2(ex2_pair(mul2(dd, a2.v[k][m])), G);
+                        const f2 P = mul2(c.v[k][m], hs[j].v[k][m]);
+                        dA.v[k][m] = fma2(dd, P, dA.v[k][m]);
+                        s2 = m ? fma2(P, a2.v[k][m], s2) : mul2(P, a2.v[k][m]);
+                    }
+                    const float2 v1 = f2_split(s1), v2 = f2_split(s2);
+                    pk[k][j] = v1.x + v1.y;
+                    pk2[k][j] = v2.x + v2.y;
+                }
+                constexpr int per = 8 / S::SP;
+#pragma unroll
+                for (int m = 0; m < S::P; ++m) {
+                    const float2 v = f2_split(db[m]);
+                    pn[j % per * S::SP + 2 * m] = v.x;
+                    pn[j % per * S::SP + 2 * m + 1] = v.y;
+                }
+                if (j % per == 0) {
+                    const int idx = lane / 4;
+                    myP[(t + idx / S::SP) * S::N + q * S::SP + idx % S::SP] = across_quads(pn, lane);
+                }
+            }
+            // lane q of the quad finishes token t0 + q; every lane of the warp has read the four tokens by now
+            float s1[S::K], s2[S::K];
+#pragma unroll
+            for (int k = 0; k < S::K; ++k) {
+                s1[k] = quad_transpose_sum(pk[k], lane);
+                s2[k] = quad_transpose_sum(pk2[k], lane);
+            }
+            __syncwarp();
+            const int at = (t0 + q) * S::RS + lc;
+            Lane<S::K>::put(sU + at, s1);
+            Lane<S::K>::put(sG + at, y0);
+            Lane<S::K>::put(sS + at, s2);
+        }
+        __syncthreads();
+
+        // ---- the elementwise end
+#pragma unroll 1
+        for (int k = 0; k < S::VPT; ++k) {
+            const int t = w.vt + k * (kTile / S::VPT);
+            if (!w.on || t >= left) continue;
+            const size_t row = (size_t)(tr + t);
+            const int at = t * S::RS + tid % S::VW * 8;
+            float x[8], d[8], g[8], z[8], o[8];
+            raw_unpack(raw_load(static_cast<const T *>(p.x) + row * p.ldx + w.c, w.whole), x);
+            raw_unpack(raw_load(static_cast<const T *>(p.dy) + row * p.ldg + w.c, w.whole), g);
+            if (p.z) {
+                raw_unpack(raw_load(static_cast<const T *>(p.z) + row * p.ldz + w.c, w.whole), z);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float sg = sigmoid(z[e]), y = fmaf(skip[e], x[e], sG[at + e]);
+                    o[e] = g[e] * y * (sg * fmaf(z[e], 1.f - sg, 1.f));
+                    g[e] *= z[e] * sg;
+                }
+                store8(static_cast<T *>(p.dz) + row * p.D + w.c, o, w.whole);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                dskip[e] = fmaf(g[e], x[e], dskip[e]);
+                o[e] = fmaf(sD[at + e], sU[at + e], skip[e] * g[e]);
+            }
+            store8(static_cast<T *>(p.dx) + row * p.D + w.c, o, w.whole);
+            if (p.softplus) raw_unpack(raw_load(static_cast<const T *>(p.dt) + row * p.ldt + w.c, w.whole), d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                o[e] = fmaf(sS[at + e], kLn2, sU[at + e] * x[e]);
+                if (p.softplus) o[e] *= sigmoid(d[e] + bias[e]);
+                dbias[e] += o[e];
+            }
+            store8(static_cast<T *>(p.ddt) + row * p.D + w.c, o, w.whole);
+        }
+        // dB and dC of the tile, over the warps
+        for (int e = tid; e < 2 * kTile * S::N; e += S::TH) {
+            const int t = e / S::N % kTile;
+            float v = 0.f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) v += sP[k * 2 * kTile * S::N + e];
+            if (t < left) {
+                float *dst = e < kTile * S::N ? p.part_b : p.part_c;
+                dst[((size_t)blk * p.B * p.T + tr + t) * S::N + e % S::N] = v;
+            }
+        }
+        __syncthreads();
+    }
+
+    if (on) {
+        dA.store(p.part_a + (size_t)unit * plane + cell);
+        if (p.dh0 && seg == 0) c.store(p.dh0 + (size_t)b * plane + cell);
+    }
+    // dskip and ddt_bias: over the threads that share the eight channels
+    float *red = smem;                                  // [thread][16]
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        red[e * S::TH + tid] = dskip[e];
+        red[(e + 8) * S::TH + tid] = dbias[e];
+    }
+    __syncthreads();
+    for (int e = tid; e < 2 * S::CH; e += S::TH) {
+        const int which = e / S::CH, lc2 = e % S::CH;
+        float v = 0.f;
+        for (int r = lc2 / 8; r < S::TH; r += S::VW) v += red[(which * 8 + lc2 % 8) * S::TH + r];
+        if (c0 + lc2 < p.D) p.part_v[((size_t)unit * 2 + which) * p.D + c0 + lc2] = v;
+    }
+}
+
+// out[c] = sum over r of part[r][c], rounded to T: few rows, many columns.
+template <typename T> __global__ void __launch_bounds__(256) sum_blocks_kernel(const float *part, int rows, long cols, T *out) {
+    const long c = ((long)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (c >= cols) return;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+        const float4 u = __ldg(reinterpret_cast<const float4 *>(part + (size_t)r * cols + c));
+        v.x += u.x;
+        v.y += u.y;
+        v.z += u.z;
+        v.w += u.w;
+    }
+    Elem<T>::store(out + c, v.x);
+    Elem<T>::store(out + c + 1, v.y);
+    Elem<T>::store(out + c + 2, v.z);
+    Elem<T>::store(out + c + 3, v.w);
+}
+
+template <typename T, int N> cudaError_t run(const SsmBwdParams &p, cudaStream_t s, int *launches) {
+    using S = Shape<N>;
+    const int tiles = (p.D + S::CH - 1) / S::CH;
+    const long units = (long)p.B * p.nseg;
+    if ((long double)units * tiles > 2147483647.0L) return cudaErrorInvalidValue;
+    cudaError_t e;
+    if (p.nseg > 1) {
+        constexpr int bytes = S::kLocal * (int)sizeof(float);
+        if (bytes > 48 * 1024 &&
+            (e = cudaFuncSetAttribute(ssm_bwd_local_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
+            return e;
+        ssm_bwd_local_kernel<T, S><<<(unsigned)(units * tiles), S::TH, bytes, s>>>(p, tiles);
+        if (launches) ++*launches;
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    constexpr int bytes = S::kMain * (int)sizeof(float);
+    if ((e = cudaFuncSetAttribute(ssm_bwd_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+    ssm_bwd_kernel<T, S><<<(unsigned)(units * tiles), S::TH, bytes, s>>>(p, tiles);
+    if (launches) ++*launches;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const long cols = (long)p.B * p.T * N;
+    const unsigned grid = (unsigned)((cols / 4 + 255) / 256);
+    sum_blocks_kernel<T><<<grid, 256, 0, s>>>(p.part_b, tiles, cols, static_cast<T *>(p.dB));
+    sum_blocks_kernel<T><<<grid, 256, 0, s>>>(p.part_c, tiles, cols, static_cast<T *>(p.dC));
+    if (launches) *launches += 2;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_sum_rows(p.part_a, units, (long)p.D * N, (long)p.D * N, p.dA, s, launches)) != cudaSuccess) return e;
+    if ((e = launch_sum_rows(p.part_v, units, p.D, 2L * p.D, p.dskip, s, launches)) != cudaSuccess) return e;
+    return launch_sum_rows(p.part_v + p.D, units, p.D, 2L * p.D, p.ddt_bias, s, launches);
+}
+
+template <typename T> cudaError_t by_state(const SsmBwdParams &p, cudaStream_t s, int *launches) {
+    switch (p.N) {
+    case 8: return run<T, 8>(p, s, launches);
+    case 16: return run<T, 16>(p, s, launches);
+    case 32: return run<T, 32>(p, s, launches);
+    }
+    return cudaErrorInvalidValue;
+}
+
+size_t round16(size_t floats) { return (floats + 3) / 4 * 4; }
+
+}  // namespace
+
+// Channels a CTA of the backward owns.
+static int bwd_channels(int N) { return N == 32 ? Shape<32>::CH : Shape<16>::CH; }
+
+// Cuts the sequences and lays out the workspace; returns its floats.
+size_t plan_ssm_bwd(SsmBwdParams &p, float *ws) {
+    const long chains = (long)p.B * ((p.D + bwd_channels(p.N) - 1) / bwd_channels(p.N));
+    const long want = 3L * device_sm_count();
+    long nseg = (want + chains - 1) / chains;
+    if (nseg > 64) nseg = 64;
+    long L = (p.T + nseg - 1) / nseg;
+    L = (L + kTile - 1) / kTile * kTile;
+    if (L < 64) L = 64;
+    p.L = L;
+    p.nseg = (int)((p.T + L - 1) / L);
+    p.tiles = (p.T + kTile - 1) / kTile;
+    const size_t plane = (size_t)p.D * p.N, units = (size_t)p.B * p.nseg, blocks = (p.D + bwd_channels(p.N) - 1) / bwd_channels(p.N);
+    size_t at = 0;
+    auto take = [&](float *&dst, size_t floats) {
+        dst = ws ? ws + at : nullptr;
+        at += round16(floats);
+    };
+    take(p.seg_h, p.nseg > 1 ? units * plane : 0);
+    take(p.seg_g, p.nseg > 1 ? units * plane : 0);
+    take(p.seg_sum, p.nseg > 1 ? units * p.D : 0);
+    take(p.tile_h, (size_t)p.B * p.tiles * plane);
+    take(p.part_a, units * plane);
+    take(p.part_v, units * 2 * p.D);
+    take(p.part_b, blocks * p.B * p.T * p.N);
+    take(p.part_c, blocks * p.B * p.T * p.N);
+    return at;
+}
+
+cudaError_t launch_ssm_bwd(const SsmBwdParams &p, bool bf16, cudaStream_t s, int *launches) {
+    return bf16 ? by_state<__nv_bfloat16>(p, s, launches) : by_state<float>(p, s, launches);
+}
+
+}  // namespace gla

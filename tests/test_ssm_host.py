@@ -111,3 +111,25 @@ def test_norm_rejects_bad_arguments(L):
     need = binding.gla_rmsnorm_bwd_workspace_size(4, 256)
     assert need == 4 * 256 * 4 and bwd(n=need - 1) == binding.GLA_ERR_WORKSPACE
     assert bwd(rows=0, dw=None) == binding.GLA_OK
+
+
+def test_selective_scan_backward_rejects_bad_arguments(L):
+    def bwd(**kw):
+        a = dict(x=FAKE, ldx=64, dt=FAKE, ldt=64, A=FAKE, Bm=FAKE, ldb=16, Cm=FAKE, ldc=16, skip=None, z=None, ldz=0,
+                 bias=None, h0=None, dy=FAKE, ldg=64, dhT=None, B=2, T=50, D=64, N=16, dtype=0, dx=FAKE + 0x100,
+                 ddt=FAKE + 0x200, dA=FAKE, dB=FAKE + 0x300, dC=FAKE + 0x400, dskip=None, dz=None, db=None, dh0=None,
+                 ws=FAKE, n=1 << 40)
+        a.update(kw)
+        return L.gla_ssm_bwd(a["x"], a["ldx"], a["dt"], a["ldt"], a["A"], a["Bm"], a["ldb"], a["Cm"], a["ldc"],
+                             a["skip"], a["z"], a["ldz"], a["bias"], 1, a["h0"], a["dy"], a["ldg"], a["dhT"], a["B"],
+                             a["T"], a["D"], a["N"], a["dtype"], a["dx"], a["ddt"], a["dA"], a["dB"], a["dC"],
+                             a["dskip"], a["dz"], a["db"], a["dh0"], a["ws"], a["n"], None)
+    for kw in (dict(x=None), dict(ldx=60), dict(dt=ODD), dict(A=None), dict(Bm=None), dict(Cm=FAKE + 1), dict(dy=None),
+               dict(dy=ODD), dict(ldg=63), dict(dx=None), dict(ddt=None), dict(dA=None), dict(dB=None), dict(dC=ODD),
+               dict(dskip=ODD), dict(db=ODD), dict(dh0=ODD), dict(dhT=ODD), dict(h0=ODD), dict(dx=FAKE),
+               dict(z=FAKE, ldz=64), dict(dz=FAKE + 0x500), dict(ws=None), dict(dtype=9), dict(B=-1), dict(T=-1)):
+        assert bwd(**kw) == binding.GLA_ERR_INVALID_ARG, kw
+    assert bwd(D=4) == bwd(N=24) == binding.GLA_ERR_UNSUPPORTED
+    need = binding.gla_ssm_bwd_workspace_size(2, 50, 64, 16)
+    assert need > 0 and bwd(n=need - 1) == binding.GLA_ERR_WORKSPACE
+    assert binding.gla_ssm_bwd_workspace_size(2, 0, 64, 16) == 0
