@@ -565,28 +565,34 @@ class _Call:
     """The tensors of one call: all on the device of the first, each checked
     for type and shape before its address is taken. The call runs with that
     device current, on `stream` or the device's current stream; what it
-    allocates (outputs, workspace) belongs to the stream it runs on."""
+    allocates (outputs, workspace) belongs to the stream it runs on. Kept
+    lean: a serving step's kernels take a few microseconds."""
+
+    __slots__ = ("torch", "device", "index", "dtype", "code", "stream", "other", "kept", "f")
 
     def __init__(self, x, stream):
-        if not x.is_cuda:
+        self.torch = torch = _torch()
+        self.device = x.device
+        self.index = x.get_device()
+        if self.index < 0:
             raise GlaError(GLA_ERR_INVALID_ARG, "argument", "tensors must live on a CUDA device")
-        self.torch = _torch()
-        self.dev = x.device
         self.dtype = x.dtype
         self.code = _dtype_code(x)
-        cuda = self.torch.cuda
-        current = cuda.current_stream(self.dev)
-        self.stream = current.cuda_stream if stream is None else _stream(stream)
+        self.f = torch.float32
         self.other = None
-        if self.stream != current.cuda_stream:
+        current = torch._C._cuda_getCurrentRawStream(self.index)
+        self.stream = current if stream is None else _stream(stream)
+        if self.stream != current:
+            cuda = torch.cuda
             if hasattr(stream, "cuda_stream"):
                 self.other = stream
             else:
-                self.other = cuda.ExternalStream(self.stream, self.dev) if self.stream else cuda.default_stream(self.dev)
+                self.other = cuda.ExternalStream(self.stream, self.device) if self.stream else cuda.default_stream(self.device)
 
-    def _check(self, t, shape, dtype, name):
-        if t.device != self.dev:
-            raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} is on {t.device}, the call's tensors on {self.dev}")
+    def _refuse(self, t, shape, dtype, name):
+        if t.get_device() != self.index:
+            raise GlaError(GLA_ERR_INVALID_ARG, "argument",
+                           f"{name} is on {t.device}, the call's tensors on {self.device}")
         if t.dtype != dtype:
             raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} must be {dtype}, got {t.dtype}")
         if t.shape != shape:
@@ -596,24 +602,32 @@ class _Call:
         """Address of a contiguous tensor (None passes); dtype None: the call's element type."""
         if t is None:
             return None
-        self._check(t, shape, self.dtype if dtype is None else dtype, name)
-        if not t.is_contiguous():
-            raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} must be contiguous")
-        return t.data_ptr()
+        if dtype is None:
+            dtype = self.dtype
+        if t.dtype is dtype and t.shape == shape and t.get_device() == self.index and t.is_contiguous():
+            return t.data_ptr()
+        self._refuse(t, shape, dtype, name)
+        raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} must be contiguous")
 
     def f32(self, t, shape, name):
-        return self.whole(t, shape, name, self.torch.float32) if t is not None else None
+        if t is None:
+            return None
+        if t.dtype is self.f and t.shape == shape and t.get_device() == self.index and t.is_contiguous():
+            return t.data_ptr()
+        return self.whole(t, shape, name, self.f)
 
     def i32(self, t, shape, name):
-        return self.whole(t, shape, name, self.torch.int32) if t is not None else None
+        return self.whole(t, shape, name, self.torch.int32)
 
     def rows(self, t, shape, name):
         """Address and row step of [..., C] rows an equal distance apart with
         contiguous columns (a column range of a wider tensor passes)."""
         if t is None:
             return None, 0
-        self._check(t, shape, self.dtype, name)
-        if t.numel() == 0 or t.is_contiguous():
+        if t.dtype is self.dtype and t.shape == shape and t.get_device() == self.index and t.is_contiguous():
+            return t.data_ptr(), shape[-1]
+        self._refuse(t, shape, self.dtype, name)
+        if t.numel() == 0:
             return t.data_ptr(), shape[-1]
         lead = [(n, st) for n, st in zip(shape[:-1], t.stride()[:-1]) if n > 1]
         step = lead[-1][1] if lead else shape[-1]
@@ -623,45 +637,55 @@ class _Call:
         return t.data_ptr(), step
 
     def empty(self, shape, dtype=None):
+        """A new tensor on the call's device and stream."""
         dtype = self.dtype if dtype is None else dtype
         if self.other is None:
-            return self.torch.empty(shape, dtype=dtype, device=self.dev)
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
         with self.torch.cuda.stream(self.other):
-            return self.torch.empty(shape, dtype=dtype, device=self.dev)
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
 
     def scratch(self, workspace, need):
         """Address and bytes of the caller's workspace, or of a new one of `need` bytes."""
         if workspace is None:
             if need == 0:
                 return None, 0
-            workspace = self.kept = self.empty(need, self.torch.uint8)
-        elif workspace.device != self.dev or not workspace.is_contiguous():
+            self.kept = self.empty(need, self.torch.uint8)
+            return self.kept.data_ptr(), need
+        if workspace.get_device() != self.index or not workspace.is_contiguous():
             raise GlaError(GLA_ERR_INVALID_ARG, "argument", "the workspace must be contiguous and on the call's device")
         return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
     def run(self, name, *args):
-        torch = self.torch
-        if self.dev.index == torch.cuda.current_device():
-            st = getattr(lib(), name)(*args, self.stream)
+        f = _entry.get(name)
+        if f is None:
+            f = _entry[name] = getattr(lib(), name)
+        if self.index == self.torch.cuda.current_device():
+            st = f(*args, self.stream)
         else:
-            with torch.cuda.device(self.dev):
-                st = getattr(lib(), name)(*args, self.stream)
-        _raise_on(st, name)
+            with self.torch.cuda.device(self.index):
+                st = f(*args, self.stream)
+        if st != GLA_OK:
+            _raise_on(st, name)
+
+
+_entry = {}   # entry points already looked up
 
 
 def _lead(t, n, name):
-    if t.dim() != n:
-        raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} has {t.dim()} dimensions, expected {n}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != n:
+        raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} has {len(shape)} dimensions, expected {n}")
+    return shape
 
 
 def _ssm_rows(c, x, dt, A, Bm, Cm, skip, z, dt_bias, softplus):
     """The arguments every selective-scan entry point begins with."""
-    D, N = x.shape[-1], _lead(A, 2, "A")[1]
-    narrow = x.shape[:-1] + (N,)
-    return (*c.rows(x, x.shape, "x"), *c.rows(dt, x.shape, "dt"), c.f32(A, (D, N), "A"), *c.rows(Bm, narrow, "Bm"),
-            *c.rows(Cm, narrow, "Cm"), c.f32(skip, (D,), "skip"), *c.rows(z, x.shape, "z"),
-            c.f32(dt_bias, (D,), "dt_bias"), int(bool(softplus)))
+    wide = x.shape
+    D, N = wide[-1], _lead(A, 2, "A")[1]
+    narrow = wide[:-1] + (N,)
+    return (*c.rows(x, wide, "x"), *c.rows(dt, wide, "dt"), c.f32(A, (D, N), "A"), *c.rows(Bm, narrow, "Bm"),
+            *c.rows(Cm, narrow, "Cm"), c.f32(skip, (D,), "skip"), *c.rows(z, wide, "z"),
+            c.f32(dt_bias, (D,), "dt_bias"), 1 if softplus else 0)
 
 
 def gla_ssm_fwd_workspace_size(B, T, D, N, dtype=GLA_BF16) -> int:

@@ -174,11 +174,12 @@ cudaError_t launch_conv_bwd(const ConvBwdParams &p, bool bf16, cudaStream_t s, i
     if (bf16) conv_bwd_kernel<__nv_bfloat16><<<(unsigned)(units * blocks), kThreads, 0, s>>>(p, blocks, tiles);
     else conv_bwd_kernel<float><<<(unsigned)(units * blocks), kThreads, 0, s>>>(p, blocks, tiles);
     if (launches) ++*launches;
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    e = launch_sum_rows(p.part, units, 4L * p.D, 5L * p.D, p.dw, s, launches);
-    if (e != cudaSuccess) return e;
-    return launch_sum_rows(p.part + 4L * p.D, units, p.D, 5L * p.D, p.db, s, launches);
+    SumJobs sums;
+    sums.add(p.part, units, 4L * p.D, 5L * p.D, p.dw);
+    sums.add(p.part + 4L * p.D, units, p.D, 5L * p.D, p.db);
+    return launch_sums(sums, s, launches);
 }
 
 }  // namespace gla

@@ -187,9 +187,23 @@ long norm_bwd_grid(long rows, int D);
 cudaError_t launch_rmsnorm_fwd(const NormParams &p, bool bf16, cudaStream_t s, int *launches);
 cudaError_t launch_rmsnorm_bwd(const NormParams &p, bool bf16, cudaStream_t s, int *launches);
 
-// out[c] = sum over rows of part[r * pitch + c], in a fixed order (reduce.cu).
-cudaError_t launch_sum_rows(const float *part, long rows, long cols, long pitch, float *out, cudaStream_t s,
-                            int *launches);
+// Sums over rows, out[c] = sum_r part[r * pitch + c], in a fixed order; the
+// outputs fp32 or bf16, several in one launch (reduce.cu). cols and pitch are
+// multiples of 4, part is 16-byte aligned; a NULL output is left out.
+struct SumJob {
+    const float *part;
+    long rows, cols, pitch;
+    void *out;
+    bool bf16;
+    unsigned block;              // its first block
+};
+struct SumJobs {
+    SumJob j[5];
+    int n = 0;
+    unsigned blocks = 0;
+    void add(const float *part, long rows, long cols, long pitch, void *out, bool bf16 = false);
+};
+cudaError_t launch_sums(const SumJobs &jobs, cudaStream_t s, int *launches);
 
 // SIMT kernels (any dk <= 128, dv <= 256; fp32 or bf16 elements).
 cudaError_t launch_fwd_simt(const FwdParams &p, bool bf16, cudaStream_t s, int *launches);

@@ -1,40 +1,85 @@
-// reduce.cu -- the second stage of the parameter gradients: the sum over rows
-// of an fp32 [rows, cols] array of partial sums, one partial per CTA of the
-// first stage. In a fixed order, so results do not change from call to call
-// (atomics would). A CTA owns 32 columns; its 32 warps take every 32nd row
-// (128 contiguous bytes each) and are added up through shared memory.
+// reduce.cu -- the second stage of the parameter gradients: sums over the rows
+// of fp32 [rows, cols] arrays of partial results, one row per CTA (or group of
+// CTAs) of the first stage. In a fixed order, so results do not change from
+// call to call (atomics would). All of a call's sums are one launch.
+//
+// Up to 32 rows, a thread adds four columns down the rows (16-byte loads);
+// more rows, a CTA owns 32 columns and its 16 warps take every sixteenth row
+// (128 contiguous bytes each, eight loads in flight), added up through shared
+// memory: one thread a column would wait for its loads one after another
+// (608 rows of 2,048 columns).
+#include "common.cuh"
 #include "kernels.h"
 
 namespace gla {
 namespace {
 
-__global__ void __launch_bounds__(1024) sum_rows_kernel(const float *part, long rows, long cols, long pitch, float *out) {
-    __shared__ float s[32][33];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const long c = (long)blockIdx.x * 32 + lane;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    if (c < cols) {
-        const float *p = part + c;
-        long r = warp;
-        for (; r + 96 < rows; r += 128)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] += p[(size_t)(r + 32 * i) * pitch];
-        for (; r < rows; r += 32) acc[0] += p[(size_t)r * pitch];
+constexpr int kThreads = 512, kFew = 32;
+
+__device__ __forceinline__ void put(const SumJob &j, long c, float v) {
+    if (j.bf16) static_cast<__nv_bfloat16 *>(j.out)[c] = __float2bfloat16_rn(v);
+    else static_cast<float *>(j.out)[c] = v;
+}
+
+__global__ void __launch_bounds__(kThreads) sum_rows_kernel(const SumJobs jobs) {
+    __shared__ float s[kThreads / 32][33];
+    int k = 0;
+    while (k + 1 < jobs.n && blockIdx.x >= jobs.j[k + 1].block) ++k;
+    const SumJob &j = jobs.j[k];
+    const long blk = (long)blockIdx.x - j.block;
+    if (j.rows <= kFew) {
+        const long c = (blk * kThreads + threadIdx.x) * 4;
+        if (c >= j.cols) return;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (long r = 0; r < j.rows; ++r) {
+            const float4 u = __ldg(reinterpret_cast<const float4 *>(j.part + (size_t)r * j.pitch + c));
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+        }
+        put(j, c, v.x);
+        put(j, c + 1, v.y);
+        put(j, c + 2, v.z);
+        put(j, c + 3, v.w);
+        return;
     }
-    s[warp][lane] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-    __syncthreads();
-    float v = s[lane][warp];   // warp w finishes column w
+    constexpr int W = kThreads / 32;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const long c = blk * 32 + lane;
+    float acc[8] = {};
+    if (c < j.cols) {
+        const float *p = j.part + c;
+        long r = warp;
+        for (; r + 7 * W < j.rows; r += 8 * W)
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    const long oc = (long)blockIdx.x * 32 + warp;
-    if (lane == 0 && oc < cols) out[oc] = v;
+            for (int i = 0; i < 8; ++i) acc[i] += __ldg(p + (size_t)(r + i * W) * j.pitch);
+        for (; r < j.rows; r += W) acc[0] += __ldg(p + (size_t)r * j.pitch);
+    }
+    s[warp][lane] = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+    __syncthreads();
+    if (warp == 0 && c < j.cols) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) v += s[i][lane];
+        put(j, c, v);
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_sum_rows(const float *part, long rows, long cols, long pitch, float *out, cudaStream_t s, int *launches) {
-    if (cols == 0 || out == nullptr) return cudaSuccess;
-    sum_rows_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(part, rows, cols, pitch, out);
+void SumJobs::add(const float *part, long rows, long cols, long pitch, void *out, bool bf16) {
+    if (!out || cols == 0) return;
+    const long per = rows <= kFew ? 4L * kThreads : 32;
+    j[n] = SumJob{part, rows, cols, pitch, out, bf16, blocks};
+    blocks += (unsigned)((cols + per - 1) / per);
+    ++n;
+}
+
+cudaError_t launch_sums(const SumJobs &jobs, cudaStream_t s, int *launches) {
+    if (jobs.n == 0) return cudaSuccess;
+    sum_rows_kernel<<<jobs.blocks, kThreads, 0, s>>>(jobs);
     if (launches) ++*launches;
     return cudaGetLastError();
 }

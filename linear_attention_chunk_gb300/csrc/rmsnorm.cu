@@ -257,7 +257,9 @@ template <typename T> cudaError_t bwd(const NormParams &p, cudaStream_t s, int *
     if (launches) ++*launches;
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.part) return e;
-    return launch_sum_rows(p.part, grid, p.D, p.D, p.dw, s, launches);
+    SumJobs sums;
+    sums.add(p.part, grid, p.D, p.D, p.dw);
+    return launch_sums(sums, s, launches);
 }
 
 }  // namespace

@@ -507,25 +507,6 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_kernel(const SsmBwdParams p,
     }
 }
 
-// out[c] = sum over r of part[r][c], rounded to T: few rows, many columns.
-template <typename T> __global__ void __launch_bounds__(256) sum_blocks_kernel(const float *part, int rows, long cols, T *out) {
-    const long c = ((long)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (c >= cols) return;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int r = 0; r < rows; ++r) {
-        const float4 u = __ldg(reinterpret_cast<const float4 *>(part + (size_t)r * cols + c));
-        v.x += u.x;
-        v.y += u.y;
-        v.z += u.z;
-        v.w += u.w;
-    }
-    Elem<T>::store(out + c, v.x);
-    Elem<T>::store(out + c + 1, v.y);
-    Elem<T>::store(out + c + 2, v.z);
-    Elem<T>::store(out + c + 3, v.w);
-}
-
 template <typename T, int N> cudaError_t run(const SsmBwdParams &p, cudaStream_t s, int *launches) {
     using S = Shape<N>;
     const int tiles = (p.D + S::CH - 1) / S::CH;
@@ -546,15 +527,15 @@ template <typename T, int N> cudaError_t run(const SsmBwdParams &p, cudaStream_t
     ssm_bwd_kernel<T, S><<<(unsigned)(units * tiles), S::TH, bytes, s>>>(p, tiles);
     if (launches) ++*launches;
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const long cols = (long)p.B * p.T * N;
-    const unsigned grid = (unsigned)((cols / 4 + 255) / 256);
-    sum_blocks_kernel<T><<<grid, 256, 0, s>>>(p.part_b, tiles, cols, static_cast<T *>(p.dB));
-    sum_blocks_kernel<T><<<grid, 256, 0, s>>>(p.part_c, tiles, cols, static_cast<T *>(p.dC));
-    if (launches) *launches += 2;
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_sum_rows(p.part_a, units, (long)p.D * N, (long)p.D * N, p.dA, s, launches)) != cudaSuccess) return e;
-    if ((e = launch_sum_rows(p.part_v, units, p.D, 2L * p.D, p.dskip, s, launches)) != cudaSuccess) return e;
-    return launch_sum_rows(p.part_v + p.D, units, p.D, 2L * p.D, p.ddt_bias, s, launches);
+    SumJobs sums;
+    const bool bf16 = sizeof(T) == 2;
+    const long cols = (long)p.B * p.T * N, plane = (long)p.D * N;
+    sums.add(p.part_b, tiles, cols, cols, p.dB, bf16);
+    sums.add(p.part_c, tiles, cols, cols, p.dC, bf16);
+    sums.add(p.part_a, units, plane, plane, p.dA);
+    sums.add(p.part_v, units, p.D, 2L * p.D, p.dskip);
+    sums.add(p.part_v + p.D, units, p.D, 2L * p.D, p.ddt_bias);
+    return launch_sums(sums, s, launches);
 }
 
 template <typename T> cudaError_t by_state(const SsmBwdParams &p, cudaStream_t s, int *launches) {
