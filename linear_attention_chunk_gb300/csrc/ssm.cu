@@ -8,18 +8,19 @@
 // form (the decays do not factor into one weight per token pair): the work is
 // one exponential and four fp32 operations per (token, channel, state).
 //
-// Layout: a CTA of W warps owns 16 W channels of one sequence (or of one
-// segment of it); a quad of lanes owns two channels, each lane N / 4 of their
-// states, in registers as fp32 pairs for the whole run. Two channels a lane
-// halve the loads of B and C: shared memory fills registers at 128 bytes a
-// clock per SM, and one channel a lane was bound by that (282 us against
-// 8 x 2048 x 2048, N = 16). Tiles of 16 tokens: every thread loads eight
+// Layout: a warp owns sixteen channels of one sequence (or of one segment of
+// it) and walks it alone, 16 tokens at a time; a CTA is only a group of such
+// warps, with no barrier between them, so their phases overlap. A quad of
+// lanes (eight apart) owns two channels, each lane N / 4 of their states, in
+// registers as fp32 pairs for the whole run. Two channels a lane halve the
+// loads of B and C: shared memory fills registers at 128 bytes a clock per SM,
+// and one channel a lane was bound by that. Per tile, every lane loads eight
 // channels of one token (16-byte accesses; the next tile's are in flight
 // during the scan), forms the input u and the step delta, and leaves
-// (delta, delta u) in shared memory; then each warp walks the tile's tokens of
-// its sixteen channels; then the thread that loaded a vector adds the skip,
-// applies the gate and stores it. Each elementwise value is computed once,
-// and the quad's sums over states are exchanged four tokens at a time.
+// (delta, delta u) in the warp's shared memory; then the warp walks the tokens;
+// then the lane that loaded a vector adds the skip, applies the gate and
+// stores it. Each elementwise value is computed once, and the quad's sums over
+// states are exchanged four tokens at a time.
 //
 // Sequences are cut into segments when they are too few to fill the GPU: one
 // launch runs every segment but a sequence's last (the first from the initial
@@ -34,11 +35,13 @@ namespace {
 
 using namespace ssm;
 
-constexpr int kTile = 16;   // tokens per tile (one vector of 8 channels per thread)
-constexpr int kYPad = 8;    // floats: rows of y start 8 banks apart
+constexpr int kTile = 16;   // tokens per tile: 2 x 16 vectors of eight channels, one a lane
+constexpr int kChan = 16;   // channels of a warp
+constexpr int kMostWarps = 4, kMinBlocks = 3;   // of a CTA; CTAs an SM holds
 
-template <int N, int W> constexpr int scan_smem_floats() {
-    return kTile * 16 * W * 2 + kTile * (16 * W + kYPad) + 2 * kTile * N;
+// Shared memory of a warp: (delta, delta u) of the tile, y, B, C, the filter.
+template <int N, bool kConv> constexpr int warp_floats() {
+    return kTile * kChan * 3 + 2 * kTile * N + (kConv ? (kTaps + 1) * kChan : 0);
 }
 
 // The unit's sequence, its segment and its tokens. False: nothing to do.
@@ -91,55 +94,66 @@ __device__ __forceinline__ bool find_unit(const SsmParams &p, long u, int *s_fou
 
 // u of one token for eight channels: SiLU of the width-4 filter over the
 // token's input and the three before it, from the window before the
-// sequence's first token (rows oldest first, the last four inputs).
+// sequence's first token (rows oldest first, the last four inputs). sW: the
+// filter of the CTA's channels in shared memory, [4 taps, bias][channel].
 template <typename T>
 __device__ __forceinline__ void conv8(const SsmParams &p, const Unit &un, long row, int c, bool whole,
-                                      const Raw8<T> &now, float (&u)[8]) {
-    float acc[8], w[kTaps][8];
-    param8(p.conv_b, c, whole, acc);
+                                      const Raw8<T> &now, const float *sW, int step, f2 (&u)[4]) {
+    f2 acc[4];
+    Raw8<T> past[3];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (sizeof(T) == 4 && i >= 4 && !whole) {
-            w[0][i] = w[1][i] = w[2][i] = w[3][i] = 0.f;
-            continue;
-        }
-        const float4 f = __ldg(reinterpret_cast<const float4 *>(p.conv_w) + c + i);
-        w[0][i] = f.x; w[1][i] = f.y; w[2][i] = f.z; w[3][i] = f.w;
+    for (int j = 0; j < 3; ++j)
+        if (row - 3 + j >= un.first)
+            past[j] = raw_load(static_cast<const T *>(p.x) + (size_t)(row - 3 + j) * p.ldx + c, whole);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(sW + kTaps * step + 4 * i);
+        acc[2 * i] = b.x;
+        acc[2 * i + 1] = b.y;
     }
 #pragma unroll
     for (int j = 0; j < kTaps; ++j) {
         const long src = row - 3 + j;
-        float v[8];
+        f2 v[4];
         if (j == 3) {
             raw_unpack(now, v);
         } else if (src >= un.first) {
-            raw_unpack(raw_load(static_cast<const T *>(p.x) + (size_t)src * p.ldx + c, whole), v);
+            raw_unpack(past[j], v);
         } else {
             // plain loads: this launch rewrites the window later
             const float4 *r = reinterpret_cast<const float4 *>(
                 p.win + ((size_t)un.slot * kTaps + (kTaps + src - un.first)) * p.D + c);
             const float4 a = r[0], b = whole ? r[1] : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+            v[0] = f2_pack(a.x, a.y);
+            v[1] = f2_pack(a.z, a.w);
+            v[2] = f2_pack(b.x, b.y);
+            v[3] = f2_pack(b.z, b.w);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[j][i], v[i], acc[i]);
+        for (int i = 0; i < 2; ++i) {
+            const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(sW + j * step + 4 * i);
+            acc[2 * i] = fma2(w.x, v[2 * i], acc[2 * i]);
+            acc[2 * i + 1] = fma2(w.y, v[2 * i + 1], acc[2 * i + 1]);
+        }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = silu(acc[i]);
+    for (int i = 0; i < 4; ++i) u[i] = silu2(acc[i]);
 }
 
-template <typename T, int N, int W, bool kFull, bool kConv>
-__global__ void __launch_bounds__(32 * W, 16 / W) ssm_scan_kernel(const SsmParams p, int tiles) {
-    constexpr int SP = N / 4, P = SP / 2, CH = 16 * W, VW = 2 * W, YS = CH + kYPad, TH = 32 * W;
+template <typename T, int N, bool kFull, bool kConv>
+__global__ void __launch_bounds__(32 * kMostWarps, kMinBlocks) ssm_scan_kernel(const SsmParams p, int tiles) {
+    constexpr int SP = N / 4, P = SP / 2;
     extern __shared__ __align__(16) float smem[];
-    float4 *sD = reinterpret_cast<float4 *>(smem);     // [kTile * VW vectors][4 channel pairs, swizzled]
-    float *sY = smem + kTile * CH * 2;                 // [kTile][YS]
-    float *sB = sY + kTile * YS;                       // [kTile][N]
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, q = lane / 8;
+    float *mine = smem + warp * warp_floats<N, kConv>();
+    float4 *sD = reinterpret_cast<float4 *>(mine);     // [kTile][8 channel pairs, swizzled]
+    float *sY = mine + kTile * kChan * 2;              // [kTile][kChan]
+    float *sB = sY + kTile * kChan;                    // [kTile][N]
     float *sC = sB + kTile * N;
+    float *sW = sC + kTile * N;                        // [taps and bias][kChan]
     __shared__ int s_found;
 
-    const int c0 = (int)(blockIdx.x % (unsigned)tiles) * CH;
+    const int c0 = ((int)(blockIdx.x % (unsigned)tiles) * (int)(blockDim.x / 32) + warp) * kChan;
     const long unit = blockIdx.x / (unsigned)tiles;
     Unit un;
     if (!find_unit(p, unit, &s_found, un)) return;
@@ -149,12 +163,12 @@ __global__ void __launch_bounds__(32 * W, 16 / W) ssm_scan_kernel(const SsmParam
     const bool last = seg0 + p.L >= un.len;
     if (!kFull && last) return;
 
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, q = lane % 4;
-    // the vector this thread loads and stores: channels c .. c+7 of token vt of every tile
-    const int vt = tid / VW, c = c0 + (tid % VW) * kVec;
+    if (c0 >= p.D) return;                             // a warp past the last channel
+    // the vector this lane loads and stores: channels c .. c+7 of token vt of every tile
+    const int vt = lane / 2, c = c0 + lane % 2 * kVec;
     const bool vec_on = c < p.D, whole = c + kVec <= p.D;
     // the two channels and the states this lane scans
-    const int ch = c0 + warp * 16 + lane / 4 * 2;
+    const int ch = c0 + lane % 8 * 2;
     const bool ch_on = ch < p.D;                       // D is even
 
     f2 a2[2][P], h[2][P];
@@ -210,15 +224,34 @@ __global__ void __launch_bounds__(32 * W, 16 / W) ssm_scan_kernel(const SsmParam
         }
     }
 
-    float bias[8];
+    if (kConv) {
+        if (lane < kChan) {
+            const bool in = c0 + lane < p.D;
+            const float4 w = in ? __ldg(reinterpret_cast<const float4 *>(p.conv_w) + c0 + lane)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+            sW[lane] = w.x;
+            sW[kChan + lane] = w.y;
+            sW[2 * kChan + lane] = w.z;
+            sW[3 * kChan + lane] = w.w;
+            sW[4 * kChan + lane] = p.conv_b && in ? p.conv_b[c0 + lane] : 0.f;
+        }
+        __syncwarp();
+    }
+    f2 bias[4], skip[4];
     param8(vec_on ? p.dt_bias : nullptr, c, whole, bias);
-    float skip[8];
     if (kFull) param8(vec_on ? p.skip : nullptr, c, whole, skip);
 
-    // one tile's inputs as they lie in memory
-    Raw8<T> rx, rd, rz;
-    constexpr int BN = (kTile * N + TH - 1) / TH;      // B (and C) elements per thread
-    T rb[BN], rc[BN];
+    // one tile's inputs as they lie in memory; B and C as vectors of eight too
+    Raw8<T> rx, rd, rz = raw_zero<T>();
+    constexpr int BV = kTile * N / 8, BL = (BV + 31) / 32;   // vectors of B (and of C), and per lane
+    Raw8<T> rb[BL], rc[BL];
+    auto narrow = [&](const void *base, long ld, long t0, int i) {
+        const int e = i * 32 + lane, t = e / (N / 8), n = e % (N / 8) * 8;
+        if (e >= BV || t0 + t >= ntok) return raw_zero<T>();
+        const T *src = static_cast<const T *>(base) + (size_t)(row0 + t0 + t) * ld + n;
+        if (reinterpret_cast<uintptr_t>(src) % 16 == 0) return raw_load(src, true);
+        return raw_gather(src);
+    };
     auto fetch = [&](long t0) {
         const long row = row0 + t0 + vt;
         const bool on = vec_on && t0 + vt < ntok;
@@ -226,11 +259,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W) ssm_scan_kernel(const SsmParam
         rd = on ? raw_load(static_cast<const T *>(p.dt) + (size_t)row * p.ldt + c, whole) : raw_zero<T>();
         if (kFull && p.z) rz = on ? raw_load(static_cast<const T *>(p.z) + (size_t)row * p.ldz + c, whole) : raw_zero<T>();
 #pragma unroll
-        for (int i = 0; i < BN; ++i) {
-            const int e = tid + i * TH, t = e / N, n = e % N;
-            const bool in = e < kTile * N && t0 + t < ntok;
-            rb[i] = in ? static_cast<const T *>(p.Bm)[(size_t)(row0 + t0 + t) * p.ldb + n] : T(0.f);
-            if (kFull) rc[i] = in ? static_cast<const T *>(p.Cm)[(size_t)(row0 + t0 + t) * p.ldc + n] : T(0.f);
+        for (int i = 0; i < BL; ++i) {
+            rb[i] = narrow(p.Bm, p.ldb, t0, i);
+            if (kFull) rc[i] = narrow(p.Cm, p.ldc, t0, i);
         }
     };
     fetch(0);
@@ -239,48 +270,53 @@ __global__ void __launch_bounds__(32 * W, 16 / W) ssm_scan_kernel(const SsmParam
     for (long t0 = 0; t0 < ntok; t0 += kTile) {
         // ---- inputs of the tile: u, delta; zero steps past the end leave the state as it is
         const bool on = vec_on && t0 + vt < ntok;
-        float u[8], dl[8];
+        f2 u[4], dl[4];
         raw_unpack(rd, dl);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            dl[i] += bias[i];
-            if (p.softplus) dl[i] = softplus(dl[i]);
-            if (!on) dl[i] = 0.f;
+        for (int i = 0; i < 4; ++i) {
+            dl[i] = add2(dl[i], bias[i]);
+            if (p.softplus) dl[i] = softplus2(dl[i]);
+            if (!on) dl[i] = 0;
         }
         if (kConv) {
             if (on) {
-                conv8(p, un, row0 + t0 + vt, c, whole, rx, u);
+                conv8(p, un, row0 + t0 + vt, c, whole, rx, sW + lane % 2 * kVec, kChan, u);
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = 0.f;
+                for (int i = 0; i < 4; ++i) u[i] = 0;
             }
         } else {
             raw_unpack(rx, u);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)                    // eight lanes' 64-byte vectors over all the banks
-            sD[tid * 4 + (i ^ ((tid >> 1) & 3))] =
-                make_float4(dl[2 * i], dl[2 * i] * u[2 * i], dl[2 * i + 1], dl[2 * i + 1] * u[2 * i + 1]);
+        for (int i = 0; i < 4; ++i) {                  // four tokens' 128-byte rows over all the banks
+            const float2 d = f2_split(dl[i]), du = f2_split(mul2(dl[i], u[i]));
+            sD[vt * 8 + lane % 2 * 4 + (i ^ (vt & 3))] = make_float4(d.x, du.x, d.y, du.y);
+        }
 #pragma unroll
-        for (int i = 0; i < BN; ++i) {
-            const int e = tid + i * TH;
-            if (e < kTile * N) {
-                sB[e] = (float)rb[i];
-                if (kFull) sC[e] = (float)rc[i];
+        for (int i = 0; i < BL; ++i) {
+            const int e = i * 32 + lane;
+            if (e < BV) {
+                f2 v[4];
+                raw_unpack(rb[i], v);
+                store8(sB + e * 8, v, true);
+                if (kFull) {
+                    raw_unpack(rc[i], v);
+                    store8(sC + e * 8, v, true);
+                }
             }
         }
         const Raw8<T> zc = rz;
-        __syncthreads();
+        __syncwarp();
         if (t0 + kTile < ntok) fetch(t0 + kTile);
 
-        // ---- the scan: the tile's tokens of this warp's sixteen channels
+        // ---- the scan: the tile's tokens
 #pragma unroll 2
         for (int t = 0; t < kTile; t += 4) {
             float part[2][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int v = (t + j) * VW + warp * 2 + lane / 16;   // the vector that holds this token's channels
-                const float4 d = sD[v * 4 + ((lane / 4 % 4) ^ ((v >> 1) & 3))];
+                const float4 d = sD[(t + j) * 8 + ((lane % 8) ^ ((t + j) & 3))];
                 const f2 *b = reinterpret_cast<const f2 *>(sB + (t + j) * N + q * SP);
                 const f2 *cc = reinterpret_cast<const f2 *>(sC + (t + j) * N + q * SP);
 #pragma unroll
@@ -302,22 +338,21 @@ __global__ void __launch_bounds__(32 * W, 16 / W) ssm_scan_kernel(const SsmParam
                 }
             }
             if (kFull)
-                *reinterpret_cast<float2 *>(sY + (t + q) * YS + warp * 16 + lane / 4 * 2) =
+                *reinterpret_cast<float2 *>(sY + (t + q) * kChan + lane % 8 * 2) =
                     make_float2(quad_transpose_sum(part[0], lane), quad_transpose_sum(part[1], lane));
         }
-        __syncthreads();
+        __syncwarp();
 
         // ---- skip, gate, store
         if (kFull && on) {
-            const float *ys = sY + vt * YS + (tid % VW) * kVec;
-            float y[8];
+            const ulonglong2 *ys = reinterpret_cast<const ulonglong2 *>(sY + vt * kChan + lane % 2 * kVec);
+            const ulonglong2 y01 = ys[0], y23 = ys[1];
+            f2 y[4] = {y01.x, y01.y, y23.x, y23.y}, z[4];
+            raw_unpack(zc, z);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = fmaf(skip[i], u[i], ys[i]);
-            if (p.z) {
-                float z[8];
-                raw_unpack(zc, z);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] *= silu(z[i]);
+            for (int i = 0; i < 4; ++i) {
+                y[i] = fma2(skip[i], u[i], y[i]);
+                if (p.z) y[i] = mul2(y[i], silu2(z[i]));
             }
             store8(static_cast<T *>(p.y) + (size_t)(row0 + t0 + vt) * p.D + c, y, whole);
         }
@@ -337,12 +372,11 @@ __global__ void __launch_bounds__(32 * W, 16 / W) ssm_scan_kernel(const SsmParam
         if (!kFull && q == 0)
             *reinterpret_cast<float2 *>(p.seg_sum + (size_t)(un.base + un.seg) * p.D + ch) = make_float2(dsum[0], dsum[1]);
     }
-    // ---- the window after the call: this CTA (the sequence's first tokens)
-    // is the only one that reads it, and has done so before the last barrier
-    if (kFull && kConv && un.seg == 0) {
-        for (int i = tid; i < CH; i += TH) {
-            const int cc = c0 + i;
-            if (cc >= p.D) break;
+    // ---- the window after the call: of these channels this warp alone reads
+    // it (at the sequence's first tokens), and has done so before the last __syncwarp
+    if (kFull && kConv && un.seg == 0 && lane < kChan) {
+        const int cc = c0 + lane;
+        if (cc < p.D) {
             float *w = p.win + (size_t)un.slot * kTaps * p.D + cc;
 #pragma unroll
             for (int k = 0; k < kTaps; ++k) {
@@ -355,15 +389,29 @@ __global__ void __launch_bounds__(32 * W, 16 / W) ssm_scan_kernel(const SsmParam
     }
 }
 
-constexpr int kWarps = 8;   // 64 channels a CTA
+// Warps per CTA: four neighbours share cache lines of the activations and of
+// B and C; fewer where that leaves the SMs with unequal numbers of warps.
+int warps_per_block(long units, int D) {
+    const int sms = device_sm_count(), groups = (D + kChan - 1) / kChan;
+    int best = 1;
+    double least = 1e30;
+    for (int w = kMostWarps; w >= 1; w /= 2) {
+        const long blocks = units * ((groups + w - 1) / w);
+        const double load = (double)((blocks + sms - 1) / sms) * w;   // warps of the fullest SM
+        if (load < least * 0.93) {
+            least = load;
+            best = w;
+        }
+    }
+    return best;
+}
 
 template <typename T, int N, bool kFull, bool kConv>
 cudaError_t launch(const SsmParams &p, long units, cudaStream_t s, int *launches) {
-    const int tiles = (p.D + 16 * kWarps - 1) / (16 * kWarps);
+    const int w = warps_per_block(units, p.D), tiles = (p.D + kChan * w - 1) / (kChan * w);
     if ((long double)units * tiles > 2147483647.0L) return cudaErrorInvalidValue;
-    constexpr int bytes = scan_smem_floats<N, kWarps>() * (int)sizeof(float);
-    auto *kern = ssm_scan_kernel<T, N, kWarps, kFull, kConv>;
-    kern<<<(unsigned)(units * tiles), 32 * kWarps, bytes, s>>>(p, tiles);
+    const int bytes = w * warp_floats<N, kConv>() * (int)sizeof(float);
+    ssm_scan_kernel<T, N, kFull, kConv><<<(unsigned)(units * tiles), 32 * w, bytes, s>>>(p, tiles);
     if (launches) ++*launches;
     return cudaGetLastError();
 }

@@ -64,21 +64,21 @@ template <> struct Lane<4> {
 };
 
 // Eight numbers, each spread over the eight quads of a warp: the sum of
-// number (lane / 4), in seven exchanges.
+// number (lane % 8), in seven exchanges.
 __device__ __forceinline__ float across_quads(const float (&v)[8], int lane) {
     float a[4], b[2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const bool up = lane & 16;
-        a[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 4], 16);
+        const bool up = lane & 4;
+        a[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 4], 4);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const bool up = lane & 8;
-        b[i] = (up ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 2], 8);
+        const bool up = lane & 2;
+        b[i] = (up ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 2], 2);
     }
-    const bool up = lane & 4;
-    return (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4);
+    const bool up = lane & 1;
+    return (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 1);
 }
 
 // Shapes of one instance: N states, K channels a lane.
@@ -108,30 +108,30 @@ template <class S> struct Where {
 // Steps past the end are 0: they leave both chains as they are.
 template <typename T, class S, bool kGrad>
 __device__ __forceinline__ void load_tile(const SsmBwdParams &p, const Where<S> &w, long row0, int ntok, float *sD, float *sU,
-                                          float *sG, float *sB, float *sC, const float (&bias)[8]) {
+                                          float *sG, float *sB, float *sC, const f2 (&bias)[4]) {
 #pragma unroll
     for (int k = 0; k < S::VPT; ++k) {
         const int t = w.vt + k * (kTile / S::VPT);
         const bool in = w.on && t < ntok;
         const size_t row = (size_t)(row0 + t);
-        float x[8], d[8], g[8];
+        f2 x[4], d[4], g[4];
         raw_unpack(in ? raw_load(static_cast<const T *>(p.x) + row * p.ldx + w.c, w.whole) : raw_zero<T>(), x);
         raw_unpack(in ? raw_load(static_cast<const T *>(p.dt) + row * p.ldt + w.c, w.whole) : raw_zero<T>(), d);
         if (kGrad) {
             raw_unpack(in ? raw_load(static_cast<const T *>(p.dy) + row * p.ldg + w.c, w.whole) : raw_zero<T>(), g);
             if (p.z && in) {
-                float z[8];
+                f2 z[4];
                 raw_unpack(raw_load(static_cast<const T *>(p.z) + row * p.ldz + w.c, w.whole), z);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] *= silu(z[i]);
+                for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], silu2(z[i]));
             }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            d[i] += bias[i];
-            if (p.softplus) d[i] = softplus(d[i]);
-            if (!in) d[i] = 0.f;
-            x[i] *= d[i];
+        for (int i = 0; i < 4; ++i) {
+            d[i] = add2(d[i], bias[i]);
+            if (p.softplus) d[i] = softplus2(d[i]);
+            if (!in) d[i] = 0;
+            x[i] = mul2(x[i], d[i]);
         }
         const int at = t * S::RS + (int)(threadIdx.x % S::VW) * 8;
         store8(sD + at, d, true);
@@ -198,12 +198,12 @@ __global__ void __launch_bounds__(S::TH, 2) ssm_bwd_local_kernel(const SsmBwdPar
     const int b = (int)(unit / p.nseg), seg = (int)(unit % p.nseg);
     const long row0 = (long)b * p.T + (long)seg * p.L;
     const int ntok = (int)min(p.L, (long)p.T - (long)seg * p.L);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, q = lane % 4;
-    const int lc = warp * S::CW + lane / 4 * S::K, ch = c0 + lc;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, q = lane / 8;
+    const int lc = warp * S::CW + lane % 8 * S::K, ch = c0 + lc;
     const size_t cell = (size_t)ch * S::N + q * S::SP;
     const bool on = ch < p.D;
     const Where<S> w(c0, p.D);
-    float bias[8];
+    f2 bias[4];
     param8(w.on ? p.dt_bias : nullptr, w.c, w.whole, bias);
 
     State<S> a2, h, pr, c;
@@ -264,12 +264,12 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_kernel(const SsmBwdParams p,
     const int b = (int)(unit / p.nseg), seg = (int)(unit % p.nseg);
     const long row0 = (long)b * p.T + (long)seg * p.L;
     const int ntok = (int)min(p.L, (long)p.T - (long)seg * p.L), ntile = (ntok + kTile - 1) / kTile;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, q = lane % 4;
-    const int lc = warp * S::CW + lane / 4 * S::K, ch = c0 + lc;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, q = lane / 8;
+    const int lc = warp * S::CW + lane % 8 * S::K, ch = c0 + lc;
     const size_t cell = (size_t)ch * S::N + q * S::SP, plane = (size_t)p.D * S::N;
     const bool on = ch < p.D;
     const Where<S> w(c0, p.D);
-    float bias[8];
+    f2 bias[4];
     param8(w.on ? p.dt_bias : nullptr, w.c, w.whole, bias);
 
     State<S> a2, h, c;
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_kernel(const SsmBwdParams p,
         __syncthreads();
     }
 
-    float skip[8], dskip[8] = {}, dbias[8] = {};
+    f2 skip[4], dskip[4] = {}, dbias[4] = {};
     param8(w.on ? p.skip : nullptr, w.c, w.whole, skip);
     State<S> dA;
     dA.zero();
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_kernel(const SsmBwdParams p,
                     pn[j % per * S::SP + 2 * m + 1] = v.y;
                 }
                 if (j % per == per - 1) {
-                    const int idx = lane / 4;
+                    const int idx = lane % 8;
                     myP[(kTile + t - per + 1 + idx / S::SP) * S::N + q * S::SP + idx % S::SP] = across_quads(pn, lane);
                 }
             }
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_kernel(const SsmBwdParams p,
                     pn[j % per * S::SP + 2 * m + 1] = v.y;
                 }
                 if (j % per == 0) {
-                    const int idx = lane / 4;
+                    const int idx = lane % 8;
                     myP[(t + idx / S::SP) * S::N + q * S::SP + idx % S::SP] = across_quads(pn, lane);
                 }
             }
@@ -445,31 +445,40 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_kernel(const SsmBwdParams p,
             if (!w.on || t >= left) continue;
             const size_t row = (size_t)(tr + t);
             const int at = t * S::RS + tid % S::VW * 8;
-            float x[8], d[8], g[8], z[8], o[8];
+            f2 x[4], d[4], g[4], z[4], o[4], s1[4], y0[4], s2[4];
+            auto take = [&](const float *src, f2 (&v)[4]) {
+                const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(src)[0], b = reinterpret_cast<const ulonglong2 *>(src)[1];
+                v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+            };
             raw_unpack(raw_load(static_cast<const T *>(p.x) + row * p.ldx + w.c, w.whole), x);
             raw_unpack(raw_load(static_cast<const T *>(p.dy) + row * p.ldg + w.c, w.whole), g);
             if (p.z) {
                 raw_unpack(raw_load(static_cast<const T *>(p.z) + row * p.ldz + w.c, w.whole), z);
+                take(sG + at, y0);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float sg = sigmoid(z[e]), y = fmaf(skip[e], x[e], sG[at + e]);
-                    o[e] = g[e] * y * (sg * fmaf(z[e], 1.f - sg, 1.f));
-                    g[e] *= z[e] * sg;
+                for (int e = 0; e < 4; ++e) {
+                    const f2 sg = sigmoid2(z[e]), y = fma2(skip[e], x[e], y0[e]), zs = mul2(z[e], sg);
+                    // SiLU'(z) = sg + z sg (1 - sg)
+                    o[e] = mul2(mul2(g[e], y), fma2(fma2(sg, both(-1.f), both(1.f)), zs, sg));
+                    g[e] = mul2(g[e], zs);
                 }
                 store8(static_cast<T *>(p.dz) + row * p.D + w.c, o, w.whole);
             }
+            take(sD + at, d);
+            take(sU + at, s1);
+            take(sS + at, s2);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                dskip[e] = fmaf(g[e], x[e], dskip[e]);
-                o[e] = fmaf(sD[at + e], sU[at + e], skip[e] * g[e]);
+            for (int e = 0; e < 4; ++e) {
+                dskip[e] = fma2(g[e], x[e], dskip[e]);
+                o[e] = fma2(d[e], s1[e], mul2(skip[e], g[e]));
             }
             store8(static_cast<T *>(p.dx) + row * p.D + w.c, o, w.whole);
             if (p.softplus) raw_unpack(raw_load(static_cast<const T *>(p.dt) + row * p.ldt + w.c, w.whole), d);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                o[e] = fmaf(sS[at + e], kLn2, sU[at + e] * x[e]);
-                if (p.softplus) o[e] *= sigmoid(d[e] + bias[e]);
-                dbias[e] += o[e];
+            for (int e = 0; e < 4; ++e) {
+                o[e] = fma2(s2[e], both(kLn2), mul2(s1[e], x[e]));
+                if (p.softplus) o[e] = mul2(o[e], sigmoid2(add2(d[e], bias[e])));
+                dbias[e] = add2(dbias[e], o[e]);
             }
             store8(static_cast<T *>(p.ddt) + row * p.D + w.c, o, w.whole);
         }
@@ -494,9 +503,12 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_kernel(const SsmBwdParams p,
     // dskip and ddt_bias: over the threads that share the eight channels
     float *red = smem;                                  // [thread][16]
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        red[e * S::TH + tid] = dskip[e];
-        red[(e + 8) * S::TH + tid] = dbias[e];
+    for (int e = 0; e < 4; ++e) {
+        const float2 u = f2_split(dskip[e]), v = f2_split(dbias[e]);
+        red[2 * e * S::TH + tid] = u.x;
+        red[(2 * e + 1) * S::TH + tid] = u.y;
+        red[(2 * e + 8) * S::TH + tid] = v.x;
+        red[(2 * e + 9) * S::TH + tid] = v.y;
     }
     __syncthreads();
     for (int e = tid; e < 2 * S::CH; e += S::TH) {

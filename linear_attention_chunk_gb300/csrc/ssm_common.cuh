@@ -52,25 +52,39 @@ __device__ __forceinline__ f2 ex2_pair(f2 x) {
     return f2_pack(ex2(v.x), ex2(v.y));
 }
 
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 both(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ f2 rcp_pair(f2 x) {
+    const float2 v = f2_split(x);
+    return f2_pack(rcp(v.x), rcp(v.y));
+}
+
 // log(1 + e^v) = max(v, 0) + log1p(w), w = e^-|v| in (0, 1], by the series
 // log1p(w) = 2 atanh(s) = 2 (s + s^3/3 + s^5/5 + ...), s = w / (2 + w) <= 1/3:
 // seven terms leave 2 s^15 / 15 < 1e-8. Relative to the result, not to 1: a
 // step of 1e-3 keeps fp32's precision, which log(1 + w) would lose.
-__device__ __forceinline__ float softplus(float v) {
-    const float w = ex2(-fabsf(v) * kLog2e);
-    const float s = w * rcp(2.f + w);
-    const float q = s * s;
-    float r = 1.f / 13.f;
-    r = fmaf(r, q, 1.f / 11.f);
-    r = fmaf(r, q, 1.f / 9.f);
-    r = fmaf(r, q, 1.f / 7.f);
-    r = fmaf(r, q, 1.f / 5.f);
-    r = fmaf(r, q, 1.f / 3.f);
-    r = fmaf(r * q, s, s);
-    return fmaf(2.f, r, fmaxf(v, 0.f));
+__device__ __forceinline__ f2 softplus2(f2 v) {
+    const float2 x = f2_split(v);
+    const f2 w = f2_pack(ex2(-fabsf(x.x) * kLog2e), ex2(-fabsf(x.y) * kLog2e));
+    const f2 s = mul2(w, rcp_pair(add2(w, both(2.f))));
+    const f2 q = mul2(s, s);
+    f2 r = fma2(both(1.f / 13.f), q, both(1.f / 11.f));
+    r = fma2(r, q, both(1.f / 9.f));
+    r = fma2(r, q, both(1.f / 7.f));
+    r = fma2(r, q, both(1.f / 5.f));
+    r = fma2(r, q, both(1.f / 3.f));
+    r = fma2(mul2(r, q), s, s);
+    return fma2(both(2.f), r, f2_pack(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
 }
+__device__ __forceinline__ float softplus(float v) { return f2_split(softplus2(both(v))).x; }
 __device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(-v * kLog2e)); }
 __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
+__device__ __forceinline__ f2 sigmoid2(f2 v) { return rcp_pair(add2(ex2_pair(mul2(v, both(-kLog2e))), both(1.f))); }
+__device__ __forceinline__ f2 silu2(f2 v) { return mul2(v, sigmoid2(v)); }
 
 // Eight consecutive channels as they lie in memory.
 template <typename T> struct Raw8 {
@@ -89,6 +103,35 @@ template <typename T> __device__ __forceinline__ Raw8<T> raw_load(const T *p, bo
     Raw8<T> r;
     r.w[0] = __ldg(reinterpret_cast<const uint4 *>(p));
     if constexpr (sizeof(T) == 4) r.w[1] = whole ? __ldg(reinterpret_cast<const uint4 *>(p) + 1) : make_uint4(0, 0, 0, 0);
+    return r;
+}
+__device__ __forceinline__ void raw_unpack(const Raw8<__nv_bfloat16> &r, f2 (&v)[4]) {
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void raw_unpack(const Raw8<float> &r, f2 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        v[2 * i] = f2_pack(__uint_as_float(r.w[i].x), __uint_as_float(r.w[i].y));
+        v[2 * i + 1] = f2_pack(__uint_as_float(r.w[i].z), __uint_as_float(r.w[i].w));
+    }
+}
+// The same from an address with no more than its element's alignment.
+__device__ __forceinline__ Raw8<__nv_bfloat16> raw_gather(const __nv_bfloat16 *p) {
+    const unsigned short *u = reinterpret_cast<const unsigned short *>(p);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = (uint32_t)__ldg(u + 2 * i) | ((uint32_t)__ldg(u + 2 * i + 1) << 16);
+    Raw8<__nv_bfloat16> r;
+    r.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    return r;
+}
+__device__ __forceinline__ Raw8<float> raw_gather(const float *p) {
+    const uint32_t *u = reinterpret_cast<const uint32_t *>(p);
+    Raw8<float> r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r.w[i] = make_uint4(__ldg(u + 4 * i), __ldg(u + 4 * i + 1), __ldg(u + 4 * i + 2), __ldg(u + 4 * i + 3));
     return r;
 }
 __device__ __forceinline__ void raw_unpack(const Raw8<__nv_bfloat16> &r, float (&v)[8]) {
@@ -116,6 +159,16 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8], bool whole
     reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     if (whole) reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
+template <typename T> __device__ __forceinline__ void store8(T *p, const f2 (&v)[4], bool whole) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 u = f2_split(v[i]);
+        f[2 * i] = u.x;
+        f[2 * i + 1] = u.y;
+    }
+    store8(p, f, whole);
+}
 // Eight fp32 parameters of consecutive channels (zeros without an array).
 __device__ __forceinline__ void param8(const float *p, int c, bool whole, float (&v)[8]) {
     if (p) {
@@ -129,19 +182,26 @@ __device__ __forceinline__ void param8(const float *p, int c, bool whole, float 
     }
 }
 
-// Four numbers, one per token, each spread over the four lanes of a quad:
-// returns the sum of number (lane % 4), in three exchanges.
-__device__ __forceinline__ float quad_transpose_sum(const float (&v)[4], int lane) {
-    const bool hi = lane & 2, lo = lane & 1;
-    float k0 = hi ? v[2] : v[0], k1 = hi ? v[3] : v[1];
-    k0 += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 2);
-    k1 += __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 2);
-    const float k = lo ? k1 : k0;
-    return k + __shfl_xor_sync(0xffffffffu, lo ? k0 : k1, 1);
+__device__ __forceinline__ void param8(const float *p, int c, bool whole, f2 (&v)[4]) {
+    float f[8];
+    param8(p, c, whole, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2_pack(f[2 * i], f[2 * i + 1]);
 }
-__device__ __forceinline__ float quad_sum(float v) {
-    v += __shfl_xor_sync(0xffffffffu, v, 1);
-    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+
+// The four lanes that share channels ("a quad") are eight apart: lane / 8 is
+// the lane's place in it, lane % 8 its channels. Eight neighbouring lanes then
+// read one 16-byte piece of B or C, which shared memory serves in two clocks a
+// warp instead of four (measured; four neighbours reading four pieces: four).
+// Four numbers, one per token, each spread over the four lanes of a quad:
+// returns the sum of number (lane / 8), in three exchanges.
+__device__ __forceinline__ float quad_transpose_sum(const float (&v)[4], int lane) {
+    const bool hi = lane & 16, lo = lane & 8;
+    float k0 = hi ? v[2] : v[0], k1 = hi ? v[3] : v[1];
+    k0 += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+    k1 += __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 16);
+    const float k = lo ? k1 : k0;
+    return k + __shfl_xor_sync(0xffffffffu, lo ? k0 : k1, 8);
 }
 
 }  // namespace ssm

@@ -16,6 +16,11 @@ using namespace ssm;
 
 constexpr int kThreads = 256;             // 64 channels per pass
 
+__device__ __forceinline__ float quad_sum(float v) {   // over four neighbouring lanes
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
 // kRows sequences per CTA column of 64 channels, all their loads up front.
 template <typename T, int N, int kRows> __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const SsmParams p, int tiles) {
     constexpr int SP = N / 4, P = SP / 2;
