@@ -8,8 +8,9 @@
 // A stream: 6 bytes an element at bf16 (x, dy in, dx out). A thread owns four
 // channels over a tile of tokens and walks it forward with the last three x
 // and dp in registers, so dx lags three tokens behind, and reads three tokens
-// past the tile's end for it (the tile's own sums leave those out). Eight
-// tokens' loads are issued at once. dw and db stay in registers and leave once
+// past the tile's end for it (the tile's own sums leave those out). The inputs
+// come through a ring of asynchronous copies, twelve tokens ahead: each thread
+// copies and reads its own, so nothing waits for another. dw and db stay in registers and leave once
 // per tile as partial sums, added in a second launch (reduce.cu).
 #include "ssm_common.cuh"
 
@@ -19,7 +20,8 @@ namespace {
 using namespace ssm;
 
 constexpr int kThreads = 128;   // 512 channels a CTA
-constexpr int kStep = 8;        // tokens loaded at once
+constexpr int kStep = 4, kStages = 4;   // tokens of a stage, stages of the ring
+constexpr int kMinBlocks = 4;
 
 template <typename T> struct Raw4 {
     uint2 w[sizeof(T) / 2];
@@ -33,12 +35,6 @@ template <typename T> __device__ __forceinline__ Raw4<T> load4(const T *p) {
         r.w[0] = make_uint2(u.x, u.y);
         r.w[1] = make_uint2(u.z, u.w);
     }
-    return r;
-}
-template <typename T> __device__ __forceinline__ Raw4<T> zero4() {
-    Raw4<T> r;
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = make_uint2(0, 0);
     return r;
 }
 __device__ __forceinline__ void unpack4(const Raw4<__nv_bfloat16> &r, f2 (&v)[2]) {
@@ -58,7 +54,8 @@ __device__ __forceinline__ void store4(float *p, f2 a, f2 b) {
     *reinterpret_cast<float4 *>(p) = make_float4(u.x, u.y, v.x, v.y);
 }
 
-template <typename T> __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvBwdParams p, int blocks, int tiles) {
+template <typename T> __global__ void __launch_bounds__(kThreads, kMinBlocks) conv_bwd_kernel(const ConvBwdParams p, int blocks, int tiles) {
+    __shared__ Raw4<T> ring[kStages * kStep * 2][kThreads];   // [token][x, dy][thread]
     const int c = ((int)(blockIdx.x % (unsigned)blocks) * kThreads + threadIdx.x) * 4;
     const long unit = blockIdx.x / (unsigned)blocks;
     if (c >= p.D) return;
@@ -97,14 +94,34 @@ template <typename T> __global__ void __launch_bounds__(kThreads) conv_bwd_kerne
         dp[j][0] = dp[j][1] = 0;
     }
     const f2 one = f2_pack(1.f, 1.f), neg = f2_pack(-kLog2e, -kLog2e), minus = f2_pack(-1.f, -1.f);
+    const long last = min(t1 + 3, (long)p.T);
+    constexpr int kBytes = 4 * (int)sizeof(T);
+    auto issue = [&](long t, int stage) {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) {
+            const bool in = t + i < last;
+            const size_t at = in ? (size_t)(t + i) * D : 0;
+            copy_async<kBytes>(&ring[(stage * kStep + i) * 2][threadIdx.x], x + at, in);
+            copy_async<kBytes>(&ring[(stage * kStep + i) * 2 + 1][threadIdx.x], dy + at, in);
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) {
+        issue(t0 + k * kStep, k);
+        copies_commit();
+    }
+    int stage = 0;
     for (long t = t0; t < t1 + 3; t += kStep) {
+        copies_wait<kStages - 2>();
         Raw4<T> rx[kStep], ry[kStep];
 #pragma unroll
         for (int i = 0; i < kStep; ++i) {
-            const bool in = t + i < min(t1 + 3, (long)p.T);
-            rx[i] = in ? load4(x + (size_t)(t + i) * D) : zero4<T>();
-            ry[i] = in ? load4(dy + (size_t)(t + i) * D) : zero4<T>();
+            rx[i] = ring[(stage * kStep + i) * 2][threadIdx.x];
+            ry[i] = ring[(stage * kStep + i) * 2 + 1][threadIdx.x];
         }
+        issue(t + (kStages - 1) * kStep, stage == 0 ? kStages - 1 : stage - 1);   // the stage read before this one
+        copies_commit();
+        stage = stage == kStages - 1 ? 0 : stage + 1;
 #pragma unroll
         for (int i = 0; i < kStep; ++i) {
             const bool own = t + i < t1, past = t + i >= p.T;

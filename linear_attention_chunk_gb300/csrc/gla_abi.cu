@@ -157,7 +157,7 @@ gla_status check_rows(const void *ptr, int64_t ld, int cols, int elem, bool vect
     if (reinterpret_cast<uintptr_t>(ptr) % align) return fail(GLA_ERR_INVALID_ARG, "%s is not %d-byte aligned", name, (int)align);
     if (ld < cols) return fail(GLA_ERR_INVALID_ARG, "%s has rows of %d elements %lld apart", name, cols, (long long)ld);
     if (vector && (ld * elem) % 16) return fail(GLA_ERR_INVALID_ARG, "%s has rows that are not 16-byte aligned", name);
-    if (ld > (1ll << 31)) return fail(GLA_ERR_INVALID_ARG, "%s has rows too far apart", name);
+    if (ld > 2147483647ll) return fail(GLA_ERR_INVALID_ARG, "%s has rows too far apart", name);
     return GLA_OK;
 }
 
@@ -167,6 +167,7 @@ gla_status check_ssm_shape(int64_t seqs, int64_t rows, int D, int N, gla_dtype d
     const int vec = dtype == GLA_BF16 ? 8 : 4;
     if (D <= 0 || D % vec != 0) return fail(GLA_ERR_UNSUPPORTED, "D=%d must be a positive multiple of %d", D, vec);
     if (N != 8 && N != 16 && N != 32) return fail(GLA_ERR_UNSUPPORTED, "N=%d is not 8, 16 or 32", N);
+    if (D > (1 << 25)) return fail(GLA_ERR_UNSUPPORTED, "D=%d is above 2^25", D);   // D * N and D * 4 fit an int
     // one CTA per 64 channels of a sequence or segment: well inside a 1-D grid
     if ((long double)(seqs + rows) * ((D + 63) / 64) > 2147483647.0L || (long double)rows * D > (long double)(1ull << 40))
         return fail(GLA_ERR_INVALID_ARG, "tensor too large");

@@ -10,8 +10,9 @@
 // eight channels, all its loads issued up front; the row's sums go through
 // shuffles and one shared-memory exchange. A block of 128, 64 or 32 channels
 // is 16, 8 or 4 neighbouring lanes, so its maximum needs shuffles only. The
-// backward's CTAs walk every G-th row, load the next while the present one is
-// summed, and keep dw of their channels in registers; the partial sums of the
+// backward's CTAs walk every G-th row, two rows ahead of them arriving by
+// asynchronous copies (one row ahead in registers kept too few bytes in
+// flight: 63 us at 16384 x 2048, now 51, 0.77 of the measured copy rate), and keep dw of their channels in registers; the partial sums of the
 // CTAs are added in a second launch (reduce.cu).
 // y is rounded once from fp32; y8 from the unrounded y.
 #include "ssm_common.cuh"
@@ -20,6 +21,9 @@ namespace gla {
 namespace {
 
 using ssm::Raw8;
+using ssm::copies_commit;
+using ssm::copies_wait;
+using ssm::copy_async;
 using ssm::param8;
 using ssm::raw_load;
 using ssm::raw_unpack;
@@ -149,21 +153,39 @@ template <typename T, int VPT> __global__ void __launch_bounds__(kMost) rmsnorm_
     }
 }
 
+// Rows in the backward's ring (2, 3, 4, 6 measured: 57, 51, 55, 58 us at 16384 x 2048); two where three
+// would not fit (fp32, D > 4096: 98 KB a row).
+template <typename T, int VPT> constexpr int ring_rows() { return sizeof(T) == 4 && VPT == 2 ? 2 : 3; }
+
 // p.x: s; rows blockIdx.x, + gridDim.x, ...; partial dw of the CTA at p.part.
 template <typename T, int VPT> __global__ void __launch_bounds__(kMost) rmsnorm_bwd_kernel(const NormParams p) {
+    constexpr int kStages = ring_rows<T, VPT>();
     __shared__ float2 s_red[2][32];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, nw = blockDim.x / 32;
-    Raw8<T> nx[VPT], ny[VPT], ns[VPT];
-    auto fetch = [&](long row) {
+    // the ring: kStages rows of s, dy, ds; a thread copies and reads its own vectors
+    extern __shared__ __align__(16) uint4 ring[];
+    constexpr int H = sizeof(T) / 2, kRow = 3 * VPT * H;   // 16-byte pieces of a thread and row
+    auto issue = [&](long row, int stage) {
+        uint4 *dst = ring + (size_t)stage * kRow * blockDim.x + tid;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (i * (int)blockDim.x + tid) * 8;
-            const bool on = c < p.D, whole = c + 8 <= p.D;
-            const size_t at = (size_t)row * p.D + c;
-            nx[i] = on ? raw_load(static_cast<const T *>(p.x) + at, whole) : raw_zero<T>();
-            ny[i] = on ? raw_load(static_cast<const T *>(p.dy) + at, whole) : raw_zero<T>();
-            ns[i] = on && p.ds ? raw_load(static_cast<const T *>(p.ds) + at, whole) : raw_zero<T>();
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const bool in = row < p.rows && c + 4 * h < p.D;   // (a piece holds 8 / H channels)
+                const size_t at = in ? (size_t)row * p.D + c + 4 * h : 0;
+                copy_async<16>(dst + ((3 * i) * H + h) * blockDim.x, static_cast<const T *>(p.x) + at, in);
+                copy_async<16>(dst + ((3 * i + 1) * H + h) * blockDim.x, static_cast<const T *>(p.dy) + at, in);
+                copy_async<16>(dst + ((3 * i + 2) * H + h) * blockDim.x,
+                               static_cast<const T *>(p.ds ? p.ds : p.x) + at, in && p.ds);
+            }
         }
+    };
+    auto held = [&](int stage, int k) {
+        Raw8<T> r;
+#pragma unroll
+        for (int h = 0; h < H; ++h) r.w[h] = ring[((size_t)stage * kRow + k * H + h) * blockDim.x + tid];
+        return r;
     };
     float w[VPT][8], dw[VPT][8];
 #pragma unroll
@@ -176,17 +198,22 @@ template <typename T, int VPT> __global__ void __launch_bounds__(kMost) rmsnorm_
             dw[i][j] = 0.f;
         }
     }
-    int par = 0;
+    int par = 0, stage = 0;
     long row = blockIdx.x;
-    if (row < p.rows) fetch(row);
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) {
+        issue(row + (long)k * gridDim.x, k);
+        copies_commit();
+    }
     for (; row < p.rows; row += gridDim.x, par ^= 1) {
+        copies_wait<kStages - 2>();
         Raw8<T> cx[VPT], cy[VPT], cs[VPT];
         float ss = 0.f, sg = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            cx[i] = nx[i];
-            cy[i] = ny[i];
-            cs[i] = ns[i];
+            cx[i] = held(stage, 3 * i);
+            cy[i] = held(stage, 3 * i + 1);
+            cs[i] = held(stage, 3 * i + 2);
             float x[8], g[8];
             raw_unpack(cx[i], x);
             raw_unpack(cy[i], g);
@@ -196,7 +223,9 @@ template <typename T, int VPT> __global__ void __launch_bounds__(kMost) rmsnorm_
                 sg = fmaf(g[j] * w[i][j], x[j], sg);
             }
         }
-        if (row + gridDim.x < p.rows) fetch(row + gridDim.x);
+        issue(row + (long)(kStages - 1) * gridDim.x, stage == 0 ? kStages - 1 : stage - 1);   // the row before's stage
+        copies_commit();
+        stage = stage == kStages - 1 ? 0 : stage + 1;
         ss = warp_sum(ss);
         sg = warp_sum(sg);
         if (nw > 1) {                                // two buffers in turn: one barrier a row
@@ -252,10 +281,13 @@ int bwd_threads(int vecs) { return round32((vecs + bwd_vpt(vecs) - 1) / bwd_vpt(
 template <typename T> cudaError_t bwd(const NormParams &p, cudaStream_t s, int *launches) {
     const int vecs = (p.D + 7) / 8, vpt = bwd_vpt(vecs), th = bwd_threads(vecs);
     const unsigned grid = (unsigned)norm_bwd_grid(p.rows, p.D);
-    if (vpt == 1) rmsnorm_bwd_kernel<T, 1><<<grid, th, 0, s>>>(p);
-    else rmsnorm_bwd_kernel<T, 2><<<grid, th, 0, s>>>(p);
+    const int bytes = (vpt == 1 ? ring_rows<T, 1>() : ring_rows<T, 2>()) * 3 * vpt * th * 8 * (int)sizeof(T);
+    auto *kern = vpt == 1 ? rmsnorm_bwd_kernel<T, 1> : rmsnorm_bwd_kernel<T, 2>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, th, bytes, s>>>(p);
     if (launches) ++*launches;
-    const cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess || !p.part) return e;
     SumJobs sums;
     sums.add(p.part, grid, p.D, p.D, p.dw);
@@ -264,10 +296,10 @@ template <typename T> cudaError_t bwd(const NormParams &p, cudaStream_t s, int *
 
 }  // namespace
 
-// CTAs of the backward: 1,024 threads an SM, each CTA walking its share of the rows.
+// CTAs of the backward: 768 threads an SM, each CTA walking its share of the rows.
 long norm_bwd_grid(long rows, int D) {
     const int th = bwd_threads((D + 7) / 8);
-    const long per_sm = 1024 / th > 8 ? 8 : 1024 / th;
+    const long per_sm = 768 / th > 8 ? 8 : 768 / th;
     const long most = per_sm * device_sm_count();
     return rows < most ? rows : most;
 }

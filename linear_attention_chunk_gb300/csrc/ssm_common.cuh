@@ -80,11 +80,35 @@ __device__ __forceinline__ f2 softplus2(f2 v) {
     r = fma2(mul2(r, q), s, s);
     return fma2(both(2.f), r, f2_pack(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
 }
-__device__ __forceinline__ float softplus(float v) { return f2_split(softplus2(both(v))).x; }
+__device__ __forceinline__ float softplus(float v) {
+    const float w = ex2(-fabsf(v) * kLog2e), s = w * rcp(2.f + w), q = s * s;
+    float r = fmaf(1.f / 13.f, q, 1.f / 11.f);
+    r = fmaf(r, q, 1.f / 9.f);
+    r = fmaf(r, q, 1.f / 7.f);
+    r = fmaf(r, q, 1.f / 5.f);
+    r = fmaf(r, q, 1.f / 3.f);
+    r = fmaf(r * q, s, s);
+    return fmaf(2.f, r, fmaxf(v, 0.f));
+}
 __device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(-v * kLog2e)); }
 __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 __device__ __forceinline__ f2 sigmoid2(f2 v) { return rcp_pair(add2(ex2_pair(mul2(v, both(-kLog2e))), both(1.f))); }
 __device__ __forceinline__ f2 silu2(f2 v) { return mul2(v, sigmoid2(v)); }
+
+// Asynchronous copies of 8 or 16 bytes into shared memory; `in` false writes
+// zeros and reads nothing.
+template <int kBytes> __device__ __forceinline__ void copy_async(void *dst, const void *src, bool in) {
+    static_assert(kBytes == 8 || kBytes == 16, "one vector");
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst), n = in ? kBytes : 0;
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft> __device__ __forceinline__ void copies_wait() {   // all but the last kLeft groups have arrived
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
 
 // Eight consecutive channels as they lie in memory.
 template <typename T> struct Raw8 {

@@ -40,7 +40,7 @@ def formula(x, res, w, eps):
 
 
 SHAPES = [(BF, 1, 8), (BF, 3, 72), (FP, 2, 4), (FP, 5, 516), (BF, 700, 1032), (BF, 2, 4096), (FP, 33, 2048),
-          (BF, 9, 8192), (FP, 3, 8192), (BF, 1100, 264)]
+          (BF, 9, 8192), (FP, 3, 8192), (BF, 1100, 264), (BF, 700, 2048)]
 
 
 @pytest.mark.parametrize("dtype,rows,D", SHAPES)
