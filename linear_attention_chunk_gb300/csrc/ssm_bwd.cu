@@ -104,47 +104,108 @@ template <class S> struct Where {
         : c(c0 + (int)(threadIdx.x % S::VW) * 8), vt((int)threadIdx.x / S::VW), on(c < D), whole(c + 8 <= D) {}
 };
 
-// One tile's delta, delta u and (kGrad) dy' into shared memory, B and C too.
-// Steps past the end are 0: they leave both chains as they are.
-template <typename T, class S, bool kGrad>
-__device__ __forceinline__ void load_tile(const SsmBwdParams &p, const Where<S> &w, long row0, int ntok, float *sD, float *sU,
-                                          float *sG, float *sB, float *sC, const f2 (&bias)[4]) {
+// A tile's inputs on their way: a thread's vectors of x, dt, dy and z and, of
+// the first threads, one vector of eight of B or C, copied asynchronously a
+// tile ahead into slots that only this thread reads. Two stages at bf16, so
+// that the elementwise end still finds its tile there; one at fp32.
+template <typename T, class S> struct Ring {
+    static constexpr int H = sizeof(T) / 2, kStages = sizeof(T) == 2 ? 2 : 1;
+    static constexpr int kPieces = (4 * S::VPT + 1) * H;            // 16-byte slots of a thread and stage
+    static constexpr int kNarrow = kTile * S::N / 8;                // vectors of B (and of C)
+    static constexpr int kFloats = kStages * kPieces * S::TH * 4;
+    static_assert(2 * kNarrow <= S::TH, "one vector of B or C a thread");
+    uint4 *slots;
+    bool wide;                                                      // B and C allow 16-byte copies
+
+    __device__ __forceinline__ Ring(const SsmBwdParams &p, float *smem) : slots(reinterpret_cast<uint4 *>(smem) + threadIdx.x) {
+        wide = ((reinterpret_cast<uintptr_t>(p.Bm) | reinterpret_cast<uintptr_t>(p.Cm) | (uintptr_t)p.ldb * sizeof(T) |
+                 (uintptr_t)p.ldc * sizeof(T)) % 16) == 0;
+    }
+    __device__ __forceinline__ void copy(int stage, int piece, const T *src, bool in, bool whole) const {
 #pragma unroll
-    for (int k = 0; k < S::VPT; ++k) {
-        const int t = w.vt + k * (kTile / S::VPT);
-        const bool in = w.on && t < ntok;
+        for (int h = 0; h < H; ++h) {
+            const bool on = in && (h == 0 || whole);
+            copy_async<16>(slots + (stage * kPieces + piece * H + h) * S::TH, reinterpret_cast<const uint4 *>(src) + (on ? h : 0), on);
+        }
+    }
+    __device__ __forceinline__ Raw8<T> held(int stage, int piece) const {
+        Raw8<T> r;
+#pragma unroll
+        for (int h = 0; h < H; ++h) r.w[h] = slots[(stage * kPieces + piece * H + h) * S::TH];
+        return r;
+    }
+    // This thread's vector of B (e < kNarrow) or C, or NULL past the tile's end.
+    __device__ __forceinline__ const T *narrow(const SsmBwdParams &p, long row0, int ntok, bool grad) const {
+        const int e = threadIdx.x, m = e % kNarrow, t = m / (S::N / 8), n = m % (S::N / 8) * 8;
+        if (e >= (grad ? 2 : 1) * kNarrow || t >= ntok) return nullptr;
         const size_t row = (size_t)(row0 + t);
-        f2 x[4], d[4], g[4];
-        raw_unpack(in ? raw_load(static_cast<const T *>(p.x) + row * p.ldx + w.c, w.whole) : raw_zero<T>(), x);
-        raw_unpack(in ? raw_load(static_cast<const T *>(p.dt) + row * p.ldt + w.c, w.whole) : raw_zero<T>(), d);
-        if (kGrad) {
-            raw_unpack(in ? raw_load(static_cast<const T *>(p.dy) + row * p.ldg + w.c, w.whole) : raw_zero<T>(), g);
-            if (p.z && in) {
-                f2 z[4];
-                raw_unpack(raw_load(static_cast<const T *>(p.z) + row * p.ldz + w.c, w.whole), z);
+        return e < kNarrow ? static_cast<const T *>(p.Bm) + row * p.ldb + n : static_cast<const T *>(p.Cm) + row * p.ldc + n;
+    }
+    template <bool kGrad> __device__ __forceinline__ void issue(const SsmBwdParams &p, const Where<S> &w, long row0, int ntok, int stage) const {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], silu2(z[i]));
+        for (int k = 0; k < S::VPT; ++k) {
+            const int t = w.vt + k * (kTile / S::VPT);
+            const bool in = w.on && t < ntok;
+            const size_t row = in ? (size_t)(row0 + t) : 0;
+            const int c = in ? w.c : 0;
+            copy(stage, 4 * k, static_cast<const T *>(p.x) + row * p.ldx + c, in, w.whole);
+            copy(stage, 4 * k + 1, static_cast<const T *>(p.dt) + row * p.ldt + c, in, w.whole);
+            if (kGrad) {
+                copy(stage, 4 * k + 2, static_cast<const T *>(p.dy) + row * p.ldg + c, in, w.whole);
+                if (p.z) copy(stage, 4 * k + 3, static_cast<const T *>(p.z) + row * p.ldz + c, in, w.whole);
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            d[i] = add2(d[i], bias[i]);
-            if (p.softplus) d[i] = softplus2(d[i]);
-            if (!in) d[i] = 0;
-            x[i] = mul2(x[i], d[i]);
+        if (wide) {
+            const T *src = narrow(p, row0, ntok, kGrad);
+            copy(stage, 4 * S::VPT, src ? src : static_cast<const T *>(p.Bm), src != nullptr, true);
         }
-        const int at = t * S::RS + (int)(threadIdx.x % S::VW) * 8;
-        store8(sD + at, d, true);
-        store8(sU + at, x, true);
-        if (kGrad) store8(sG + at, g, true);
+        copies_commit();
     }
-    for (int e = threadIdx.x; e < kTile * S::N; e += S::TH) {
-        const int t = e / S::N, n = e % S::N;
-        const size_t row = (size_t)(row0 + t);
-        sB[e] = t < ntok ? Elem<T>::load(static_cast<const T *>(p.Bm) + row * p.ldb + n) : 0.f;
-        if (kGrad) sC[e] = t < ntok ? Elem<T>::load(static_cast<const T *>(p.Cm) + row * p.ldc + n) : 0.f;
+    // The tile's delta, delta u and (kGrad) dy', B and C, into shared memory.
+    // Steps past the end are 0: they leave both chains as they are.
+    template <bool kGrad>
+    __device__ __forceinline__ void take(const SsmBwdParams &p, const Where<S> &w, long row0, int ntok, int stage, float *sD, float *sU,
+                                         float *sG, float *sB, const f2 (&bias)[4]) const {
+#pragma unroll
+        for (int k = 0; k < S::VPT; ++k) {
+            const int t = w.vt + k * (kTile / S::VPT);
+            const bool in = w.on && t < ntok;
+            f2 x[4], d[4], g[4];
+            raw_unpack(held(stage, 4 * k), x);
+            raw_unpack(held(stage, 4 * k + 1), d);
+            if (kGrad) {
+                raw_unpack(held(stage, 4 * k + 2), g);
+                if (p.z) {
+                    f2 z[4];
+                    raw_unpack(held(stage, 4 * k + 3), z);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], silu2(z[i]));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                d[i] = add2(d[i], bias[i]);
+                if (p.softplus) d[i] = softplus2(d[i]);
+                if (!in) d[i] = 0;
+                x[i] = mul2(x[i], d[i]);
+            }
+            const int at = t * S::RS + (int)(threadIdx.x % S::VW) * 8;
+            store8(sD + at, d, true);
+            store8(sU + at, x, true);
+            if (kGrad) store8(sG + at, g, true);
+        }
+        if (threadIdx.x < (kGrad ? 2 : 1) * kNarrow) {             // C follows B
+            f2 v[4];
+            if (wide) {
+                raw_unpack(held(stage, 4 * S::VPT), v);
+            } else {
+                const T *src = narrow(p, row0, ntok, kGrad);
+                raw_unpack(src ? raw_gather(src) : raw_zero<T>(), v);
+            }
+            store8(sB + threadIdx.x * 8, v, true);
+        }
     }
-}
+};
 
 template <class S> struct State {
     f2 v[S::K][S::P];
@@ -190,7 +251,7 @@ __device__ __forceinline__ void advance(State<S> &h, const State<S> &a2, const f
 // Of every segment: the state it ends in from zero (seg_h), the c that leaves
 // its first token from zero (seg_g), and the sum of its steps.
 template <typename T, class S>
-__global__ void __launch_bounds__(S::TH, 2) ssm_bwd_local_kernel(const SsmBwdParams p, int tiles) {
+__global__ void __launch_bounds__(S::TH, 3) ssm_bwd_local_kernel(const SsmBwdParams p, int tiles) {
     extern __shared__ __align__(16) float smem[];
     float *sD = smem, *sU = sD + S::kRow, *sG = sU + S::kRow, *sB = sG + S::kRow, *sC = sB + kTile * S::N;
     const int c0 = (int)(blockIdx.x % (unsigned)tiles) * S::CH;
@@ -216,8 +277,12 @@ __global__ void __launch_bounds__(S::TH, 2) ssm_bwd_local_kernel(const SsmBwdPar
 #pragma unroll
         for (int i = 0; i < S::P; ++i) pr.v[k][i] = f2_pack(1.f, 1.f);
     float sum[S::K] = {};
+    const Ring<T, S> ring(p, smem + S::kLocal);
+    ring.template issue<true>(p, w, row0, ntok, 0);
     for (int t0 = 0; t0 < ntok; t0 += kTile) {
-        load_tile<T, S, true>(p, w, row0 + t0, ntok - t0, sD, sU, sG, sB, sC, bias);
+        copies_wait<0>();
+        ring.template take<true>(p, w, row0 + t0, ntok - t0, 0, sD, sU, sG, sB, bias);
+        if (t0 + kTile < ntok) ring.template issue<true>(p, w, row0 + t0 + kTile, ntok - t0 - kTile, 0);
         __syncthreads();
 #pragma unroll 2
         for (int t = 0; t < kTile; ++t) {
@@ -253,7 +318,7 @@ __global__ void __launch_bounds__(S::TH, 2) ssm_bwd_local_kernel(const SsmBwdPar
 
 // ----------------------------------------------------------- second launch
 template <typename T, class S>
-__global__ void __launch_bounds__(S::TH, 3) ssm_bwd_kernel(const SsmBwdParams p, int tiles) {
+__global__ void __launch_bounds__(S::TH, 2) ssm_bwd_kernel(const SsmBwdParams p, int tiles) {
     extern __shared__ __align__(16) float smem[];
     float *sD = smem, *sU = sD + S::kRow, *sG = sU + S::kRow, *sS = sG + S::kRow, *sB = sS + S::kRow;
     float *sC = sB + kTile * S::N;
@@ -297,9 +362,13 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_kernel(const SsmBwdParams p,
 
     // ---- forward sweep: the state entering every tile
     float *tile_h = p.tile_h + ((size_t)b * p.tiles + (size_t)seg * p.L / kTile) * plane + cell;
+    const Ring<T, S> ring(p, smem + S::kMain);
+    if (ntile > 1) ring.template issue<false>(p, w, row0, kTile, 0);
     for (int i = 0; i + 1 < ntile; ++i) {
         if (on) h.store(tile_h + (size_t)i * plane);
-        load_tile<T, S, false>(p, w, row0 + i * kTile, kTile, sD, sU, nullptr, sB, nullptr, bias);
+        copies_wait<0>();
+        ring.template take<false>(p, w, row0 + i * kTile, kTile, 0, sD, sU, nullptr, sB, bias);
+        if (i + 2 < ntile) ring.template issue<false>(p, w, row0 + (i + 1) * kTile, kTile, 0);
         __syncthreads();
 #pragma unroll 2
         for (int t = 0; t < kTile; ++t) advance<S>(h, a2, sD + t * S::RS + lc, sU + t * S::RS + lc, sB + t * S::N + q * S::SP);
@@ -313,10 +382,16 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_kernel(const SsmBwdParams p,
     f2 *ck = sH + (size_t)warp * 3 * S::K * S::P * 32 + lane;
     float *myP = sP + warp * 2 * kTile * S::N;
 
+    int stage = 0;
+    ring.template issue<true>(p, w, row0 + (long)(ntile - 1) * kTile, ntok - (ntile - 1) * kTile, stage);
     for (int i = ntile - 1; i >= 0; --i) {
         const long tr = row0 + (long)i * kTile;
         const int left = min(kTile, ntok - i * kTile);
-        load_tile<T, S, true>(p, w, tr, left, sD, sU, sG, sB, sC, bias);
+        copies_wait<0>();
+        ring.template take<true>(p, w, tr, left, stage, sD, sU, sG, sB, bias);
+        const int kept = stage;
+        if (Ring<T, S>::kStages == 2) stage ^= 1;
+        if (i > 0) ring.template issue<true>(p, w, tr - kTile, kTile, stage);
         if (i + 1 < ntile && on) h.load(tile_h + (size_t)i * plane);
         __syncthreads();
         // ---- forward through the tile's first twelve tokens
@@ -450,10 +525,14 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_kernel(const SsmBwdParams p,
                 const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(src)[0], b = reinterpret_cast<const ulonglong2 *>(src)[1];
                 v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
             };
-            raw_unpack(raw_load(static_cast<const T *>(p.x) + row * p.ldx + w.c, w.whole), x);
-            raw_unpack(raw_load(static_cast<const T *>(p.dy) + row * p.ldg + w.c, w.whole), g);
+            auto again = [&](int piece, const void *base, long ld) {
+                if (Ring<T, S>::kStages == 2) return ring.held(kept, 4 * k + piece);
+                return raw_load(static_cast<const T *>(base) + row * ld + w.c, w.whole);
+            };
+            raw_unpack(again(0, p.x, p.ldx), x);
+            raw_unpack(again(2, p.dy, p.ldg), g);
             if (p.z) {
-                raw_unpack(raw_load(static_cast<const T *>(p.z) + row * p.ldz + w.c, w.whole), z);
+                raw_unpack(again(3, p.z, p.ldz), z);
                 take(sG + at, y0);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -473,7 +552,7 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_kernel(const SsmBwdParams p,
                 o[e] = fma2(d[e], s1[e], mul2(skip[e], g[e]));
             }
             store8(static_cast<T *>(p.dx) + row * p.D + w.c, o, w.whole);
-            if (p.softplus) raw_unpack(raw_load(static_cast<const T *>(p.dt) + row * p.ldt + w.c, w.whole), d);
+            if (p.softplus) raw_unpack(again(1, p.dt, p.ldt), d);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 o[e] = fma2(s2[e], both(kLn2), mul2(s1[e], x[e]));
@@ -526,15 +605,14 @@ template <typename T, int N> cudaError_t run(const SsmBwdParams &p, cudaStream_t
     if ((long double)units * tiles > 2147483647.0L) return cudaErrorInvalidValue;
     cudaError_t e;
     if (p.nseg > 1) {
-        constexpr int bytes = S::kLocal * (int)sizeof(float);
-        if (bytes > 48 * 1024 &&
-            (e = cudaFuncSetAttribute(ssm_bwd_local_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
+        constexpr int bytes = (S::kLocal + Ring<T, S>::kFloats) * (int)sizeof(float);
+        if ((e = cudaFuncSetAttribute(ssm_bwd_local_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
             return e;
         ssm_bwd_local_kernel<T, S><<<(unsigned)(units * tiles), S::TH, bytes, s>>>(p, tiles);
         if (launches) ++*launches;
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    constexpr int bytes = S::kMain * (int)sizeof(float);
+    constexpr int bytes = (S::kMain + Ring<T, S>::kFloats) * (int)sizeof(float);
     if ((e = cudaFuncSetAttribute(ssm_bwd_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
     ssm_bwd_kernel<T, S><<<(unsigned)(units * tiles), S::TH, bytes, s>>>(p, tiles);
     if (launches) ++*launches;
@@ -563,18 +641,22 @@ size_t round16(size_t floats) { return (floats + 3) / 4 * 4; }
 
 }  // namespace
 
+constexpr int kRounds = 4, kLeast = 32;
+
 // Channels a CTA of the backward owns.
 static int bwd_channels(int N) { return N == 32 ? Shape<32>::CH : Shape<16>::CH; }
 
 // Cuts the sequences and lays out the workspace; returns its floats.
 size_t plan_ssm_bwd(SsmBwdParams &p, float *ws) {
     const long chains = (long)p.B * ((p.D + bwd_channels(p.N) - 1) / bwd_channels(p.N));
-    const long want = 3L * device_sm_count();
-    long nseg = (want + chains - 1) / chains;
+    // Four rounds of the two CTAs an SM holds: the cut costs nothing but the
+    // folds (the first launch walks every token once, whatever the cut).
+    long nseg = kRounds * 2L * device_sm_count() / chains;
+    if (nseg < 1) nseg = 1;
     if (nseg > 64) nseg = 64;
     long L = (p.T + nseg - 1) / nseg;
     L = (L + kTile - 1) / kTile * kTile;
-    if (L < 64) L = 64;
+    if (L < kLeast) L = kLeast;
     p.L = L;
     p.nseg = (int)((p.T + L - 1) / L);
     p.tiles = (p.T + kTile - 1) / kTile;
