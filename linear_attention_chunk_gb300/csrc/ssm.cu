@@ -37,11 +37,12 @@ using namespace ssm;
 
 constexpr int kTile = 16;   // tokens per tile: 2 x 16 vectors of eight channels, one a lane
 constexpr int kChan = 16;   // channels of a warp
-constexpr int kMostWarps = 4, kMinBlocks = 3;   // of a CTA; CTAs an SM holds
+constexpr int kMostWarps = 4, kMinBlocks = 4;   // of a CTA; CTAs an SM holds
 
-// Shared memory of a warp: (delta, delta u) of the tile, y, B, C, the filter.
-template <int N, bool kConv> constexpr int warp_floats() {
-    return kTile * kChan * 3 + 2 * kTile * N + (kConv ? (kTaps + 1) * kChan : 0);
+// Shared memory of a warp: (delta, delta u) of the tile, y, B, C; the filter
+// and the inputs of this tile and the one before (as they lie in memory).
+template <typename T, int N, bool kConv> constexpr int warp_floats() {
+    return kTile * kChan * 3 + 2 * kTile * N + (kConv ? (kTaps + 1) * kChan + 2 * 32 * 2 * (int)sizeof(T) : 0);
 }
 
 // The unit's sequence, its segment and its tokens. False: nothing to do.
@@ -92,52 +93,30 @@ __device__ __forceinline__ bool find_unit(const SsmParams &p, long u, int *s_fou
     return true;
 }
 
-// u of one token for eight channels: SiLU of the width-4 filter over the
-// token's input and the three before it, from the window before the
-// sequence's first token (rows oldest first, the last four inputs). sW: the
-// filter of the CTA's channels in shared memory, [4 taps, bias][channel].
+// The filter's input at a row before the unit's first token, eight channels:
+// from x inside the sequence, from the window before its first token (rows
+// oldest first, the last four inputs).
 template <typename T>
-__device__ __forceinline__ void conv8(const SsmParams &p, const Unit &un, long row, int c, bool whole,
-                                      const Raw8<T> &now, const float *sW, int step, f2 (&u)[4]) {
-    f2 acc[4];
-    Raw8<T> past[3];
-#pragma unroll
-    for (int j = 0; j < 3; ++j)
-        if (row - 3 + j >= un.first)
-            past[j] = raw_load(static_cast<const T *>(p.x) + (size_t)(row - 3 + j) * p.ldx + c, whole);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(sW + kTaps * step + 4 * i);
-        acc[2 * i] = b.x;
-        acc[2 * i + 1] = b.y;
+__device__ __forceinline__ void before(const SsmParams &p, const Unit &un, long src, int c, bool whole, f2 (&v)[4]) {
+    if (src >= un.first) {
+        raw_unpack(raw_load(static_cast<const T *>(p.x) + (size_t)src * p.ldx + c, whole), v);
+        return;
     }
-#pragma unroll
-    for (int j = 0; j < kTaps; ++j) {
-        const long src = row - 3 + j;
-        f2 v[4];
-        if (j == 3) {
-            raw_unpack(now, v);
-        } else if (src >= un.first) {
-            raw_unpack(past[j], v);
-        } else {
-            // plain loads: this launch rewrites the window later
-            const float4 *r = reinterpret_cast<const float4 *>(
-                p.win + ((size_t)un.slot * kTaps + (kTaps + src - un.first)) * p.D + c);
-            const float4 a = r[0], b = whole ? r[1] : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[0] = f2_pack(a.x, a.y);
-            v[1] = f2_pack(a.z, a.w);
-            v[2] = f2_pack(b.x, b.y);
-            v[3] = f2_pack(b.z, b.w);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(sW + j * step + 4 * i);
-            acc[2 * i] = fma2(w.x, v[2 * i], acc[2 * i]);
-            acc[2 * i + 1] = fma2(w.y, v[2 * i + 1], acc[2 * i + 1]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = silu2(acc[i]);
+    // plain loads: this launch rewrites the window later
+    const float4 *r = reinterpret_cast<const float4 *>(p.win + ((size_t)un.slot * kTaps + (kTaps + src - un.first)) * p.D + c);
+    const float4 a = r[0], b = whole ? r[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+    v[0] = f2_pack(a.x, a.y);
+    v[1] = f2_pack(a.z, a.w);
+    v[2] = f2_pack(b.x, b.y);
+    v[3] = f2_pack(b.z, b.w);
+}
+
+__device__ __forceinline__ void four(const float *src, f2 (&v)[4]) {   // eight floats of shared memory
+    const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(src)[0], b = reinterpret_cast<const ulonglong2 *>(src)[1];
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = b.x;
+    v[3] = b.y;
 }
 
 template <typename T, int N, bool kFull, bool kConv>
@@ -145,12 +124,13 @@ __global__ void __launch_bounds__(32 * kMostWarps, kMinBlocks) ssm_scan_kernel(c
     constexpr int SP = N / 4, P = SP / 2;
     extern __shared__ __align__(16) float smem[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, q = lane / 8;
-    float *mine = smem + warp * warp_floats<N, kConv>();
+    float *mine = smem + warp * warp_floats<T, N, kConv>();
     float4 *sD = reinterpret_cast<float4 *>(mine);     // [kTile][8 channel pairs, swizzled]
     float *sY = mine + kTile * kChan * 2;              // [kTile][kChan]
     float *sB = sY + kTile * kChan;                    // [kTile][N]
     float *sC = sB + kTile * N;
     float *sW = sC + kTile * N;                        // [taps and bias][kChan]
+    uint4 *sX = reinterpret_cast<uint4 *>(sW + (kTaps + 1) * kChan);   // [tile parity][piece][vector]
     __shared__ int s_found;
 
     const int c0 = ((int)(blockIdx.x % (unsigned)tiles) * (int)(blockDim.x / 32) + warp) * kChan;
@@ -159,7 +139,7 @@ __global__ void __launch_bounds__(32 * kMostWarps, kMinBlocks) ssm_scan_kernel(c
     if (!find_unit(p, unit, &s_found, un)) return;
     const long seg0 = (long)un.seg * p.L;
     const long row0 = un.first + seg0;
-    const long ntok = min((long)p.L, un.len - seg0);
+    const int ntok = (int)min((long)p.L, un.len - seg0);
     const bool last = seg0 + p.L >= un.len;
     if (!kFull && last) return;
 
@@ -241,52 +221,100 @@ __global__ void __launch_bounds__(32 * kMostWarps, kMinBlocks) ssm_scan_kernel(c
     param8(vec_on ? p.dt_bias : nullptr, c, whole, bias);
     if (kFull) param8(vec_on ? p.skip : nullptr, c, whole, skip);
 
-    // one tile's inputs as they lie in memory; B and C as vectors of eight too
-    Raw8<T> rx, rd, rz = raw_zero<T>();
+    // One tile's inputs as they lie in memory; B and C as vectors of eight too.
+    // A lane past the last channel repeats the warp's first vector, and nothing
+    // of it is kept; tokens past the end are looked after in the last tile only.
+    constexpr int H = sizeof(T) / 2;
     constexpr int BV = kTile * N / 8, BL = (BV + 31) / 32;   // vectors of B (and of C), and per lane
-    Raw8<T> rb[BL], rc[BL];
-    auto narrow = [&](const void *base, long ld, long t0, int i) {
-        const int e = i * 32 + lane, t = e / (N / 8), n = e % (N / 8) * 8;
-        if (e >= BV || t0 + t >= ntok) return raw_zero<T>();
-        const T *src = static_cast<const T *>(base) + (size_t)(row0 + t0 + t) * ld + n;
-        if (reinterpret_cast<uintptr_t>(src) % 16 == 0) return raw_load(src, true);
-        return raw_gather(src);
-    };
-    auto fetch = [&](long t0) {
-        const long row = row0 + t0 + vt;
-        const bool on = vec_on && t0 + vt < ntok;
-        rx = on ? raw_load(static_cast<const T *>(p.x) + (size_t)row * p.ldx + c, whole) : raw_zero<T>();
-        rd = on ? raw_load(static_cast<const T *>(p.dt) + (size_t)row * p.ldt + c, whole) : raw_zero<T>();
-        if (kFull && p.z) rz = on ? raw_load(static_cast<const T *>(p.z) + (size_t)row * p.ldz + c, whole) : raw_zero<T>();
+    const int cv = vec_on ? c : c0;
+    const bool cw = vec_on ? whole : c0 + kVec <= p.D;
+    const T *px = static_cast<const T *>(p.x) + (size_t)(row0 + vt) * p.ldx + cv;
+    const T *pd = static_cast<const T *>(p.dt) + (size_t)(row0 + vt) * p.ldt + cv;
+    const T *pz = kFull && p.z ? static_cast<const T *>(p.z) + (size_t)(row0 + vt) * p.ldz + cv : nullptr;
+    const int bt = lane / (N / 8), bn = lane % (N / 8) * 8;  // token and first state of this lane's first vector
+    const T *pb = static_cast<const T *>(p.Bm) + (size_t)(row0 + bt) * p.ldb + bn;
+    const T *pc = static_cast<const T *>(p.Cm) + (size_t)(row0 + bt) * p.ldc + bn;
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.Bm) | reinterpret_cast<uintptr_t>(p.Cm) | (uintptr_t)p.ldb * sizeof(T) |
+                        (uintptr_t)p.ldc * sizeof(T)) % 16) == 0;
+    Raw8<T> rx, rd, rz = raw_zero<T>(), rb[BL], rc[BL];
+    auto narrow = [&](const T *src) { return wide ? raw_load(src, true) : raw_gather(src); };
+    auto fetch = [&](int left) {                             // the next tile, of which `left` tokens exist
+        constexpr int step = 32 / (N / 8);                   // tokens from one of this lane's vectors to the next
+        if (left >= kTile) {
+            rx = raw_load(px, cw);
+            rd = raw_load(pd, cw);
+            if (pz) rz = raw_load(pz, cw);
 #pragma unroll
-        for (int i = 0; i < BL; ++i) {
-            rb[i] = narrow(p.Bm, p.ldb, t0, i);
-            if (kFull) rc[i] = narrow(p.Cm, p.ldc, t0, i);
+            for (int i = 0; i < BL; ++i) {
+                if (BV % 32 != 0 && lane >= BV) break;
+                rb[i] = narrow(pb + (size_t)(i * step) * p.ldb);
+                if (kFull) rc[i] = narrow(pc + (size_t)(i * step) * p.ldc);
+            }
+        } else {
+            const bool in = vt < left;
+            rx = in ? raw_load(px, cw) : raw_zero<T>();
+            rd = in ? raw_load(pd, cw) : raw_zero<T>();
+            if (pz) rz = in ? raw_load(pz, cw) : raw_zero<T>();
+#pragma unroll
+            for (int i = 0; i < BL; ++i) {
+                const bool on = i * 32 + lane < BV && bt + i * step < left;
+                rb[i] = on ? narrow(pb + (size_t)(i * step) * p.ldb) : raw_zero<T>();
+                if (kFull) rc[i] = on ? narrow(pc + (size_t)(i * step) * p.ldc) : raw_zero<T>();
+            }
         }
+        px += (size_t)kTile * p.ldx;
+        pd += (size_t)kTile * p.ldt;
+        if (pz) pz += (size_t)kTile * p.ldz;
+        pb += (size_t)kTile * p.ldb;
+        pc += (size_t)kTile * p.ldc;
     };
-    fetch(0);
+    fetch(ntok);
 
+    T *py = static_cast<T *>(p.y) + (size_t)(row0 + vt) * p.D + c;
     float dsum[2] = {0.f, 0.f};
-    for (long t0 = 0; t0 < ntok; t0 += kTile) {
+    int par = 0;                                             // the tile's parity
+    for (int left = ntok; left > 0; left -= kTile, par ^= 1) {
         // ---- inputs of the tile: u, delta; zero steps past the end leave the state as it is
-        const bool on = vec_on && t0 + vt < ntok;
         f2 u[4], dl[4];
         raw_unpack(rd, dl);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             dl[i] = add2(dl[i], bias[i]);
             if (p.softplus) dl[i] = softplus2(dl[i]);
-            if (!on) dl[i] = 0;
         }
-        if (kConv) {
-            if (on) {
-                conv8(p, un, row0 + t0 + vt, c, whole, rx, sW + lane % 2 * kVec, kChan, u);
-            } else {
+        if (left < kTile && vt >= left)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) u[i] = 0;
+            for (int i = 0; i < 4; ++i) dl[i] = 0;
+        raw_unpack(rx, u);
+        if (kConv) {
+            // the three rows before this lane's come from the lanes that loaded them, in this tile or the one before
+#pragma unroll
+            for (int i = 0; i < H; ++i) sX[(par * H + i) * 32 + lane] = rx.w[i];
+            __syncwarp();
+            const float *w = sW + lane % 2 * kVec;
+            f2 acc[4];
+            four(w + kTaps * kChan, acc);
+#pragma unroll
+            for (int j = 0; j < kTaps; ++j) {
+                f2 v[4], wj[4];
+                if (j == kTaps - 1) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = u[i];
+                } else if (left == ntok && vt < 3 - j) {     // before the unit
+                    before<T>(p, un, row0 + vt - 3 + j, cv, cw, v);
+                } else {
+                    const int from = lane - 2 * (3 - j);
+                    Raw8<T> r;
+#pragma unroll
+                    for (int i = 0; i < H; ++i) r.w[i] = sX[((from < 0 ? par ^ 1 : par) * H + i) * 32 + (from & 31)];
+                    raw_unpack(r, v);
+                }
+                four(w + j * kChan, wj);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i] = fma2(wj[i], v[i], acc[i]);
             }
-        } else {
-            raw_unpack(rx, u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = left < kTile && vt >= left ? 0 : silu2(acc[i]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {                  // four tokens' 128-byte rows over all the banks
@@ -308,32 +336,44 @@ __global__ void __launch_bounds__(32 * kMostWarps, kMinBlocks) ssm_scan_kernel(c
         }
         const Raw8<T> zc = rz;
         __syncwarp();
-        if (t0 + kTile < ntok) fetch(t0 + kTile);
+        if (left > kTile) fetch(left - kTile);
 
         // ---- the scan: the tile's tokens
-#pragma unroll 2
+#pragma unroll
         for (int t = 0; t < kTile; t += 4) {
-            float part[2][4];
+            // the decays and products of four tokens first, then the chain through them
+            f2 e[4][2][P], x[4][2][P];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float4 d = sD[(t + j) * 8 + ((lane % 8) ^ ((t + j) & 3))];
                 const f2 *b = reinterpret_cast<const f2 *>(sB + (t + j) * N + q * SP);
-                const f2 *cc = reinterpret_cast<const f2 *>(sC + (t + j) * N + q * SP);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const f2 dd = k ? f2_pack(d.z, d.z) : f2_pack(d.x, d.x);
                     const f2 du = k ? f2_pack(d.w, d.w) : f2_pack(d.y, d.y);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        e[j][k][i] = ex2_pair(mul2(dd, a2[k][i]));
+                        x[j][k][i] = mul2(du, b[i]);
+                    }
+                    if (!kFull) dsum[k] += k ? d.z : d.x;
+                }
+            }
+            float part[2][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f2 *cc = reinterpret_cast<const f2 *>(sC + (t + j) * N + q * SP);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
                     f2 y = 0;
 #pragma unroll
                     for (int i = 0; i < P; ++i) {
-                        h[k][i] = fma2(ex2_pair(mul2(dd, a2[k][i])), h[k][i], mul2(du, b[i]));
+                        h[k][i] = fma2(e[j][k][i], h[k][i], x[j][k][i]);
                         if (kFull) y = i == 0 ? mul2(h[k][i], cc[i]) : fma2(h[k][i], cc[i], y);
                     }
                     if (kFull) {
                         const float2 ys = f2_split(y);
                         part[k][j] = ys.x + ys.y;
-                    } else {
-                        dsum[k] += k ? d.z : d.x;
                     }
                 }
             }
@@ -344,17 +384,17 @@ __global__ void __launch_bounds__(32 * kMostWarps, kMinBlocks) ssm_scan_kernel(c
         __syncwarp();
 
         // ---- skip, gate, store
-        if (kFull && on) {
-            const ulonglong2 *ys = reinterpret_cast<const ulonglong2 *>(sY + vt * kChan + lane % 2 * kVec);
-            const ulonglong2 y01 = ys[0], y23 = ys[1];
-            f2 y[4] = {y01.x, y01.y, y23.x, y23.y}, z[4];
+        if (kFull) {
+            f2 y[4], z[4];
+            four(sY + vt * kChan + lane % 2 * kVec, y);
             raw_unpack(zc, z);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 y[i] = fma2(skip[i], u[i], y[i]);
                 if (p.z) y[i] = mul2(y[i], silu2(z[i]));
             }
-            store8(static_cast<T *>(p.y) + (size_t)(row0 + t0 + vt) * p.D + c, y, whole);
+            if (vec_on && (left >= kTile || vt < left)) store8(py, y, whole);
+            py += (size_t)kTile * p.D;
         }
     }
 
@@ -410,7 +450,7 @@ template <typename T, int N, bool kFull, bool kConv>
 cudaError_t launch(const SsmParams &p, long units, cudaStream_t s, int *launches) {
     const int w = warps_per_block(units, p.D), tiles = (p.D + kChan * w - 1) / (kChan * w);
     if ((long double)units * tiles > 2147483647.0L) return cudaErrorInvalidValue;
-    const int bytes = w * warp_floats<N, kConv>() * (int)sizeof(float);
+    const int bytes = w * warp_floats<T, N, kConv>() * (int)sizeof(float);
     ssm_scan_kernel<T, N, kFull, kConv><<<(unsigned)(units * tiles), 32 * w, bytes, s>>>(p, tiles);
     if (launches) ++*launches;
     return cudaGetLastError();
@@ -453,9 +493,9 @@ SsmPlan plan_ssm(long nseq, long rows, int D, bool varlen) {
     if (!varlen && warps >= want) return SsmPlan{mean, 1};
     long nseg = (2 * want + warps - 1) / warps;
     long L = (mean + nseg - 1) / nseg;
-    L = (L + 127) / 128 * 128;
+    L = (L + 63) / 64 * 64;
     if (varlen && L > 512) L = 512;
-    if (!varlen && L >= mean) return SsmPlan{mean, 1};
+    if (!varlen && 2 * L >= mean) return SsmPlan{mean, 1};   // two segments cost as much as they save
     if (varlen && L >= rows) return SsmPlan{rows, nseq};
     pl.L = L;
     pl.slots = varlen ? rows / L + nseq : nseq * ((mean + L - 1) / L);
