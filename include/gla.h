@@ -399,7 +399,8 @@ gla_status gla_conv1d_step(const void *x, const float *w, const float *b, float 
  *   A [D, N] fp32 (negative for a decay; not its logarithm), skip [D] fp32 or
  *     NULL (0), dt_bias [D] fp32 or NULL (0), z or NULL (no gate).
  *   y: contiguous rows of D. States [*, D, N] fp32, N fastest.
- *   D a multiple of 8 (bf16) or 4 (fp32); N = 8, 16 or 32. y may not be x, dt or z.
+ *   D a multiple of 8 (bf16) or 4 (fp32), at most 2^25; N = 8, 16 or 32. y
+ *   may not overlap an input.
  *
  * gla_ssm_fwd: B sequences of T tokens, x, dt, z, y [B, T, D], Bm, Cm
  *   [B, T, N] (token rows ld_* apart throughout, b-th sequence's first row at
@@ -414,8 +415,8 @@ gla_status gla_conv1d_step(const void *x, const float *w, const float *b, float 
  *   (decreasing offset, offset past total_T, slot outside the pool) skips its
  *   sequence and the next gla_check() reports GLA_ERR_INVALID_ARG; where
  *   offsets decrease, other sequences may be skipped with it.
- * gla_ssm_step: one token per sequence, rows [nseq, *], on the same pools;
- *   a bad slot skips its sequence likewise.
+ * gla_ssm_step: one token per sequence, rows [nseq, *], on the same pools and
+ *   distinct slots; a bad slot skips its sequence likewise.
  * gla_ssm_fwd and gla_ssm_varlen cut sequences into segments that run in
  *   parallel when workspace_bytes is at least the *_workspace_size query
  *   (0: nothing to gain); with less they run one chain per sequence and
@@ -452,7 +453,7 @@ gla_status gla_ssm_step(const void *x, int64_t ld_x, const void *dt, int64_t ld_
  *   contiguous: dx, ddt, dz [B, T, D] and dB, dC [B, T, N] of `dtype`, dA
  *   [D, N], dskip, ddt_bias [D] and dh0 [B, D, N] fp32. dz goes with z (both
  *   or neither); dskip, ddt_bias, dh0 may be NULL (not wanted). Outputs may
- *   not alias inputs.
+ *   not overlap inputs (dh0 neither h0 nor dhT, except when B*T = 0).
  *   workspace: at least gla_ssm_bwd_workspace_size() bytes (required when
  *   B*T > 0): a state per 16 tokens and partial sums. Sums run in a fixed
  *   order: the same call gives the same bits. B*T = 0 zeroes the sums, and

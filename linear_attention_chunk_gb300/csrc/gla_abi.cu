@@ -168,8 +168,8 @@ gla_status check_ssm_shape(int64_t seqs, int64_t rows, int D, int N, gla_dtype d
     if (D <= 0 || D % vec != 0) return fail(GLA_ERR_UNSUPPORTED, "D=%d must be a positive multiple of %d", D, vec);
     if (N != 8 && N != 16 && N != 32) return fail(GLA_ERR_UNSUPPORTED, "N=%d is not 8, 16 or 32", N);
     if (D > (1 << 25)) return fail(GLA_ERR_UNSUPPORTED, "D=%d is above 2^25", D);   // D * N and D * 4 fit an int
-    // one CTA per 64 channels of a sequence or segment: well inside a 1-D grid
-    if ((long double)(seqs + rows) * ((D + 63) / 64) > 2147483647.0L || (long double)rows * D > (long double)(1ull << 40))
+    // at most one CTA per 16 channels of a sequence or segment: inside a 1-D grid
+    if ((long double)(seqs + rows) * ((D + 15) / 16) > 2147483647.0L || (long double)rows * D > (long double)(1ull << 40))
         return fail(GLA_ERR_INVALID_ARG, "tensor too large");
     return GLA_OK;
 }
@@ -819,6 +819,8 @@ gla_status gla_ssm_bwd(const void *x, int64_t ld_x, const void *dt, int64_t ld_d
     for (const void *out : {(const void *)dx, (const void *)ddt, (const void *)dz, (const void *)dB, (const void *)dC})
         if (out && (out == x || out == dt || out == z || out == dy || out == Bm || out == Cm))
             return fail(GLA_ERR_INVALID_ARG, "an output may not alias an input");
+    // every segment of a sequence reads its h0 and dhT, the first writes dh0
+    if (dh0 && (dh0 == h0 || dh0 == dhT)) return fail(GLA_ERR_INVALID_ARG, "dh0 may not alias h0 or dhT");
     REQUIRE_PTR(workspace, "workspace");
     const size_t need = gla_ssm_bwd_workspace_size(B, T, D, N, dtype);
     if (workspace_bytes < need)

@@ -327,3 +327,76 @@ def test_another_stream_and_two_captured_graphs(gla):
     torch.cuda.synchronize()
     for o, r in zip(outs, want):
         assert torch.equal(o[0], r[0]) and torch.equal(o[1], r[1])
+
+
+def test_offsets_past_32_bits(gla):
+    """Pools of more than 2^31 elements (slots at the far end) and rows that lie more than 2^31 elements into x."""
+    D, N, slots = 4096, 16, 33000
+    pool = torch.empty(slots, D, N, device="cuda")          # 8.7 GB, only two slots are touched
+    win = torch.empty(slots, 4, D, device="cuda")
+    assert pool.numel() > 1 << 31
+    use = [slots - 1, 5]
+    small, wsmall, w, b = pools(2, D, N, 3)
+    s = inputs((2,), D, N, BF, 12)
+    for i, k in enumerate(use):
+        pool[k], win[k] = small[i], wsmall[i]
+    y = call_step(gla, s, pool, i32(use), w, b, win)
+    y1 = call_step(gla, s, small, None, w, b, wsmall)
+    gla.gla_check()
+    assert torch.equal(y, y1)
+    for i, k in enumerate(use):
+        assert torch.equal(pool[k], small[i]) and torch.equal(win[k], wsmall[i])
+    rows, wide = 70000, 32768
+    big = torch.empty(rows, wide, dtype=BF, device="cuda")
+    assert big.numel() > 1 << 31
+    s = inputs((40,), 64, N, BF, 13)
+    far = big[rows - 40:, wide - 64:]
+    far.copy_(s["x"])
+    # the packed call sees all rows; only the last 40 belong to a sequence
+    z = torch.zeros(rows, 64, dtype=BF, device="cuda")
+    t = {k: (torch.cat([torch.zeros(rows - 40, v.shape[1], dtype=BF, device="cuda"), v]) if k in ("dt", "Bm", "Cm") else v)
+         for k, v in s.items()}
+    t["x"], t["z"] = big[:, wide - 64:], None
+    s["z"] = None
+    p1, w1, w, b = pools(1, 64, N, 4)
+    p2, w2 = p1.clone(), w1.clone()
+    ya = call_varlen(gla, t, i32([rows - 40, rows]), p1, None, w, b, w1, y=z)
+    yb = call_varlen(gla, s, i32([0, 40]), p2, None, w, b, w2)
+    gla.gla_check()
+    close(ya[rows - 40:], d(yb), d(yb).abs() + 1, 40, "y")
+    close(p1, d(p2), d(p2).abs() + 1, 40, "state")
+    assert torch.equal(w1, w2) and not ya[:rows - 40].any()
+
+
+def test_calls_on_two_streams_at_once(gla):
+    """Nothing is shared between calls but the status word."""
+    s = [inputs((2, 600), 136, 16, BF, k) for k in (21, 22)]
+    want = [call_fwd(gla, v) for v in s]
+    streams = [torch.cuda.Stream() for _ in s]
+    torch.cuda.synchronize()
+    got = [[call_fwd(gla, v, stream=st) for v, st in zip(s, streams)] for _ in range(5)]
+    torch.cuda.synchronize()
+    for rep in got:
+        for g, r in zip(rep, want):
+            assert torch.equal(g[0], r[0]) and torch.equal(g[1], r[1])
+
+
+def test_wrong_tensors_are_refused(gla):
+    s = inputs((2, 9), 16, 16, BF, 1)
+    for name, bad in (("dt", s["dt"].float()), ("dt", s["dt"][:, :8]), ("Bm", s["Bm"][..., :8].contiguous()),
+                      ("A", s["A"].double()), ("A", s["A"].t()), ("skip", s["skip"][:8]), ("z", s["z"].cpu()),
+                      ("x", s["x"].half()), ("x", s["x"].cpu())):
+        with pytest.raises(gla.GlaError):
+            call_fwd(gla, dict(s, **{name: bad}))
+    with pytest.raises(gla.GlaError):
+        call_fwd(gla, s, torch.zeros(2, 16, 8, device="cuda"))
+    with pytest.raises(gla.GlaError):
+        call_fwd(gla, s, y=s["x"])
+    pool = torch.zeros(2, 16, 16, device="cuda")
+    t = {k: (v[0] if k in ("x", "dt", "z", "Bm", "Cm") else v) for k, v in s.items()}
+    with pytest.raises(gla.GlaError):
+        call_varlen(gla, t, torch.tensor([0, 9], device="cuda"), pool)          # int64 offsets
+    with pytest.raises(gla.GlaError):
+        call_varlen(gla, t, i32([0, 3, 6, 9]), pool)                            # three sequences, two slots
+    with pytest.raises(gla.GlaError):
+        call_step(gla, t, pool.view(1, 32, 16))

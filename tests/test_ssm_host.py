@@ -40,12 +40,13 @@ def test_selective_scan_rejects_bad_arguments(L):
         return L.gla_ssm_step(*head(a), a["cw"], a["cb"], a["slots"], a["pool"], a["win"], a["n_slots"], a["nseq"],
                               a["D"], a["N"], a["dtype"], a["y"], None)
     for f in (fwd, var, step):
-        for kw in (dict(x=None), dict(x=ODD), dict(ldx=56), dict(ldx=68), dict(dt=None), dict(A=ODD), dict(Bm=None),
+        for kw in (dict(x=None), dict(x=ODD), dict(ldx=56), dict(ldx=68), dict(ldx=1 << 31), dict(dt=None), dict(A=ODD), dict(Bm=None),
                    dict(Bm=FAKE + 1), dict(ldb=15), dict(Cm=None), dict(z=ODD, ldz=64), dict(z=FAKE, ldz=60),
                    dict(y=None), dict(y=FAKE), dict(y=ODD), dict(dtype=2), dict(skip=ODD), dict(bias=ODD)):
             assert f(**kw) == binding.GLA_ERR_INVALID_ARG, (f.__name__, kw)
             assert L.gla_last_launch_count() == 0
-        for kw in (dict(D=60), dict(D=62, dtype=1), dict(D=0), dict(N=12), dict(N=64)):
+        for kw in (dict(D=60), dict(D=62, dtype=1), dict(D=0), dict(N=12), dict(N=64),
+                   dict(D=1 << 26, ldx=1 << 26, ldt=1 << 26)):
             assert f(**kw) == binding.GLA_ERR_UNSUPPORTED, (f.__name__, kw)
     assert fwd(B=-1) == fwd(T=-1) == fwd(h0=ODD) == fwd(hT=ODD) == binding.GLA_ERR_INVALID_ARG
     assert fwd(B=1 << 20, T=1 << 20) == binding.GLA_ERR_INVALID_ARG       # too large
@@ -127,7 +128,8 @@ def test_selective_scan_backward_rejects_bad_arguments(L):
     for kw in (dict(x=None), dict(ldx=60), dict(dt=ODD), dict(A=None), dict(Bm=None), dict(Cm=FAKE + 1), dict(dy=None),
                dict(dy=ODD), dict(ldg=63), dict(dx=None), dict(ddt=None), dict(dA=None), dict(dB=None), dict(dC=ODD),
                dict(dskip=ODD), dict(db=ODD), dict(dh0=ODD), dict(dhT=ODD), dict(h0=ODD), dict(dx=FAKE),
-               dict(z=FAKE, ldz=64), dict(dz=FAKE + 0x500), dict(ws=None), dict(dtype=9), dict(B=-1), dict(T=-1)):
+               dict(z=FAKE, ldz=64), dict(dz=FAKE + 0x500), dict(ws=None), dict(dtype=9), dict(B=-1), dict(T=-1),
+               dict(dh0=FAKE, h0=FAKE), dict(dh0=FAKE, dhT=FAKE)):
         assert bwd(**kw) == binding.GLA_ERR_INVALID_ARG, kw
     assert bwd(D=4) == bwd(N=24) == binding.GLA_ERR_UNSUPPORTED
     need = binding.gla_ssm_bwd_workspace_size(2, 50, 64, 16)
