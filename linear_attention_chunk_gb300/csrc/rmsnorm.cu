@@ -6,14 +6,15 @@
 //     dx = ds + (g - xn mean(g xn)) / sqrt(mean(s^2) + eps),  dw = sum over rows of dy xn.
 //
 // Streams over HBM: forward 7 bytes an element (bf16 x and res in, s and e4m3
-// out), backward 8. A CTA holds a row in registers, each thread VPT vectors of
-// eight channels, all its loads issued up front; the row's sums go through
-// shuffles and one shared-memory exchange. A block of 128, 64 or 32 channels
-// is 16, 8 or 4 neighbouring lanes, so its maximum needs shuffles only. The
-// backward's CTAs walk every G-th row, two rows ahead of them arriving by
-// asynchronous copies (one row ahead in registers kept too few bytes in
-// flight: 63 us at 16384 x 2048, now 51, 0.77 of the measured copy rate), and keep dw of their channels in registers; the partial sums of the
-// CTAs are added in a second launch (reduce.cu).
+// out), backward 8. A CTA walks every G-th row, the rows ahead of it arriving
+// by asynchronous copies (a thread copies and reads its own vectors of eight
+// channels); one row ahead in registers kept too few bytes in flight (backward
+// 63 us at 16384 x 2048, now 51, 0.77 of the measured copy rate; forward with
+// 8-bit output at 16384 x 4096 86, now 75, 0.93). A row's sums
+// go through shuffles and one shared-memory exchange. A block of 128, 64 or 32
+// channels is 16, 8 or 4 neighbouring lanes, so its maximum needs shuffles
+// only. w, and the backward's dw, of a thread's channels stay in registers; the
+// CTAs' partial sums of dw are added in a second launch (reduce.cu).
 // y is rounded once from fp32; y8 from the unrounded y.
 #include "ssm_common.cuh"
 
@@ -55,100 +56,123 @@ __device__ __forceinline__ float lanes_max(float v, int lanes) {
     return v;
 }
 
+// Eight values over `inv` as e4m3, stored.
+template <typename T> __device__ __forceinline__ void store_e4m3(unsigned char *dst, const float (&v)[8], float inv, bool whole) {
+    uint32_t *o = reinterpret_cast<uint32_t *>(dst);
+    const uint32_t a = e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    const uint32_t b = e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+    if (sizeof(T) == 2) {
+        *reinterpret_cast<uint2 *>(o) = make_uint2(a, b);
+    } else {
+        o[0] = a;
+        if (whole) o[1] = b;
+    }
+}
+__device__ __forceinline__ float scale_of(float top) { return top == 0.f ? 1.f : max_nan(top / kTop, 1.17549435e-38f); }
+
+// Rows in the forward's ring, and its threads on an SM (16384 x 4096 with 8-bit output, rows 2, 3, 4 at 768
+// threads: 75, 78, 81 us; at 1,024: 77, 87, 85).
+constexpr int kFwdRows = 2, kFwdThreads = 768;
+
+// Rows blockIdx.x, + gridDim.x, ...
 template <typename T, int VPT> __global__ void __launch_bounds__(kMost) rmsnorm_fwd_kernel(const NormParams p) {
-    __shared__ float s_sum[32], s_max[32];
+    extern __shared__ __align__(16) uint4 ring[];       // kFwdRows rows of x and res; a thread copies and reads its own
+    __shared__ float s_sum[2][32], s_max[2][32];
+    constexpr int H = sizeof(T) / 2, kRow = 2 * VPT * H;   // 16-byte pieces of a thread and row
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, nw = blockDim.x / 32;
-    const long row = blockIdx.x;
-    const T *x = static_cast<const T *>(p.x) + (size_t)row * p.D;
-    const T *res = p.res ? static_cast<const T *>(p.res) + (size_t)row * p.D : nullptr;
-
-    Raw8<T> rx[VPT], rr[VPT];
+    const int groups = p.group ? (p.D + p.group - 1) / p.group : 1;
+    auto issue = [&](long row, int stage) {
+        uint4 *dst = ring + (size_t)stage * kRow * blockDim.x + tid;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = (i * (int)blockDim.x + tid) * 8;
-        rx[i] = c < p.D ? raw_load(x + c, c + 8 <= p.D) : raw_zero<T>();
-        rr[i] = res && c < p.D ? raw_load(res + c, c + 8 <= p.D) : raw_zero<T>();
-    }
-    float v[VPT][8], ss = 0.f;
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (i * (int)blockDim.x + tid) * 8;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        float r[8];
-        raw_unpack(rx[i], v[i]);
-        raw_unpack(rr[i], r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (res) v[i][j] += r[j];
-            ss = fmaf(v[i][j], v[i][j], ss);
-        }
-    }
-    ss = warp_sum(ss);
-    if (nw > 1) {
-        if (lane == 0) s_sum[warp] = ss;
-        __syncthreads();
-        ss = warp_sum(lane < nw ? s_sum[lane] : 0.f);
-    }
-    const float rinv = rsqrtf(ss / (float)p.D + p.eps);
-
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = (i * (int)blockDim.x + tid) * 8;
-        const bool on = c < p.D, whole = c + 8 <= p.D;
-        if (p.s_out && on) store8(static_cast<T *>(p.s_out) + (size_t)row * p.D + c, v[i], whole);
-        float w[8];
-        param8(on ? p.w : nullptr, c, whole, w);
-        float m = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[i][j] *= rinv;
-            if (p.w) v[i][j] *= w[j];
-            if (!on) v[i][j] = 0.f;
-            m = max_nan(m, fabsf(v[i][j]));
-        }
-        if (p.y && on) store8(static_cast<T *>(p.y) + (size_t)row * p.D + c, v[i], whole);
-        if (p.y8 && p.group) {
-            m = lanes_max(m, p.group / 8);
-            const float scale = m == 0.f ? 1.f : max_nan(m / kTop, 1.17549435e-38f);
-            const float inv = 1.f / scale;
-            const int per = p.group / 8;             // lanes of a block
-            if (on && lane % per == 0)
-                p.scale[(size_t)row * ((p.D + p.group - 1) / p.group) + c / p.group] = scale;
-            if (on) {
-                uint32_t *o = reinterpret_cast<uint32_t *>(p.y8 + (size_t)row * p.D + c);
-                const uint32_t a = e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
-                const uint32_t b = e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
-                if (sizeof(T) == 2) {
-                    *reinterpret_cast<uint2 *>(o) = make_uint2(a, b);
-                } else {
-                    o[0] = a;
-                    if (whole) o[1] = b;
-                }
+            for (int h = 0; h < H; ++h) {
+                const bool in = row < p.rows && c + 4 * h < p.D;
+                const size_t at = in ? (size_t)row * p.D + c + 4 * h : 0;
+                copy_async<16>(dst + (2 * i * H + h) * blockDim.x, static_cast<const T *>(p.x) + at, in);
+                if (p.res) copy_async<16>(dst + ((2 * i + 1) * H + h) * blockDim.x, static_cast<const T *>(p.res) + at, in);
             }
         }
-        top = max_nan(top, m);
-    }
-    if (!p.y8 || p.group) return;
-    top = lanes_max(top, 32);
-    if (nw > 1) {
-        if (lane == 0) s_max[warp] = top;
-        __syncthreads();
-        top = lanes_max(lane < nw ? s_max[lane] : 0.f, 32);
-    }
-    const float scale = top == 0.f ? 1.f : max_nan(top / kTop, 1.17549435e-38f);
-    const float inv = 1.f / scale;
-    if (tid == 0) p.scale[row] = scale;
+        copies_commit();
+    };
+    auto held = [&](int stage, int k) {
+        Raw8<T> r;
+#pragma unroll
+        for (int h = 0; h < H; ++h) r.w[h] = ring[((size_t)stage * kRow + k * H + h) * blockDim.x + tid];
+        return r;
+    };
+    long row = blockIdx.x;
+#pragma unroll
+    for (int k = 0; k < kFwdRows - 1; ++k) issue(row + (long)k * gridDim.x, k);
+    float w[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (i * (int)blockDim.x + tid) * 8;
-        if (c >= p.D) break;
-        uint32_t *o = reinterpret_cast<uint32_t *>(p.y8 + (size_t)row * p.D + c);
-        const uint32_t a = e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
-        const uint32_t b = e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
-        if (sizeof(T) == 2) {
-            *reinterpret_cast<uint2 *>(o) = make_uint2(a, b);
-        } else {
-            o[0] = a;
-            if (c + 8 <= p.D) o[1] = b;
+        param8(p.w && c < p.D ? p.w : nullptr, c, c + 8 <= p.D, w[i]);
+        if (!p.w)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[i][j] = 1.f;
+    }
+    int par = 0, stage = 0;
+    for (; row < p.rows; row += gridDim.x, par ^= 1) {
+        copies_wait<kFwdRows - 2>();
+        float v[VPT][8], ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            raw_unpack(held(stage, 2 * i), v[i]);
+            if (p.res) {
+                float r[8];
+                raw_unpack(held(stage, 2 * i + 1), r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+        }
+        issue(row + (long)(kFwdRows - 1) * gridDim.x, stage == 0 ? kFwdRows - 1 : stage - 1);   // the row before's stage
+        stage = stage == kFwdRows - 1 ? 0 : stage + 1;
+        ss = warp_sum(ss);
+        if (nw > 1) {                                   // two buffers in turn: one barrier a sum
+            if (lane == 0) s_sum[par][warp] = ss;
+            __syncthreads();
+            ss = warp_sum(lane < nw ? s_sum[par][lane] : 0.f);
+        }
+        const float rinv = rsqrtf(ss / (float)p.D + p.eps);
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (i * (int)blockDim.x + tid) * 8;
+            const bool on = c < p.D, whole = c + 8 <= p.D;
+            const size_t at = (size_t)row * p.D + c;
+            if (p.s_out && on) store8(static_cast<T *>(p.s_out) + at, v[i], whole);
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[i][j] = on ? v[i][j] * rinv * w[i][j] : 0.f;   // (a lane past the end: its zeros, also where rinv is NaN)
+                m = max_nan(m, fabsf(v[i][j]));
+            }
+            if (p.y && on) store8(static_cast<T *>(p.y) + at, v[i], whole);
+            if (p.y8 && p.group) {
+                const float scale = scale_of(lanes_max(m, p.group / 8));
+                if (on && lane % (p.group / 8) == 0) p.scale[(size_t)row * groups + c / p.group] = scale;
+                if (on) store_e4m3<T>(p.y8 + at, v[i], 1.f / scale, whole);
+            }
+            top = max_nan(top, m);
+        }
+        if (!p.y8 || p.group) continue;
+        top = lanes_max(top, 32);
+        if (nw > 1) {
+            if (lane == 0) s_max[par][warp] = top;
+            __syncthreads();
+            top = lanes_max(lane < nw ? s_max[par][lane] : 0.f, 32);
+        }
+        const float scale = scale_of(top), inv = 1.f / scale;
+        if (tid == 0) p.scale[row] = scale;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (i * (int)blockDim.x + tid) * 8;
+            if (c < p.D) store_e4m3<T>(p.y8 + (size_t)row * p.D + c, v[i], inv, c + 8 <= p.D);
         }
     }
 }
@@ -265,11 +289,15 @@ int round32(int v) { return (v + 31) / 32 * 32; }
 template <typename T> cudaError_t fwd(const NormParams &p, cudaStream_t s, int *launches) {
     const int vecs = (p.D + 7) / 8;
     // Few rows: one vector a thread, the shortest chain. Many: two, so that a
-    // thread has four loads in flight and a row half the warps to exchange with.
+    // row has half the warps to exchange with.
     const int vpt = vecs > kMost || (p.rows > 2L * device_sm_count() && vecs > 32) ? 2 : 1;
     const int th = round32((vecs + vpt - 1) / vpt);
-    if (vpt == 1) rmsnorm_fwd_kernel<T, 1><<<(unsigned)p.rows, th, 0, s>>>(p);
-    else rmsnorm_fwd_kernel<T, 2><<<(unsigned)p.rows, th, 0, s>>>(p);
+    const long held = (long)(kFwdThreads / th > 16 ? 16 : kFwdThreads / th) * device_sm_count();
+    const int bytes = kFwdRows * 2 * vpt * th * 8 * (int)sizeof(T);
+    auto *kern = vpt == 1 ? rmsnorm_fwd_kernel<T, 1> : rmsnorm_fwd_kernel<T, 2>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)(p.rows < held ? p.rows : held), th, bytes, s>>>(p);
     if (launches) ++*launches;
     return cudaGetLastError();
 }
