@@ -28,6 +28,15 @@
 // steps; in the second launch each segment folds the ones before it,
 // h <- exp(A sum delta) h + h_local, and runs from there. No CTA waits on
 // another.
+//
+// Measured: 8 x 2048 x 2048 at N = 16, bf16 with the gate, 221 us (271 MB; the
+// exponentials and multiply-adds alone about 80 us): 55 instructions a token
+// and 16 channels, and seven warps an SM that issue every second clock. Packed
+// prompts of 16,024 tokens x 4,096 with the filter 614 us in two launches.
+// Slower: one channel a lane with 1, 2 or 4 lanes a channel (238 to 303 us), a
+// ring of asynchronous copies (no change: it does not wait for DRAM), a helper
+// warp for the elementwise work (227 to 268 us), two or three segments (268 to
+// 306 us).
 #include "ssm_common.cuh"
 
 namespace gla {

@@ -12,9 +12,9 @@
 //     over tokens:     dA = sum delta P,  dskip = sum dy' u,  ddt_bias = sum ddt;  dh0 = c_{-1}
 //
 // Two chains run against each other in time, so every state is needed once
-// more after the forward sweep has passed it. A CTA owns 32 W channels (a
-// quad of lanes four of them, each lane a quarter of their states) of one
-// segment of a sequence: it sweeps forward and leaves the state entering every
+// more after the forward sweep has passed it. A CTA of four warps owns 128
+// channels (a quad of lanes four of them, each lane a quarter of their states;
+// half as many at N = 32) of one segment of a sequence: it sweeps forward and leaves the state entering every
 // 16-token tile in the workspace (read back soon after, from L2), then takes
 // the tiles from the last to the first: forward through the tile, keeping the
 // state before every fourth token in shared memory, then for each four tokens,
@@ -31,6 +31,13 @@
 // leaves each segment's state from zero and its c from zero together, with one
 // exponential a state (c needs the running product of the decays), and the
 // second folds the segments before and behind its own.
+//
+// Bound by instructions: about 415 a token and 32 channels in the second launch
+// (four exponentials a state, 160 packed multiply-adds, 60 for the two kinds of
+// exchanges), 116 in the first. 4 x 2048 x 2048, N = 16: 518 us, of which the
+// second launch 404 at 45 % of the issue slots (two CTAs an SM: the states take
+// 253 registers; three with spills took 640), the first 98, the sums 16.
+// Loading a tile's inputs without copying them ahead cost another 200 us.
 #include "ssm_common.cuh"
 
 namespace gla {
@@ -44,7 +51,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 template <int K> struct Lane;      // K channels' numbers as one shared-memory access
 template <> struct Lane<2> {
-    using type = float2;
     static __device__ __forceinline__ void get(const float *p, float (&v)[2]) {
         const float2 u = *reinterpret_cast<const float2 *>(p);
         v[0] = u.x; v[1] = u.y;
@@ -456,6 +462,11 @@ __global__ void __launch_bounds__(S::TH, 2) ssm_bwd_kernel(const SsmBwdParams p,
             float y0[S::K];
 #pragma unroll
             for (int k = 0; k < S::K; ++k) y0[k] = quad_transpose_sum(pk[k], lane);
+            // past the end the step is 0, but 0 x inf would not be: no state there
+            if (t0 + 4 > left)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (t0 + j >= left) hs[j].zero();
             // back through them
             float pk2[S::K][4];
 #pragma unroll

@@ -1,6 +1,7 @@
 // ssm_common.cuh -- device helpers of the selective state-space kernels
-// (ssm.cu, ssm_step.cu, ssm_bwd.cu): fp32 pairs, the step's softplus and the
-// SiLU gate, and vectors of eight channels in either element type.
+// (ssm.cu, ssm_step.cu, ssm_bwd.cu), the Conv1d's gradients (conv_bwd.cu) and
+// the norm (rmsnorm.cu): fp32 pairs, the step's softplus and the SiLU gate,
+// asynchronous copies, and vectors of eight channels in either element type.
 #pragma once
 
 #include "common.cuh"

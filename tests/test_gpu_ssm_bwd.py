@@ -224,6 +224,19 @@ def test_nan_in_one_sequence_stays_there(gla):
     assert torch.isnan(got["dA"][3]).all() and not torch.isnan(got["dA"][4]).any()
 
 
+@pytest.mark.parametrize("T", [16, 21])
+def test_an_infinite_last_input_leaves_finite_what_does_not_depend_on_it(gla, T):
+    s = inputs((1, T), 16, 16, FP, 52)
+    dy, h0, dhT = extras(s, True, 9)
+    s["x"][0, T - 1, 3] = float("inf")
+    got = call(gla, s, dy, h0, dhT)
+    ref, _ = reference(s, dy, h0, dhT)
+    gla.gla_check()
+    for k in ("dA", "dx", "dh0"):                             # none reads the last state
+        assert torch.isfinite(ref[k]).all() and torch.isfinite(got[k]).all(), k
+    assert torch.isinf(got["dskip"][3]) and torch.isfinite(got["dskip"][:3]).all()
+
+
 def test_capture_beside_an_eager_call_and_another_stream(gla):
     s = inputs((1, 300), 64, 16, BF, 61)
     dy, h0, dhT = extras(s, True, 10)
