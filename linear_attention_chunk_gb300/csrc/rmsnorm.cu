@@ -286,6 +286,12 @@ template <typename T, int VPT> __global__ void __launch_bounds__(kMost) rmsnorm_
 
 int round32(int v) { return (v + 31) / 32 * 32; }
 
+// More than the default 48 KB (1 KB of them for the kernels' own arrays) has to be asked for.
+template <typename K> cudaError_t allow_smem(K *kern, int bytes) {
+    if (bytes <= 47 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 template <typename T> cudaError_t fwd(const NormParams &p, cudaStream_t s, int *launches) {
     const int vecs = (p.D + 7) / 8;
     // Few rows: one vector a thread, the shortest chain. Many: two, so that a
@@ -295,7 +301,7 @@ template <typename T> cudaError_t fwd(const NormParams &p, cudaStream_t s, int *
     const long held = (long)(kFwdThreads / th > 16 ? 16 : kFwdThreads / th) * device_sm_count();
     const int bytes = kFwdRows * 2 * vpt * th * 8 * (int)sizeof(T);
     auto *kern = vpt == 1 ? rmsnorm_fwd_kernel<T, 1> : rmsnorm_fwd_kernel<T, 2>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = allow_smem(kern, bytes);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)(p.rows < held ? p.rows : held), th, bytes, s>>>(p);
     if (launches) ++*launches;
@@ -311,7 +317,7 @@ template <typename T> cudaError_t bwd(const NormParams &p, cudaStream_t s, int *
     const unsigned grid = (unsigned)norm_bwd_grid(p.rows, p.D);
     const int bytes = (vpt == 1 ? ring_rows<T, 1>() : ring_rows<T, 2>()) * 3 * vpt * th * 8 * (int)sizeof(T);
     auto *kern = vpt == 1 ? rmsnorm_bwd_kernel<T, 1> : rmsnorm_bwd_kernel<T, 2>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = allow_smem(kern, bytes);
     if (e != cudaSuccess) return e;
     kern<<<grid, th, bytes, s>>>(p);
     if (launches) ++*launches;
