@@ -5,8 +5,8 @@
 // (dp past the sequence's end is 0; x before its first token is the window,
 // a constant).
 //
-// A stream: 6 bytes an element at bf16 (x, dy in, dx out): 403 MB in 82 us at
-// 8 x 2048 x 4096, 0.72 of the measured copy rate, the rest instructions. A thread owns four
+// A stream: 6 bytes an element at bf16 (x, dy in, dx out): 403 MB in 84 us
+// at 8 x 2048 x 4096 with the sums, 0.71 of the measured copy rate, the rest instructions. A thread owns four
 // channels over a tile of tokens and walks it forward with the last three x
 // and dp in registers, so dx lags three tokens behind, and reads three tokens
 // past the tile's end for it (the tile's own sums leave those out). The inputs
@@ -24,7 +24,7 @@ using namespace ssm;
 
 constexpr int kThreads = 128;   // 512 channels a CTA
 constexpr int kStep = 4, kStages = 4;   // tokens of a stage, stages of the ring
-constexpr int kMinBlocks = 4;   // measured at 8 x 2048 x 4096: 82 us, at 5 (spills) 108
+constexpr int kMinBlocks = 4;   // measured at 8 x 2048 x 4096: 84 us, at 5 (spills) 108
 static_assert(kStep >= 3, "a tile's first step covers the three tokens that dx lags behind");
 
 template <typename T> struct Raw4 {

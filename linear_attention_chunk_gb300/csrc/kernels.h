@@ -195,6 +195,7 @@ struct SumJob {
     long rows, cols, pitch;
     void *out;
     bool bf16;
+    int width;                   // columns of a CTA, where there are many rows
     unsigned block;              // its first block
 };
 struct SumJobs {

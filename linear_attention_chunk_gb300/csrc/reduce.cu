@@ -3,11 +3,12 @@
 // CTAs) of the first stage. In a fixed order, so results do not change from
 // call to call (atomics would). All of a call's sums are one launch.
 //
-// Up to 32 rows, a thread adds four columns down the rows (16-byte loads);
-// more rows, a CTA owns 32 columns and its 16 warps take every sixteenth row
-// (128 contiguous bytes each, eight loads in flight), added up through shared
-// memory: one thread a column would wait for its loads one after another
-// (608 rows of 2,048 columns).
+// Up to 32 rows, a thread adds four columns down the rows (16-byte loads).
+// More rows, a CTA owns 32 columns and its 16 warps take every sixteenth row
+// (128 contiguous bytes each), added up by shuffles and through shared memory.
+// Few columns and many rows, where such CTAs would leave most SMs idle and
+// wait for several rounds of loads: 8 columns and 64 groups of eight lanes, so that 456 rows are one round of loads (norm
+// gradients at 16384 x 2048: 51 -> 49 us; with 20,480 columns of 128 rows it cost 6 us).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -22,7 +23,7 @@ __device__ __forceinline__ void put(const SumJob &j, long c, float v) {
 }
 
 __global__ void __launch_bounds__(kThreads) sum_rows_kernel(const SumJobs jobs) {
-    __shared__ float s[kThreads / 32][33];
+    __shared__ float s[kThreads / 32][32];
     int k = 0;
     while (k + 1 < jobs.n && blockIdx.x >= jobs.j[k + 1].block) ++k;
     const SumJob &j = jobs.j[k];
@@ -46,23 +47,28 @@ __global__ void __launch_bounds__(kThreads) sum_rows_kernel(const SumJobs jobs) 
         return;
     }
     constexpr int W = kThreads / 32;
+    const int w = j.width, G = kThreads / w;   // columns, groups of lanes
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const long c = blk * 32 + lane;
+    const long c = blk * w + lane % w;
     float acc[8] = {};
     if (c < j.cols) {
         const float *p = j.part + c;
-        long r = warp;
-        for (; r + 7 * W < j.rows; r += 8 * W)
+        long r = threadIdx.x / w;
+        for (; r + 7 * G < j.rows; r += 8 * G)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] += __ldg(p + (size_t)(r + i * W) * j.pitch);
-        for (; r < j.rows; r += W) acc[0] += __ldg(p + (size_t)r * j.pitch);
+            for (int i = 0; i < 8; ++i) acc[i] += __ldg(p + (size_t)(r + i * G) * j.pitch);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (r + i * G < j.rows) acc[i] += __ldg(p + (size_t)(r + i * G) * j.pitch);
     }
-    s[warp][lane] = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+    float v = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+    for (int off = 16; off >= w; off /= 2) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (lane < w) s[warp][lane] = v;
     __syncthreads();
-    if (warp == 0 && c < j.cols) {
-        float v = 0.f;
+    if (threadIdx.x < w && c < j.cols) {
+        v = 0.f;
 #pragma unroll
-        for (int i = 0; i < W; ++i) v += s[i][lane];
+        for (int i = 0; i < W; ++i) v += s[i][threadIdx.x];
         put(j, c, v);
     }
 }
@@ -71,8 +77,9 @@ __global__ void __launch_bounds__(kThreads) sum_rows_kernel(const SumJobs jobs) 
 
 void SumJobs::add(const float *part, long rows, long cols, long pitch, void *out, bool bf16) {
     if (!out || cols == 0) return;
-    const long per = rows <= kFew ? 4L * kThreads : 32;
-    j[n] = SumJob{part, rows, cols, pitch, out, bf16, blocks};
+    const int width = cols < 64L * device_sm_count() && rows > 256 ? 8 : 32;   // (two CTAs of 32 columns an SM; two rounds of loads)
+    const long per = rows <= kFew ? 4L * kThreads : width;
+    j[n] = SumJob{part, rows, cols, pitch, out, bf16, width, blocks};
     blocks += (unsigned)((cols + per - 1) / per);
     ++n;
 }
