@@ -412,9 +412,9 @@ gla_status gla_conv1d_step(const void *x, const float *w, const float *b, float 
  *   [n_slots, 4, D], both fp32, at slots[n] (NULL: n), read and overwritten.
  *   Slots of one call are distinct. An empty sequence leaves its slot
  *   untouched; rows past the last sequence are left as they were. A bad entry
- *   (decreasing offset, offset past total_T, slot outside the pool) skips its
- *   sequence and the next gla_check() reports GLA_ERR_INVALID_ARG; where
- *   offsets decrease, other sequences may be skipped with it.
+ *   (negative offset, offset past total_T, slot outside the pool) skips its
+ *   sequence, a decreasing offset all of them, and the next gla_check()
+ *   reports GLA_ERR_INVALID_ARG.
  * gla_ssm_step: one token per sequence, rows [nseq, *], on the same pools and
  *   distinct slots; a bad slot skips its sequence likewise.
  * gla_ssm_fwd and gla_ssm_varlen cut sequences into segments that run in

@@ -84,6 +84,7 @@ __device__ __forceinline__ bool find_unit(const SsmParams &p, long u, int *s_fou
         const int slot = p.slots ? p.slots[n] : n;
         if (s < 0 || e < s || e > p.rows || slot < 0 || slot >= p.n_slots) {
             if (u == 0) atomicOr(p.status, kDevBadState);
+            if (e < s) atomicMin(s_found, -1);          // segments of several sequences would share slots: none runs
             continue;
         }
         const long b = s / p.L + n;
@@ -91,7 +92,7 @@ __device__ __forceinline__ bool find_unit(const SsmParams &p, long u, int *s_fou
     }
     __syncthreads();
     const int n = *s_found;
-    if (n >= p.nseq) return false;
+    if (n < 0 || n >= p.nseq) return false;
     un.seq = n;
     un.first = p.cu_seqlens[n];
     un.len = p.cu_seqlens[n + 1] - un.first;

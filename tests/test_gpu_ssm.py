@@ -234,6 +234,21 @@ def test_bad_entries_skip_their_sequence_and_are_reported(gla):
     gla.gla_check()                                         # reported once
 
 
+@pytest.mark.parametrize("cu", [[0, 1000, 0, 1000], [0, 20, 10, 1000], [500, 1000, 400, 300]])
+def test_decreasing_offsets_run_no_sequence(gla, cu):
+    """Overlapping sequences of several segments would mix in the workspace and in y: pools, windows and y
+    are left alone, and the error is reported."""
+    D, N = 24, 16
+    s = inputs((1000,), D, N, FP, 5)
+    pool, win, w, b = pools(3, D, N, 2)
+    p1, w1, y = pool.clone(), win.clone(), torch.full((1000, D), 7.0, device="cuda")
+    call_varlen(gla, s, i32(cu), p1, None, w, b, w1, y=y)
+    with pytest.raises(gla.GlaError) as e:
+        gla.gla_check()
+    assert e.value.status == gla.GLA_ERR_INVALID_ARG
+    assert torch.equal(p1, pool) and torch.equal(w1, win) and (y == 7).all()
+
+
 # ------------------------------------------------------------ single tokens
 def call_step(gla, s, pool, slots=None, w=None, b=None, win=None, **kw):
     return gla.gla_ssm_step(s["x"], s["dt"], s["A"], s["Bm"], s["Cm"], pool, s["skip"], s["z"], s["dt_bias"], slots,
