@@ -6,13 +6,14 @@
 // a constant).
 //
 // A stream: 6 bytes an element at bf16 (x, dy in, dx out): 403 MB in 84 us
-// at 8 x 2048 x 4096 with the sums, 0.71 of the measured copy rate, the rest instructions. A thread owns four
-// channels over a tile of tokens and walks it forward with the last three x
-// and dp in registers, so dx lags three tokens behind, and reads three tokens
-// past the tile's end for it (the tile's own sums leave those out). The inputs
-// come through a ring of asynchronous copies, twelve tokens ahead: each thread
-// copies and reads its own, so nothing waits for another. dw and db stay in registers and leave once
-// per tile as partial sums, added in a second launch (reduce.cu).
+// at 8 x 2048 x 4096 with the sums, 0.71 of the measured copy rate, the rest
+// instructions. A thread owns four channels over a tile of tokens and walks it
+// forward with the last three x and dp in registers, so dx lags three tokens
+// behind, and reads three tokens past the tile's end for it (the tile's own
+// sums leave those out). The inputs come through a ring of asynchronous
+// copies, twelve tokens ahead: each thread copies and reads its own, so
+// nothing waits for another. dw and db stay in registers and leave once per
+// tile as partial sums, added in a second launch (reduce.cu).
 #include <type_traits>
 
 #include "ssm_common.cuh"
@@ -59,7 +60,8 @@ __device__ __forceinline__ void store4(float *p, f2 a, f2 b) {
 }
 
 template <typename T> __global__ void __launch_bounds__(kThreads, kMinBlocks) conv_bwd_kernel(const ConvBwdParams p, int blocks, int tiles) {
-    __shared__ Raw4<T> ring[kStages * kStep * 2][kThreads];   // [token][x, dy][thread]
+    extern __shared__ __align__(16) unsigned char smem[];
+    Raw4<T> (*ring)[kThreads] = reinterpret_cast<Raw4<T> (*)[kThreads]>(smem);   // [stage][token][x, dy][thread]
     const int c = ((int)(blockIdx.x % (unsigned)blocks) * kThreads + threadIdx.x) * 4;
     const long unit = blockIdx.x / (unsigned)blocks;
     if (c >= p.D) return;
@@ -202,10 +204,14 @@ cudaError_t launch_conv_bwd(const ConvBwdParams &p, bool bf16, cudaStream_t s, i
     const int blocks = (p.D + 4 * kThreads - 1) / (4 * kThreads), tiles = (p.T + p.tile - 1) / p.tile;
     const long units = (long)p.B * tiles;
     if ((long double)units * blocks > 2147483647.0L) return cudaErrorInvalidValue;
-    if (bf16) conv_bwd_kernel<__nv_bfloat16><<<(unsigned)(units * blocks), kThreads, 0, s>>>(p, blocks, tiles);
-    else conv_bwd_kernel<float><<<(unsigned)(units * blocks), kThreads, 0, s>>>(p, blocks, tiles);
+    const int bytes = kStages * kStep * 2 * kThreads * 4 * (bf16 ? 2 : 4);   // 32 KB, 64 KB at fp32
+    auto *kern = bf16 ? conv_bwd_kernel<__nv_bfloat16> : conv_bwd_kernel<float>;
+    cudaError_t e = cudaSuccess;
+    if (bytes > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)(units * blocks), kThreads, bytes, s>>>(p, blocks, tiles);
     if (launches) ++*launches;
-    const cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     SumJobs sums;
     sums.add(p.part, units, 4L * p.D, 5L * p.D, p.dw);
