@@ -474,7 +474,7 @@ size_t gla_ssm_bwd_workspace_size(int B, int T, int D, int N, gla_dtype dtype);
  * gradient, and none comes from a later call through win_out. dx may not be
  * x or dy. workspace: at least gla_conv1d_bwd_workspace_size() bytes (partial
  * sums of dw and db; required when B*T > 0). Sums run in a fixed order: the
- * same call gives the same bits. B*T = 0 zeroes dw and db.
+ * same call gives the same bits. B*T = 0 zeroes dw and db. T <= 2^31 - 257.
  */
 gla_status gla_conv1d_bwd(const void *x, const float *w, const float *b, const void *dy, const float *win_in, int B,
                           int T, int D, gla_dtype dtype, void *dx, float *dw, float *db, void *workspace,
@@ -491,7 +491,8 @@ size_t gla_conv1d_bwd_workspace_size(int B, int T, int D, gla_dtype dtype);
  *   [rows, ceil(D / group)] fp32, the last block shorter) or 0 for one a row
  *   (scale [rows]). scale = max|y| / 448 over the block, at least 2^-126, and 1
  *   where every y is 0; a NaN in a block makes its scale NaN. y and y8 are each
- *   rounded once, from fp32. y and y8 may not overlap an input.
+ *   rounded once, from fp32. Squares are summed in fp32 (above 3e38 the sum is
+ *   infinite and y is 0). y and y8 may not overlap an input.
  * gla_rmsnorm_bwd: gradients of L = <dy, y> + <ds, s> with s given: with
  *   xn = s / sqrt(mean(s^2) + eps) and g = dy w,
  *     dx = ds + (g - xn mean(g xn)) / sqrt(mean(s^2) + eps)   (x's and res's alike)

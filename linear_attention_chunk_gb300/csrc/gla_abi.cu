@@ -101,6 +101,13 @@ gla_status check_conv_shape(int B, int T, int D, gla_dtype dtype) {
     return GLA_OK;
 }
 
+gla_status check_conv_bwd_shape(int B, int T, int D, gla_dtype dtype) {
+    const gla_status st = check_conv_shape(B, T, D, dtype);
+    if (st == GLA_OK && T > 2147483647 - 256)   // the kernel's token numbers, a tile and a step past the end, stay ints
+        return fail(GLA_ERR_INVALID_ARG, "T=%d is too long", T);
+    return st;
+}
+
 // The decode step with or without the mixer epilogue (g == NULL: plain o).
 gla_status decode_common(const void *q, const void *k, const void *v, const float *log_lambda, float *S_inout,
                          float scale, const void *g, const float *aug, const float *norm_w, float eps, int N,
@@ -698,7 +705,7 @@ gla_status gla_ssm_fwd(const void *x, int64_t ld_x, const void *dt, int64_t ld_d
                 nullptr, nullptr, h0, hT, nullptr, nullptr, nullptr, B, B, T, D, N, softplus, (long)B * T, y};
     if ((st = check_ssm_inputs(p, dtype)) != GLA_OK) return st;
     REQUIRE_PTR(y, "y");
-    if (y == x || y == dt || y == z) return fail(GLA_ERR_INVALID_ARG, "y may not alias an input");
+    if (y == x || y == dt || y == z || y == Bm || y == Cm) return fail(GLA_ERR_INVALID_ARG, "y may not alias an input");
     ssm_workspace(p, plan_ssm(B, p.rows, D, false), workspace, workspace_bytes, false);
     e = launch_ssm_scan(p, dtype == GLA_BF16, s, &launches);
     t_launches = launches;
@@ -730,7 +737,7 @@ gla_status gla_ssm_varlen(const void *x, int64_t ld_x, const void *dt, int64_t l
     if (total_T == 0) return GLA_OK;   // every sequence is empty: no state changes
     if ((st = check_ssm_inputs(p, dtype)) != GLA_OK) return st;
     REQUIRE_PTR(y, "y");
-    if (y == x || y == dt || y == z) return fail(GLA_ERR_INVALID_ARG, "y may not alias an input");
+    if (y == x || y == dt || y == z || y == Bm || y == Cm) return fail(GLA_ERR_INVALID_ARG, "y may not alias an input");
     if ((st = status_word(&p.status)) != GLA_OK) return st;
     ssm_workspace(p, plan_ssm(nseq, total_T, D, true), workspace, workspace_bytes, true);
     int launches = 0;
@@ -760,7 +767,7 @@ gla_status gla_ssm_step(const void *x, int64_t ld_x, const void *dt, int64_t ld_
     if ((st = check_ssm_pools(p)) != GLA_OK) return st;
     if ((st = check_ssm_inputs(p, dtype)) != GLA_OK) return st;
     REQUIRE_PTR(y, "y");
-    if (y == x || y == dt || y == z) return fail(GLA_ERR_INVALID_ARG, "y may not alias an input");
+    if (y == x || y == dt || y == z || y == Bm || y == Cm) return fail(GLA_ERR_INVALID_ARG, "y may not alias an input");
     if ((st = status_word(&p.status)) != GLA_OK) return st;
     int launches = 0;
     const cudaError_t e = launch_ssm_step(p, dtype == GLA_BF16, static_cast<cudaStream_t>(stream), &launches);
@@ -834,7 +841,7 @@ gla_status gla_ssm_bwd(const void *x, int64_t ld_x, const void *dt, int64_t ld_d
 }
 
 size_t gla_conv1d_bwd_workspace_size(int B, int T, int D, gla_dtype dtype) {
-    if (check_conv_shape(B, T, D, dtype) != GLA_OK || B == 0 || T == 0) return 0;
+    if (check_conv_bwd_shape(B, T, D, dtype) != GLA_OK || B == 0 || T == 0) return 0;
     const int tile = conv_bwd_tile(B, T, D);
     return (size_t)B * ((T + tile - 1) / tile) * 5 * D * sizeof(float);
 }
@@ -844,7 +851,7 @@ gla_status gla_conv1d_bwd(const void *x, const float *w, const float *b, const v
                           size_t workspace_bytes, void *stream) {
     t_err[0] = 0;
     t_launches = 0;
-    gla_status st = check_conv_shape(B, T, D, dtype);
+    gla_status st = check_conv_bwd_shape(B, T, D, dtype);
     if (st != GLA_OK) return st;
     OPTIONAL_PTR(b, "b");
     OPTIONAL_PTR(win_in, "win_in");

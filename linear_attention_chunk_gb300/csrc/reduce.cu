@@ -7,8 +7,9 @@
 // More rows, a CTA owns 32 columns and its 16 warps take every sixteenth row
 // (128 contiguous bytes each), added up by shuffles and through shared memory.
 // Few columns and many rows, where such CTAs would leave most SMs idle and
-// wait for several rounds of loads: 8 columns and 64 groups of eight lanes, so that 456 rows are one round of loads (norm
-// gradients at 16384 x 2048: 51 -> 49 us; with 20,480 columns of 128 rows it cost 6 us).
+// wait for several rounds of loads: 8 columns and 64 groups of eight lanes, so
+// that 456 rows are one round of loads (norm gradients at 16384 x 2048: 51 ->
+// 49 us; with 20,480 columns of 128 rows it cost 6 us).
 #include "common.cuh"
 #include "kernels.h"
 

@@ -14,12 +14,13 @@
 // Two chains run against each other in time, so every state is needed once
 // more after the forward sweep has passed it. A CTA of four warps owns 128
 // channels (a quad of lanes four of them, each lane a quarter of their states;
-// half as many at N = 32) of one segment of a sequence: it sweeps forward and leaves the state entering every
-// 16-token tile in the workspace (read back soon after, from L2), then takes
-// the tiles from the last to the first: forward through the tile, keeping the
-// state before every fourth token in shared memory, then for each four tokens,
-// last first, the four states again in registers (64 of them) with y0 and dC
-// on the way, and back through them with G. States are thus recomputed, never
+// half as many at N = 32) of one segment of a sequence: it sweeps forward and
+// leaves the state entering every 16-token tile in the workspace (read back
+// soon after, from L2), then takes the tiles from the last to the first:
+// forward through the tile, keeping the state before every fourth token in
+// shared memory, then for each four tokens, last first, the four states again
+// in registers (64 of them) with y0 and dC on the way, and back through them
+// with G. States are thus recomputed, never
 // stored per token (64 bytes a token and channel) nor divided back.
 // Sums over states are exchanged inside a quad, four tokens at a time; sums
 // over channels between the quads, eight numbers over eight quads, then added
@@ -36,7 +37,7 @@
 // (four exponentials a state, 160 packed multiply-adds, 60 for the two kinds of
 // exchanges), 116 in the first. 4 x 2048 x 2048, N = 16: 518 us, of which the
 // second launch 404 at 45 % of the issue slots (two CTAs an SM: the states take
-// 253 registers; three with spills took 640), the first 98, the sums 16.
+// 244 registers; three with spills took 640), the first 98, the sums 16.
 // Loading a tile's inputs without copying them ahead cost another 200 us.
 #include "ssm_common.cuh"
 
@@ -670,7 +671,7 @@ size_t plan_ssm_bwd(SsmBwdParams &p, float *ws) {
     if (L < kLeast) L = kLeast;
     p.L = L;
     p.nseg = (int)((p.T + L - 1) / L);
-    p.tiles = (p.T + kTile - 1) / kTile;
+    p.tiles = (int)(((long)p.T + kTile - 1) / kTile);
     const size_t plane = (size_t)p.D * p.N, units = (size_t)p.B * p.nseg, blocks = (p.D + bwd_channels(p.N) - 1) / bwd_channels(p.N);
     size_t at = 0;
     auto take = [&](float *&dst, size_t floats) {
