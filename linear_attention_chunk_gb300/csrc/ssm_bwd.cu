@@ -14,30 +14,30 @@
 // Two chains run against each other in time, so every state is needed once
 // more after the forward sweep has passed it. A CTA of four warps owns 128
 // channels (a quad of lanes four of them, each lane a quarter of their states;
-// half as many at N = 32) of one segment of a sequence: it sweeps forward and
-// leaves the state entering every 16-token tile in the workspace (read back
-// soon after, from L2), then takes the tiles from the last to the first:
+// half as many at N = 32) of one segment of a sequence. A first launch sweeps
+// the segment forward from zero and leaves the state entering every 16-token
+// tile, and the sum of its steps so far, in the workspace; with the state h
+// that enters the segment, tile_h + exp(A tile_sum) h is the state entering
+// the tile. The second launch takes the tiles from the last to the first:
 // forward through the tile, keeping the state before every fourth token in
 // shared memory, then for each four tokens, last first, the four states again
 // in registers (64 of them) with y0 and dC on the way, and back through them
-// with G. States are thus recomputed, never
-// stored per token (64 bytes a token and channel) nor divided back.
+// with G. States are thus recomputed, never stored per token (64 bytes a token
+// and channel) nor divided back.
 // Sums over states are exchanged inside a quad, four tokens at a time; sums
 // over channels between the quads, eight numbers over eight quads, then added
-// over the warps of the CTA through shared memory and over CTAs in a second
+// over the warps of the CTA through shared memory and over CTAs in a last
 // launch, in a fixed order. The elementwise ends (loads, SiLU, softplus, the
 // products above) are vectors of eight channels a thread, as in the forward.
 //
-// Few sequences are cut into segments as in the forward: a first launch
-// leaves each segment's state from zero and its c from zero together, with one
-// exponential a state (c needs the running product of the decays), and the
-// second folds the segments before and behind its own.
+// Few sequences are cut into segments as in the forward: the first launch then
+// leaves each segment's state from zero and its c from zero too, with the same
+// exponentials (c needs the running product of the decays), and the second
+// folds the segments before and behind its own.
 //
-// Bound by instructions: about 415 a token and 32 channels in the second launch
-// (four exponentials a state, 160 packed multiply-adds, 60 for the two kinds of
-// exchanges), 116 in the first. 4 x 2048 x 2048, N = 16: 518 us, of which the
-// second launch 404 at 45 % of the issue slots (two CTAs an SM: the states take
-// 244 registers; three with spills took 640), the first 98, the sums 16.
+// Bound by instructions. 4 x 2048 x 2048, N = 16: 482 us. Sweeping the segment
+// again in the second launch instead of keeping the first's states: 513. Two
+// CTAs an SM: the states take 234 registers; three with spills took 640.
 // Loading a tile's inputs without copying them ahead cost another 200 us.
 #include "ssm_common.cuh"
 
@@ -255,9 +255,11 @@ __device__ __forceinline__ void advance(State<S> &h, const State<S> &a2, const f
 }
 
 // ------------------------------------------------------------ first launch
-// Of every segment: the state it ends in from zero (seg_h), the c that leaves
-// its first token from zero (seg_g), and the sum of its steps.
-template <typename T, class S>
+// Of every tile: the state entering it, from zero at the segment's start, and
+// the sum of the steps since (tile_h, tile_sum). With kCut (several segments a
+// sequence), of every segment: the state it ends in from zero (seg_h), the c
+// that leaves its first token from zero (seg_g), and the sum of its steps.
+template <typename T, class S, bool kCut>
 __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_local_kernel(const SsmBwdParams p, int tiles) {
     extern __shared__ __align__(16) float smem[];
     float *sD = smem, *sU = sD + S::kRow, *sG = sU + S::kRow, *sB = sG + S::kRow, *sC = sB + kTile * S::N;
@@ -284,37 +286,48 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_local_kernel(const SsmBwdPar
 #pragma unroll
         for (int i = 0; i < S::P; ++i) pr.v[k][i] = f2_pack(1.f, 1.f);
     float sum[S::K] = {};
+    auto enter = [&](size_t tile) {
+        if (!on) return;
+        h.store(p.tile_h + tile * p.D * S::N + cell);
+        if (q == 0) Lane<S::K>::put(p.tile_sum + tile * p.D + ch, sum);
+    };
     const Ring<T, S> ring(p, smem + S::kLocal);
-    ring.template issue<true>(p, w, row0, ntok, 0);
-    for (int t0 = 0; t0 < ntok; t0 += kTile) {
+    const size_t first = (size_t)b * p.tiles + (size_t)seg * p.L / kTile;   // of the segment's tiles
+    const int end = kCut ? ntok : ntok - kTile;                             // not cut: only what enters the last tile
+    ring.template issue<kCut>(p, w, row0, ntok, 0);
+    for (int t0 = 0; t0 < end; t0 += kTile) {
         copies_wait<0>();
-        ring.template take<true>(p, w, row0 + t0, ntok - t0, 0, sD, sU, sG, sB, bias);
-        if (t0 + kTile < ntok) ring.template issue<true>(p, w, row0 + t0 + kTile, ntok - t0 - kTile, 0);
+        ring.template take<kCut>(p, w, row0 + t0, ntok - t0, 0, sD, sU, sG, sB, bias);
+        if (t0 + kTile < end) ring.template issue<kCut>(p, w, row0 + t0 + kTile, ntok - t0 - kTile, 0);
+        if (t0 > 0) enter(first + t0 / kTile);
         __syncthreads();
 #pragma unroll 2
         for (int t = 0; t < kTile; ++t) {
             float d[S::K], u[S::K], g[S::K];
             Lane<S::K>::get(sD + t * S::RS + lc, d);
             Lane<S::K>::get(sU + t * S::RS + lc, u);
-            Lane<S::K>::get(sG + t * S::RS + lc, g);
+            if (kCut) Lane<S::K>::get(sG + t * S::RS + lc, g);
             const f2 *bb = reinterpret_cast<const f2 *>(sB + t * S::N + q * S::SP);
             const f2 *cc = reinterpret_cast<const f2 *>(sC + t * S::N + q * S::SP);
 #pragma unroll
             for (int k = 0; k < S::K; ++k) {
-                const f2 dd = f2_pack(d[k], d[k]), uu = f2_pack(u[k], u[k]), gg = f2_pack(g[k], g[k]);
+                const f2 dd = f2_pack(d[k], d[k]), uu = f2_pack(u[k], u[k]), gg = kCut ? f2_pack(g[k], g[k]) : 0;
                 sum[k] += d[k];
 #pragma unroll
                 for (int i = 0; i < S::P; ++i) {
                     const f2 a = ex2_pair(mul2(dd, a2.v[k][i]));
                     h.v[k][i] = fma2(a, h.v[k][i], mul2(uu, bb[i]));
-                    pr.v[k][i] = mul2(pr.v[k][i], a);
-                    c.v[k][i] = fma2(pr.v[k][i], mul2(gg, cc[i]), c.v[k][i]);
+                    if (kCut) {
+                        pr.v[k][i] = mul2(pr.v[k][i], a);
+                        c.v[k][i] = fma2(pr.v[k][i], mul2(gg, cc[i]), c.v[k][i]);
+                    }
                 }
             }
         }
         __syncthreads();
     }
-    if (on) {
+    if (!kCut) enter(first + end / kTile + (end % kTile > 0));
+    if (kCut && on) {
         h.store(p.seg_h + (size_t)unit * p.D * S::N + cell);
         c.store(p.seg_g + (size_t)unit * p.D * S::N + cell);
         if (q == 0)
@@ -363,32 +376,55 @@ __global__ void __launch_bounds__(S::TH, 2) ssm_bwd_kernel(const SsmBwdParams p,
                 for (int i = 0; i < S::P; ++i) s.v[k][i] = fma2(ex2_pair(mul2(dd, a2.v[k][i])), s.v[k][i], e.v[k][i]);
             }
         };
+#pragma unroll 4
         for (int s = 0; s < seg; ++s) fold(h, p.seg_h, (size_t)(unit - seg + s));
+#pragma unroll 4
         for (int s = p.nseg - 1; s > seg; --s) fold(c, p.seg_g, (size_t)(unit - seg + s));
     }
 
-    // ---- forward sweep: the state entering every tile
-    float *tile_h = p.tile_h + ((size_t)b * p.tiles + (size_t)seg * p.L / kTile) * plane + cell;
+    const size_t first = (size_t)b * p.tiles + (size_t)seg * p.L / kTile;   // of the segment's tiles
     const Ring<T, S> ring(p, smem + S::kMain);
-    if (ntile > 1) ring.template issue<false>(p, w, row0, kTile, 0);
-    for (int i = 0; i + 1 < ntile; ++i) {
-        if (on) h.store(tile_h + (size_t)i * plane);
-        copies_wait<0>();
-        ring.template take<false>(p, w, row0 + i * kTile, kTile, 0, sD, sU, nullptr, sB, bias);
-        if (i + 2 < ntile) ring.template issue<false>(p, w, row0 + (i + 1) * kTile, kTile, 0);
-        __syncthreads();
-#pragma unroll 2
-        for (int t = 0; t < kTile; ++t) advance<S>(h, a2, sD + t * S::RS + lc, sU + t * S::RS + lc, sB + t * S::N + q * S::SP);
-        __syncthreads();
-    }
-
     f2 skip[4], dskip[4] = {}, dbias[4] = {};
     param8(w.on ? p.skip : nullptr, w.c, w.whole, skip);
     State<S> dA;
     dA.zero();
     f2 *ck = sH + (size_t)warp * 3 * S::K * S::P * 32 + lane;
     float *myP = sP + warp * 2 * kTile * S::N;
-
+    auto keep = [&](int s, const State<S> &v) {
+#pragma unroll
+        for (int k = 0; k < S::K; ++k)
+#pragma unroll
+            for (int j = 0; j < S::P; ++j) ck[(s * S::K * S::P + k * S::P + j) * 32] = v.v[k][j];
+    };
+    auto kept_state = [&](int s, State<S> &v) {
+#pragma unroll
+        for (int k = 0; k < S::K; ++k)
+#pragma unroll
+            for (int j = 0; j < S::P; ++j) v.v[k][j] = ck[(s * S::K * S::P + k * S::P + j) * 32];
+    };
+    // The state entering a tile is exp(A tile_sum) h + tile_h, h the one
+    // entering the segment. The three wait in the lane's own places: copied
+    // there while the tile behind is finished, h out of the workspace (the
+    // fence: it is read back as if by another thread).
+    auto entering = [&](int i) {
+        const bool in = on && i > 0;                    // tile 0: h itself
+        const size_t tile = first + i;
+        const float *src = in ? p.tile_h + tile * plane + cell : p.tile_h, *hin = on ? p.seg_in + (size_t)unit * plane + cell : p.seg_in;
+        const float *sum = in ? p.tile_sum + tile * p.D + ch : p.tile_sum;
+#pragma unroll
+        for (int k = 0; k < S::K; k += 2) copy_async<8>(ck + k / 2 * 32, in ? sum + k : sum, in);   // in the first place
+#pragma unroll
+        for (int k = 0; k < S::K; ++k)
+#pragma unroll
+            for (int j = 0; j < S::P; ++j) {
+                copy_async<8>(ck + (2 * S::K * S::P + k * S::P + j) * 32, in ? src + k * S::N + 2 * j : src, in);
+                copy_async<8>(ck + (S::K * S::P + k * S::P + j) * 32, on ? hin + k * S::N + 2 * j : hin, on);
+            }
+        copies_commit();
+    };
+    if (on) h.store(p.seg_in + (size_t)unit * plane + cell);
+    __threadfence();
+    entering(ntile - 1);
     int stage = 0;
     ring.template issue<true>(p, w, row0 + (long)(ntile - 1) * kTile, ntok - (ntile - 1) * kTile, stage);
     for (int i = ntile - 1; i >= 0; --i) {
@@ -399,17 +435,25 @@ __global__ void __launch_bounds__(S::TH, 2) ssm_bwd_kernel(const SsmBwdParams p,
         const int kept = stage;
         if (Ring<T, S>::kStages == 2) stage ^= 1;
         if (i > 0) ring.template issue<true>(p, w, tr - kTile, kTile, stage);
-        if (i + 1 < ntile && on) h.load(tile_h + (size_t)i * plane);
         __syncthreads();
         // ---- forward through the tile's first twelve tokens
         State<S> hs[4];
-        hs[0] = h;
+        {
+            State<S> in;
+            kept_state(2, hs[0]);
+            kept_state(1, in);
+#pragma unroll
+            for (int k = 0; k < S::K; ++k) {
+                const float2 pair = f2_split(ck[k / 2 * 32]);
+                const f2 sum = both(k % 2 ? pair.y : pair.x);
+#pragma unroll
+                for (int j = 0; j < S::P; ++j)
+                    hs[0].v[k][j] = fma2(ex2_pair(mul2(sum, a2.v[k][j])), in.v[k][j], hs[0].v[k][j]);
+            }
+        }
 #pragma unroll
         for (int s = 0; s < 3; ++s) {
-#pragma unroll
-            for (int k = 0; k < S::K; ++k)
-#pragma unroll
-                for (int j = 0; j < S::P; ++j) ck[(s * S::K * S::P + k * S::P + j) * 32] = hs[0].v[k][j];
+            keep(s, hs[0]);
 #pragma unroll
             for (int t = 4 * s; t < 4 * s + 4; ++t)
                 advance<S>(hs[0], a2, sD + t * S::RS + lc, sU + t * S::RS + lc, sB + t * S::N + q * S::SP);
@@ -417,11 +461,8 @@ __global__ void __launch_bounds__(S::TH, 2) ssm_bwd_kernel(const SsmBwdParams p,
         // ---- four tokens at a time, the last first
 #pragma unroll 1
         for (int s = 3; s >= 0; --s) {
-            if (s < 3)
-#pragma unroll
-                for (int k = 0; k < S::K; ++k)
-#pragma unroll
-                    for (int j = 0; j < S::P; ++j) hs[0].v[k][j] = ck[(s * S::K * S::P + k * S::P + j) * 32];
+            if (s < 3) kept_state(s, hs[0]);
+            if (s == 0 && i > 0) entering(i - 1);       // (the places have been read)
             const int t0 = 4 * s;
             float pk[S::K][4];                          // a sum over states, per channel and token
             float pn[8];                                // a sum over channels, per token and state
@@ -616,11 +657,11 @@ template <typename T, int N> cudaError_t run(const SsmBwdParams &p, cudaStream_t
     const long units = (long)p.B * p.nseg;
     if ((long double)units * tiles > 2147483647.0L) return cudaErrorInvalidValue;
     cudaError_t e;
-    if (p.nseg > 1) {
+    if (p.T > kTile) {
         constexpr int bytes = (S::kLocal + Ring<T, S>::kFloats) * (int)sizeof(float);
-        if ((e = cudaFuncSetAttribute(ssm_bwd_local_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
-            return e;
-        ssm_bwd_local_kernel<T, S><<<(unsigned)(units * tiles), S::TH, bytes, s>>>(p, tiles);
+        auto *kern = p.nseg > 1 ? ssm_bwd_local_kernel<T, S, true> : ssm_bwd_local_kernel<T, S, false>;
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+        kern<<<(unsigned)(units * tiles), S::TH, bytes, s>>>(p, tiles);
         if (launches) ++*launches;
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
@@ -681,7 +722,9 @@ size_t plan_ssm_bwd(SsmBwdParams &p, float *ws) {
     take(p.seg_h, p.nseg > 1 ? units * plane : 0);
     take(p.seg_g, p.nseg > 1 ? units * plane : 0);
     take(p.seg_sum, p.nseg > 1 ? units * p.D : 0);
+    take(p.seg_in, units * plane);
     take(p.tile_h, (size_t)p.B * p.tiles * plane);
+    take(p.tile_sum, (size_t)p.B * p.tiles * p.D);
     take(p.part_a, units * plane);
     take(p.part_v, units * 2 * p.D);
     take(p.part_b, blocks * p.B * p.T * p.N);
