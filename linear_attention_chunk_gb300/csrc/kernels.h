@@ -152,7 +152,7 @@ struct SsmBwdParams {
     float *dA, *dskip, *ddt_bias, *dh0;
     long L;
     int nseg, tiles;
-    float *seg_h, *seg_g, *seg_sum, *seg_in, *tile_h, *tile_sum, *part_a, *part_v, *part_b, *part_c;
+    float *seg_h, *seg_g, *seg_sum, *tile_h, *tile_sum, *part_a, *part_v, *part_b, *part_c;
 };
 size_t plan_ssm_bwd(SsmBwdParams &p, float *ws);
 cudaError_t launch_ssm_bwd(const SsmBwdParams &p, bool bf16, cudaStream_t s, int *launches);

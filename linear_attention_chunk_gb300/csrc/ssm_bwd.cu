@@ -18,7 +18,7 @@
 // the segment forward from zero and leaves the state entering every 16-token
 // tile, and the sum of its steps so far, in the workspace; with the state h
 // that enters the segment, tile_h + exp(A tile_sum) h is the state entering
-// the tile. The second launch takes the tiles from the last to the first:
+// the tile. The main launch takes the tiles from the last to the first:
 // forward through the tile, keeping the state before every fourth token in
 // shared memory, then for each four tokens, last first, the four states again
 // in registers (64 of them) with y0 and dC on the way, and back through them
@@ -32,13 +32,18 @@
 //
 // Few sequences are cut into segments as in the forward: the first launch then
 // leaves each segment's state from zero and its c from zero too, with the same
-// exponentials (c needs the running product of the decays), and the second
-// folds the segments before and behind its own.
+// exponentials (c needs the running product of the decays), and a small launch
+// carries both from segment to segment.
 //
-// Bound by instructions. 4 x 2048 x 2048, N = 16: 482 us. Sweeping the segment
-// again in the second launch instead of keeping the first's states: 513. Two
-// CTAs an SM: the states take 234 registers; three with spills took 640.
-// Loading a tile's inputs without copying them ahead cost another 200 us.
+// Bound by instructions and, at two CTAs an SM, by their latency: 4 x 2048 x
+// 2048, N = 16: 451 us, of which the main launch about 320 at 46 % of the issue
+// slots (370 instructions a token and 32 channels), the first 105 (its
+// multiply-adds alone 60), the sums 16. Each CTA folding the segments itself:
+// 482; sweeping the segment again instead of keeping the first launch's states:
+// 513. The states take 250 registers; three CTAs with spills took 640. Loading
+// a tile's inputs without copying them ahead cost another 200 us. States paired
+// over channels instead of over N, so that no step or input has to be copied
+// into both halves of a pair: as many instructions, and more of shared memory.
 #include "ssm_common.cuh"
 
 namespace gla {
@@ -47,7 +52,7 @@ namespace {
 using namespace ssm;
 
 constexpr int kTile = 16;          // tokens per tile
-constexpr int kWarps = 4;
+constexpr int kWarps = 4, kFoldThreads = 128;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int K> struct Lane;      // K channels' numbers as one shared-memory access
@@ -301,7 +306,7 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_local_kernel(const SsmBwdPar
         if (t0 + kTile < end) ring.template issue<kCut>(p, w, row0 + t0 + kTile, ntok - t0 - kTile, 0);
         if (t0 > 0) enter(first + t0 / kTile);
         __syncthreads();
-#pragma unroll 2
+#pragma unroll 4
         for (int t = 0; t < kTile; ++t) {
             float d[S::K], u[S::K], g[S::K];
             Lane<S::K>::get(sD + t * S::RS + lc, d);
@@ -336,7 +341,45 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_local_kernel(const SsmBwdPar
     }
 }
 
-// ----------------------------------------------------------- second launch
+// ------------------------------------------------- between them, when cut
+// From what the segments do from zero, the state entering each of them (in
+// seg_h's place; blockIdx.y 0) and the c entering it from behind (in seg_g's
+// place; 1). Two states a thread; the loads of kAhead segments at once.
+template <int N> __global__ void __launch_bounds__(kFoldThreads) ssm_bwd_fold_kernel(const SsmBwdParams p) {
+    constexpr int kAhead = 8;
+    const long pairs = (long)p.D * N / 2, i = (long)blockIdx.x * kFoldThreads + threadIdx.x;
+    if (i >= p.B * pairs) return;
+    const long b = i / pairs, e = i % pairs * 2;
+    const size_t plane = (size_t)p.D * N;
+    const bool back = blockIdx.y;
+    const float *first = back ? p.dhT : p.h0;
+    float *seg = (back ? p.seg_g : p.seg_h) + b * p.nseg * plane + e;
+    const float *sums = p.seg_sum + b * p.nseg * p.D + e / N;
+    const float2 a = *reinterpret_cast<const float2 *>(p.A + e);
+    const float2 v0 = first ? *reinterpret_cast<const float2 *>(first + b * plane + e) : make_float2(0.f, 0.f);
+    const f2 a2 = f2_pack(a.x * kLog2e, a.y * kLog2e);
+    f2 v = f2_pack(v0.x, v0.y);
+    for (int s = 0; s < p.nseg; s += kAhead) {
+        float2 own[kAhead];
+        float sum[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (s + k >= p.nseg) break;
+            const long u = back ? p.nseg - 1 - s - k : s + k;
+            own[k] = *reinterpret_cast<const float2 *>(seg + u * plane);
+            sum[k] = sums[u * p.D];
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (s + k >= p.nseg) break;
+            const long u = back ? p.nseg - 1 - s - k : s + k;
+            *reinterpret_cast<float2 *>(seg + u * plane) = f2_split(v);
+            v = fma2(ex2_pair(mul2(both(sum[k]), a2)), v, f2_pack(own[k].x, own[k].y));
+        }
+    }
+}
+
+// ------------------------------------------------------------ last launch
 template <typename T, class S>
 __global__ void __launch_bounds__(S::TH, 2) ssm_bwd_kernel(const SsmBwdParams p, int tiles) {
     extern __shared__ __align__(16) float smem[];
@@ -357,29 +400,15 @@ __global__ void __launch_bounds__(S::TH, 2) ssm_bwd_kernel(const SsmBwdParams p,
     f2 bias[4];
     param8(w.on ? p.dt_bias : nullptr, w.c, w.whole, bias);
 
-    State<S> a2, h, c;
+    // the state entering the segment and the c entering it from behind
+    const float *hin = p.nseg > 1 ? p.seg_h + (size_t)unit * plane : p.h0 ? p.h0 + (size_t)b * plane : nullptr;
+    const float *cin = p.nseg > 1 ? p.seg_g + (size_t)unit * plane : p.dhT ? p.dhT + (size_t)b * plane : nullptr;
+    State<S> a2, c;
     a2.zero();
-    h.zero();
     c.zero();
     if (on) {
         a2.load(p.A + cell, kLog2e);
-        if (p.h0) h.load(p.h0 + (size_t)b * plane + cell);
-        if (p.dhT) c.load(p.dhT + (size_t)b * plane + cell);
-        auto fold = [&](State<S> &s, const float *seg_s, size_t u) {
-            State<S> e;
-            e.load(seg_s + u * plane + cell);
-#pragma unroll
-            for (int k = 0; k < S::K; ++k) {
-                const float d = p.seg_sum[u * p.D + ch + k];
-                const f2 dd = f2_pack(d, d);
-#pragma unroll
-                for (int i = 0; i < S::P; ++i) s.v[k][i] = fma2(ex2_pair(mul2(dd, a2.v[k][i])), s.v[k][i], e.v[k][i]);
-            }
-        };
-#pragma unroll 4
-        for (int s = 0; s < seg; ++s) fold(h, p.seg_h, (size_t)(unit - seg + s));
-#pragma unroll 4
-        for (int s = p.nseg - 1; s > seg; --s) fold(c, p.seg_g, (size_t)(unit - seg + s));
+        if (cin) c.load(cin + cell);
     }
 
     const size_t first = (size_t)b * p.tiles + (size_t)seg * p.L / kTile;   // of the segment's tiles
@@ -403,13 +432,13 @@ __global__ void __launch_bounds__(S::TH, 2) ssm_bwd_kernel(const SsmBwdParams p,
             for (int j = 0; j < S::P; ++j) v.v[k][j] = ck[(s * S::K * S::P + k * S::P + j) * 32];
     };
     // The state entering a tile is exp(A tile_sum) h + tile_h, h the one
-    // entering the segment. The three wait in the lane's own places: copied
-    // there while the tile behind is finished, h out of the workspace (the
-    // fence: it is read back as if by another thread).
+    // entering the segment. The three wait in the lane's own places, copied
+    // there while the tile behind is finished.
     auto entering = [&](int i) {
         const bool in = on && i > 0;                    // tile 0: h itself
         const size_t tile = first + i;
-        const float *src = in ? p.tile_h + tile * plane + cell : p.tile_h, *hin = on ? p.seg_in + (size_t)unit * plane + cell : p.seg_in;
+        const bool h_on = on && hin;
+        const float *src = in ? p.tile_h + tile * plane + cell : p.tile_h, *h = h_on ? hin + cell : p.tile_h;
         const float *sum = in ? p.tile_sum + tile * p.D + ch : p.tile_sum;
 #pragma unroll
         for (int k = 0; k < S::K; k += 2) copy_async<8>(ck + k / 2 * 32, in ? sum + k : sum, in);   // in the first place
@@ -418,12 +447,10 @@ __global__ void __launch_bounds__(S::TH, 2) ssm_bwd_kernel(const SsmBwdParams p,
 #pragma unroll
             for (int j = 0; j < S::P; ++j) {
                 copy_async<8>(ck + (2 * S::K * S::P + k * S::P + j) * 32, in ? src + k * S::N + 2 * j : src, in);
-                copy_async<8>(ck + (S::K * S::P + k * S::P + j) * 32, on ? hin + k * S::N + 2 * j : hin, on);
+                copy_async<8>(ck + (S::K * S::P + k * S::P + j) * 32, h_on ? h + k * S::N + 2 * j : h, h_on);
             }
         copies_commit();
     };
-    if (on) h.store(p.seg_in + (size_t)unit * plane + cell);
-    __threadfence();
     entering(ntile - 1);
     int stage = 0;
     ring.template issue<true>(p, w, row0 + (long)(ntile - 1) * kTile, ntok - (ntile - 1) * kTile, stage);
@@ -665,6 +692,12 @@ template <typename T, int N> cudaError_t run(const SsmBwdParams &p, cudaStream_t
         if (launches) ++*launches;
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
+    if (p.nseg > 1) {
+        const dim3 grid((unsigned)(((long)p.B * p.D * N / 2 + kFoldThreads - 1) / kFoldThreads), 2);
+        ssm_bwd_fold_kernel<N><<<grid, kFoldThreads, 0, s>>>(p);
+        if (launches) ++*launches;
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
     constexpr int bytes = (S::kMain + Ring<T, S>::kFloats) * (int)sizeof(float);
     if ((e = cudaFuncSetAttribute(ssm_bwd_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
     ssm_bwd_kernel<T, S><<<(unsigned)(units * tiles), S::TH, bytes, s>>>(p, tiles);
@@ -722,7 +755,6 @@ size_t plan_ssm_bwd(SsmBwdParams &p, float *ws) {
     take(p.seg_h, p.nseg > 1 ? units * plane : 0);
     take(p.seg_g, p.nseg > 1 ? units * plane : 0);
     take(p.seg_sum, p.nseg > 1 ? units * p.D : 0);
-    take(p.seg_in, units * plane);
     take(p.tile_h, (size_t)p.B * p.tiles * plane);
     take(p.tile_sum, (size_t)p.B * p.tiles * p.D);
     take(p.part_a, units * plane);
