@@ -16,7 +16,7 @@
 namespace gla {
 namespace {
 
-constexpr int kThreads = 512, kFew = 32;
+constexpr int kThreads = 512, kFew = 32, kBatch = 8;
 
 __device__ __forceinline__ void put(const SumJob &j, long c, float v) {
     if (j.bf16) static_cast<__nv_bfloat16 *>(j.out)[c] = __float2bfloat16_rn(v);
@@ -33,13 +33,19 @@ __global__ void __launch_bounds__(kThreads) sum_rows_kernel(const SumJobs jobs) 
         const long c = (blk * kThreads + threadIdx.x) * 4;
         if (c >= j.cols) return;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (long r = 0; r < j.rows; ++r) {
-            const float4 u = __ldg(reinterpret_cast<const float4 *>(j.part + (size_t)r * j.pitch + c));
-            v.x += u.x;
-            v.y += u.y;
-            v.z += u.z;
-            v.w += u.w;
+        for (long r = 0; r < j.rows; r += kBatch) {       // loads together, also of the last rows
+            float4 u[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                u[i] = r + i < j.rows ? __ldg(reinterpret_cast<const float4 *>(j.part + (size_t)(r + i) * j.pitch + c))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                v.x += u[i].x;
+                v.y += u[i].y;
+                v.z += u[i].z;
+                v.w += u[i].w;
+            }
         }
         put(j, c, v.x);
         put(j, c + 1, v.y);
@@ -54,13 +60,9 @@ __global__ void __launch_bounds__(kThreads) sum_rows_kernel(const SumJobs jobs) 
     float acc[8] = {};
     if (c < j.cols) {
         const float *p = j.part + c;
-        long r = threadIdx.x / w;
-        for (; r + 7 * G < j.rows; r += 8 * G)
+        for (long r = threadIdx.x / w; r < j.rows; r += 8 * G)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] += __ldg(p + (size_t)(r + i * G) * j.pitch);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (r + i * G < j.rows) acc[i] += __ldg(p + (size_t)(r + i * G) * j.pitch);
+            for (int i = 0; i < 8; ++i) acc[i] += r + i * G < j.rows ? __ldg(p + (size_t)(r + i * G) * j.pitch) : 0.f;
     }
     float v = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
     for (int off = 16; off >= w; off /= 2) v += __shfl_xor_sync(0xffffffffu, v, off);

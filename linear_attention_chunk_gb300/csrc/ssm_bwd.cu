@@ -36,7 +36,7 @@
 // carries both from segment to segment.
 //
 // Bound by instructions and, at two CTAs an SM, by their latency: 4 x 2048 x
-// 2048, N = 16: 451 us, of which the main launch about 320 at 46 % of the issue
+// 2048, N = 16: 449 us, of which the main launch about 320 at 46 % of the issue
 // slots (370 instructions a token and 32 channels), the first 105 (its
 // multiply-adds alone 60), the sums 16. Each CTA folding the segments itself:
 // 482; sweeping the segment again instead of keeping the first launch's states:
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_local_kernel(const SsmBwdPar
 // seg_h's place; blockIdx.y 0) and the c entering it from behind (in seg_g's
 // place; 1). Two states a thread; the loads of kAhead segments at once.
 template <int N> __global__ void __launch_bounds__(kFoldThreads) ssm_bwd_fold_kernel(const SsmBwdParams p) {
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 16;
     const long pairs = (long)p.D * N / 2, i = (long)blockIdx.x * kFoldThreads + threadIdx.x;
     if (i >= p.B * pairs) return;
     const long b = i / pairs, e = i % pairs * 2;
@@ -727,7 +727,7 @@ size_t round16(size_t floats) { return (floats + 3) / 4 * 4; }
 
 }  // namespace
 
-constexpr int kRounds = 4, kLeast = 32;
+constexpr int kRounds = 4, kMostSegments = 128;
 
 // Channels a CTA of the backward owns.
 static int bwd_channels(int N) { return N == 32 ? Shape<32>::CH : Shape<16>::CH; }
@@ -735,14 +735,16 @@ static int bwd_channels(int N) { return N == 32 ? Shape<32>::CH : Shape<16>::CH;
 // Cuts the sequences and lays out the workspace; returns its floats.
 size_t plan_ssm_bwd(SsmBwdParams &p, float *ws) {
     const long chains = (long)p.B * ((p.D + bwd_channels(p.N) - 1) / bwd_channels(p.N));
-    // Four rounds of the two CTAs an SM holds: the cut costs nothing but the
-    // folds (the first launch walks every token once, whatever the cut).
+    // Four rounds of the two CTAs an SM holds: the cut costs little (the first
+    // launch walks every token once, whatever the cut). 2, 3, 4, 6, 8 rounds at
+    // 4 x 2048 x 2048: 495, 475, 455, 455, 461 us. At most 128 segments, a tile
+    // each at least: 1 x 4096 x 128 in 64, 128, 256: 55, 41, 46 us; segments of
+    // two tiles at least: 2 x 301 x 516 38 us instead of 32.
     long nseg = kRounds * 2L * device_sm_count() / chains;
     if (nseg < 1) nseg = 1;
-    if (nseg > 64) nseg = 64;
+    if (nseg > kMostSegments) nseg = kMostSegments;
     long L = (p.T + nseg - 1) / nseg;
     L = (L + kTile - 1) / kTile * kTile;
-    if (L < kLeast) L = kLeast;
     p.L = L;
     p.nseg = (int)((p.T + L - 1) / L);
     p.tiles = (int)(((long)p.T + kTile - 1) / kTile);
