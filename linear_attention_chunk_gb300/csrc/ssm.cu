@@ -29,13 +29,19 @@
 // h <- exp(A sum delta) h + h_local, and runs from there. No CTA waits on
 // another.
 //
-// Measured: 8 x 2048 x 2048 at N = 16, bf16 with the gate, 221 us (271 MB; the
+// Where no SM gets more than eight warps (`roomy`), the registers are there to
+// read a step's four tokens from shared memory while the four before are
+// walked: 8 x 2048 x 2048 201 us instead of 221; with more warps the registers
+// that this takes cost more (packed prompts, below: 666 us).
+//
+// Measured: 8 x 2048 x 2048 at N = 16, bf16 with the gate, 201 us (271 MB; the
 // exponentials and multiply-adds alone about 80 us): 55 instructions a token
 // and 16 channels, and seven warps an SM that issue every second clock. Packed
 // prompts of 16,024 tokens x 4,096 with the filter 614 us in two launches.
-// Slower: one channel a lane with 1, 2 or 4 lanes a channel (238 to 303 us), a
-// ring of asynchronous copies (no change: it does not wait for DRAM), a helper
-// warp for the elementwise work (227 to 268 us), two or three segments (268 to
+// Slower for the first: one channel a lane with 1, 2 or 4 lanes a channel (238
+// to 303 us), a ring of asynchronous copies (no change: it does not wait for
+// DRAM), a helper warp for the elementwise work (227 to 268 us), the next
+// tile's elementwise work beside the scan (213), two or three segments (268 to
 // 306 us).
 #include "ssm_common.cuh"
 
@@ -46,7 +52,7 @@ using namespace ssm;
 
 constexpr int kTile = 16;   // tokens per tile: 2 x 16 vectors of eight channels, one a lane
 constexpr int kChan = 16;   // channels of a warp
-constexpr int kMostWarps = 4, kMinBlocks = 4;   // of a CTA; CTAs an SM holds
+constexpr int kMostWarps = 4, kMinBlocks = 4, kRoomyBlocks = 2;   // of a CTA; CTAs an SM holds (roomy: two)
 
 // Shared memory of a warp: (delta, delta u) of the tile, y, B, C; the filter
 // and the inputs of this tile and the one before (as they lie in memory).
@@ -129,8 +135,8 @@ __device__ __forceinline__ void four(const float *src, f2 (&v)[4]) {   // eight 
     v[3] = b.y;
 }
 
-template <typename T, int N, bool kFull, bool kConv>
-__global__ void __launch_bounds__(32 * kMostWarps, kMinBlocks) ssm_scan_kernel(const SsmParams p, int tiles) {
+template <typename T, int N, bool kFull, bool kConv, bool kRoomy>
+__global__ void __launch_bounds__(32 * kMostWarps, kRoomy ? kRoomyBlocks : kMinBlocks) ssm_scan_kernel(const SsmParams p, int tiles) {
     constexpr int SP = N / 4, P = SP / 2;
     extern __shared__ __align__(16) float smem[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, q = lane / 8;
@@ -349,22 +355,39 @@ __global__ void __launch_bounds__(32 * kMostWarps, kMinBlocks) ssm_scan_kernel(c
         if (left > kTile) fetch(left - kTile);
 
         // ---- the scan: the tile's tokens
+        float4 d4[2][4];                               // four tokens' delta and delta u, B, C
+        f2 b4[2][4][P], c4[2][4][P];
+        auto look = [&](int t, int at) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                d4[at][j] = sD[(t + j) * 8 + ((lane % 8) ^ ((t + j) & 3))];
+                const f2 *b = reinterpret_cast<const f2 *>(sB + (t + j) * N + q * SP);
+                const f2 *cc = reinterpret_cast<const f2 *>(sC + (t + j) * N + q * SP);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    b4[at][j][i] = b[i];
+                    if (kFull) c4[at][j][i] = cc[i];
+                }
+            }
+        };
+        if (kRoomy) look(0, 0);
 #pragma unroll
         for (int t = 0; t < kTile; t += 4) {
+            const int at = kRoomy ? t / 4 % 2 : 0;
+            if (!kRoomy) look(t, 0);
+            if (kRoomy && t + 4 < kTile) look(t + 4, at ^ 1);
             // the decays and products of four tokens first, then the chain through them
             f2 e[4][2][P], x[4][2][P];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float4 d = sD[(t + j) * 8 + ((lane % 8) ^ ((t + j) & 3))];
-                const f2 *b = reinterpret_cast<const f2 *>(sB + (t + j) * N + q * SP);
+                const float4 d = d4[at][j];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const f2 dd = k ? f2_pack(d.z, d.z) : f2_pack(d.x, d.x);
-                    const f2 du = k ? f2_pack(d.w, d.w) : f2_pack(d.y, d.y);
+                    const f2 dd = both(k ? d.z : d.x), du = both(k ? d.w : d.y);
 #pragma unroll
                     for (int i = 0; i < P; ++i) {
                         e[j][k][i] = ex2_pair(mul2(dd, a2[k][i]));
-                        x[j][k][i] = mul2(du, b[i]);
+                        x[j][k][i] = mul2(du, b4[at][j][i]);
                     }
                     if (!kFull) dsum[k] += k ? d.z : d.x;
                 }
@@ -372,14 +395,13 @@ __global__ void __launch_bounds__(32 * kMostWarps, kMinBlocks) ssm_scan_kernel(c
             float part[2][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const f2 *cc = reinterpret_cast<const f2 *>(sC + (t + j) * N + q * SP);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     f2 y = 0;
 #pragma unroll
                     for (int i = 0; i < P; ++i) {
                         h[k][i] = fma2(e[j][k][i], h[k][i], x[j][k][i]);
-                        if (kFull) y = i == 0 ? mul2(h[k][i], cc[i]) : fma2(h[k][i], cc[i], y);
+                        if (kFull) y = i == 0 ? mul2(h[k][i], c4[at][j][i]) : fma2(h[k][i], c4[at][j][i], y);
                     }
                     if (kFull) {
                         const float2 ys = f2_split(y);
@@ -461,7 +483,11 @@ cudaError_t launch(const SsmParams &p, long units, cudaStream_t s, int *launches
     const int w = warps_per_block(units, p.D), tiles = (p.D + kChan * w - 1) / (kChan * w);
     if ((long double)units * tiles > 2147483647.0L) return cudaErrorInvalidValue;
     const int bytes = w * warp_floats<T, N, kConv>() * (int)sizeof(float);
-    ssm_scan_kernel<T, N, kFull, kConv><<<(unsigned)(units * tiles), 32 * w, bytes, s>>>(p, tiles);
+    const long per_sm = (units * tiles + device_sm_count() - 1) / device_sm_count() * w;   // warps of the fullest SM
+    auto *kern = ssm_scan_kernel<T, N, kFull, kConv, false>;
+    if constexpr (kFull)
+        if (per_sm <= kRoomyBlocks * kMostWarps) kern = ssm_scan_kernel<T, N, kFull, kConv, true>;
+    kern<<<(unsigned)(units * tiles), 32 * w, bytes, s>>>(p, tiles);
     if (launches) ++*launches;
     return cudaGetLastError();
 }

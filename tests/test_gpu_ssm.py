@@ -415,3 +415,14 @@ def test_wrong_tensors_are_refused(gla):
         call_varlen(gla, t, i32([0, 3, 6, 9]), pool)                            # three sequences, two slots
     with pytest.raises(gla.GlaError):
         call_step(gla, t, pool.view(1, 32, 16))
+
+
+# ------------------------------------------------------------ more chains than the SMs hold eight warps of
+@pytest.mark.parametrize("dtype,N", [(BF, 16), (FP, 16), (FP, 8), (BF, 32), (BF, 8), (FP, 32)])
+def test_many_chains_match_the_definition(gla, dtype, N):
+    test_fwd_matches_the_definition(gla, dtype, 43, 19, 520, N, True, True, True, True)
+
+
+@pytest.mark.parametrize("dtype,N,filt", [(BF, 16, True), (FP, 16, True), (BF, 32, True), (FP, 8, False), (BF, 8, True)])
+def test_many_packed_sequences_match_the_definition(gla, dtype, N, filt):
+    test_varlen_matches_the_definition(gla, dtype, [i * 7 % 38 for i in range(43)], 520, N, filt)
