@@ -288,3 +288,16 @@ def test_a_training_pass_of_the_block(gla):
     for name, have in (("x", dx), ("w", dw), ("cw", dcw), ("cb", dcb), ("A", got["dA"])):
         want = leaves[name].grad
         assert (d(have) - want).abs().max() <= 1e-4 * want.abs().max(), name
+
+
+@pytest.mark.parametrize("dtype,B,T,D,N,gate,state", [
+    (BF, 620, 37, 8, 16, True, True), (FP, 620, 17, 12, 8, True, False), (FP, 613, 32, 4, 32, False, True),
+    (BF, 86, 33, 968, 16, True, True), (FP, 620, 48, 4, 16, True, True)])
+def test_more_chains_than_the_gpu_holds_are_not_cut(gla, dtype, B, T, D, N, gate, state):
+    test_gradients_match_the_formulas(gla, dtype, B, T, D, N, gate, True, True, state)
+    assert gla.gla_last_launch_count() == 3                 # states entering the tiles, gradients, sums
+
+
+def test_many_short_segments(gla):
+    test_gradients_match_the_formulas(gla, FP, 1, 2100, 12, 16, True, True, True, True)
+    assert gla.gla_last_launch_count() == 4                 # and the states carried between segments
