@@ -26,6 +26,7 @@ using namespace ssm;
 constexpr int kThreads = 128;   // 512 channels a CTA
 constexpr int kStep = 4, kStages = 4;   // tokens of a stage, stages of the ring
 constexpr int kMinBlocks = 4;   // measured at 8 x 2048 x 4096: 84 us, at 5 (spills) 108
+constexpr int kLeastTile = 16, kMostTile = 256, kMostRounds = 16, kStart = 16;   // see conv_bwd_tile
 static_assert(kStep >= 3, "a tile's first step covers the three tokens that dx lags behind");
 
 template <typename T> struct Raw4 {
@@ -64,6 +65,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kMinBlocks) co
     Raw4<T> (*ring)[kThreads] = reinterpret_cast<Raw4<T> (*)[kThreads]>(smem);   // [stage][token][x, dy][thread]
     const int c = ((int)(blockIdx.x % (unsigned)blocks) * kThreads + threadIdx.x) * 4;
     const long unit = blockIdx.x / (unsigned)blocks;
+    let_next_start();
     if (c >= p.D) return;
     const long b = unit / tiles;
     const int t0 = (int)(unit % tiles) * p.tile, t1 = min(t0 + p.tile, p.T), last = min(t1 + 3, p.T);
@@ -190,14 +192,27 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kMinBlocks) co
 
 }  // namespace
 
-// Tokens per tile: long enough that the three extra tokens and the partial
-// sums (20 bytes a channel and tile) stay small, short enough to give every
-// SM four CTAs.
+// Tokens per tile: as many tiles as fill a whole number of rounds of the CTAs
+// that the GPU holds, of the rounds up to kMostRounds the ones that cost least
+// when a tile costs its tokens and kStart more (three tokens past its end, the
+// first loads, its partial sums). 8 x 2048 x 4096: tiles of 228, 576 CTAs in
+// one round; of 128, 1,024 CTAs in one and two thirds: 84 us.
 int conv_bwd_tile(int B, int T, int D) {
-    const long blocks = (D + 4 * kThreads - 1) / (4 * kThreads), want = 4L * device_sm_count();
-    int tile = 128;
-    while (tile > 16 && (long)B * ((T + tile - 1) / tile) * blocks < want) tile /= 2;
-    return tile;
+    const long chains = (long)B * ((D + 4 * kThreads - 1) / (4 * kThreads)), held = (long)kMinBlocks * device_sm_count();
+    long best = kMostTile, least = -1;
+    for (long r = 1; r <= kMostRounds; ++r) {
+        const long n = r * held / chains;      // tiles of a sequence
+        if (n < 1) continue;
+        long tile = (((long)T + n - 1) / n + kStep - 1) / kStep * kStep;
+        if (tile < kLeastTile) tile = kLeastTile;
+        if (tile > kMostTile) tile = kMostTile;
+        const long ctas = chains * ((T + tile - 1) / tile), cost = (ctas + held - 1) / held * (tile + kStart);
+        if (least < 0 || cost < least) {
+            least = cost;
+            best = tile;
+        }
+    }
+    return (int)best;
 }
 
 cudaError_t launch_conv_bwd(const ConvBwdParams &p, bool bf16, cudaStream_t s, int *launches) {

@@ -10,8 +10,7 @@
 // wait for several rounds of loads: 8 columns and 64 groups of eight lanes, so
 // that 456 rows are one round of loads (norm gradients at 16384 x 2048: 51 ->
 // 49 us; with 20,480 columns of 128 rows it cost 6 us).
-#include "common.cuh"
-#include "kernels.h"
+#include "ssm_common.cuh"
 
 namespace gla {
 namespace {
@@ -25,6 +24,7 @@ __device__ __forceinline__ void put(const SumJob &j, long c, float v) {
 
 __global__ void __launch_bounds__(kThreads) sum_rows_kernel(const SumJobs jobs) {
     __shared__ float s[kThreads / 32][32];
+    ssm::wait_for_previous();   // (and plain loads: the read-only path may run ahead of it)
     int k = 0;
     while (k + 1 < jobs.n && blockIdx.x >= jobs.j[k + 1].block) ++k;
     const SumJob &j = jobs.j[k];
@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(kThreads) sum_rows_kernel(const SumJobs jobs) 
             float4 u[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
-                u[i] = r + i < j.rows ? __ldg(reinterpret_cast<const float4 *>(j.part + (size_t)(r + i) * j.pitch + c))
+                u[i] = r + i < j.rows ? __ldcg(reinterpret_cast<const float4 *>(j.part + (size_t)(r + i) * j.pitch + c))
                                       : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) sum_rows_kernel(const SumJobs jobs) 
         const float *p = j.part + c;
         for (long r = threadIdx.x / w; r < j.rows; r += 8 * G)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] += r + i * G < j.rows ? __ldg(p + (size_t)(r + i * G) * j.pitch) : 0.f;
+            for (int i = 0; i < 8; ++i) acc[i] += r + i * G < j.rows ? __ldcg(p + (size_t)(r + i * G) * j.pitch) : 0.f;
     }
     float v = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
     for (int off = 16; off >= w; off /= 2) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -89,9 +89,9 @@ void SumJobs::add(const float *part, long rows, long cols, long pitch, void *out
 
 cudaError_t launch_sums(const SumJobs &jobs, cudaStream_t s, int *launches) {
     if (jobs.n == 0) return cudaSuccess;
-    sum_rows_kernel<<<jobs.blocks, kThreads, 0, s>>>(jobs);
-    if (launches) ++*launches;
-    return cudaGetLastError();
+    const cudaError_t e = ssm::launch_behind(sum_rows_kernel, dim3(jobs.blocks), kThreads, 0, s, jobs);
+    if (e == cudaSuccess && launches) ++*launches;
+    return e;
 }
 
 }  // namespace gla

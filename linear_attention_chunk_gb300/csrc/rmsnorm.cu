@@ -185,6 +185,7 @@ template <typename T, int VPT> constexpr int ring_rows() { return sizeof(T) == 4
 template <typename T, int VPT> __global__ void __launch_bounds__(kMost) rmsnorm_bwd_kernel(const NormParams p) {
     constexpr int kStages = ring_rows<T, VPT>();
     __shared__ float2 s_red[2][32];
+    ssm::let_next_start();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, nw = blockDim.x / 32;
     // the ring: kStages rows of s, dy, ds; a thread copies and reads its own vectors
     extern __shared__ __align__(16) uint4 ring[];

@@ -268,6 +268,7 @@ template <typename T, class S, bool kCut>
 __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_local_kernel(const SsmBwdParams p, int tiles) {
     extern __shared__ __align__(16) float smem[];
     float *sD = smem, *sU = sD + S::kRow, *sG = sU + S::kRow, *sB = sG + S::kRow, *sC = sB + kTile * S::N;
+    let_next_start();
     const int c0 = (int)(blockIdx.x % (unsigned)tiles) * S::CH;
     const long unit = blockIdx.x / (unsigned)tiles;
     const int b = (int)(unit / p.nseg), seg = (int)(unit % p.nseg);
@@ -346,6 +347,8 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_local_kernel(const SsmBwdPar
 // seg_h's place; blockIdx.y 0) and the c entering it from behind (in seg_g's
 // place; 1). Two states a thread; the loads of kAhead segments at once.
 template <int N> __global__ void __launch_bounds__(kFoldThreads) ssm_bwd_fold_kernel(const SsmBwdParams p) {
+    wait_for_previous();
+    let_next_start();
     constexpr int kAhead = 16;
     const long pairs = (long)p.D * N / 2, i = (long)blockIdx.x * kFoldThreads + threadIdx.x;
     if (i >= p.B * pairs) return;
@@ -387,6 +390,8 @@ __global__ void __launch_bounds__(S::TH, 2) ssm_bwd_kernel(const SsmBwdParams p,
     float *sC = sB + kTile * S::N;
     f2 *sH = reinterpret_cast<f2 *>(sC + kTile * S::N);        // [warp][3][K * P][lane]
     float *sP = reinterpret_cast<float *>(sH) + S::kCkpt;      // [warp][B, C][token][N]
+    wait_for_previous();
+    let_next_start();
     const int blk = (int)(blockIdx.x % (unsigned)tiles), c0 = blk * S::CH;
     const long unit = blockIdx.x / (unsigned)tiles;
     const int b = (int)(unit / p.nseg), seg = (int)(unit % p.nseg);
@@ -694,15 +699,20 @@ template <typename T, int N> cudaError_t run(const SsmBwdParams &p, cudaStream_t
     }
     if (p.nseg > 1) {
         const dim3 grid((unsigned)(((long)p.B * p.D * N / 2 + kFoldThreads - 1) / kFoldThreads), 2);
-        ssm_bwd_fold_kernel<N><<<grid, kFoldThreads, 0, s>>>(p);
+        if ((e = launch_behind(ssm_bwd_fold_kernel<N>, grid, kFoldThreads, 0, s, p)) != cudaSuccess) return e;
         if (launches) ++*launches;
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     constexpr int bytes = (S::kMain + Ring<T, S>::kFloats) * (int)sizeof(float);
     if ((e = cudaFuncSetAttribute(ssm_bwd_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
-    ssm_bwd_kernel<T, S><<<(unsigned)(units * tiles), S::TH, bytes, s>>>(p, tiles);
+    const dim3 grid((unsigned)(units * tiles));
+    if (p.T > kTile) {
+        e = launch_behind(ssm_bwd_kernel<T, S>, grid, S::TH, bytes, s, p, tiles);
+    } else {
+        ssm_bwd_kernel<T, S><<<grid, S::TH, bytes, s>>>(p, tiles);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return e;
     if (launches) ++*launches;
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     SumJobs sums;
     const bool bf16 = sizeof(T) == 2;
     const long cols = (long)p.B * p.T * N, plane = (long)p.D * N;

@@ -111,6 +111,28 @@ template <int kLeft> __device__ __forceinline__ void copies_wait() {   // all bu
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
+// A launch that follows another of the same call on the same stream and reads
+// what that leaves: its CTAs may start as soon as all of the other's have
+// (`let_next_start`) and SMs have room, and begin with `wait_for_previous`,
+// which returns when the other launch is done and its writes are visible. It
+// hides the gap between the two (sums of the norm's gradients: 49 -> 46 us a call).
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kern)(P...), dim3 grid, int threads, int bytes, cudaStream_t s, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Eight consecutive channels as they lie in memory.
 template <typename T> struct Raw8 {
     uint4 w[sizeof(T) / 2];

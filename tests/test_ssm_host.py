@@ -80,7 +80,7 @@ def test_conv_backward_rejects_bad_arguments(L):
     assert bwd(D=12) == bwd(D=0) == binding.GLA_ERR_UNSUPPORTED
     assert bwd(B=1, T=(1 << 31) - 256, D=8) == binding.GLA_ERR_INVALID_ARG          # token numbers past an int
     assert binding.gla_conv1d_bwd_workspace_size(1, (1 << 31) - 256, 8) == 0
-    assert binding.gla_conv1d_bwd_workspace_size(1, (1 << 31) - 257, 8) == ((1 << 31) - 257 + 127) // 128 * 5 * 8 * 4
+    assert binding.gla_conv1d_bwd_workspace_size(1, (1 << 31) - 257, 8) > 0
     need = binding.gla_conv1d_bwd_workspace_size(2, 50, 64)
     assert need >= 2 * 5 * 64 * 4 and bwd(n=need - 1) == binding.GLA_ERR_WORKSPACE
     assert binding.gla_conv1d_bwd_workspace_size(0, 50, 64) == 0
