@@ -5,8 +5,8 @@
 // (dp past the sequence's end is 0; x before its first token is the window,
 // a constant).
 //
-// A stream: 6 bytes an element at bf16 (x, dy in, dx out): 403 MB in 84 us
-// at 8 x 2048 x 4096 with the sums, 0.71 of the measured copy rate, the rest
+// A stream: 6 bytes an element at bf16 (x, dy in, dx out): 403 MB in 81 us
+// at 8 x 2048 x 4096 with the sums, 0.74 of the measured copy rate, the rest
 // instructions. A thread owns four channels over a tile of tokens and walks it
 // forward with the last three x and dp in registers, so dx lags three tokens
 // behind, and reads three tokens past the tile's end for it (the tile's own
@@ -25,7 +25,7 @@ using namespace ssm;
 
 constexpr int kThreads = 128;   // 512 channels a CTA
 constexpr int kStep = 4, kStages = 4;   // tokens of a stage, stages of the ring
-constexpr int kMinBlocks = 4;   // measured at 8 x 2048 x 4096: 84 us, at 5 (spills) 108
+constexpr int kMinBlocks = 4;   // measured at 8 x 2048 x 4096: 84 us (tiles of 128), at 5 (spills) 108
 constexpr int kLeastTile = 16, kMostTile = 256, kMostRounds = 16, kStart = 16;   // see conv_bwd_tile
 static_assert(kStep >= 3, "a tile's first step covers the three tokens that dx lags behind");
 
@@ -196,7 +196,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kMinBlocks) co
 // that the GPU holds, of the rounds up to kMostRounds the ones that cost least
 // when a tile costs its tokens and kStart more (three tokens past its end, the
 // first loads, its partial sums). 8 x 2048 x 4096: tiles of 228, 576 CTAs in
-// one round; of 128, 1,024 CTAs in one and two thirds: 84 us.
+// one round; of 128, 1,024 CTAs in one and two thirds: 1 us more.
 int conv_bwd_tile(int B, int T, int D) {
     const long chains = (long)B * ((D + 4 * kThreads - 1) / (4 * kThreads)), held = (long)kMinBlocks * device_sm_count();
     long best = kMostTile, least = -1;

@@ -9,7 +9,7 @@
 // out), backward 8. A CTA walks every G-th row, the rows ahead of it arriving
 // by asynchronous copies (a thread copies and reads its own vectors of eight
 // channels); one row ahead in registers kept too few bytes in flight (backward
-// 63 us at 16384 x 2048, now 49, 0.80 of the measured copy rate; forward with
+// 63 us at 16384 x 2048, now 46, 0.85 of the measured copy rate; forward with
 // 8-bit output at 16384 x 4096 86, now 75, 0.93). A row's sums
 // go through shuffles and one shared-memory exchange. A block of 128, 64 or 32
 // channels is 16, 8 or 4 neighbouring lanes, so its maximum needs shuffles

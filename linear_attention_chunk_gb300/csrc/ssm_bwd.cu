@@ -36,8 +36,8 @@
 // carries both from segment to segment.
 //
 // Bound by instructions and, at two CTAs an SM, by their latency: 4 x 2048 x
-// 2048, N = 16: 449 us, of which the main launch about 320 at 46 % of the issue
-// slots (370 instructions a token and 32 channels), the first 105 (its
+// 2048, N = 16: 444 us, of which the main launch about 320 at 49 % of the issue
+// slots (361 instructions a token and 32 channels), the first 105 (its
 // multiply-adds alone 60), the sums 16. Each CTA folding the segments itself:
 // 482; sweeping the segment again instead of keeping the first launch's states:
 // 513. The states take 250 registers; three CTAs with spills took 640. Loading
