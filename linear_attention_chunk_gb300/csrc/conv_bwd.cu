@@ -119,8 +119,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kMinBlocks) co
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) issue(t0 + k * kStep, k);
     T *dx = static_cast<T *>(p.dx) + ((size_t)b * p.T + t0) * D + c;   // the token three behind
-    // kStep tokens from t on; kInside: all of them the tile's own. Past the
-    // sequence's end dy is 0 and so is dp.
+    // kStep tokens from t on; kInside: all of them the tile's own.
     auto step = [&](int t, int stage, auto inside) {
         constexpr bool kInside = decltype(inside)::value;
         Raw4<T> rx[kStep], ry[kStep];
@@ -143,7 +142,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kMinBlocks) co
                 a = fma2(w[3][e], xv[e], a);
                 const f2 sg = rcp_pair(add2(ex2_pair(mul2(a, neg)), one));
                 // sg (1 + a (1 - sg)); where a overflows the exponential, sg = 0 and a (1 - sg) is finite
-                const f2 d = mul2(g[e], mul2(sg, fma2(a, fma2(sg, minus, one), one)));
+                f2 d = mul2(g[e], mul2(sg, fma2(a, fma2(sg, minus, one), one)));
+                if (!kInside && t + i >= last) d = 0;   // behind the end: dy is 0, but 0 x NaN (a may overflow there) is not
                 if (kInside || t + i < t1) {
                     dw[0][e] = fma2(d, h[0][e], dw[0][e]);
                     dw[1][e] = fma2(d, h[1][e], dw[1][e]);
