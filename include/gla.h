@@ -396,8 +396,10 @@ gla_status gla_conv1d_step(const void *x, const float *w, const float *b, float 
  *     ld_*: elements from one token's row to the next (a column range of a
  *     wider projection output can be passed as it is). Rows of x, dt and z
  *     start 16-byte aligned; Bm and Cm need only their element's alignment.
- *   A [D, N] fp32 (negative for a decay; not its logarithm), skip [D] fp32 or
- *     NULL (0), dt_bias [D] fp32 or NULL (0), z or NULL (no gate).
+ *   A [D, N] fp32 (negative for a decay; not its logarithm; -inf, as the lowest
+ *     finite value, clears the state at a step above 0, and a step of 0 keeps
+ *     it), skip [D] fp32 or NULL (0), dt_bias [D] fp32 or NULL (0), z or NULL
+ *     (no gate).
  *   y: contiguous rows of D. States [*, D, N] fp32, N fastest.
  *   D a multiple of 8 (bf16) or 4 (fp32), at most 2^25; N = 8, 16 or 32. y
  *   may not overlap an input.

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(32 * kMostWarps, kRoomy ? kRoomyBlocks : kMinB
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const float2 a = __ldg(reinterpret_cast<const float2 *>(p.A + cell + k * N) + i);
-                a2[k][i] = f2_pack(a.x * kLog2e, a.y * kLog2e);
+                a2[k][i] = f2_pack(rate_log2(a.x), rate_log2(a.y));
                 if (src) {
                     const float2 v = reinterpret_cast<const float2 *>(src + k * N)[i];
                     h[k][i] = f2_pack(v.x, v.y);

@@ -227,13 +227,22 @@ template <class S> struct State {
 #pragma unroll
             for (int i = 0; i < S::P; ++i) v[k][i] = 0;
     }
-    __device__ __forceinline__ void load(const float *src, float f = 1.f) {   // src: the first channel's, in [D, N]
+    __device__ __forceinline__ void load(const float *src) {                   // src: the first channel's, in [D, N]
 #pragma unroll
         for (int k = 0; k < S::K; ++k)
 #pragma unroll
             for (int i = 0; i < S::P; ++i) {
                 const float2 u = reinterpret_cast<const float2 *>(src + k * S::N)[i];
-                v[k][i] = f2_pack(u.x * f, u.y * f);
+                v[k][i] = f2_pack(u.x, u.y);
+            }
+    }
+    __device__ __forceinline__ void load_rates(const float *src) {             // as load, of A
+#pragma unroll
+        for (int k = 0; k < S::K; ++k)
+#pragma unroll
+            for (int i = 0; i < S::P; ++i) {
+                const float2 u = reinterpret_cast<const float2 *>(src + k * S::N)[i];
+                v[k][i] = f2_pack(rate_log2(u.x), rate_log2(u.y));
             }
     }
     __device__ __forceinline__ void store(float *dst) const {
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__(S::TH, 3) ssm_bwd_local_kernel(const SsmBwdPar
 
     State<S> a2, h, pr, c;
     a2.zero();
-    if (on) a2.load(p.A + cell, kLog2e);
+    if (on) a2.load_rates(p.A + cell);
     h.zero();
     c.zero();
 #pragma unroll
@@ -360,7 +369,7 @@ template <int N> __global__ void __launch_bounds__(kFoldThreads) ssm_bwd_fold_ke
     const float *sums = p.seg_sum + b * p.nseg * p.D + e / N;
     const float2 a = *reinterpret_cast<const float2 *>(p.A + e);
     const float2 v0 = first ? *reinterpret_cast<const float2 *>(first + b * plane + e) : make_float2(0.f, 0.f);
-    const f2 a2 = f2_pack(a.x * kLog2e, a.y * kLog2e);
+    const f2 a2 = f2_pack(rate_log2(a.x), rate_log2(a.y));
     f2 v = f2_pack(v0.x, v0.y);
     for (int s = 0; s < p.nseg; s += kAhead) {
         float2 own[kAhead];
@@ -412,7 +421,7 @@ __global__ void __launch_bounds__(S::TH, 2) ssm_bwd_kernel(const SsmBwdParams p,
     a2.zero();
     c.zero();
     if (on) {
-        a2.load(p.A + cell, kLog2e);
+        a2.load_rates(p.A + cell);
         if (cin) c.load(cin + cell);
     }
 

@@ -4,6 +4,8 @@
 // asynchronous copies, and vectors of eight channels in either element type.
 #pragma once
 
+#include <cfloat>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -48,6 +50,12 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// A rate, held to the lowest finite number: 0 x -inf is NaN, and a step of 0
+// (also of the tokens behind a sequence's end) keeps the state at any rate.
+// rate_log2: the rate of 2^x, rate * log2(e), which for a finite rate may be -inf.
+__device__ __forceinline__ float finite_rate(float a) { return a < -FLT_MAX ? -FLT_MAX : a; }   // (NaN stays NaN)
+__device__ __forceinline__ float rate_log2(float a) { return finite_rate(a * kLog2e); }
+
 __device__ __forceinline__ f2 ex2_pair(f2 x) {
     const float2 v = f2_split(x);
     return f2_pack(ex2(v.x), ex2(v.y));

@@ -98,7 +98,11 @@ template <typename T, int N, bool kConv> __global__ void __launch_bounds__(kThre
     float *hb = p.hT + (size_t)c * N + q * V, *wb = p.win + c;
     Narrow<float, V> a[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) a[i].load(p.A + (size_t)c * N + i * 4 * V + q * V, true);
+    for (int i = 0; i < P; ++i) {
+        a[i].load(p.A + (size_t)c * N + i * 4 * V + q * V, true);
+#pragma unroll
+        for (int k = 0; k < V; ++k) a[i].w[k] = __float_as_uint(finite_rate(a[i].get(k)));
+    }
     const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = p.skip ? p.skip[c] : 0.f;
     float4 tw = make_float4(0.f, 0.f, 0.f, 0.f);
     float tb = 0.f;
