@@ -568,7 +568,7 @@ class _Call:
     allocates (outputs, workspace) belongs to the stream it runs on. Kept
     lean: a serving step's kernels take a few microseconds."""
 
-    __slots__ = ("torch", "device", "index", "dtype", "code", "stream", "other", "kept", "f")
+    __slots__ = ("torch", "device", "index", "here", "dtype", "code", "stream", "other", "kept", "f")
 
     def __init__(self, x, stream):
         self.torch = torch = _torch()
@@ -576,6 +576,7 @@ class _Call:
         self.index = x.get_device()
         if self.index < 0:
             raise GlaError(GLA_ERR_INVALID_ARG, "argument", "tensors must live on a CUDA device")
+        self.here = self.index == torch.cuda.current_device()
         self.dtype = x.dtype
         self.code = _dtype_code(x)
         self.f = torch.float32
@@ -644,9 +645,18 @@ class _Call:
         with self.torch.cuda.stream(self.other):
             return self.torch.empty(shape, dtype=dtype, device=self.device)
 
-    def scratch(self, workspace, need):
-        """Address and bytes of the caller's workspace, or of a new one of `need` bytes."""
+    def scratch(self, workspace, size, *shape):
+        """Address and bytes of the caller's workspace, or of a new one of
+        size(*shape) bytes, asked with the call's device current: the plan
+        behind it depends on that device's SMs. size None: no workspace."""
         if workspace is None:
+            if size is None:
+                return None, 0
+            if self.here:
+                need = size(*shape, self.code)
+            else:
+                with self.torch.cuda.device(self.index):
+                    need = size(*shape, self.code)
             if need == 0:
                 return None, 0
             self.kept = self.empty(need, self.torch.uint8)
@@ -659,7 +669,7 @@ class _Call:
         f = _entry.get(name)
         if f is None:
             f = _entry[name] = getattr(lib(), name)
-        if self.index == self.torch.cuda.current_device():
+        if self.here:
             st = f(*args, self.stream)
         else:
             with self.torch.cuda.device(self.index):
@@ -711,9 +721,8 @@ def gla_ssm_fwd(x, dt, A, Bm, Cm, skip=None, z=None, dt_bias=None, h0=None, *, s
         y = c.empty((B, T, D))
     if hT is None and want_hT:
         hT = c.empty((B, D, N), c.torch.float32)
-    need = gla_ssm_fwd_workspace_size(B, T, D, N, c.code) if workspace is None else 0
     c.run("gla_ssm_fwd", *args, c.f32(h0, (B, D, N), "h0"), B, T, D, N, c.code, c.whole(y, (B, T, D), "y"),
-          c.f32(hT, (B, D, N), "hT"), *c.scratch(workspace, need))
+          c.f32(hT, (B, D, N), "hT"), *c.scratch(workspace, gla_ssm_fwd_workspace_size, B, T, D, N))
     return y, hT
 
 
@@ -738,9 +747,9 @@ def gla_ssm_varlen(x, dt, A, Bm, Cm, cu_seqlens, state_pool, skip=None, z=None, 
     w, b, sl, pool, win, k = _pools(c, nseq, D, N, state_pool, slots, conv_w, conv_b, win_pool)
     if y is None:
         y = c.empty((total_T, D))
-    need = gla_ssm_varlen_workspace_size(nseq, total_T, D, N, c.code) if workspace is None else 0
     c.run("gla_ssm_varlen", *args, w, b, c.i32(cu_seqlens, (nseq + 1,), "cu_seqlens"), sl, pool, win, k, nseq,
-          total_T, D, N, c.code, c.whole(y, (total_T, D), "y"), *c.scratch(workspace, need))
+          total_T, D, N, c.code, c.whole(y, (total_T, D), "y"),
+          *c.scratch(workspace, gla_ssm_varlen_workspace_size, nseq, total_T, D, N))
     return y
 
 
@@ -789,10 +798,10 @@ def gla_ssm_bwd(x, dt, A, Bm, Cm, dy, skip=None, z=None, dt_bias=None, h0=None, 
         ddt_bias = c.empty((D,), f32)
     if dh0 is None and want_dh0:
         dh0 = c.empty(state, f32)
-    need = gla_ssm_bwd_workspace_size(B, T, D, N, c.code) if workspace is None else 0
     c.run("gla_ssm_bwd", *args, c.whole(dx, wide, "dx"), c.whole(ddt, wide, "ddt"), c.f32(dA, (D, N), "dA"),
           c.whole(dB, narrow, "dB"), c.whole(dC, narrow, "dC"), c.f32(dskip, (D,), "dskip"), c.whole(dz, wide, "dz"),
-          c.f32(ddt_bias, (D,), "ddt_bias"), c.f32(dh0, state, "dh0"), *c.scratch(workspace, need))
+          c.f32(ddt_bias, (D,), "ddt_bias"), c.f32(dh0, state, "dh0"),
+          *c.scratch(workspace, gla_ssm_bwd_workspace_size, B, T, D, N))
     return dx, ddt, dA, dB, dC, dskip, dz, ddt_bias, dh0
 
 
@@ -813,9 +822,8 @@ def gla_conv1d_bwd(x, w, b, dy, win_in=None, *, dx=None, dw=None, db=None, want_
     dw = c.empty((D, 4), f32) if dw is None else dw
     if db is None and want_db:
         db = c.empty((D,), f32)
-    need = gla_conv1d_bwd_workspace_size(B, T, D, c.code) if workspace is None else 0
     c.run("gla_conv1d_bwd", *args, B, T, D, c.code, c.whole(dx, x.shape, "dx"), c.f32(dw, (D, 4), "dw"),
-          c.f32(db, (D,), "db"), *c.scratch(workspace, need))
+          c.f32(db, (D,), "db"), *c.scratch(workspace, gla_conv1d_bwd_workspace_size, B, T, D))
     return dx, dw, db
 
 
@@ -871,9 +879,9 @@ def gla_rmsnorm_bwd(s, w, dy, ds=None, eps=1e-6, *, dx=None, dw=None, want_dw=Tr
     dx = c.empty(s.shape) if dx is None else dx
     if dw is None and want_dw:
         dw = c.empty((D,), c.torch.float32)
-    need = gla_rmsnorm_bwd_workspace_size(rows, D, c.code) if workspace is None and dw is not None else 0
+    size = None if dw is None else gla_rmsnorm_bwd_workspace_size
     c.run("gla_rmsnorm_bwd", *args, float(eps), rows, D, c.code, c.whole(dx, s.shape, "dx"), c.f32(dw, (D,), "dw"),
-          *c.scratch(workspace, need))
+          *c.scratch(workspace, size, rows, D))
     return dx, dw
 
 
