@@ -174,6 +174,8 @@ def lib():
 
 
 def _status_name(status: int) -> str:
+    if _lib is None and not os.path.exists(LIB_PATH):   # that error itself: lib() holds its lock and would only repeat it
+        return f"status {status}"
     try:
         return lib().gla_status_string(int(status)).decode()
     except Exception:
