@@ -422,7 +422,9 @@ gla_status gla_conv1d_step(const void *x, const float *w, const float *b, float 
  * gla_ssm_fwd and gla_ssm_varlen cut sequences into segments that run in
  *   parallel when workspace_bytes is at least the *_workspace_size query
  *   (0: nothing to gain); with less they run one chain per sequence and
- *   channel: the same result up to rounding, never a failure.
+ *   channel: the same result up to rounding, never a failure. The queries of
+ *   these and of the gradients below depend on the SMs of the current device:
+ *   ask on the device that the call runs on.
  */
 gla_status gla_ssm_fwd(const void *x, int64_t ld_x, const void *dt, int64_t ld_dt, const float *A, const void *Bm,
                        int64_t ld_B, const void *Cm, int64_t ld_C, const float *skip, const void *z, int64_t ld_z,
@@ -459,7 +461,8 @@ gla_status gla_ssm_step(const void *x, int64_t ld_x, const void *dt, int64_t ld_
  *   workspace: at least gla_ssm_bwd_workspace_size() bytes (required when
  *   B*T > 0): a state per 16 tokens and partial sums. Sums run in a fixed
  *   order: the same call gives the same bits. B*T = 0 zeroes the sums, and
- *   dh0 = dhT.
+ *   dh0 = dhT. Where a step is exactly 0 (its softplus underflows) and a rate
+ *   so low that P A leaves fp32, ddt is NaN.
  */
 gla_status gla_ssm_bwd(const void *x, int64_t ld_x, const void *dt, int64_t ld_dt, const float *A, const void *Bm,
                        int64_t ld_B, const void *Cm, int64_t ld_C, const float *skip, const void *z, int64_t ld_z,
@@ -499,6 +502,8 @@ size_t gla_conv1d_bwd_workspace_size(int B, int T, int D, gla_dtype dtype);
  *   xn = s / sqrt(mean(s^2) + eps) and g = dy w,
  *     dx = ds + (g - xn mean(g xn)) / sqrt(mean(s^2) + eps)   (x's and res's alike)
  *     dw = sum over rows of dy xn
+ *   s as gla_rmsnorm_fwd stores it is rounded to `dtype`, while its y comes from
+ *   the unrounded sum: at bf16 the gradient is that of the norm at the rounded s.
  *   s, dy, ds (or NULL: zero), dx [rows, D] of `dtype` (dx may be dy or ds),
  *   dw [D] fp32 or NULL (not wanted); workspace: at least
  *   gla_rmsnorm_bwd_workspace_size() bytes when dw is wanted and rows > 0.

@@ -25,7 +25,7 @@ using namespace ssm;
 
 constexpr int kThreads = 128;   // 512 channels a CTA
 constexpr int kStep = 4, kStages = 4;   // tokens of a stage, stages of the ring
-constexpr int kMinBlocks = 4;   // measured at 8 x 2048 x 4096: 84 us (tiles of 128), at 5 (spills) 108
+constexpr int kMinBlocks = 4;   // measured at 8 x 2048 x 4096, bf16: 84 us (tiles of 128), at 5 (spills) 108; at fp32 three fit (64 KB each)
 constexpr int kLeastTile = 16, kMostTile = 256, kMostRounds = 16, kStart = 16;   // see conv_bwd_tile
 static_assert(kStep >= 3, "a tile's first step covers the three tokens that dx lags behind");
 
@@ -196,7 +196,9 @@ template <typename T> __global__ void __launch_bounds__(kThreads, kMinBlocks) co
 // that the GPU holds, of the rounds up to kMostRounds the ones that cost least
 // when a tile costs its tokens and kStart more (three tokens past its end, the
 // first loads, its partial sums). 8 x 2048 x 4096: tiles of 228, 576 CTAs in
-// one round; of 128, 1,024 CTAs in one and two thirds: 1 us more.
+// one round; of 128, 1,024 CTAs in one and two thirds: 1 us more. The rule
+// counts bf16's four CTAs an SM; at fp32 three fit, and a round is a round and a
+// third: 8 x 2048 x 2048 86 us (0.69 of the copy rate), x 4096 156 (0.76).
 int conv_bwd_tile(int B, int T, int D) {
     const long chains = (long)B * ((D + 4 * kThreads - 1) / (4 * kThreads)), held = (long)kMinBlocks * device_sm_count();
     long best = kMostTile, least = -1;

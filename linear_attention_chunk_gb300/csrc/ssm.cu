@@ -518,8 +518,20 @@ cudaError_t launch_ssm_scan(const SsmParams &p, bool bf16, cudaStream_t s, int *
     return bf16 ? by_state<__nv_bfloat16, false>(p, s, launches) : by_state<float, false>(p, s, launches);
 }
 
-// The segment length: a multiple of the tile, long enough that the first
-// launch's work (about 0.9 of the second's) buys parallelism.
+// The segment length, a multiple of the tile. A token costs the first launch
+// two thirds of what it costs the second (packed prompts of 16,024 tokens x
+// 4,096 with the filter: 211 us for the 12,800 that it walks, then 401).
+// Equal-length sequences are cut where there are fewer than twelve groups of
+// eight channels (half a warp's) an SM, into twice as many pieces. Cut and
+// whole, us, B x 2048 x 2048: B = 1: 59, 135; 2: 91, 137; 3: 145, 139; 4: 166,
+// 143; 5: 201, 195; 6: 227, 199; 7: 268, 199; 8 is left whole: 201. So the rule
+// cuts too far from three such sequences on.
+// Packed prompts are always cut, into 512 tokens at most: the prompts above 615
+// and 629 us, with 5,120 channels 756 and 645, 64 prompts of 512 tokens x 4,096
+// 773 and 754, of 2,048 tokens 4,401 and 2,893. It gains where few long prompts
+// would leave SMs idle and costs where there are chains enough.
+// The last launch folds the segments one after another: 1 x 4096 x 128 31 us
+// instead of 264, 1 x 65536 x 256 180 instead of 4,112.
 SsmPlan plan_ssm(long nseq, long rows, int D, bool varlen) {
     const long warps = nseq * ((D + 7) / 8);
     const long want = (long)device_sm_count() * 12;

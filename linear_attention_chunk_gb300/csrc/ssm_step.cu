@@ -3,7 +3,12 @@
 // channel) it moves 128 bytes of state at N = 16 (64 in, 64 out), 28 of the
 // window and 8 of activations: an HBM stream, bound by the bytes in flight
 // (860 MB at 1,280 sequences of 4,096 channels in 165 us: 5.2 TB/s, 0.77 of the
-// measured copy rate).
+// measured copy rate; without the filter 141 us, 0.74). The other instances at
+// that size, with and without the filter: N = 8 131 and 102 us (0.59, 0.54 of
+// the copy rate), N = 32 553 and 281 (0.41, 0.73); fp32 N = 8 125 and 102 (0.67,
+// 0.60), N = 16 235 and 143 (0.56, 0.78), N = 32 814 and 485 (0.28, 0.43). With
+// the filter fp32 N = 16 and both of N = 32 spill at the 80 registers of six
+// CTAs an SM, as does fp32 N = 32 without it.
 //
 // A warp owns eight channels of four sequences. Elementwise work is lane
 // (channel, sequence)'s: the filter over the window and the new input, the
@@ -22,7 +27,8 @@ using namespace ssm;
 
 constexpr int kThreads = 128;   // 32 channels
 constexpr int kSeqs = 4, kStages = 3;
-constexpr int kMinBlocks = 6;   // measured 3, 4, 5, 6, 7: 248, 221, 194, 164, 175 us at 1280 x 4096 (N = 16, filter on)
+// CTAs an SM, of all instances, measured at bf16, N = 16 with the filter: 3, 4, 5, 6, 7: 248, 221, 194, 164, 175 us at 1280 x 4096
+constexpr int kMinBlocks = 6;
 
 // Four numbers, each spread over four neighbouring lanes: the sum of number
 // (lane % 4), in three exchanges.
@@ -220,7 +226,9 @@ template <typename T, int N> cudaError_t run(const SsmParams &p, cudaStream_t s,
     const bool wide = ((reinterpret_cast<uintptr_t>(p.Bm) | reinterpret_cast<uintptr_t>(p.Cm) |
                         (uintptr_t)p.ldb * sizeof(T) | (uintptr_t)p.ldc * sizeof(T)) % piece) == 0;
     const int groups = (p.nseq + kSeqs - 1) / kSeqs, tiles = (p.D + kThreads / 4 - 1) / (kThreads / 4);
-    // as many CTAs as the GPU holds at once, each walking every gridDim.y-th group
+    // as many CTAs as the GPU holds at once, each walking every gridDim.y-th
+    // group; at N = 32 the ring takes 48 KB, four fit an SM, and the grid is a
+    // round and a half
     const int held = kMinBlocks * device_sm_count() / tiles, rows = held > 0 ? held : 1;
     const dim3 grid(tiles, groups < rows ? groups : rows);
     if (p.conv_w) ssm_step_kernel<T, N, true><<<grid, kThreads, 0, s>>>(p, wide);
