@@ -517,6 +517,123 @@ gla_status gla_rmsnorm_bwd(const void *s, const float *w, const void *dy, const 
 size_t gla_rmsnorm_bwd_workspace_size(int64_t rows, int D, gla_dtype dtype);
 
 /*
+ * Trees of drafted tokens over a state pool: speculative decoding, where a
+ * draft model proposes a tree of tokens for each sequence, the model scores
+ * all of them in one call, and the path that is accepted is kept. Per sequence
+ * and head, for node i with parent p(i) (-1: the sequence's state page):
+ *     S_i = exp(g_i) S_p(i) + k_i v_i^T   (S_-1: the page),   o_i = scale S_i^T q_i
+ * with g_i = log_lambda[h], or (*_gated) a log-decay per node and head: what
+ * gla_decode_step would give along every path, without a copy of the page for
+ * each. A decay of 0 (log-decay -inf, or a product that underflows) clears
+ * what lies before it.
+ *   Trees are packed one behind another: sequence n's nodes are
+ *   [cu_nodes[n], cu_nodes[n+1]) (int32 [nseq + 1] in device memory), parents
+ *   [total_T] int32 hold each node's parent counted within its tree, always
+ *   before the node itself (-1 <= parents[i] < i; several nodes may have -1);
+ *   at most GLA_TREE_MAX_NODES nodes a tree. slots as gla_chunk_fwd_varlen.
+ *   A sequence with a bad entry (offset, slot, parent, accepted node, too many
+ *   nodes) is skipped and the next gla_check() reports GLA_ERR_INVALID_ARG.
+ *   Nodes of different paths never mix, also where one is not finite.
+ *   q, k [total_T, H, dk], v [total_T, H, dv] of `dtype`, heads contiguous,
+ *   ld_*: elements from one token's row to the next (a column range of a wider
+ *   projection output can be passed as it is); rows 16-byte aligned at bf16.
+ *   dk, dv as the other calls: GLA_BF16 96 and 192, GLA_FP32 up to 128 and 256.
+ *   Arrays of node, slot and page numbers here and below, and the decays, need
+ *   their element's alignment only (a slice of a longer array passes).
+ *
+ * gla_tree_fwd, gla_tree_fwd_gated: o [total_T, H, dv] (contiguous) of every
+ *   node; state_pool [n_slots, H, dk, dv] is only read, so sequences may share
+ *   a slot. log_lambda [H], g [total_T, H] fp32. Rows of no tree are left as
+ *   they were. o may not overlap an input.
+ * gla_tree_commit, gla_tree_commit_gated: last [nseq] int32 in device memory,
+ *   the last accepted node of each tree, counted within it (-1: none): the
+ *   page becomes S_last, the others stay. With x [total_T, D] and win_pool
+ *   [n_slots, 4, D] fp32 (both or neither) also the Conv1d's window: its last
+ *   four inputs, those of the accepted path last. Slots of one call are distinct.
+ *   D a multiple of 8 (bf16) or 4 (fp32).
+ * gla_conv1d_tree: gla_conv1d_fwd along each node's path: y [total_T, D] of
+ *   every node from x [total_T, D] (rows ld_x apart) of the node and its last
+ *   three ancestors, behind the root those of the window, which stays as it is.
+ * Each call is one launch.
+ */
+#define GLA_TREE_MAX_NODES 64
+gla_status gla_tree_fwd(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                        const float *log_lambda, float scale, const int *cu_nodes, const int *parents,
+                        const int *slots, const float *state_pool, int n_slots, int nseq, int total_T, int H, int dk,
+                        int dv, gla_dtype dtype, void *o, void *stream);
+gla_status gla_tree_fwd_gated(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                              const float *g, float scale, const int *cu_nodes, const int *parents, const int *slots,
+                              const float *state_pool, int n_slots, int nseq, int total_T, int H, int dk, int dv,
+                              gla_dtype dtype, void *o, void *stream);
+gla_status gla_tree_commit(const void *k, int64_t ld_k, const void *v, int64_t ld_v, const float *log_lambda,
+                           const int *cu_nodes, const int *parents, const int *last, const int *slots,
+                           float *state_pool, const void *x, int64_t ld_x, float *win_pool, int n_slots, int nseq,
+                           int total_T, int H, int dk, int dv, int D, gla_dtype dtype, void *stream);
+gla_status gla_tree_commit_gated(const void *k, int64_t ld_k, const void *v, int64_t ld_v, const float *g,
+                                 const int *cu_nodes, const int *parents, const int *last, const int *slots,
+                                 float *state_pool, const void *x, int64_t ld_x, float *win_pool, int n_slots,
+                                 int nseq, int total_T, int H, int dk, int dv, int D, gla_dtype dtype, void *stream);
+gla_status gla_conv1d_tree(const void *x, int64_t ld_x, const float *w, const float *b, const int *cu_nodes,
+                           const int *parents, const int *slots, const float *win_pool, int n_slots, int nseq,
+                           int total_T, int D, gla_dtype dtype, void *y, void *stream);
+
+/*
+ * Pages of the pools (states, conv windows, of one or of many layers): a pool
+ * is n_slots pages of page_bytes[i] bytes one behind another at pools[i]
+ * (16-byte aligned; page_bytes a multiple of 4, at best of 16); pools and
+ * page_bytes are host arrays of n_pools <= GLA_PAGES_MAX_POOLS entries, page
+ * numbers int32 in device memory. A page number outside [0, n_slots) skips its
+ * pair and the next gla_check() reports GLA_ERR_INVALID_ARG.
+ *
+ * gla_pages_copy: page dst[i] becomes a copy of page src[i] in every pool, for
+ *   i < n: one prompt continued several times takes the same source with
+ *   several targets. Targets are distinct, and none is another pair's source
+ *   (src[i] == dst[i] does nothing).
+ * gla_pages_clear: the n pages become zeros, as a new sequence needs them.
+ * gla_pages_compact: live [n_slots] bytes, nonzero: in use. With L pages in
+ *   use, those at L and above move into the free ones below L, the lowest into
+ *   the lowest and so on; the pages that they leave keep their contents. map
+ *   [n_slots] gets each page's new number (-1: not in use), count [1] gets L.
+ *   Two launches; workspace: at least gla_pages_compact_workspace_size() bytes.
+ */
+#define GLA_PAGES_MAX_POOLS 128
+gla_status gla_pages_copy(void *const *pools, const int64_t *page_bytes, int n_pools, int n_slots, const int *src,
+                          const int *dst, int n, void *stream);
+gla_status gla_pages_clear(void *const *pools, const int64_t *page_bytes, int n_pools, int n_slots, const int *slots,
+                           int n, void *stream);
+gla_status gla_pages_compact(void *const *pools, const int64_t *page_bytes, int n_pools, int n_slots,
+                             const unsigned char *live, int *map, int *count, void *workspace, size_t workspace_bytes,
+                             void *stream);
+size_t gla_pages_compact_workspace_size(int n_slots);
+
+/*
+ * The layer norm in front of a layer ("i14 and the Laplace 3B architecture",
+ * paragraph "Normalisation and convolution"), over rows of D channels:
+ *     s = x + res,   y = w (s - mean(s)) / sqrt(var(s) + eps) + b
+ * with the variance over D (not D - 1).
+ * gla_layernorm_fwd: x, res [rows, D] of `dtype` (res NULL: s = x), w, b [D]
+ *   fp32 or NULL (one, zero), eps >= 0; s_out [rows, D] (s rounded to `dtype`;
+ *   may be res or x) or NULL, y [rows, D], rounded once, from fp32. The
+ *   variance is that of s - mean(s), in fp32. y may not overlap an input.
+ * gla_layernorm_bwd: gradients of L = <dy, y> + <ds, s> with s given (at bf16
+ *   the norm's at the rounded s): with xn = (s - mean(s)) / sqrt(var(s) + eps)
+ *   and g = dy w,
+ *     dx = ds + (g - mean(g) - xn mean(g xn)) / sqrt(var(s) + eps)   (x's and res's alike)
+ *     dw = sum over rows of dy xn,   db = sum over rows of dy
+ *   s, dy, ds (or NULL: zero), dx [rows, D] of `dtype` (dx may be dy or ds),
+ *   dw, db [D] fp32 or NULL (not wanted); workspace: at least
+ *   gla_layernorm_bwd_workspace_size() bytes when either is wanted and rows > 0.
+ *   rows = 0 zeroes them. Sums run in a fixed order.
+ * D a multiple of 8 (bf16) or 4 (fp32), at most 8192.
+ */
+gla_status gla_layernorm_fwd(const void *x, const void *res, const float *w, const float *b, float eps, int64_t rows,
+                             int D, gla_dtype dtype, void *s_out, void *y, void *stream);
+gla_status gla_layernorm_bwd(const void *s, const float *w, const void *dy, const void *ds, float eps, int64_t rows,
+                             int D, gla_dtype dtype, void *dx, float *dw, float *db, void *workspace,
+                             size_t workspace_bytes, void *stream);
+size_t gla_layernorm_bwd_workspace_size(int64_t rows, int D, gla_dtype dtype);
+
+/*
  * gla_selftest_wait_timeout -- diagnostic of the device-side failure
  * detection, with no fault and no hang: one kernel waits on two mbarriers
  * that nothing completes. The first wait gives up after limit_us (1 to

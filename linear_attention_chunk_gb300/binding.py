@@ -30,6 +30,15 @@ Functions:
   gla_rmsnorm(x, w=None, res=None, eps=1e-6)                              -> (y, s)  s = x + res
   gla_rmsnorm_q8(x, w=None, res=None, eps=1e-6, group=128)                -> (y8 e4m3, scale, s)
   gla_rmsnorm_bwd(s, w, dy, ds=None, eps=1e-6)                            -> (dx, dw)
+  gla_layernorm(x, w=None, b=None, res=None, eps=1e-6)                    -> (y, s)  s = x + res
+  gla_layernorm_bwd(s, w, dy, ds=None, eps=1e-6)                          -> (dx, dw, db)
+  gla_tree_fwd(q, k, v, log_lambda, cu_nodes, parents, state_pool, ...)   -> o  drafted trees, the pool only read
+  gla_tree_fwd_gated(q, k, v, g, cu_nodes, parents, state_pool, ...)      -> o  per-token decay
+  gla_tree_commit(k, v, log_lambda, cu_nodes, parents, last, state_pool, ...) -> state_pool  (pools updated)
+  gla_tree_commit_gated(k, v, g, cu_nodes, parents, last, state_pool, ...)    -> state_pool  (pools updated)
+  gla_conv1d_tree(x, w, b, cu_nodes, parents, win_pool, slots=None)       -> y  the windows only read
+  gla_pages_copy(pools, src, dst), gla_pages_clear(pools, slots)          (pools updated)
+  gla_pages_compact(pools, live)                                          -> (map, count)  (pools updated)
   gla_check(stream=None), gla_status_string(code), gla_version()
   gla_chunk_fwd_workspace_size(...), gla_chunk_bwd_workspace_size(...)
 `lib()` returns the loaded ctypes library for callers that hold raw pointers.
@@ -55,7 +64,10 @@ ABI_FUNCTIONS = ("gla_chunk_fwd", "gla_chunk_fwd_workspace_size", "gla_chunk_fwd
                  "gla_ssm_varlen", "gla_ssm_varlen_workspace_size", "gla_ssm_step",
                  "gla_ssm_bwd", "gla_ssm_bwd_workspace_size",
                  "gla_conv1d_bwd", "gla_conv1d_bwd_workspace_size", "gla_rmsnorm_fwd", "gla_rmsnorm_bwd",
-                 "gla_rmsnorm_bwd_workspace_size", "gla_selftest_wait_timeout", "gla_check",
+                 "gla_rmsnorm_bwd_workspace_size", "gla_tree_fwd", "gla_tree_fwd_gated", "gla_tree_commit",
+                 "gla_tree_commit_gated", "gla_conv1d_tree", "gla_pages_copy", "gla_pages_clear", "gla_pages_compact",
+                 "gla_pages_compact_workspace_size", "gla_layernorm_fwd", "gla_layernorm_bwd",
+                 "gla_layernorm_bwd_workspace_size", "gla_selftest_wait_timeout", "gla_check",
                  "gla_status_string", "gla_last_error", "gla_last_launch_count", "gla_version")
 
 
@@ -157,6 +169,32 @@ def lib():
             L.gla_rmsnorm_bwd.restype = _i
             L.gla_rmsnorm_bwd_workspace_size.argtypes = [_ll, _i, _i]
             L.gla_rmsnorm_bwd_workspace_size.restype = _sz
+            heads = [_vp, _ll]
+            for name in ("gla_tree_fwd", "gla_tree_fwd_gated"):
+                f = getattr(L, name)
+                f.argtypes = heads * 3 + [_vp, _f, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp]
+                f.restype = _i
+            for name in ("gla_tree_commit", "gla_tree_commit_gated"):
+                f = getattr(L, name)
+                f.argtypes = heads * 2 + [_vp] * 6 + heads + [_vp] + [_i] * 8 + [_vp]
+                f.restype = _i
+            L.gla_conv1d_tree.argtypes = heads + [_vp] * 6 + [_i] * 5 + [_vp, _vp]
+            L.gla_conv1d_tree.restype = _i
+            pools = [ctypes.POINTER(_vp), ctypes.POINTER(_ll), _i, _i]
+            L.gla_pages_copy.argtypes = pools + [_vp, _vp, _i, _vp]
+            L.gla_pages_copy.restype = _i
+            L.gla_pages_clear.argtypes = pools + [_vp, _i, _vp]
+            L.gla_pages_clear.restype = _i
+            L.gla_pages_compact.argtypes = pools + [_vp, _vp, _vp, _vp, _sz, _vp]
+            L.gla_pages_compact.restype = _i
+            L.gla_pages_compact_workspace_size.argtypes = [_i]
+            L.gla_pages_compact_workspace_size.restype = _sz
+            L.gla_layernorm_fwd.argtypes = [_vp, _vp, _vp, _vp, _f, _ll, _i, _i, _vp, _vp, _vp]
+            L.gla_layernorm_fwd.restype = _i
+            L.gla_layernorm_bwd.argtypes = [_vp, _vp, _vp, _vp, _f, _ll, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]
+            L.gla_layernorm_bwd.restype = _i
+            L.gla_layernorm_bwd_workspace_size.argtypes = [_ll, _i, _i]
+            L.gla_layernorm_bwd_workspace_size.restype = _sz
             L.gla_selftest_wait_timeout.argtypes = [ctypes.c_uint, _vp, _vp]
             L.gla_selftest_wait_timeout.restype = _i
             L.gla_check.argtypes = [_vp]
@@ -572,7 +610,7 @@ class _Call:
 
     __slots__ = ("torch", "device", "index", "here", "dtype", "code", "stream", "other", "kept", "f")
 
-    def __init__(self, x, stream):
+    def __init__(self, x, stream, element=True):
         self.torch = torch = _torch()
         self.device = x.device
         self.index = x.get_device()
@@ -580,7 +618,7 @@ class _Call:
             raise GlaError(GLA_ERR_INVALID_ARG, "argument", "tensors must live on a CUDA device")
         self.here = self.index == torch.cuda.current_device()
         self.dtype = x.dtype
-        self.code = _dtype_code(x)
+        self.code = _dtype_code(x) if element else None
         self.f = torch.float32
         self.other = None
         current = torch._C._cuda_getCurrentRawStream(self.index)
@@ -885,6 +923,206 @@ def gla_rmsnorm_bwd(s, w, dy, ds=None, eps=1e-6, *, dx=None, dw=None, want_dw=Tr
     c.run("gla_rmsnorm_bwd", *args, float(eps), rows, D, c.code, c.whole(dx, s.shape, "dx"), c.f32(dw, (D,), "dw"),
           *c.scratch(workspace, size, rows, D))
     return dx, dw
+
+
+def gla_layernorm(x, w=None, b=None, res=None, eps=1e-6, *, y=None, s=None, stream=None):
+    """Residual addition and layer norm over the last dimension: x, res [..., D],
+    w, b [D] fp32 or None. Returns (y, s): s = x + res (may be given as res, in
+    place), or None without res; y = w (s - mean(s)) / sqrt(var(s) + eps) + b."""
+    rows, D = _norm_rows(x)
+    c = _Call(x, stream)
+    y = c.empty(x.shape) if y is None else y
+    if s is None and res is not None:
+        s = c.empty(x.shape)
+    c.run("gla_layernorm_fwd", c.whole(x, x.shape, "x"), c.whole(res, x.shape, "res"), c.f32(w, (D,), "w"),
+          c.f32(b, (D,), "b"), float(eps), rows, D, c.code, c.whole(s, x.shape, "s"), c.whole(y, x.shape, "y"))
+    return y, s
+
+
+def gla_layernorm_bwd_workspace_size(rows, D, dtype=GLA_BF16) -> int:
+    return int(lib().gla_layernorm_bwd_workspace_size(rows, D, dtype))
+
+
+def gla_layernorm_bwd(s, w, dy, ds=None, eps=1e-6, *, dx=None, dw=None, db=None, want_dw=True, want_db=True,
+                      workspace=None, stream=None):
+    """Gradients of gla_layernorm: s (x + res, or x), dy, ds (the gradient that
+    reaches s itself, or None) [..., D], w [D] or None. Returns (dx, dw, db):
+    dx is x's and res's alike, dw and db [D] fp32 (None with want_dw=False,
+    want_db=False)."""
+    rows, D = _norm_rows(s)
+    c = _Call(s, stream)
+    args = (c.whole(s, s.shape, "s"), c.f32(w, (D,), "w"), c.whole(dy, s.shape, "dy"), c.whole(ds, s.shape, "ds"))
+    dx = c.empty(s.shape) if dx is None else dx
+    if dw is None and want_dw:
+        dw = c.empty((D,), c.torch.float32)
+    if db is None and want_db:
+        db = c.empty((D,), c.torch.float32)
+    size = None if dw is None and db is None else gla_layernorm_bwd_workspace_size
+    c.run("gla_layernorm_bwd", *args, float(eps), rows, D, c.code, c.whole(dx, s.shape, "dx"), c.f32(dw, (D,), "dw"),
+          c.f32(db, (D,), "db"), *c.scratch(workspace, size, rows, D))
+    return dx, dw, db
+
+
+def _heads(c, t, shape, name):
+    """Address and row step of [T, H, d] token rows an equal distance apart,
+    each with contiguous heads (a column range of a wider tensor passes)."""
+    if t.dtype is c.dtype and t.shape == shape and t.get_device() == c.index and t.is_contiguous():
+        return t.data_ptr(), shape[1] * shape[2]
+    c._refuse(t, shape, c.dtype, name)
+    T, H, d = shape
+    step = t.stride(0) if T > 1 else H * d
+    if t.numel() and (d > 1 and t.stride(2) != 1 or H > 1 and t.stride(1) != d or step < H * d):
+        raise GlaError(GLA_ERR_INVALID_ARG, "argument",
+                       f"{name} must have contiguous heads and token rows an equal distance apart")
+    return t.data_ptr(), step
+
+
+def _tree_args(c, T, cu_nodes, parents, slots):
+    """The trees of a call: addresses of the offsets, parents and slots, and the number of sequences."""
+    if cu_nodes.dim() != 1 or cu_nodes.numel() < 1:
+        raise GlaError(GLA_ERR_INVALID_ARG, "argument", "cu_nodes must hold one offset more than there are sequences")
+    nseq = cu_nodes.numel() - 1
+    return c.i32(cu_nodes, (nseq + 1,), "cu_nodes"), c.i32(parents, (T,), "parents"), c.i32(slots, (nseq,), "slots"), nseq
+
+
+def _tree_fwd(name, q, k, v, decay, gated, cu_nodes, parents, state_pool, slots, scale, o, stream):
+    T, H, dk = _lead(q, 3, "q")
+    dv = _lead(v, 3, "v")[2]
+    c = _Call(q, stream)
+    if scale is None:
+        scale = 1.0 / math.sqrt(dk)
+    cu, par, sl, nseq = _tree_args(c, T, cu_nodes, parents, slots)
+    n_slots = _lead(state_pool, 4, "state_pool")[0]
+    args = (*_heads(c, q, (T, H, dk), "q"), *_heads(c, k, (T, H, dk), "k"), *_heads(c, v, (T, H, dv), "v"),
+            c.f32(decay, (T, H) if gated else (H,), "g" if gated else "log_lambda"), float(scale), cu, par, sl,
+            c.f32(state_pool, (n_slots, H, dk, dv), "state_pool"), n_slots, nseq, T, H, dk, dv, c.code)
+    o = c.empty((T, H, dv)) if o is None else o
+    c.run(name, *args, c.whole(o, (T, H, dv), "o"))
+    return o
+
+
+def gla_tree_fwd(q, k, v, log_lambda, cu_nodes, parents, state_pool, slots=None, scale=None, *, o=None, stream=None):
+    """The outputs of drafted tokens: trees packed one behind another, tree n =
+    nodes [cu_nodes[n], cu_nodes[n+1]) (int32 CUDA tensor, at most 64 each),
+    parents [T] int32 (within the tree, before the node; -1: the sequence's
+    state). q, k [T,H,dk], v [T,H,dv] (column ranges of wider tensors pass),
+    state_pool [n_slots,H,dk,dv] fp32, read at slots[n] (int32 CUDA tensor, or
+    None for slot n) and left as it is. Returns o [T,H,dv]: what
+    gla_decode_step would give along each node's path."""
+    return _tree_fwd("gla_tree_fwd", q, k, v, log_lambda, False, cu_nodes, parents, state_pool, slots, scale, o, stream)
+
+
+def gla_tree_fwd_gated(q, k, v, g, cu_nodes, parents, state_pool, slots=None, scale=None, *, o=None, stream=None):
+    """gla_tree_fwd with a decay per node: g [T,H] fp32 (natural log, <= 0;
+    -inf clears the state along the node's path)."""
+    return _tree_fwd("gla_tree_fwd_gated", q, k, v, g, True, cu_nodes, parents, state_pool, slots, scale, o, stream)
+
+
+def _tree_commit(name, k, v, decay, gated, cu_nodes, parents, last, state_pool, slots, x, win_pool, stream):
+    T, H, dk = _lead(k, 3, "k")
+    dv = _lead(v, 3, "v")[2]
+    c = _Call(k, stream)
+    cu, par, sl, nseq = _tree_args(c, T, cu_nodes, parents, slots)
+    n_slots = _lead(state_pool, 4, "state_pool")[0]
+    D = 0 if x is None else _lead(x, 2, "x")[1]
+    c.run(name, *_heads(c, k, (T, H, dk), "k"), *_heads(c, v, (T, H, dv), "v"),
+          c.f32(decay, (T, H) if gated else (H,), "g" if gated else "log_lambda"), cu, par,
+          c.i32(last, (nseq,), "last"), sl, c.f32(state_pool, (n_slots, H, dk, dv), "state_pool"),
+          *c.rows(x, (T, D), "x"), c.f32(win_pool, (n_slots, 4, D), "win_pool"), n_slots, nseq, T, H, dk, dv, D, c.code)
+    return state_pool
+
+
+def gla_tree_commit(k, v, log_lambda, cu_nodes, parents, last, state_pool, slots=None, *, x=None, win_pool=None,
+                    stream=None):
+    """Keeps the accepted path of each tree of gla_tree_fwd: state_pool
+    [n_slots,H,dk,dv] fp32 at slots[n] becomes the state after node last[n]
+    (int32 CUDA tensor, within the tree; -1: it stays). With x [T,D] (the
+    Conv1d's inputs) and win_pool [n_slots,4,D] fp32 the windows take the path's
+    inputs likewise. Returns state_pool."""
+    return _tree_commit("gla_tree_commit", k, v, log_lambda, False, cu_nodes, parents, last, state_pool, slots, x,
+                        win_pool, stream)
+
+
+def gla_tree_commit_gated(k, v, g, cu_nodes, parents, last, state_pool, slots=None, *, x=None, win_pool=None,
+                          stream=None):
+    """gla_tree_commit with a decay per node: g [T,H] fp32, as gla_tree_fwd_gated."""
+    return _tree_commit("gla_tree_commit_gated", k, v, g, True, cu_nodes, parents, last, state_pool, slots, x, win_pool,
+                        stream)
+
+
+def gla_conv1d_tree(x, w, b, cu_nodes, parents, win_pool, slots=None, *, y=None, stream=None):
+    """The causal Conv1d with SiLU along each path of the trees of gla_tree_fwd:
+    x [T,D], w [D,4], b [D] or None; behind a tree's root the inputs of
+    win_pool [n_slots,4,D] fp32 at slots[n], which stays as it is. Returns y [T,D]."""
+    T, D = _lead(x, 2, "x")
+    c = _Call(x, stream)
+    cu, par, sl, nseq = _tree_args(c, T, cu_nodes, parents, slots)
+    n_slots = _lead(win_pool, 3, "win_pool")[0]
+    args = (*c.rows(x, (T, D), "x"), c.f32(w, (D, 4), "w"), c.f32(b, (D,), "b"), cu, par, sl,
+            c.f32(win_pool, (n_slots, 4, D), "win_pool"), n_slots, nseq, T, D, c.code)
+    y = c.empty((T, D)) if y is None else y
+    c.run("gla_conv1d_tree", *args, c.whole(y, (T, D), "y"))
+    return y
+
+
+class _PagesCall(_Call):
+    """A call over pools of any element type, one or a sequence of [n_slots, ...] tensors."""
+
+    __slots__ = ("pools",)
+
+    def __init__(self, pools, stream):
+        torch = _torch()
+        pools = [pools] if isinstance(pools, torch.Tensor) else list(pools)
+        if not pools:
+            raise GlaError(GLA_ERR_INVALID_ARG, "argument", "no pools")
+        super().__init__(pools[0], stream, element=False)
+        n = pools[0].shape[0] if pools[0].dim() else 0
+        for t in pools:
+            if t.get_device() != self.index or not t.is_contiguous() or t.dim() < 1 or t.shape[0] != n:
+                raise GlaError(GLA_ERR_INVALID_ARG, "argument",
+                               "pools must be contiguous, on one device and of as many pages each")
+        k = len(pools)
+        size = [t.numel() // n * t.element_size() if n else 4 for t in pools]
+        self.pools = ((_vp * k)(*[t.data_ptr() for t in pools]), (_ll * k)(*size), k if n else 0, n)
+
+
+def gla_pages_copy(pools, src, dst, *, stream=None):
+    """Copies pages of the pools (a tensor [n_slots, ...] or several, of any
+    type, as many pages each): page dst[i] becomes page src[i] (int32 CUDA
+    tensors), in every pool. A source may have several targets (one prompt
+    continued several times); targets are distinct and no other pair's source."""
+    c = _PagesCall(pools, stream)
+    n = _lead(src, 1, "src")[0]
+    c.run("gla_pages_copy", *c.pools, c.i32(src, (n,), "src"), c.i32(dst, (n,), "dst"), n)
+
+
+def gla_pages_clear(pools, slots, *, stream=None):
+    """Fills the pages `slots` (int32 CUDA tensor) of the pools with zeros, as a
+    new sequence needs them; pools as gla_pages_copy."""
+    c = _PagesCall(pools, stream)
+    n = _lead(slots, 1, "slots")[0]
+    c.run("gla_pages_clear", *c.pools, c.i32(slots, (n,), "slots"), n)
+
+
+def gla_pages_compact_workspace_size(n_slots, dtype=None) -> int:
+    return int(lib().gla_pages_compact_workspace_size(n_slots))
+
+
+def gla_pages_compact(pools, live, *, map=None, count=None, workspace=None, stream=None):
+    """Moves the pages in use to the front of the pools (as gla_pages_copy):
+    live [n_slots] bool or uint8 CUDA tensor. With L pages in use, those at L
+    and above move into the free ones below, in ascending order. Returns (map
+    [n_slots] int32: each page's new number, -1 where not in use; count [1]
+    int32: L), on the device."""
+    c = _PagesCall(pools, stream)
+    n = c.pools[3]
+    i32 = c.torch.int32
+    kind = c.torch.bool if live.dtype == c.torch.bool else c.torch.uint8
+    map = c.empty((n,), i32) if map is None else map
+    count = c.empty((1,), i32) if count is None else count
+    c.run("gla_pages_compact", *c.pools, c.whole(live, (n,), "live", kind), c.i32(map, (n,), "map"),
+          c.i32(count, (1,), "count"), *c.scratch(workspace, gla_pages_compact_workspace_size, n))
+    return map, count
 
 
 def gla_selftest_wait_timeout(limit_us=20000, *, stream=None):

@@ -91,6 +91,18 @@ gla_status check_chunk_shape(int B, int T, int H, int dk, int dv, int chunk, gla
         if ((p) && !aligned16(p)) return fail(GLA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name); \
     } while (0)
 
+// Device arrays of 4-byte numbers that kernels read one by one (a slice of a longer one passes).
+#define REQUIRE_INTS(p, name)                                                             \
+    do {                                                                                  \
+        if (!(p)) return fail(GLA_ERR_INVALID_ARG, "%s is NULL", name);                   \
+        OPTIONAL_INTS(p, name);                                                           \
+    } while (0)
+
+#define OPTIONAL_INTS(p, name)                                                            \
+    do {                                                                                  \
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(GLA_ERR_INVALID_ARG, "%s is not 4-byte aligned", name); \
+    } while (0)
+
 // Shape checks of the Conv1d entry points (B sequences of T tokens of D channels).
 gla_status check_conv_shape(int B, int T, int D, gla_dtype dtype) {
     if (dtype != GLA_BF16 && dtype != GLA_FP32) return fail(GLA_ERR_INVALID_ARG, "dtype %d is not GLA_BF16/GLA_FP32", (int)dtype);
@@ -209,6 +221,57 @@ gla_status check_ssm_pools(const SsmParams &p) {
     if ((p.conv_w != nullptr) != (p.win != nullptr))
         return fail(GLA_ERR_INVALID_ARG, "conv_w and win_pool come together");
     if (p.conv_b && !p.conv_w) return fail(GLA_ERR_INVALID_ARG, "conv_b without conv_w");
+    return GLA_OK;
+}
+
+// Shape checks of the calls over trees of drafted tokens: the state's part.
+gla_status check_tree_shape(int nseq, int total_T, int H, int dk, int dv, gla_dtype dtype) {
+    if (dtype != GLA_BF16 && dtype != GLA_FP32) return fail(GLA_ERR_INVALID_ARG, "dtype %d is not GLA_BF16/GLA_FP32", (int)dtype);
+    if (nseq < 0 || total_T < 0 || H < 0) return fail(GLA_ERR_INVALID_ARG, "negative size nseq=%d total_T=%d H=%d", nseq, total_T, H);
+    if (dk <= 0 || dv <= 0) return fail(GLA_ERR_INVALID_ARG, "dk=%d dv=%d must be positive", dk, dv);
+    if (dtype == GLA_BF16 && (dk != 96 || dv != 192))
+        return fail(GLA_ERR_UNSUPPORTED, "GLA_BF16 needs dk=96, dv=192 (got %d, %d)", dk, dv);
+    if (dtype == GLA_FP32 && (dk > 128 || dv > 256))
+        return fail(GLA_ERR_UNSUPPORTED, "GLA_FP32 needs dk <= 128, dv <= 256 (got %d, %d)", dk, dv);
+    if ((long double)nseq * H > 2147483647.0L) return fail(GLA_ERR_INVALID_ARG, "nseq*H too large");
+    if ((long double)H * (dk > dv ? dk : dv) > 2147483647.0L) return fail(GLA_ERR_INVALID_ARG, "H=%d too large", H);
+    return GLA_OK;
+}
+
+// The trees and the pool's slots.
+gla_status check_trees(const TreeParams &p) {
+    if (p.n_slots < 0) return fail(GLA_ERR_INVALID_ARG, "negative n_slots=%d", p.n_slots);
+    if (!p.slots && p.n_slots < p.nseq)
+        return fail(GLA_ERR_INVALID_ARG, "without slots the pool needs nseq=%d slots, has %d", p.nseq, p.n_slots);
+    REQUIRE_INTS(p.cu, "cu_nodes");
+    OPTIONAL_INTS(p.slots, "slots");
+    if (p.total_T > 0) REQUIRE_INTS(p.parents, "parents");
+    return GLA_OK;
+}
+
+// An array of [total_T, H, d] rows: 16-byte loads at bf16, single elements at fp32.
+gla_status check_heads(const void *ptr, int64_t ld, int H, int d, gla_dtype dtype, const char *name) {
+    return check_rows(ptr, ld, H * d, dtype == GLA_BF16 ? 2 : 4, dtype == GLA_BF16, name);
+}
+
+// The pools of a call over pages.
+gla_status check_pools(PageParams &p, void *const *pools, const int64_t *page_bytes, int n_pools, int n_slots) {
+    if (n_pools < 0 || n_slots < 0) return fail(GLA_ERR_INVALID_ARG, "negative size n_pools=%d n_slots=%d", n_pools, n_slots);
+    if (n_pools > kMaxPools) return fail(GLA_ERR_UNSUPPORTED, "%d pools in one call, at most %d", n_pools, kMaxPools);
+    if (n_pools > 0 && (!pools || !page_bytes)) return fail(GLA_ERR_INVALID_ARG, "pools or page_bytes is NULL");
+    long double all = 0;
+    for (int i = 0; i < n_pools; ++i) {
+        REQUIRE_PTR(pools[i], "a pool");
+        if (page_bytes[i] <= 0 || page_bytes[i] % 4 != 0)
+            return fail(GLA_ERR_UNSUPPORTED, "pages of %lld bytes: a positive multiple of 4 is needed", (long long)page_bytes[i]);
+        if (page_bytes[i] > (1ll << 36)) return fail(GLA_ERR_INVALID_ARG, "pages of %lld bytes are too large", (long long)page_bytes[i]);
+        all += page_bytes[i];
+        p.pool[i] = pools[i];
+        p.bytes[i] = (long)page_bytes[i];
+    }
+    if (all * n_slots > (long double)(1ull << 48) || all > (long double)(1ull << 40)) return fail(GLA_ERR_INVALID_ARG, "pools too large");
+    p.n_pools = n_pools;
+    p.n_slots = n_slots;
     return GLA_OK;
 }
 
@@ -946,6 +1009,268 @@ gla_status gla_rmsnorm_bwd(const void *s_in, const float *w, const void *dy, con
     return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_rmsnorm_bwd launch");
 }
 
+// The readout of every node of the trees; log_lambda or g.
+static gla_status tree_common(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                              const float *log_lambda, const float *g, float scale, const int *cu_nodes,
+                              const int *parents, const int *slots, const float *state_pool, int n_slots, int nseq,
+                              int total_T, int H, int dk, int dv, gla_dtype dtype, void *o, void *stream) {
+    t_err[0] = 0;
+    t_launches = 0;
+    gla_status st = check_tree_shape(nseq, total_T, H, dk, dv, dtype);
+    if (st != GLA_OK) return st;
+    if (nseq == 0 || H == 0) return GLA_OK;
+    TreeParams p{};
+    p.q = q, p.k = k, p.v = v, p.ldq = (long)ld_q, p.ldk = (long)ld_k, p.ldv = (long)ld_v;
+    p.log_lambda = log_lambda, p.g = g, p.scale = scale;
+    p.cu = cu_nodes, p.parents = parents, p.slots = slots, p.pool = const_cast<float *>(state_pool);
+    p.n_slots = n_slots, p.nseq = nseq, p.total_T = total_T, p.H = H, p.dk = dk, p.dv = dv, p.o = o;
+    if ((st = check_trees(p)) != GLA_OK) return st;
+    if (total_T == 0) return GLA_OK;
+    REQUIRE_PTR(state_pool, "state_pool");
+    OPTIONAL_INTS(log_lambda, "log_lambda");
+    OPTIONAL_INTS(g, "g");
+    if ((st = check_heads(q, ld_q, H, dk, dtype, "q")) != GLA_OK) return st;
+    if ((st = check_heads(k, ld_k, H, dk, dtype, "k")) != GLA_OK) return st;
+    if ((st = check_heads(v, ld_v, H, dv, dtype, "v")) != GLA_OK) return st;
+    REQUIRE_PTR(o, "o");
+    if (o == q || o == k || o == v || o == state_pool) return fail(GLA_ERR_INVALID_ARG, "o may not alias an input");
+    if ((st = status_word(&p.status)) != GLA_OK) return st;
+    int launches = 0;
+    const cudaError_t e = launch_tree_fwd(p, dtype == GLA_BF16, static_cast<cudaStream_t>(stream), &launches);
+    t_launches = launches;
+    return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_tree_fwd launch");
+}
+
+gla_status gla_tree_fwd(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                        const float *log_lambda, float scale, const int *cu_nodes, const int *parents,
+                        const int *slots, const float *state_pool, int n_slots, int nseq, int total_T, int H, int dk,
+                        int dv, gla_dtype dtype, void *o, void *stream) {
+    if (nseq > 0 && H > 0 && total_T > 0 && !log_lambda) {
+        reset_call_state();
+        return fail(GLA_ERR_INVALID_ARG, "log_lambda is NULL");
+    }
+    return tree_common(q, ld_q, k, ld_k, v, ld_v, log_lambda, nullptr, scale, cu_nodes, parents, slots, state_pool,
+                       n_slots, nseq, total_T, H, dk, dv, dtype, o, stream);
+}
+
+gla_status gla_tree_fwd_gated(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                              const float *g, float scale, const int *cu_nodes, const int *parents, const int *slots,
+                              const float *state_pool, int n_slots, int nseq, int total_T, int H, int dk, int dv,
+                              gla_dtype dtype, void *o, void *stream) {
+    if (nseq > 0 && H > 0 && total_T > 0 && !g) {
+        reset_call_state();
+        return fail(GLA_ERR_INVALID_ARG, "g is NULL");
+    }
+    return tree_common(q, ld_q, k, ld_k, v, ld_v, nullptr, g, scale, cu_nodes, parents, slots, state_pool, n_slots,
+                       nseq, total_T, H, dk, dv, dtype, o, stream);
+}
+
+// The accepted paths, kept; log_lambda or g.
+static gla_status commit_common(const void *k, int64_t ld_k, const void *v, int64_t ld_v, const float *log_lambda,
+                                const float *g, const int *cu_nodes, const int *parents, const int *last,
+                                const int *slots, float *state_pool, const void *x, int64_t ld_x, float *win_pool,
+                                int n_slots, int nseq, int total_T, int H, int dk, int dv, int D, gla_dtype dtype,
+                                void *stream) {
+    t_err[0] = 0;
+    t_launches = 0;
+    gla_status st = check_tree_shape(nseq, total_T, H, dk, dv, dtype);
+    if (st != GLA_OK) return st;
+    if ((x != nullptr) != (win_pool != nullptr)) return fail(GLA_ERR_INVALID_ARG, "x and win_pool come together");
+    if (x && (st = check_conv_shape(1, total_T, D, dtype)) != GLA_OK) return st;
+    if (nseq == 0) return GLA_OK;
+    TreeParams p{};
+    p.k = k, p.v = v, p.ldk = (long)ld_k, p.ldv = (long)ld_v, p.log_lambda = log_lambda, p.g = g;
+    p.cu = cu_nodes, p.parents = parents, p.slots = slots, p.last = last, p.pool = state_pool;
+    p.n_slots = n_slots, p.nseq = nseq, p.total_T = total_T, p.H = H, p.dk = dk, p.dv = dv;
+    p.x = x, p.ldx = (long)ld_x, p.win = win_pool, p.D = x ? D : 0;
+    if ((st = check_trees(p)) != GLA_OK) return st;
+    REQUIRE_INTS(last, "last");
+    if (total_T == 0) return GLA_OK;   // every tree is empty: nothing to keep
+    if (H > 0) {
+        REQUIRE_PTR(state_pool, "state_pool");
+        if ((st = check_heads(k, ld_k, H, dk, dtype, "k")) != GLA_OK) return st;
+        if ((st = check_heads(v, ld_v, H, dv, dtype, "v")) != GLA_OK) return st;
+        REQUIRE_INTS(g ? g : log_lambda, "the decay (log_lambda or g)");
+    }
+    if (x) {
+        if ((st = check_rows(x, ld_x, D, dtype == GLA_BF16 ? 2 : 4, true, "x")) != GLA_OK) return st;
+        REQUIRE_PTR(win_pool, "win_pool");
+    }
+    if (H == 0 && !x) return GLA_OK;
+    if ((long double)nseq * ((long double)H + D) > 2147483647.0L) return fail(GLA_ERR_INVALID_ARG, "nseq*(H+D) too large");
+    if ((st = status_word(&p.status)) != GLA_OK) return st;
+    int launches = 0;
+    const cudaError_t e = launch_tree_commit(p, dtype == GLA_BF16, static_cast<cudaStream_t>(stream), &launches);
+    t_launches = launches;
+    return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_tree_commit launch");
+}
+
+gla_status gla_tree_commit(const void *k, int64_t ld_k, const void *v, int64_t ld_v, const float *log_lambda,
+                           const int *cu_nodes, const int *parents, const int *last, const int *slots,
+                           float *state_pool, const void *x, int64_t ld_x, float *win_pool, int n_slots, int nseq,
+                           int total_T, int H, int dk, int dv, int D, gla_dtype dtype, void *stream) {
+    return commit_common(k, ld_k, v, ld_v, log_lambda, nullptr, cu_nodes, parents, last, slots, state_pool, x, ld_x,
+                         win_pool, n_slots, nseq, total_T, H, dk, dv, D, dtype, stream);
+}
+
+gla_status gla_tree_commit_gated(const void *k, int64_t ld_k, const void *v, int64_t ld_v, const float *g,
+                                 const int *cu_nodes, const int *parents, const int *last, const int *slots,
+                                 float *state_pool, const void *x, int64_t ld_x, float *win_pool, int n_slots,
+                                 int nseq, int total_T, int H, int dk, int dv, int D, gla_dtype dtype, void *stream) {
+    return commit_common(k, ld_k, v, ld_v, nullptr, g, cu_nodes, parents, last, slots, state_pool, x, ld_x, win_pool,
+                         n_slots, nseq, total_T, H, dk, dv, D, dtype, stream);
+}
+
+gla_status gla_conv1d_tree(const void *x, int64_t ld_x, const float *w, const float *b, const int *cu_nodes,
+                           const int *parents, const int *slots, const float *win_pool, int n_slots, int nseq,
+                           int total_T, int D, gla_dtype dtype, void *y, void *stream) {
+    t_err[0] = 0;
+    t_launches = 0;
+    gla_status st = check_conv_shape(nseq, total_T, D, dtype);
+    if (st != GLA_OK) return st;
+    OPTIONAL_PTR(b, "b");
+    if (nseq == 0) return GLA_OK;
+    TreeParams p{};
+    p.cu = cu_nodes, p.parents = parents, p.slots = slots, p.n_slots = n_slots, p.nseq = nseq, p.total_T = total_T;
+    p.x = x, p.ldx = (long)ld_x, p.w = w, p.b = b, p.win = const_cast<float *>(win_pool), p.D = D, p.y = y;
+    if ((st = check_trees(p)) != GLA_OK) return st;
+    if (total_T == 0) return GLA_OK;
+    if ((st = check_rows(x, ld_x, D, dtype == GLA_BF16 ? 2 : 4, true, "x")) != GLA_OK) return st;
+    REQUIRE_PTR(w, "w");
+    REQUIRE_PTR(win_pool, "win_pool");
+    REQUIRE_PTR(y, "y");
+    if (y == x || y == win_pool) return fail(GLA_ERR_INVALID_ARG, "y may not alias x or the windows");
+    if ((long double)nseq * D > 2147483647.0L) return fail(GLA_ERR_INVALID_ARG, "nseq*D too large");
+    if ((st = status_word(&p.status)) != GLA_OK) return st;
+    int launches = 0;
+    const cudaError_t e = launch_conv_tree(p, dtype == GLA_BF16, static_cast<cudaStream_t>(stream), &launches);
+    t_launches = launches;
+    return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_conv1d_tree launch");
+}
+
+// n page numbers of pools: copied from src, or (src NULL) cleared.
+static gla_status pages_common(void *const *pools, const int64_t *page_bytes, int n_pools, int n_slots, bool copy,
+                               const int *src, const int *dst, int n, const char *name, void *stream) {
+    t_err[0] = 0;
+    t_launches = 0;
+    PageParams p{};
+    gla_status st = check_pools(p, pools, page_bytes, n_pools, n_slots);
+    if (st != GLA_OK) return st;
+    if (n < 0) return fail(GLA_ERR_INVALID_ARG, "negative n=%d", n);
+    if (n == 0 || n_pools == 0) return GLA_OK;
+    if (copy) REQUIRE_INTS(src, "src");
+    REQUIRE_INTS(dst, copy ? "dst" : "slots");
+    p.n = n, p.src = copy ? src : nullptr, p.dst = dst;
+    if ((st = status_word(&p.status)) != GLA_OK) return st;
+    int launches = 0;
+    const cudaError_t e = launch_pages_move(p, static_cast<cudaStream_t>(stream), &launches);
+    t_launches = launches;
+    return e == cudaSuccess ? GLA_OK : cuda_fail(e, name);
+}
+
+gla_status gla_pages_copy(void *const *pools, const int64_t *page_bytes, int n_pools, int n_slots, const int *src,
+                          const int *dst, int n, void *stream) {
+    return pages_common(pools, page_bytes, n_pools, n_slots, true, src, dst, n, "gla_pages_copy launch", stream);
+}
+
+gla_status gla_pages_clear(void *const *pools, const int64_t *page_bytes, int n_pools, int n_slots, const int *slots,
+                           int n, void *stream) {
+    return pages_common(pools, page_bytes, n_pools, n_slots, false, nullptr, slots, n, "gla_pages_clear launch", stream);
+}
+
+size_t gla_pages_compact_workspace_size(int n_slots) {
+    return n_slots < 0 ? 0 : (size_t)(2 * ((long)n_slots / 2 + 1) + 1) * sizeof(int);
+}
+
+gla_status gla_pages_compact(void *const *pools, const int64_t *page_bytes, int n_pools, int n_slots,
+                             const unsigned char *live, int *map, int *count, void *workspace, size_t workspace_bytes,
+                             void *stream) {
+    t_err[0] = 0;
+    t_launches = 0;
+    PageParams p{};
+    gla_status st = check_pools(p, pools, page_bytes, n_pools, n_slots);
+    if (st != GLA_OK) return st;
+    REQUIRE_INTS(count, "count");
+    if (n_slots > 0) {
+        if (!live) return fail(GLA_ERR_INVALID_ARG, "live is NULL");
+        REQUIRE_INTS(map, "map");
+    }
+    REQUIRE_INTS(workspace, "workspace");
+    const size_t need = gla_pages_compact_workspace_size(n_slots);
+    if (workspace_bytes < need)
+        return fail(GLA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+    p.live = live, p.map = map, p.count = count, p.moves = static_cast<int *>(workspace);
+    if ((st = status_word(&p.status)) != GLA_OK) return st;
+    int launches = 0;
+    const cudaError_t e = launch_pages_compact(p, static_cast<cudaStream_t>(stream), &launches);
+    t_launches = launches;
+    return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_pages_compact launch");
+}
+
+gla_status gla_layernorm_fwd(const void *x, const void *res, const float *w, const float *b, float eps, int64_t rows,
+                             int D, gla_dtype dtype, void *s_out, void *y, void *stream) {
+    t_err[0] = 0;
+    t_launches = 0;
+    gla_status st = check_norm_shape(rows, D, dtype);
+    if (st != GLA_OK) return st;
+    if (!(eps >= 0.f)) return fail(GLA_ERR_INVALID_ARG, "eps must be >= 0");
+    OPTIONAL_PTR(res, "res");
+    OPTIONAL_PTR(w, "w");
+    OPTIONAL_PTR(b, "b");
+    OPTIONAL_PTR(s_out, "s_out");
+    if (rows == 0) return GLA_OK;
+    REQUIRE_PTR(x, "x");
+    REQUIRE_PTR(y, "y");
+    if (y == x || y == res || y == s_out) return fail(GLA_ERR_INVALID_ARG, "y may not alias x, res or s_out");
+    LayerNormParams p{x, res, w, b, eps, (long)rows, D, s_out, y};
+    int launches = 0;
+    const cudaError_t e = launch_layernorm_fwd(p, dtype == GLA_BF16, static_cast<cudaStream_t>(stream), &launches);
+    t_launches = launches;
+    return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_layernorm_fwd launch");
+}
+
+size_t gla_layernorm_bwd_workspace_size(int64_t rows, int D, gla_dtype dtype) {
+    if (check_norm_shape(rows, D, dtype) != GLA_OK || rows == 0) return 0;
+    return (size_t)layernorm_bwd_grid((long)rows, D) * 2 * D * sizeof(float);
+}
+
+gla_status gla_layernorm_bwd(const void *s_in, const float *w, const void *dy, const void *ds, float eps, int64_t rows,
+                             int D, gla_dtype dtype, void *dx, float *dw, float *db, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+    t_err[0] = 0;
+    t_launches = 0;
+    gla_status st = check_norm_shape(rows, D, dtype);
+    if (st != GLA_OK) return st;
+    if (!(eps >= 0.f)) return fail(GLA_ERR_INVALID_ARG, "eps must be >= 0");
+    OPTIONAL_PTR(w, "w");
+    OPTIONAL_PTR(ds, "ds");
+    OPTIONAL_PTR(dw, "dw");
+    OPTIONAL_PTR(db, "db");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int launches = 0;
+    if (rows == 0) {
+        cudaError_t e = dw ? cudaMemsetAsync(dw, 0, (size_t)D * sizeof(float), s) : cudaSuccess;
+        if (e == cudaSuccess && db) e = cudaMemsetAsync(db, 0, (size_t)D * sizeof(float), s);
+        return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_layernorm_bwd(rows=0)");
+    }
+    REQUIRE_PTR(s_in, "s");
+    REQUIRE_PTR(dy, "dy");
+    REQUIRE_PTR(dx, "dx");
+    if (dx == s_in) return fail(GLA_ERR_INVALID_ARG, "dx may not alias s");
+    const bool sums = dw || db;
+    if (sums) {
+        REQUIRE_PTR(workspace, "workspace");
+        const size_t need = gla_layernorm_bwd_workspace_size(rows, D, dtype);
+        if (workspace_bytes < need)
+            return fail(GLA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+    }
+    LayerNormParams p{s_in, nullptr, w, nullptr, eps, (long)rows, D, nullptr, nullptr, dy, ds, dx, dw, db,
+                      sums ? static_cast<float *>(workspace) : nullptr};
+    const cudaError_t e = launch_layernorm_bwd(p, dtype == GLA_BF16, s, &launches);
+    t_launches = launches;
+    return e == cudaSuccess ? GLA_OK : cuda_fail(e, "gla_layernorm_bwd launch");
+}
+
 gla_status gla_selftest_wait_timeout(unsigned int limit_us, int *result, void *stream) {
     t_err[0] = 0;
     t_launches = 0;
@@ -976,8 +1301,8 @@ gla_status gla_check(void *stream) {
         if (e != cudaSuccess) return cuda_fail(e, "clear status word");
         if (word & kDevTimeout) return fail(GLA_ERR_TIMEOUT, "a device-side wait timed out (status 0x%x)", word);
         if (word & kDevBadState)
-            return fail(GLA_ERR_INVALID_ARG, "a sequence had a bad cu_seqlens or slots entry and was skipped "
-                                             "(status 0x%x)", word);
+            return fail(GLA_ERR_INVALID_ARG, "a sequence had a bad cu_seqlens or slots entry (or a tree's offset, parent "
+                                             "or accepted node, or a page number) and was skipped (status 0x%x)", word);
         return fail(GLA_ERR_CUDA, "device reported an internal error (status 0x%x)", word);
     }
     return GLA_OK;

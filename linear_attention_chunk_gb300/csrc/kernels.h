@@ -187,6 +187,63 @@ long norm_bwd_grid(long rows, int D);
 cudaError_t launch_rmsnorm_fwd(const NormParams &p, bool bf16, cudaStream_t s, int *launches);
 cudaError_t launch_rmsnorm_bwd(const NormParams &p, bool bf16, cudaStream_t s, int *launches);
 
+// Trees of drafted tokens over the state pool (tree.cu). Packed nodes: tree n
+// is nodes [cu[n], cu[n+1]), parents local to the tree (-1: the state itself).
+// k, v, q: [total_T, H, d] with token rows ld* elements apart; o contiguous.
+struct TreeParams {
+    const void *q, *k, *v;
+    long ldq, ldk, ldv;
+    const float *log_lambda;     // [H], or
+    const float *g;              // [total_T, H]
+    float scale;
+    const int *cu, *parents, *slots, *last;
+    float *pool;                 // [n_slots, H, dk, dv]
+    int n_slots, nseq, total_T, H, dk, dv;
+    void *o;
+    // The convolution: inputs [total_T, D] (rows ldx apart), windows [n_slots, 4, D].
+    const void *x;
+    long ldx;
+    const float *w, *b;
+    float *win;
+    int D;
+    void *y;
+    unsigned int *status;
+};
+cudaError_t launch_tree_fwd(const TreeParams &p, bool bf16, cudaStream_t s, int *launches);
+cudaError_t launch_tree_commit(const TreeParams &p, bool bf16, cudaStream_t s, int *launches);
+cudaError_t launch_conv_tree(const TreeParams &p, bool bf16, cudaStream_t s, int *launches);
+
+// Copies and clears of pages in several pools at once (pages.cu).
+constexpr int kMaxPools = 128;
+struct PageParams {
+    void *pool[kMaxPools];
+    long bytes[kMaxPools];       // of a page: a multiple of 4
+    int n_pools, n_slots, n;     // n: pairs, or pages to clear
+    const int *src, *dst;        // src NULL: clear
+    const unsigned char *live;   // compact: [n_slots]
+    int *map, *count;            // compact: [n_slots], [1]
+    int *moves;                  // compact's workspace: sources, then targets, then their number
+    unsigned int *status;
+};
+cudaError_t launch_pages_move(const PageParams &p, cudaStream_t s, int *launches);
+cudaError_t launch_pages_compact(PageParams &p, cudaStream_t s, int *launches);
+
+// Residual addition, layer norm and its gradients (layernorm.cu).
+struct LayerNormParams {
+    const void *x, *res;         // forward: s = x + res (res or NULL); backward: x is s
+    const float *w, *b;          // [D] or NULL (one, zero)
+    float eps;
+    long rows;
+    int D;
+    void *s_out, *y;             // s_out or NULL
+    const void *dy, *ds;         // backward: ds or NULL
+    void *dx;
+    float *dw, *db, *part;       // part [layernorm_bwd_grid, 2 D], or NULL (neither wanted)
+};
+long layernorm_bwd_grid(long rows, int D);
+cudaError_t launch_layernorm_fwd(const LayerNormParams &p, bool bf16, cudaStream_t s, int *launches);
+cudaError_t launch_layernorm_bwd(const LayerNormParams &p, bool bf16, cudaStream_t s, int *launches);
+
 // Sums over rows, out[c] = sum_r part[r * pitch + c], in a fixed order; the
 // outputs fp32 or bf16, several in one launch (reduce.cu). cols and pitch are
 // multiples of 4, part is 16-byte aligned; a NULL output is left out.

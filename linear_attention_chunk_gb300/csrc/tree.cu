@@ -1,0 +1,276 @@
+// tree.cu -- trees of drafted tokens over the state pool: the serving steps of
+// speculative decoding, where a draft model proposes a tree of tokens for each
+// sequence, the model scores all of them at once, and the path that is
+// accepted is kept. Per sequence and head, for node i with parent p(i) (-1:
+// the sequence's state page S itself):
+//     S_i = exp(g_i) S_p(i) + k_i v_i^T,   S_-1 = S,   o_i = scale S_i^T q_i
+// (g_i = log_lambda[h] for the fixed per-head decay). Unrolled along the path
+// from the state to i, with D_i the decay of all its nodes and W_ij that of
+// the nodes behind j, up to i:
+//     o_i = scale ( D_i S^T q_i + sum_{j on the path} W_ij (q_i . k_j) v_j ),
+// so no node's state is formed and the page is read once for all of them.
+// A decay of 0 clears what lies before it, also where that is not finite.
+// The commit forms S_last alone and stores it; the convolution in front of the
+// mixer reads the last three inputs of each node's path, behind the root those
+// of the sequence's window.
+#include "ssm_common.cuh"
+#include "tree_common.cuh"
+
+namespace gla {
+namespace {
+
+using namespace tree;
+
+constexpr int kThreads = 256, kBlock = 16;   // threads of a CTA; nodes a thread sums at once
+
+__host__ __device__ constexpr int round4(int v) { return (v + 3) / 4 * 4; }
+
+// Any head sizes and element type: one CTA per (sequence, head), a thread a
+// state column. fp32's validation mode.
+template <typename T> __global__ void __launch_bounds__(kThreads) tree_fwd_kernel(const TreeParams p) {
+    extern __shared__ float4 smem4[];
+    __shared__ int par[kNodes];
+    __shared__ unsigned long long path[kNodes];
+    __shared__ float far[kNodes], gate[kNodes];
+    const int n = blockIdx.x / p.H, h = blockIdx.x % p.H, tid = threadIdx.x;
+    const Tree t = open_tree(p, n, par);
+    if (t.nodes <= 0) {
+        if (t.nodes < 0 && tid == 0) atomicOr(p.status, kDevBadState);
+        return;
+    }
+    const int M = t.nodes, dk = p.dk, dv = p.dv, ldq = round4(dk);
+    float *qs = reinterpret_cast<float *>(smem4), *ks = qs + kNodes * ldq, *P = ks + kNodes * ldq;
+    const T *q = static_cast<const T *>(p.q) + (size_t)t.first * p.ldq + (size_t)h * dk;
+    const T *k = static_cast<const T *>(p.k) + (size_t)t.first * p.ldk + (size_t)h * dk;
+    const T *v = static_cast<const T *>(p.v) + (size_t)t.first * p.ldv + (size_t)h * dv;
+    for (int e = tid; e < M * ldq; e += kThreads) {
+        const int i = e / ldq, c = e % ldq;
+        qs[e] = c < dk ? Elem<T>::load(q + (size_t)i * p.ldq + c) : 0.f;
+        ks[e] = c < dk ? Elem<T>::load(k + (size_t)i * p.ldk + c) : 0.f;
+    }
+    const float l2 = p.g ? 0.f : log2_of_decay(p.log_lambda[h]);
+    if (p.g && tid < M) gate[tid] = p.g[(size_t)(t.first + tid) * p.H + h];
+    __syncthreads();
+    if (tid < M) path[tid] = walk(tid, par, p.g ? gate : nullptr, l2, far[tid], [&](int j, float w) { P[tid * kNodes + j] = w; });
+    __syncthreads();
+    for (int e = tid; e < M * M; e += kThreads) {
+        const int i = e / M, j = e % M;
+        if (!(path[i] >> j & 1)) continue;
+        float dot = 0.f;
+        for (int c = 0; c < dk; ++c) dot = fmaf(qs[i * ldq + c], ks[j * ldq + c], dot);
+        P[i * kNodes + j] *= dot;
+    }
+    __syncthreads();
+    const int lanes = (dv + 31) / 32 * 32, groups = kThreads / lanes;
+    const int c = tid % lanes, grp = tid / lanes;
+    if (grp >= groups || c >= dv) return;
+    const float *S = p.pool + (t.slot * p.H + h) * ((size_t)dk * dv) + c;
+    T *o = static_cast<T *>(p.o) + ((size_t)t.first * p.H + h) * dv + c;
+    for (int nb = grp * kBlock; nb < M; nb += groups * kBlock) {
+        float acc[kBlock] = {};
+        for (int r = 0; r < dk; r += 4) {
+            float s[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s[u] = r + u < dk ? __ldg(S + (size_t)(r + u) * dv) : 0.f;
+#pragma unroll
+            for (int i = 0; i < kBlock; ++i) {
+                const float4 a = *reinterpret_cast<const float4 *>(qs + (nb + i) * ldq + r);
+                acc[i] = fmaf(a.x, s[0], fmaf(a.y, s[1], fmaf(a.z, s[2], fmaf(a.w, s[3], acc[i]))));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBlock; ++i) {
+            if (nb + i >= M) break;
+            float sum = far[nb + i] == 0.f ? 0.f : far[nb + i] * acc[i];
+            for (unsigned long long m = path[nb + i]; m; m &= m - 1) {
+                const int j = __ffsll((long long)m) - 1;
+                sum = fmaf(P[(nb + i) * kNodes + j], Elem<T>::load(v + (size_t)j * p.ldv + c), sum);
+            }
+            Elem<T>::store(o + (size_t)(nb + i) * p.H * dv, p.scale * sum);
+        }
+    }
+}
+
+// ----------------------------------------------------------------- commit
+constexpr int kCommit = 192;   // threads; at 96 x 192 the layout of the decode step: four columns of every fourth row
+
+// The window's new rows for four channels: the last four inputs of the path,
+// before them what the window held.
+template <typename T> __device__ void commit_window(const TreeParams &p, const Tree &t, int last, const int *par, int c) {
+    if (c >= p.D) return;
+    float *win = p.win + (size_t)t.slot * ssm::kTaps * p.D + c;
+    int at[ssm::kTaps], len = 0;
+    for (int j = last; j >= 0 && len < ssm::kTaps; j = par[j]) at[len++] = j;
+    float4 row[ssm::kTaps];
+#pragma unroll
+    for (int r = 0; r < ssm::kTaps; ++r) {
+        const int back = ssm::kTaps - 1 - r;
+        if (back < len) {
+            const T *x = static_cast<const T *>(p.x) + (size_t)(t.first + at[back]) * p.ldx + c;
+            row[r] = make_float4(Elem<T>::load(x), Elem<T>::load(x + 1), Elem<T>::load(x + 2), Elem<T>::load(x + 3));
+        } else {
+            row[r] = *reinterpret_cast<const float4 *>(win + (size_t)(r + len) * p.D);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < ssm::kTaps; ++r) *reinterpret_cast<float4 *>(win + (size_t)r * p.D) = row[r];
+}
+
+// One CTA per (sequence, head), and behind a sequence's heads its window's
+// channels, 768 a CTA. k0: 96 x 192.
+template <typename T, bool k0> __global__ void __launch_bounds__(kCommit) tree_commit_kernel(const TreeParams p, int per) {
+    extern __shared__ float4 smem4[];
+    __shared__ int par[kNodes], way[kNodes], s_len;
+    __shared__ float s_w[kNodes], gate[kNodes], s_far;
+    float *kt = reinterpret_cast<float *>(smem4);          // [path node][dk], decayed
+    const int n = blockIdx.x / per, h = blockIdx.x % per, tid = threadIdx.x;
+    const int last = p.last[n];
+    const Tree t = open_tree(p, n, par);
+    if (t.nodes < 0 || last < -1 || last >= t.nodes) {
+        if (tid == 0) atomicOr(p.status, kDevBadState);
+        return;
+    }
+    if (last < 0) return;
+    if (h >= p.H) {
+        commit_window<T>(p, t, last, par, ((h - p.H) * kCommit + tid) * 4);
+        return;
+    }
+    const int dk = k0 ? 96 : p.dk, dv = k0 ? 192 : p.dv;
+    float *S = p.pool + (t.slot * p.H + h) * ((size_t)dk * dv);
+    constexpr int kCols = 48, kRows = 24;
+    const int cg = tid % kCols, rg = tid / kCols;
+    float4 s[k0 ? kRows : 1];
+    if constexpr (k0) {
+#pragma unroll
+        for (int m = 0; m < kRows; ++m) s[m] = __ldcs(reinterpret_cast<const float4 *>(S) + (rg + 4 * m) * kCols + cg);
+    }
+    if (p.g && tid < t.nodes) gate[tid] = p.g[(size_t)(t.first + tid) * p.H + h];
+    __syncthreads();
+    if (tid == 0) {
+        int len = 0;
+        walk(last, par, p.g ? gate : nullptr, p.g ? 0.f : log2_of_decay(p.log_lambda[h]), s_far, [&](int j, float w) {
+            way[len] = j;
+            s_w[len++] = w;
+        });
+        s_len = len;
+    }
+    __syncthreads();
+    const int len = s_len;
+    const float far = s_far;
+    for (int e = tid; e < len * dk; e += kCommit) {
+        const int j = e / dk, r = e % dk;
+        kt[e] = s_w[j] * Elem<T>::load(static_cast<const T *>(p.k) + (size_t)(t.first + way[j]) * p.ldk + (size_t)h * dk + r);
+    }
+    __syncthreads();
+    const T *v = static_cast<const T *>(p.v) + (size_t)t.first * p.ldv + (size_t)h * dv;
+    if constexpr (k0) {
+#pragma unroll
+        for (int m = 0; m < kRows; ++m)
+            s[m] = far == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                              : make_float4(far * s[m].x, far * s[m].y, far * s[m].z, far * s[m].w);
+        for (int j = 0; j < len; ++j) {
+            const T *vj = v + (size_t)way[j] * p.ldv + 4 * cg;
+            const float a = Elem<T>::load(vj), b = Elem<T>::load(vj + 1), c = Elem<T>::load(vj + 2), d = Elem<T>::load(vj + 3);
+#pragma unroll
+            for (int m = 0; m < kRows; ++m) {
+                const float kr = kt[j * 96 + rg + 4 * m];
+                s[m].x = fmaf(kr, a, s[m].x);
+                s[m].y = fmaf(kr, b, s[m].y);
+                s[m].z = fmaf(kr, c, s[m].z);
+                s[m].w = fmaf(kr, d, s[m].w);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < kRows; ++m) __stcs(reinterpret_cast<float4 *>(S) + (rg + 4 * m) * kCols + cg, s[m]);
+    } else {
+        for (int e = tid; e < dk * dv; e += kCommit) {
+            const int r = e / dv, c = e % dv;
+            float x = far == 0.f ? 0.f : far * S[e];
+            for (int j = 0; j < len; ++j) x = fmaf(kt[j * dk + r], Elem<T>::load(v + (size_t)way[j] * p.ldv + c), x);
+            S[e] = x;
+        }
+    }
+}
+
+// ------------------------------------------------------------- convolution
+constexpr int kConv = 128;   // threads, eight channels each
+
+template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(const TreeParams p, int per) {
+    __shared__ int par[kNodes];
+    const int n = blockIdx.x / per, tid = threadIdx.x, c = ((int)(blockIdx.x % per) * kConv + tid) * 8;
+    const Tree t = open_tree(p, n, par);
+    if (t.nodes < 0 && tid == 0) atomicOr(p.status, kDevBadState);
+    if (t.nodes <= 0 || c >= p.D) return;
+    const bool whole = c + 8 <= p.D;
+    const T *x = static_cast<const T *>(p.x) + (size_t)t.first * p.ldx + c;
+    const float *win = p.win + (size_t)t.slot * ssm::kTaps * p.D + c;
+    T *y = static_cast<T *>(p.y) + (size_t)t.first * p.D + c;
+    float w[8][4], b[8];
+    ssm::param8(p.b, c, whole, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float4 a = c + j < p.D ? __ldg(reinterpret_cast<const float4 *>(p.w) + c + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+        w[j][0] = a.x; w[j][1] = a.y; w[j][2] = a.z; w[j][3] = a.w;
+    }
+    for (int i = 0; i < t.nodes; ++i) {
+        float acc[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = b[j];
+        int a = i;                                        // a node, or -1 - r: r rows before the window's last
+#pragma unroll
+        for (int tap = 3; tap >= 0; --tap) {
+            float u[8];
+            if (a >= 0) {
+                ssm::raw_unpack(ssm::raw_load(x + (size_t)a * p.ldx, whole), u);
+                a = par[a];
+            } else {
+                ssm::param8(win + (size_t)(4 + a) * p.D, 0, whole, u);
+                --a;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = fmaf(w[j][tap], u[j], acc[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = ssm::silu(acc[j]);
+        ssm::store8(y + (size_t)i * p.D, acc, whole);
+    }
+}
+
+template <typename T> cudaError_t fwd_any(const TreeParams &p, cudaStream_t s, int *launches) {
+    const int bytes = (2 * kNodes * round4(p.dk) + kNodes * kNodes) * (int)sizeof(float);
+    cudaError_t e = cudaFuncSetAttribute(tree_fwd_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    tree_fwd_kernel<T><<<(unsigned)((size_t)p.nseq * p.H), kThreads, bytes, s>>>(p);
+    if (launches) ++*launches;
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t commit(const TreeParams &p, cudaStream_t s, int *launches) {
+    const int per = p.H + (p.x ? (p.D + 4 * kCommit - 1) / (4 * kCommit) : 0);
+    const int bytes = kNodes * p.dk * (int)sizeof(float);   // at most 32 KB
+    auto *kern = p.dk == 96 && p.dv == 192 ? tree_commit_kernel<T, true> : tree_commit_kernel<T, false>;
+    kern<<<(unsigned)((size_t)p.nseq * per), kCommit, bytes, s>>>(p, per);
+    if (launches) ++*launches;
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t conv(const TreeParams &p, cudaStream_t s, int *launches) {
+    const int per = (p.D + 8 * kConv - 1) / (8 * kConv);
+    conv_tree_kernel<T><<<(unsigned)((size_t)p.nseq * per), kConv, 0, s>>>(p, per);
+    if (launches) ++*launches;
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tree_fwd(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {
+    return bf16 ? fwd_any<__nv_bfloat16>(p, s, launches) : fwd_any<float>(p, s, launches);
+}
+cudaError_t launch_tree_commit(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {
+    return bf16 ? commit<__nv_bfloat16>(p, s, launches) : commit<float>(p, s, launches);
+}
+cudaError_t launch_conv_tree(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {
+    return bf16 ? conv<__nv_bfloat16>(p, s, launches) : conv<float>(p, s, launches);
+}
+
+}  // namespace gla
