@@ -264,6 +264,7 @@ template <typename T> cudaError_t conv(const TreeParams &p, cudaStream_t s, int 
 }  // namespace
 
 cudaError_t launch_tree_fwd(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {
+    if (bf16 && tree_fwd_tc_fits(p)) return launch_tree_fwd_tc(p, s, launches);
     return bf16 ? fwd_any<__nv_bfloat16>(p, s, launches) : fwd_any<float>(p, s, launches);
 }
 cudaError_t launch_tree_commit(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {
