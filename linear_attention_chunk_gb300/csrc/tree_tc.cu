@@ -234,7 +234,7 @@ __device__ __forceinline__ void producer(const TreeParams &p, const CUtensorMap 
     }
 }
 
-template <bool kGate> __global__ void __maxnreg__(144) tree_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm, const TreeParams p) {
+template <bool kGate> __global__ void __launch_bounds__(kThreads, 2) tree_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm, const TreeParams p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = smem_u32(sm);
@@ -269,11 +269,55 @@ template <bool kGate> __global__ void __maxnreg__(144) tree_fwd_tc_kernel(const 
         wait(FULL_M + (it & 1), (uint32_t)(it >> 1) & 1u);
         const int M = ok ? m->nodes : 0, tiles = (M + 15) / 16;
         const uint32_t par = (uint32_t)done & 1u;
-        float acc[4][4][4];
-        uint32_t pair[2][2][4];   // P of at most two 16 x 16 tiles: high and low halves
+        named_sync(1, kSlices * 32);   // every warp is done with the unit before's P
         if (M > 0) {
-            // Q S: a step of 16 rows of S at a time
+            // P, tile by tile below the diagonal, the tiles dealt out to the warps
             wait(FULL_Q, par);
+            wait(FULL_K, par);
+            const float factor = ok ? m->factor : 0.f;
+#pragma unroll 1
+            for (int x = warp; ok && x < tiles * (tiles + 1) / 2; x += kSlices) {
+                const int ti = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, tj = x - ti * (ti + 1) / 2;
+                float c[2][4] = {};
+#pragma unroll
+                for (int ks = 0; ks < kDk / 16; ++ks) {
+                    uint32_t a[4], b[4];
+                    ldmatrix4(a, sQ + (ti * 16 + a_row) * kPitchQ + (ks * 16 + a_col) * 2);
+                    ldmatrix4(b, sK + (tj * 16 + b_row) * kPitchQ + (ks * 16 + b_col) * 2);
+                    mma16816(c[0], a, b[0], b[1]);
+                    mma16816(c[1], a, b[2], b[3]);
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int i = ti * 16 + g + 8 * r;
+                    const unsigned long long path = m->path[i];
+                    const float2 si = m->sum[i];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int j = tj * 16 + b * 8 + 2 * q4;
+                        float v[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float2 sj = m->sum[j + e];
+                            const float w = exp2f(((si.x - sj.x) + (si.y - sj.y)) * factor);
+                            // (a fixed decay of 0: a node's own weight is 2^(-inf 0))
+                            v[e] = !(path >> (j + e) & 1) || w == 0.f ? 0.f : (i == j + e ? 1.f : w) * c[b][2 * r + e];
+                        }
+                        uint32_t hi, lo;
+                        split(v[0], v[1], hi, lo);
+                        const uint32_t at = (uint32_t)i * kPitchP + (uint32_t)j * 2;
+                        *reinterpret_cast<uint32_t *>(sm + kOffPh + at) = hi;
+                        *reinterpret_cast<uint32_t *>(sm + kOffPl + at) = lo;
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(FREE_K));
+        }
+        named_sync(1, kSlices * 32);
+        if (M > 0) {
+            float acc[4][4][4];
+            // Q S: a step of 16 rows of S at a time
             wait(FULL_S + warp, par);
             const uint32_t sS = base + (uint32_t)((done * kSlices + warp) % kStages) * kBox;
 #pragma unroll
@@ -310,7 +354,10 @@ template <bool kGate> __global__ void __maxnreg__(144) tree_fwd_tc_kernel(const 
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(EMPTY_S + warp));
+            if (lane == 0) {
+                mbar_arrive(bar(EMPTY_S + warp));
+                mbar_arrive(bar(FREE_Q));
+            }
             // the state's decay: 0 clears it, whatever it holds
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -324,70 +371,6 @@ template <bool kGate> __global__ void __maxnreg__(144) tree_fwd_tc_kernel(const 
                             acc[i][t][c] = f == 0.f ? 0.f : f * acc[i][t][c];
                         }
                 }
-            // P, tile by tile below the diagonal, the tiles dealt out to the warps
-            wait(FULL_K, par);
-            if (ok) {
-                const float factor = m->factor;
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const int x = warp + n * kSlices;
-                    if (x >= tiles * (tiles + 1) / 2) break;
-                    const int ti = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, tj = x - ti * (ti + 1) / 2;
-                    float c[2][4] = {};
-#pragma unroll
-                    for (int ks = 0; ks < kDk / 16; ++ks) {
-                        uint32_t a[4], b[4];
-                        ldmatrix4(a, sQ + (ti * 16 + a_row) * kPitchQ + (ks * 16 + a_col) * 2);
-                        ldmatrix4(b, sK + (tj * 16 + b_row) * kPitchQ + (ks * 16 + b_col) * 2);
-                        mma16816(c[0], a, b[0], b[1]);
-                        mma16816(c[1], a, b[2], b[3]);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int i = ti * 16 + g + 8 * r;
-                        const unsigned long long path = m->path[i];
-                        const float2 si = m->sum[i];
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            float v[2];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int j = tj * 16 + b * 8 + 2 * q4 + e;
-                                const float2 sj = m->sum[j];
-                                const float w = exp2f(((si.x - sj.x) + (si.y - sj.y)) * factor);
-                                // (a fixed decay of 0: a node's own weight is 2^(-inf 0))
-                                v[e] = !(path >> j & 1) || w == 0.f ? 0.f : (i == j ? 1.f : w) * c[b][2 * r + e];
-                            }
-                            split(v[0], v[1], pair[n][0][2 * r + b], pair[n][1][2 * r + b]);
-                        }
-                    }
-                }
-            }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(FREE_Q));
-                mbar_arrive(bar(FREE_K));
-            }
-        }
-        named_sync(1, kSlices * 32);   // every warp is done with the unit before's P
-        if (M > 0 && ok) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int x = warp + n * kSlices;
-                if (x >= tiles * (tiles + 1) / 2) break;
-                const int ti = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, tj = x - ti * (ti + 1) / 2;
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const uint32_t at = (uint32_t)(ti * 16 + g + 8 * r) * kPitchP + (uint32_t)(tj * 16 + b * 8 + 2 * q4) * 2;
-                        *reinterpret_cast<uint32_t *>(sm + kOffPh + at) = pair[n][0][2 * r + b];
-                        *reinterpret_cast<uint32_t *>(sm + kOffPl + at) = pair[n][1][2 * r + b];
-                    }
-            }
-        }
-        named_sync(1, kSlices * 32);
-        if (M > 0) {
             // P V: 16 nodes j at a time
             wait(FULL_V, par);
             bool dirty = false;
