@@ -5,23 +5,30 @@
 // bytes fp32), so the call is bound by HBM: the pages, q, k, v and o once.
 //
 // S goes from HBM to the tensor cores by way of shared memory and registers
-// alone: a ring of TMA boxes (96 rows x 32 channels, 128-byte swizzle), one
-// consumer warp a box, which splits each entry into two bf16 halves (hi + lo,
-// 2^-17 of the entry: drafted tokens get the values that the decode step's fp32
-// arithmetic gives, to a few 2^-17) and multiplies Q by both. A box has too few
-// products a byte to wait for tcgen05's operand layouts in shared memory (the
-// halves would have to be written there first); warp-level products on
-// registers leave the tensor pipe far from its limit. P = W o Q K^T is split likewise.
+// alone: a ring of six TMA stages of 16 rows (128-byte swizzle), whose entries
+// the consumer warps split into two bf16 halves (hi + lo, 2^-17 of the entry:
+// drafted tokens get the values that the decode step's fp32 arithmetic gives,
+// to a few 2^-17) and multiply Q by both. A stage has too few products a byte
+// to pay for tcgen05's operand layouts (the halves would first go back to
+// shared memory); warp-level products take them from registers. P = W o Q K^T
+// is split likewise.
 //
-// One producer warp per CTA runs ahead: offsets, parents and decays of the next
-// unit, the paths as bit masks and running sums by pointer doubling, the rows of
-// q, k and v by bulk copies. Two CTAs on an SM: one's product phases lie under
-// the other's loads.
+// One CTA an SM, no CTA-wide barrier, every hand-over by mbarrier:
+//   warp 17      the trees, up to four units (sequence, head) ahead: offsets,
+//                parents and decays, the paths as bit masks and running sums by
+//                pointer doubling;
+//   warp 16      TMA, a unit ahead: 16 rows of q, k or v a copy (a tree's last
+//                copy may hold rows of the next one), a stage of S as it comes free;
+//   warps 12-15  P of the unit ahead, 16 x 16 tiles below the diagonal;
+//   warps 0-11   16 channels each: Q S step by step, the decay, P V, the rows out.
+// (Two CTAs of six consumer warps that did all of it in turn, P between CTA
+// barriers and one warp a slice of S: 112 us where this one takes MEASURED at
+// 256 trees of up to 32 nodes, H = 16, and 101 at 128 of 48 to 64.)
 //
-// Accumulator columns: of the four 8-column tiles of a box, column n of tile t
-// is channel 4 n + t. A thread's entries of S are then 16-byte loads (the
+// Accumulator columns: of the two 8-column tiles of a warp, column n of tile t
+// is channel 2 n + t. A thread's entries of S are then 8-byte loads (the
 // swizzle keeps them free of bank conflicts), and the channels of a row that it
-// ends with are eight neighbours, stored as 16 bytes.
+// ends with are four neighbours; four threads store a 32-byte sector.
 #include "ptx.cuh"
 #include "tmap.h"
 #include "tree_common.cuh"
@@ -32,30 +39,35 @@ namespace {
 using namespace ptx;
 using tree::kNodes;
 
-constexpr int kDk = 96, kDv = 192, kSlice = 32, kSlices = kDv / kSlice;   // consumer warps: one a slice of channels
-constexpr int kThreads = (kSlices + 1) * 32, kStages = 3;
-constexpr uint32_t kBox = kDk * kSlice * 4;
-constexpr uint32_t kPitchQ = kDk * 2 + 16, kPitchV = kDv * 2 + 16, kPitchP = kNodes * 2 + 16;   // (16 more: no bank conflicts)
-constexpr uint32_t kOffQ = kStages * kBox, kOffK = kOffQ + kNodes * kPitchQ, kOffV = kOffK + kNodes * kPitchQ,
-                   kOffPh = kOffV + kNodes * kPitchV, kOffPl = kOffPh + kNodes * kPitchP, kOffMeta = kOffPl + kNodes * kPitchP;
+constexpr int kDk = 96, kDv = 192, kSteps = kDk / 16;
+constexpr int kConsumers = 12, kScorers = 4, kThreads = (kConsumers + kScorers + 2) * 32;
+constexpr int kMetas = 4;
+constexpr uint32_t kBox = 16 * 128, kStage = 6 * kBox;   // S: 16 rows x 32 channels; x 192
+constexpr uint32_t kTileQ = 16 * kDk * 2, kTileV = 16 * kDv * 2, kNodeQ = kNodes / 16 * kTileQ, kNodeV = kNodes / 16 * kTileV;
+constexpr uint32_t kPitchP = kNodes * 2 + 16;   // (16 more: no bank conflicts)
+constexpr uint32_t kOffQ = kSteps * kStage, kOffK = kOffQ + 2 * kNodeQ, kOffV = kOffK + 2 * kNodeQ, kOffPh = kOffV + 2 * kNodeV,
+                   kOffPl = kOffPh + 2 * kNodes * kPitchP, kOffMeta = kOffPl + 2 * kNodes * kPitchP;   // (a unit's and the next one's)
 constexpr float kClear = -104.f;   // e^-104 is 0 in fp32
 constexpr float kLog2e = 1.4426950408889634f;
 
-// A unit's tree, made by the producer.
+// A unit's tree.
 struct Meta {
     unsigned long long path[kNodes];   // the nodes on the path that no decay of 0 cuts off, the node itself included
     float2 sum[kNodes];                // their summed logs (fixed decay: their number), high and low part
     float far[kNodes];                 // the state's decay
     float factor;                      // W_ij = 2^(factor (sum_i - sum_j))
-    int first, nodes, pad;
+    int first, nodes, row;             // row: the first of its page in the pool, as rows of dv
 };
-// The boxes of a unit take the ring's stages in turn, but their barriers go by slice: a waiter sees every phase of its own.
-enum { FULL_S = 0, EMPTY_S = FULL_S + kSlices, FULL_Q = EMPTY_S + kSlices, FULL_K, FULL_V, FREE_Q, FREE_K, FREE_V, FULL_M, FREE_M = FULL_M + 2, BARS = FREE_M + 2 };
-constexpr uint32_t kOffNext = kOffMeta + 2 * sizeof(Meta), kOffBars = kOffNext + kNodes * 4, kOffAbort = kOffBars + BARS * 8,
+enum { FULL_S = 0, EMPTY_S = FULL_S + kSteps, FULL_M = EMPTY_S + kSteps, FREE_M = FULL_M + kMetas, FULL_QK = FREE_M + kMetas, FULL_V = FULL_QK + 2, FULL_P = FULL_V + 2, FREE = FULL_P + 2, BARS = FREE + 2 };
+constexpr uint32_t kOffNext = kOffMeta + kMetas * sizeof(Meta), kOffBars = kOffNext + kNodes * 4, kOffAbort = kOffBars + BARS * 8,
                    kSmem = kOffAbort + 16 + 1024;   // (1,024: the base is rounded up for the swizzle)
+struct Maps {
+    CUtensorMap s, q, k, v;
+};
+static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -65,19 +77,24 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
                  : "r"(at)
                  : "memory");
 }
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1)
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
 }
-__device__ __forceinline__ float4 lds4(uint32_t at) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+// Rows of q or k: tiles of 16 rows, of which each has three pieces of 32
+// columns with the 64-byte swizzle. Address of row r's columns c .. c + 7.
+__device__ __forceinline__ uint32_t at_q(uint32_t base, uint32_t r, uint32_t c) {
+    return base + (r >> 4) * kTileQ + (c >> 5) * 1024 + sw64_offset(r & 15, (c & 31) >> 3);
+}
+__device__ __forceinline__ float2 lds2f(uint32_t at) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
     return v;
 }
-__device__ __forceinline__ uint2 lds2(uint32_t at) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+__device__ __forceinline__ uint32_t lds1(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
     return v;
 }
 // Two numbers as their bf16 halves: x = hi + lo up to 2^-17.
@@ -97,60 +114,64 @@ __device__ __forceinline__ float2 add_parts(float2 a, float2 b) {   // high and 
     return make_float2(h, e - (h - s));
 }
 
-// What the producer reads of a unit ahead of time.
-struct Ahead {
-    int first, nodes, slot;   // nodes -1: a bad offset or slot
-    int par[2];               // of nodes lane and lane + 32
-    float gate[2];
-};
-
+// The trees of the units, one warp. A unit's offsets are read two units ahead, its parents and decays one.
 template <bool kGate>
-__device__ __forceinline__ void producer(const TreeParams &p, const CUtensorMap *tm, unsigned char *sm, uint32_t base, const WaitCtl &ctl, long units) {
+__device__ __forceinline__ void planner(const TreeParams &p, unsigned char *sm, uint32_t base, const WaitCtl &ctl, uint32_t units) {
     const int lane = threadIdx.x % 32;
     auto bar = [&](int i) { return base + kOffBars + 8u * (uint32_t)i; };
     int *next = reinterpret_cast<int *>(sm + kOffNext);
-    auto offsets = [&](long u, Ahead &a) {
-        if (u >= units) return;
-        const int n = (int)(u / p.H);
-        const int lo = __ldg(p.cu + n), hi = __ldg(p.cu + n + 1);
-        a.slot = p.slots ? __ldg(p.slots + n) : n;
-        a.first = lo;
-        a.nodes = lo < 0 || hi < lo || hi > p.total_T || hi - lo > kNodes || a.slot < 0 || a.slot >= p.n_slots ? -1 : hi - lo;
+    const uint32_t H = (uint32_t)p.H;
+    struct Offsets {
+        int lo, hi, slot;
     };
-    auto nodes = [&](long u, Ahead &a) {
-        if (u >= units) return;
+    struct Nodes {
+        int first, count, slot;   // count -1: a bad offset or slot
+        int par[2];               // of nodes lane and lane + 32
+        float gate[2];
+    };
+    auto offsets = [&](uint32_t u) {
+        Offsets r{0, 0, 0};
+        if (u < units) {
+            const uint32_t n = u / H;
+            r.lo = __ldg(p.cu + n);
+            r.hi = __ldg(p.cu + n + 1);
+            r.slot = p.slots ? __ldg(p.slots + n) : (int)n;
+        }
+        return r;
+    };
+    auto nodes = [&](uint32_t u, const Offsets &r) {
+        Nodes a;
+        a.first = r.lo;
+        a.slot = r.slot;
+        a.count = r.lo < 0 || r.hi < r.lo || r.hi > p.total_T || r.hi - r.lo > kNodes || r.slot < 0 || r.slot >= p.n_slots ? -1 : r.hi - r.lo;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = lane + 32 * e;
-            a.par[e] = i < a.nodes ? __ldg(p.parents + a.first + i) : -1;
-            if (kGate) a.gate[e] = i < a.nodes ? __ldg(p.g + (size_t)(a.first + i) * p.H + u % p.H) : 0.f;
+            const bool in = u < units && i < a.count;
+            a.par[e] = in ? __ldg(p.parents + a.first + i) : -1;
+            a.gate[e] = kGate && in ? __ldg(p.g + (size_t)(a.first + i) * H + u % H) : 0.f;
         }
+        return a;
     };
-    auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, ctl)); };
-    Ahead a[2];   // this unit's and the next one's
-    offsets(blockIdx.x, a[0]);
-    nodes(blockIdx.x, a[0]);
-    offsets((long)blockIdx.x + gridDim.x, a[1]);
-    long boxes = 0, done = 0;
-    bool ok = true;
+    Nodes ahead = nodes(blockIdx.x, offsets(blockIdx.x));
+    Offsets further = offsets(blockIdx.x + gridDim.x);
     int it = 0;
-    for (long u = blockIdx.x; u < units && ok; u += gridDim.x, ++it) {
-        Ahead now = a[0];
-        a[0] = a[1];
-        nodes(u + gridDim.x, a[0]);
-        offsets(u + 2L * gridDim.x, a[1]);
-        const int h = (int)(u % p.H);
-        bool bad = now.nodes < 0;
+    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x, ++it) {
+        Nodes now = ahead;
+        ahead = nodes(u + gridDim.x, further);
+        further = offsets(u + 2 * gridDim.x);
+        const int h = (int)(u % H), s = it % kMetas;
+        bool bad = now.count < 0;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) bad |= lane + 32 * e < now.nodes && (now.par[e] < -1 || now.par[e] >= lane + 32 * e);
+        for (int e = 0; e < 2; ++e) bad |= lane + 32 * e < now.count && (now.par[e] < -1 || now.par[e] >= lane + 32 * e);
         if (__any_sync(0xffffffffu, bad)) {
-            now.nodes = 0;
+            now.count = 0;
             if (lane == 0) atomicOr(p.status, kDevBadState);
         }
-        const int s = it & 1, M = now.nodes;
-        if (it >= 2 && !(ok = wait(FREE_M + s, (uint32_t)((it >> 1) - 1) & 1u))) break;
+        const int M = now.count;
+        if (it >= kMetas && !__all_sync(0xffffffffu, mbar_wait(bar(FREE_M + s), (uint32_t)(it / kMetas - 1) & 1u, ctl))) return;
         Meta *m = reinterpret_cast<Meta *>(sm + kOffMeta) + s;
-        const float fixed = kGate ? 0.f : p.log_lambda[h];
+        const float fixed = kGate ? 0.f : __ldg(p.log_lambda + h);
         const float factor = kGate ? kLog2e : log2_of_decay(fixed);
         // Pointer doubling: node x's path so far, and the node it goes on from (-1: the state, -2: cut off by a decay of 0).
         int ptr[2];
@@ -173,12 +194,12 @@ __device__ __forceinline__ void producer(const TreeParams &p, const CUtensorMap 
             float2 add[2];
             int on[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (ptr[e] >= 0) {
-                    up[e] = m->path[ptr[e]];
-                    add[e] = m->sum[ptr[e]];
-                    on[e] = next[ptr[e]];
-                }
+            for (int e = 0; e < 2; ++e) {
+                const int x = ptr[e] < 0 ? 0 : ptr[e];
+                up[e] = m->path[x];
+                add[e] = m->sum[x];
+                on[e] = next[x];
+            }
             __syncwarp();
 #pragma unroll
             for (int e = 0; e < 2; ++e)
@@ -195,168 +216,209 @@ __device__ __forceinline__ void producer(const TreeParams &p, const CUtensorMap 
             m->factor = factor;
             m->first = now.first;
             m->nodes = M;
+            m->row = (now.slot * p.H + h) * kDk;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(FULL_M + s));
-        if (M == 0) continue;
-        auto rows = [&](int full, uint32_t off, const void *src, long ld, uint32_t bytes, uint32_t pitch) {
-            if (lane == 0) mbar_arrive_expect_tx(bar(full), (uint32_t)M * bytes);
-            __syncwarp();
-            for (int i = lane; i < M; i += 32)
-                bulk_load(base + off + (uint32_t)i * pitch,
-                          static_cast<const char *>(src) + (size_t)(now.first + i) * ld * 2 + (size_t)h * bytes, bytes, bar(full));
-        };
-        auto box = [&](int j) {   // box number `boxes`: into the stage of the box kStages before it
-            const long last = boxes - kStages;
-            if (last >= 0 && !(ok = wait(EMPTY_S + (int)(last % kSlices), (uint32_t)(last / kSlices) & 1u))) return;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar(FULL_S + j), kBox);
-                tma_load_2d(base + (uint32_t)(boxes % kStages) * kBox, tm, bar(FULL_S + j), j * kSlice, (now.slot * p.H + h) * kDk);
-            }
-            ++boxes;
-        };
-        const uint32_t par = (uint32_t)(done - 1) & 1u;
-        for (int j = 0; j < kStages && ok; ++j) box(j);
-        if (!ok || (done > 0 && !(ok = wait(FREE_Q, par)))) break;
-        rows(FULL_Q, kOffQ, p.q, p.ldq, kDk * 2, kPitchQ);
-        if (done > 0 && !(ok = wait(FREE_K, par))) break;
-        rows(FULL_K, kOffK, p.k, p.ldk, kDk * 2, kPitchQ);
-        for (int j = kStages; j < kSlices && ok; ++j) box(j);
-        if (!ok || (done > 0 && !(ok = wait(FREE_V, par)))) break;
-        rows(FULL_V, kOffV, p.v, p.ldv, kDv * 2, kPitchV);
-        ++done;
-    }
-    if (!ok) {   // a wait gave up: the copies in flight land before the CTA ends
-        for (long k = boxes > kStages ? boxes - kStages : 0; k < boxes; ++k)
-            mbar_wait_drain(bar(FULL_S + (int)(k % kSlices)), (uint32_t)(k / kSlices) & 1u, 1000000ull);
-        for (int b : {FULL_Q, FULL_K, FULL_V})
-            for (long k = done > 0 ? done - 1 : 0; k <= done; ++k) mbar_wait_drain(bar(b), (uint32_t)k & 1u, 1000000ull);
     }
 }
 
-template <bool kGate> __global__ void __launch_bounds__(kThreads, 2) tree_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm, const TreeParams p) {
+// The copies of the units, one warp.
+__device__ __forceinline__ void producer(const Maps &maps, const TreeParams &p, unsigned char *sm, uint32_t base, const WaitCtl &ctl, uint32_t units) {
+    const int lane = threadIdx.x % 32;
+    auto bar = [&](int i) { return base + kOffBars + 8u * (uint32_t)i; };
+    auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, ctl)); };
+    int done = 0, it = 0, stages = 0;   // units with nodes, units, stages filled
+    bool ok = true;
+    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x, ++it) {
+        const int s = it & 1, t = it % kMetas, h = (int)(u % (uint32_t)p.H);
+        if (!(ok = wait(FULL_M + t, (uint32_t)(it / kMetas) & 1u))) break;
+        const Meta *m = reinterpret_cast<const Meta *>(sm + kOffMeta) + t;
+        const int M = m->nodes, first = m->first, row = m->row, tiles = (M + 15) / 16;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(FREE_M + t));
+        if (it >= 2 && !(ok = wait(FREE + s, (uint32_t)((it >> 1) - 1) & 1u))) break;
+        if (lane == 0) {   // (of an empty tree nothing is copied, but the barriers go on)
+            mbar_arrive_expect_tx(bar(FULL_QK + s), (uint32_t)tiles * 2 * kTileQ);
+            for (int i = 0; i < tiles; ++i) {
+                const uint32_t at = (uint32_t)s * kNodeQ + (uint32_t)i * kTileQ;
+                tma_load_3d(base + kOffQ + at, &maps.q, bar(FULL_QK + s), 0, first + i * 16, h * 3);
+                tma_load_3d(base + kOffK + at, &maps.k, bar(FULL_QK + s), 0, first + i * 16, h * 3);
+            }
+            mbar_arrive_expect_tx(bar(FULL_V + s), (uint32_t)tiles * kTileV);
+            for (int i = 0; i < tiles; ++i)
+                tma_load_3d(base + kOffV + (uint32_t)s * kNodeV + (uint32_t)i * kTileV, &maps.v, bar(FULL_V + s), 0, first + i * 16, h * 3);
+        }
+        if (M == 0) continue;
+        for (int j = 0; j < kSteps; ++j) {
+            if (done > 0 && !(ok = wait(EMPTY_S + j, (uint32_t)(done - 1) & 1u))) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar(FULL_S + j), kStage);
+                tma_load_3d(base + (uint32_t)j * kStage, &maps.s, bar(FULL_S + j), 0, row + j * 16, 0);
+            }
+            stages = done * kSteps + j + 1;
+        }
+        if (!ok) break;
+        ++done;
+    }
+    if (!ok) {   // a wait gave up: the copies in flight land before the CTA ends
+        for (int k = stages > kSteps ? stages - kSteps : 0; k < stages; ++k)
+            mbar_wait_drain(bar(FULL_S + k % kSteps), (uint32_t)(k / kSteps) & 1u, 1000000ull);
+        for (int k = it > 1 ? it - 1 : 0; k <= it; ++k)
+            for (int b : {FULL_QK, FULL_V}) mbar_wait_drain(bar(b + (k & 1)), (uint32_t)(k >> 1) & 1u, 1000000ull);
+    }
+}
+
+// P of every unit, the tiles dealt out to the scorers' warps.
+__device__ __forceinline__ void scorer(unsigned char *sm, uint32_t base, const WaitCtl &ctl, uint32_t units, int warp) {
+    const int lane = threadIdx.x % 32, g = lane / 4, q4 = lane % 4;
+    const uint32_t a_row = lane % 16, a_col = lane / 16 * 8;                            // ldmatrix: A fragments of 16 rows
+    const uint32_t b_row = (lane & 7) + (lane >> 4) * 8, b_col = (lane >> 3 & 1) * 8;   // and B fragments of 16 columns
+    auto bar = [&](int i) { return base + kOffBars + 8u * (uint32_t)i; };
+    auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, ctl)); };
+    int it = 0;
+    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x, ++it) {
+        const int s = it & 1, meta = it % kMetas;
+        const uint32_t par = (uint32_t)(it >> 1) & 1u;
+        if (!wait(FULL_M + meta, (uint32_t)(it / kMetas) & 1u) || !wait(FULL_QK + s, par)) return;
+        const Meta *m = reinterpret_cast<const Meta *>(sm + kOffMeta) + meta;
+        const int tiles = (m->nodes + 15) / 16;
+        const float factor = m->factor;
+        const uint32_t sQ = base + kOffQ + (uint32_t)s * kNodeQ, sK = base + kOffK + (uint32_t)s * kNodeQ;
+        for (int x = warp; x < tiles * (tiles + 1) / 2; x += kScorers) {
+            const int ti = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, tj = x - ti * (ti + 1) / 2;
+            float c[2][4] = {};
+#pragma unroll
+            for (int half = 0; half < kSteps; half += 3) {
+                uint32_t a[3][4], b[3][4];
+#pragma unroll
+                for (int ks = 0; ks < 3; ++ks) {
+                    ldmatrix4(a[ks], at_q(sQ, ti * 16 + a_row, (half + ks) * 16 + a_col));
+                    ldmatrix4(b[ks], at_q(sK, tj * 16 + b_row, (half + ks) * 16 + b_col));
+                }
+#pragma unroll
+                for (int ks = 0; ks < 3; ++ks) {
+                    mma16816(c[0], a[ks], b[ks][0], b[ks][1]);
+                    mma16816(c[1], a[ks], b[ks][2], b[ks][3]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int i = ti * 16 + g + 8 * r;
+                const unsigned long long path = m->path[i];
+                const float2 si = m->sum[i];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int j = tj * 16 + b * 8 + 2 * q4;
+                    float v[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 sj = m->sum[j + e];
+                        const float w = exp2f(((si.x - sj.x) + (si.y - sj.y)) * factor);
+                        // (a fixed decay of 0: a node's own weight is 2^(-inf 0))
+                        v[e] = !(path >> (j + e) & 1) || w == 0.f ? 0.f : (i == j + e ? 1.f : w) * c[b][2 * r + e];
+                    }
+                    uint32_t hi, lo;
+                    split(v[0], v[1], hi, lo);
+                    const uint32_t at = (uint32_t)(s * kNodes + i) * kPitchP + (uint32_t)j * 2;
+                    *reinterpret_cast<uint32_t *>(sm + kOffPh + at) = hi;
+                    *reinterpret_cast<uint32_t *>(sm + kOffPl + at) = lo;
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(bar(FULL_P + s));
+            mbar_arrive(bar(FREE + s));
+            mbar_arrive(bar(FREE_M + meta));
+        }
+    }
+}
+
+template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = smem_u32(sm);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const long units = (long)p.nseq * p.H;
+    const uint32_t units = (uint32_t)p.nseq * (uint32_t)p.H;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + kOffAbort);
     const WaitCtl ctl{abort_flag, p.status};
     auto bar = [&](int i) { return base + kOffBars + 8u * (uint32_t)i; };
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        for (int i = 0; i < BARS; ++i)   // one arrival (a copy's, the slice's warp, the producer), or one a consumer warp
-            mbar_init(bar(i), (i >= FREE_Q && i <= FREE_V) || i >= FREE_M ? kSlices : 1);
+        for (int i = 0; i < BARS; ++i)   // arrivals: one of a copy or the producer, or one a warp
+            mbar_init(bar(i), i >= FREE ? kConsumers + kScorers : i >= FULL_P ? kScorers : i >= FREE_M && i < FULL_QK ? kConsumers + kScorers + 1
+                              : i >= EMPTY_S && i < FULL_M ? kConsumers : 1);
         fence_mbar_init();
-        prefetch_tmap(&tm);
+        prefetch_tmap(&maps.s);
+        prefetch_tmap(&maps.q);
+        prefetch_tmap(&maps.k);
+        prefetch_tmap(&maps.v);
     }
     __syncthreads();
-    if (warp == kSlices) {
-        producer<kGate>(p, &tm, sm, base, ctl, units);
+    if (warp == kConsumers + kScorers + 1) {
+        planner<kGate>(p, sm, base, ctl, units);
+        return;
+    }
+    if (warp == kConsumers + kScorers) {
+        producer(maps, p, sm, base, ctl, units);
+        return;
+    }
+    if (warp >= kConsumers) {
+        scorer(sm, base, ctl, units, warp - kConsumers);
         return;
     }
     const int g = lane / 4, q4 = lane % 4;   // a fragment's row (or column), its pair of columns (or rows)
-    const uint32_t sQ = base + kOffQ, sK = base + kOffK, sV = base + kOffV, sPh = base + kOffPh, sPl = base + kOffPl;
-    const uint32_t a_row = lane % 16, a_col = lane / 16 * 8;                        // ldmatrix: A fragments of 16 rows
-    const uint32_t b_row = (lane & 7) + (lane >> 4) * 8, b_col = (lane >> 3 & 1) * 8;   // and B fragments of 16 columns
-    // Never left before its end: the warps meet twice a unit, also when a wait has given up.
-    bool ok = true;
-    long done = 0;
-    int it = 0;
-    auto wait = [&](int b, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(b), parity, ctl)); };
-    for (long u = blockIdx.x; u < units; u += gridDim.x, ++it) {
-        const Meta *m = reinterpret_cast<const Meta *>(sm + kOffMeta) + (it & 1);
-        wait(FULL_M + (it & 1), (uint32_t)(it >> 1) & 1u);
-        const int M = ok ? m->nodes : 0, tiles = (M + 15) / 16;
-        const uint32_t par = (uint32_t)done & 1u;
-        named_sync(1, kSlices * 32);   // every warp is done with the unit before's P
+    const uint32_t a_row = lane % 16, a_col = lane / 16 * 8;
+    // This thread's entries of a stage: channels 2 g, 2 g + 1 of the warp's 16, rows 2 q4, 2 q4 + 1 and eight below those
+    const uint32_t box = base + (uint32_t)(warp / 2) * kBox + (uint32_t)(g & 1) * 8, chunk = (uint32_t)(warp & 1) * 4 + (uint32_t)(g >> 1);
+    const uint32_t x0 = box + (uint32_t)(2 * q4) * 128 + ((chunk ^ (uint32_t)(2 * q4)) << 4);
+    const uint32_t x1 = box + (uint32_t)(2 * q4 + 1) * 128 + ((chunk ^ (uint32_t)(2 * q4 + 1)) << 4);
+    auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, ctl)); };
+    int done = 0, it = 0;
+    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x, ++it) {
+        const int s = it & 1, meta = it % kMetas;
+        const uint32_t par = (uint32_t)(it >> 1) & 1u;
+        if (!wait(FULL_M + meta, (uint32_t)(it / kMetas) & 1u) || !wait(FULL_QK + s, par)) return;
+        const Meta *m = reinterpret_cast<const Meta *>(sm + kOffMeta) + meta;
+        const int M = m->nodes, tiles = (M + 15) / 16;
         if (M > 0) {
-            // P, tile by tile below the diagonal, the tiles dealt out to the warps
-            wait(FULL_Q, par);
-            wait(FULL_K, par);
-            const float factor = ok ? m->factor : 0.f;
-#pragma unroll 1
-            for (int x = warp; ok && x < tiles * (tiles + 1) / 2; x += kSlices) {
-                const int ti = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, tj = x - ti * (ti + 1) / 2;
-                float c[2][4] = {};
-#pragma unroll
-                for (int ks = 0; ks < kDk / 16; ++ks) {
-                    uint32_t a[4], b[4];
-                    ldmatrix4(a, sQ + (ti * 16 + a_row) * kPitchQ + (ks * 16 + a_col) * 2);
-                    ldmatrix4(b, sK + (tj * 16 + b_row) * kPitchQ + (ks * 16 + b_col) * 2);
-                    mma16816(c[0], a, b[0], b[1]);
-                    mma16816(c[1], a, b[2], b[3]);
-                }
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int i = ti * 16 + g + 8 * r;
-                    const unsigned long long path = m->path[i];
-                    const float2 si = m->sum[i];
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const int j = tj * 16 + b * 8 + 2 * q4;
-                        float v[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float2 sj = m->sum[j + e];
-                            const float w = exp2f(((si.x - sj.x) + (si.y - sj.y)) * factor);
-                            // (a fixed decay of 0: a node's own weight is 2^(-inf 0))
-                            v[e] = !(path >> (j + e) & 1) || w == 0.f ? 0.f : (i == j + e ? 1.f : w) * c[b][2 * r + e];
-                        }
-                        uint32_t hi, lo;
-                        split(v[0], v[1], hi, lo);
-                        const uint32_t at = (uint32_t)i * kPitchP + (uint32_t)j * 2;
-                        *reinterpret_cast<uint32_t *>(sm + kOffPh + at) = hi;
-                        *reinterpret_cast<uint32_t *>(sm + kOffPl + at) = lo;
-                    }
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(FREE_K));
-        }
-        named_sync(1, kSlices * 32);
-        if (M > 0) {
-            float acc[4][4][4];
-            // Q S: a step of 16 rows of S at a time
-            wait(FULL_S + warp, par);
-            const uint32_t sS = base + (uint32_t)((done * kSlices + warp) % kStages) * kBox;
+            const uint32_t sQ = base + kOffQ + (uint32_t)s * kNodeQ;
+            float acc[4][2][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) acc[i][t][c] = 0.f;
-            if (ok) {
-#pragma unroll 2
-                for (int ks = 0; ks < kDk / 16; ++ks) {
-                    const uint32_t r = (uint32_t)(ks * 16 + 2 * q4);
-                    const uint32_t e = sS + r * 128 + (((uint32_t)g ^ (r & 7u)) << 4), f = sS + (r + 1) * 128 + (((uint32_t)g ^ ((r + 1) & 7u)) << 4);
-                    const float4 x0 = lds4(e), x1 = lds4(f), x2 = lds4(e + 1024), x3 = lds4(f + 1024);
-                    uint32_t hi[4][2], lo[4][2];
-                    split(x0.x, x1.x, hi[0][0], lo[0][0]);
-                    split(x0.y, x1.y, hi[1][0], lo[1][0]);
-                    split(x0.z, x1.z, hi[2][0], lo[2][0]);
-                    split(x0.w, x1.w, hi[3][0], lo[3][0]);
-                    split(x2.x, x3.x, hi[0][1], lo[0][1]);
-                    split(x2.y, x3.y, hi[1][1], lo[1][1]);
-                    split(x2.z, x3.z, hi[2][1], lo[2][1]);
-                    split(x2.w, x3.w, hi[3][1], lo[3][1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (i >= tiles) break;
-                        uint32_t a[4];
-                        ldmatrix4(a, sQ + (i * 16 + a_row) * kPitchQ + (ks * 16 + a_col) * 2);
+            for (int ks = 0; ks < kSteps; ++ks) {
+                if (!wait(FULL_S + ks, (uint32_t)done & 1u)) return;
+                const uint32_t st = (uint32_t)ks * kStage;
+                const float2 y0 = lds2f(x0 + st), y1 = lds2f(x1 + st), y2 = lds2f(x0 + st + 1024), y3 = lds2f(x1 + st + 1024);
+                uint32_t hi[2][2], lo[2][2];
+                split(y0.x, y1.x, hi[0][0], lo[0][0]);
+                split(y0.y, y1.y, hi[1][0], lo[1][0]);
+                split(y2.x, y3.x, hi[0][1], lo[0][1]);
+                split(y2.y, y3.y, hi[1][1], lo[1][1]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(EMPTY_S + ks));
+                uint32_t a[4][4];
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) mma16816(acc[i][t], a, hi[t][0], hi[t][1]);
+                for (int i = 0; i < 4; ++i)
+                    if (i < tiles) ldmatrix4(a[i], at_q(sQ, i * 16 + a_row, ks * 16 + a_col));
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) mma16816(acc[i][t], a, lo[t][0], lo[t][1]);
+                for (int i = 0; i < 4; ++i)
+                    if (i < tiles) {
+                        mma16816(acc[i][0], a[i], hi[0][0], hi[0][1]);
+                        mma16816(acc[i][1], a[i], hi[1][0], hi[1][1]);
                     }
-                }
-            }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(EMPTY_S + warp));
-                mbar_arrive(bar(FREE_Q));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < tiles) {
+                        mma16816(acc[i][0], a[i], lo[0][0], lo[0][1]);
+                        mma16816(acc[i][1], a[i], lo[1][0], lo[1][1]);
+                    }
             }
             // the state's decay: 0 clears it, whatever it holds
 #pragma unroll
@@ -364,7 +426,7 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 2) tree_fwd_tc
                 if (i < tiles) {
                     const float f0 = m->far[i * 16 + g], f1 = m->far[i * 16 + g + 8];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
+                    for (int t = 0; t < 2; ++t)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const float f = c < 2 ? f0 : f1;
@@ -372,86 +434,96 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 2) tree_fwd_tc
                         }
                 }
             // P V: 16 nodes j at a time
-            wait(FULL_V, par);
+            if (!wait(FULL_V + s, par) || !wait(FULL_P + s, par)) return;
+            // (of a tile of v, three pieces of 64 channels with the 128-byte swizzle; channels 2 g, 2 g + 1 of the warp's 16)
+            const uint32_t sV = base + kOffV + (uint32_t)s * kNodeV + (uint32_t)(warp / 4) * 2048 + (uint32_t)(g & 3) * 4;
+            const uint32_t cV = (uint32_t)(warp & 3) * 2 + (uint32_t)(g >> 2);
+            const uint32_t sPh = base + kOffPh + (uint32_t)s * kNodes * kPitchP, sPl = base + kOffPl + (uint32_t)s * kNodes * kPitchP;
             bool dirty = false;
-            if (ok) {
 #pragma unroll
-                for (int js = 0; js < 4; ++js) {
-                    if (js >= tiles) break;
-                    uint2 x[4];
-                    uint32_t odd = 0;
+            for (int js = 0; js < 4; ++js) {
+                if (js >= tiles) break;
+                uint32_t x[4], odd = 0;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int j = js * 16 + 2 * q4 + (r & 1) + (r >> 1) * 8;
-                        x[r] = lds2(sV + (uint32_t)j * kPitchV + (uint32_t)(warp * kSlice * 2 + g * 8));
-                        if (j >= M) x[r] = make_uint2(0, 0);   // (rows that no copy has written)
-                        odd |= (mul_bf16x2(x[r].x, 0) | mul_bf16x2(x[r].y, 0)) & 0x7fff7fffu;   // not 0: an element that is not finite
-                    }
-                    // One that is not finite would reach every node by way of 0 x inf: it is left out here and added on its paths below.
-                    if (__any_sync(0xffffffffu, odd != 0)) {
-                        dirty = true;
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t j = (uint32_t)(2 * q4 + (r & 1) + (r >> 1) * 8);
+                    x[r] = lds1(sV + (uint32_t)js * kTileV + j * 128 + ((cV ^ (j & 7u)) << 4));
+                    if (js * 16 + (int)j >= M) x[r] = 0;             // (rows of another tree)
+                    odd |= mul_bf16x2(x[r], 0) & 0x7fff7fffu;        // not 0: an element that is not finite
+                }
+                // One that is not finite would reach every node by way of 0 x inf: it is left out here and added on its paths below.
+                if (__any_sync(0xffffffffu, odd != 0)) {
+                    dirty = true;
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) x[r] = make_uint2(finite2(x[r].x), finite2(x[r].y));
-                    }
-                    uint32_t b[4][2];
+                    for (int r = 0; r < 4; ++r) x[r] = finite2(x[r]);
+                }
+                uint32_t b[2][2];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        b[0][r] = __byte_perm(x[2 * r].x, x[2 * r + 1].x, 0x5410);
-                        b[1][r] = __byte_perm(x[2 * r].x, x[2 * r + 1].x, 0x7632);
-                        b[2][r] = __byte_perm(x[2 * r].y, x[2 * r + 1].y, 0x5410);
-                        b[3][r] = __byte_perm(x[2 * r].y, x[2 * r + 1].y, 0x7632);
-                    }
+                for (int r = 0; r < 2; ++r) {
+                    b[0][r] = __byte_perm(x[2 * r], x[2 * r + 1], 0x5410);
+                    b[1][r] = __byte_perm(x[2 * r], x[2 * r + 1], 0x7632);
+                }
 #pragma unroll
-                    for (int i = js; i < 4; ++i) {
-                        if (i >= tiles) break;
-                        uint32_t h[4], l[4];
-                        const uint32_t at = (i * 16 + a_row) * kPitchP + (js * 16 + a_col) * 2;
-                        ldmatrix4(h, sPh + at);
-                        ldmatrix4(l, sPl + at);
+                for (int part = 0; part < 2; ++part) {
+                    uint32_t a[4][4];
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) mma16816(acc[i][t], h, b[t][0], b[t][1]);
+                    for (int i = js; i < 4; ++i)
+                        if (i < tiles) ldmatrix4(a[i], (part ? sPl : sPh) + (i * 16 + a_row) * kPitchP + (js * 16 + a_col) * 2);
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) mma16816(acc[i][t], l, b[t][0], b[t][1]);
-                    }
+                    for (int i = js; i < 4; ++i)
+                        if (i < tiles) {
+                            mma16816(acc[i][0], a[i], b[0][0], b[0][1]);
+                            mma16816(acc[i][1], a[i], b[1][0], b[1][1]);
+                        }
                 }
             }
-            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + ((size_t)m->first * p.H + u % p.H) * kDv + warp * kSlice + 8 * q4;
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + ((size_t)m->first * p.H + u % (uint32_t)p.H) * kDv + warp * 16 + 4 * q4;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int x = i * 16 + g + 8 * r;
-                    if (!ok || x >= M) continue;
+                    if (x >= M) continue;
                     if (dirty) {
+                        const __nv_bfloat16 *ph = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPh + (uint32_t)(s * kNodes + x) * kPitchP);
+                        const __nv_bfloat16 *pl = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPl + (uint32_t)(s * kNodes + x) * kPitchP);
                         for (unsigned long long path = m->path[x]; path; path &= path - 1) {
                             const int j = __ffsll((long long)path) - 1;
-                            const uint32_t at = (uint32_t)x * kPitchP + (uint32_t)j * 2;
-                            const float w = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPh + at)) +
-                                            __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPl + at));
-                            const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffV + (uint32_t)j * kPitchV) + warp * kSlice + 8 * q4;
+                            const float w = __bfloat162float(ph[j]) + __bfloat162float(pl[j]);
+                            // channels 4 q4 .. 4 q4 + 3 of the warp's 16
+                            const uint32_t piece = kOffV + (uint32_t)s * kNodeV + (uint32_t)(j >> 4) * kTileV + (uint32_t)(warp / 4) * 2048 + (uint32_t)(j & 15) * 128;
+                            const uint32_t c16 = ((uint32_t)(warp & 3) * 2 + (uint32_t)(q4 >> 1)) ^ (uint32_t)(j & 7);
+                            const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(sm + piece + c16 * 16 + (uint32_t)(q4 & 1) * 8);
 #pragma unroll
-                            for (int t = 0; t < 4; ++t)
+                            for (int t = 0; t < 2; ++t)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    const float y = __bfloat162float(v[4 * e + t]);
+                                    const float y = __bfloat162float(v[2 * e + t]);
                                     if (!isfinite(y) && w != 0.f) acc[i][t][2 * r + e] += w * y;
                                 }
                         }
                     }
-                    uint4 y;
-                    y.x = pack_bf16x2(p.scale * acc[i][0][2 * r], p.scale * acc[i][1][2 * r]);
-                    y.y = pack_bf16x2(p.scale * acc[i][2][2 * r], p.scale * acc[i][3][2 * r]);
-                    y.z = pack_bf16x2(p.scale * acc[i][0][2 * r + 1], p.scale * acc[i][1][2 * r + 1]);
-                    y.w = pack_bf16x2(p.scale * acc[i][2][2 * r + 1], p.scale * acc[i][3][2 * r + 1]);
-                    *reinterpret_cast<uint4 *>(o + (size_t)x * p.H * kDv) = y;
+                    *reinterpret_cast<uint2 *>(o + (size_t)x * p.H * kDv) =
+                        make_uint2(pack_bf16x2(p.scale * acc[i][0][2 * r], p.scale * acc[i][1][2 * r]),
+                                   pack_bf16x2(p.scale * acc[i][0][2 * r + 1], p.scale * acc[i][1][2 * r + 1]));
                 }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(FREE_V));
             ++done;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(FREE_M + (it & 1)));
+        if (lane == 0) {
+            mbar_arrive(bar(FREE + s));
+            mbar_arrive(bar(FREE_M + meta));
+        }
     }
+}
+
+// A map of three dimensions, each of them `dims` elements `strides` bytes apart (the first contiguous).
+bool make_map(CUtensorMap *m, CUtensorMapDataType type, const void *at, cuuint64_t d0, cuuint64_t d1, cuuint64_t s1, cuuint64_t d2,
+              cuuint64_t s2, cuuint32_t b0, cuuint32_t b1, cuuint32_t b2, CUtensorMapSwizzle swizzle) {
+    const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {s1, s2};
+    const cuuint32_t box[3] = {b0, b1, b2}, es[3] = {1, 1, 1};
+    return encode_tiled_fn()(m, type, 3, const_cast<void *>(at), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -461,19 +533,20 @@ bool tree_fwd_tc_fits(const TreeParams &p) {
 }
 
 cudaError_t launch_tree_fwd_tc(const TreeParams &p, cudaStream_t s, int *launches) {
-    const EncodeTiledFn enc = encode_tiled_fn();
-    if (!enc) return cudaErrorNotSupported;
-    CUtensorMap tm;
-    const cuuint64_t dims[2] = {kDv, (cuuint64_t)p.n_slots * p.H * kDk}, strides[1] = {kDv * 4};
-    const cuuint32_t box[2] = {kSlice, kDk}, es[2] = {1, 1};
-    if (enc(&tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.pool, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    if (!encode_tiled_fn()) return cudaErrorNotSupported;
+    Maps maps;
+    const cuuint64_t T = (cuuint64_t)p.total_T, H = (cuuint64_t)p.H;
+    const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (!make_map(&maps.s, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.pool, 32, (cuuint64_t)p.n_slots * H * kDk, kDv * 4, 6, 128, 32, 16, 6, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&maps.q, bf16, p.q, 32, T, (cuuint64_t)p.ldq * 2, 3 * H, 64, 32, 16, 3, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !make_map(&maps.k, bf16, p.k, 32, T, (cuuint64_t)p.ldk * 2, 3 * H, 64, 32, 16, 3, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !make_map(&maps.v, bf16, p.v, 64, T, (cuuint64_t)p.ldv * 2, 3 * H, 128, 64, 16, 3, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     auto *kern = p.g ? tree_fwd_tc_kernel<true> : tree_fwd_tc_kernel<false>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
-    const long units = (long)p.nseq * p.H, most = 2L * device_sm_count();
-    kern<<<(unsigned)(units < most ? units : most), kThreads, kSmem, s>>>(tm, p);
+    const long units = (long)p.nseq * p.H, most = device_sm_count();
+    kern<<<(unsigned)(units < most ? units : most), kThreads, kSmem, s>>>(maps, p);
     if (launches) ++*launches;
     return cudaGetLastError();
 }
