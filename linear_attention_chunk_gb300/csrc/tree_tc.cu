@@ -41,7 +41,7 @@ using tree::kNodes;
 
 constexpr int kDk = 96, kDv = 192, kSteps = kDk / 16;
 constexpr int kConsumers = 12, kScorers = 4, kThreads = (kConsumers + kScorers + 2) * 32;
-constexpr int kMetas = 4;
+constexpr int kMetas = 4, kHalf = kSteps / 2;   // (the stages of S are waited for and released three at a time)
 constexpr uint32_t kBox = 16 * 128, kStage = 6 * kBox;   // S: 16 rows x 32 channels; x 192
 constexpr uint32_t kTileQ = 16 * kDk * 2, kTileV = 16 * kDv * 2, kNodeQ = kNodes / 16 * kTileQ, kNodeV = kNodes / 16 * kTileV;
 constexpr uint32_t kPitchP = kNodes * 2 + 16;   // (16 more: no bank conflicts)
@@ -58,7 +58,7 @@ struct Meta {
     float factor;                      // W_ij = 2^(factor (sum_i - sum_j))
     int first, nodes, row;             // row: the first of its page in the pool, as rows of dv
 };
-enum { FULL_S = 0, EMPTY_S = FULL_S + kSteps, FULL_M = EMPTY_S + kSteps, FREE_M = FULL_M + kMetas, FULL_QK = FREE_M + kMetas, FULL_V = FULL_QK + 2, FULL_P = FULL_V + 2, FREE = FULL_P + 2, BARS = FREE + 2 };
+enum { FULL_S = 0, EMPTY_S = FULL_S + 2, FULL_M = EMPTY_S + 2, FREE_M = FULL_M + kMetas, FULL_N = FREE_M + kMetas, FULL_P = FULL_N + 2, FREE = FULL_P + 2, BARS = FREE + 2 };
 constexpr uint32_t kOffNext = kOffMeta + kMetas * sizeof(Meta), kOffBars = kOffNext + kNodes * 4, kOffAbort = kOffBars + BARS * 8,
                    kSmem = kOffAbort + 16 + 1024;   // (1,024: the base is rounded up for the swizzle)
 struct Maps {
@@ -228,7 +228,7 @@ __device__ __forceinline__ void producer(const Maps &maps, const TreeParams &p, 
     const int lane = threadIdx.x % 32;
     auto bar = [&](int i) { return base + kOffBars + 8u * (uint32_t)i; };
     auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, ctl)); };
-    int done = 0, it = 0, stages = 0;   // units with nodes, units, stages filled
+    int done = 0, it = 0, halves = 0;   // units with nodes, units, halves of S
     bool ok = true;
     for (uint32_t u = blockIdx.x; u < units; u += gridDim.x, ++it) {
         const int s = it & 1, t = it % kMetas, h = (int)(u % (uint32_t)p.H);
@@ -239,33 +239,30 @@ __device__ __forceinline__ void producer(const Maps &maps, const TreeParams &p, 
         if (lane == 0) mbar_arrive(bar(FREE_M + t));
         if (it >= 2 && !(ok = wait(FREE + s, (uint32_t)((it >> 1) - 1) & 1u))) break;
         if (lane == 0) {   // (of an empty tree nothing is copied, but the barriers go on)
-            mbar_arrive_expect_tx(bar(FULL_QK + s), (uint32_t)tiles * 2 * kTileQ);
+            mbar_arrive_expect_tx(bar(FULL_N + s), (uint32_t)tiles * (2 * kTileQ + kTileV));
             for (int i = 0; i < tiles; ++i) {
                 const uint32_t at = (uint32_t)s * kNodeQ + (uint32_t)i * kTileQ;
-                tma_load_3d(base + kOffQ + at, &maps.q, bar(FULL_QK + s), 0, first + i * 16, h * 3);
-                tma_load_3d(base + kOffK + at, &maps.k, bar(FULL_QK + s), 0, first + i * 16, h * 3);
+                tma_load_3d(base + kOffQ + at, &maps.q, bar(FULL_N + s), 0, first + i * 16, h * 3);
+                tma_load_3d(base + kOffK + at, &maps.k, bar(FULL_N + s), 0, first + i * 16, h * 3);
+                tma_load_3d(base + kOffV + (uint32_t)s * kNodeV + (uint32_t)i * kTileV, &maps.v, bar(FULL_N + s), 0, first + i * 16, h * 3);
             }
-            mbar_arrive_expect_tx(bar(FULL_V + s), (uint32_t)tiles * kTileV);
-            for (int i = 0; i < tiles; ++i)
-                tma_load_3d(base + kOffV + (uint32_t)s * kNodeV + (uint32_t)i * kTileV, &maps.v, bar(FULL_V + s), 0, first + i * 16, h * 3);
         }
         if (M == 0) continue;
-        for (int j = 0; j < kSteps; ++j) {
-            if (done > 0 && !(ok = wait(EMPTY_S + j, (uint32_t)(done - 1) & 1u))) break;
+        for (int half = 0; half < 2; ++half) {
+            if (done > 0 && !(ok = wait(EMPTY_S + half, (uint32_t)(done - 1) & 1u))) break;
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar(FULL_S + j), kStage);
-                tma_load_3d(base + (uint32_t)j * kStage, &maps.s, bar(FULL_S + j), 0, row + j * 16, 0);
+                mbar_arrive_expect_tx(bar(FULL_S + half), kHalf * kStage);
+                for (int j = half * kHalf; j < (half + 1) * kHalf; ++j)
+                    tma_load_3d(base + (uint32_t)j * kStage, &maps.s, bar(FULL_S + half), 0, row + j * 16, 0);
             }
-            stages = done * kSteps + j + 1;
+            ++halves;
         }
         if (!ok) break;
         ++done;
     }
     if (!ok) {   // a wait gave up: the copies in flight land before the CTA ends
-        for (int k = stages > kSteps ? stages - kSteps : 0; k < stages; ++k)
-            mbar_wait_drain(bar(FULL_S + k % kSteps), (uint32_t)(k / kSteps) & 1u, 1000000ull);
-        for (int k = it > 1 ? it - 1 : 0; k <= it; ++k)
-            for (int b : {FULL_QK, FULL_V}) mbar_wait_drain(bar(b + (k & 1)), (uint32_t)(k >> 1) & 1u, 1000000ull);
+        for (int k = halves > 2 ? halves - 2 : 0; k < halves; ++k) mbar_wait_drain(bar(FULL_S + (k & 1)), (uint32_t)(k >> 1) & 1u, 1000000ull);
+        for (int k = it > 1 ? it - 1 : 0; k <= it; ++k) mbar_wait_drain(bar(FULL_N + (k & 1)), (uint32_t)(k >> 1) & 1u, 1000000ull);
     }
 }
 
@@ -280,7 +277,7 @@ __device__ __forceinline__ void scorer(unsigned char *sm, uint32_t base, const W
     for (uint32_t u = blockIdx.x; u < units; u += gridDim.x, ++it) {
         const int s = it & 1, meta = it % kMetas;
         const uint32_t par = (uint32_t)(it >> 1) & 1u;
-        if (!wait(FULL_M + meta, (uint32_t)(it / kMetas) & 1u) || !wait(FULL_QK + s, par)) return;
+        if (!wait(FULL_N + s, par)) return;   // (and with it the plan, which the copies' warp has waited for)
         const Meta *m = reinterpret_cast<const Meta *>(sm + kOffMeta) + meta;
         const int tiles = (m->nodes + 15) / 16;
         const float factor = m->factor;
@@ -347,7 +344,7 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         for (int i = 0; i < BARS; ++i)   // arrivals: one of a copy or the producer, or one a warp
-            mbar_init(bar(i), i >= FREE ? kConsumers + kScorers : i >= FULL_P ? kScorers : i >= FREE_M && i < FULL_QK ? kConsumers + kScorers + 1
+            mbar_init(bar(i), i >= FREE ? kConsumers + kScorers : i >= FULL_P ? kScorers : i >= FREE_M && i < FULL_N ? kConsumers + kScorers + 1
                               : i >= EMPTY_S && i < FULL_M ? kConsumers : 1);
         fence_mbar_init();
         prefetch_tmap(&maps.s);
@@ -379,7 +376,7 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
     for (uint32_t u = blockIdx.x; u < units; u += gridDim.x, ++it) {
         const int s = it & 1, meta = it % kMetas;
         const uint32_t par = (uint32_t)(it >> 1) & 1u;
-        if (!wait(FULL_M + meta, (uint32_t)(it / kMetas) & 1u) || !wait(FULL_QK + s, par)) return;
+        if (!wait(FULL_N + s, par)) return;   // (and with it the plan, which the copies' warp has waited for)
         const Meta *m = reinterpret_cast<const Meta *>(sm + kOffMeta) + meta;
         const int M = m->nodes, tiles = (M + 15) / 16;
         if (M > 0) {
@@ -391,18 +388,30 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) acc[i][t][c] = 0.f;
+            const auto entries = [&](int ks, float2 (&y)[4]) {
+                const uint32_t st = (uint32_t)ks * kStage;
+                y[0] = lds2f(x0 + st);
+                y[1] = lds2f(x1 + st);
+                y[2] = lds2f(x0 + st + 1024);
+                y[3] = lds2f(x1 + st + 1024);
+            };
+            if (!wait(FULL_S, (uint32_t)done & 1u)) return;
+            float2 y[2][4];   // a step's and the next one's
+            entries(0, y[0]);
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks) {
-                if (!wait(FULL_S + ks, (uint32_t)done & 1u)) return;
-                const uint32_t st = (uint32_t)ks * kStage;
-                const float2 y0 = lds2f(x0 + st), y1 = lds2f(x1 + st), y2 = lds2f(x0 + st + 1024), y3 = lds2f(x1 + st + 1024);
+                if (ks == kHalf - 1 && !wait(FULL_S + 1, (uint32_t)done & 1u)) return;
+                if (ks < kSteps - 1) entries(ks + 1, y[(ks + 1) & 1]);
+                const float2(&now)[4] = y[ks & 1];
                 uint32_t hi[2][2], lo[2][2];
-                split(y0.x, y1.x, hi[0][0], lo[0][0]);
-                split(y0.y, y1.y, hi[1][0], lo[1][0]);
-                split(y2.x, y3.x, hi[0][1], lo[0][1]);
-                split(y2.y, y3.y, hi[1][1], lo[1][1]);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(EMPTY_S + ks));
+                split(now[0].x, now[1].x, hi[0][0], lo[0][0]);
+                split(now[0].y, now[1].y, hi[1][0], lo[1][0]);
+                split(now[2].x, now[3].x, hi[0][1], lo[0][1]);
+                split(now[2].y, now[3].y, hi[1][1], lo[1][1]);
+                if (ks % kHalf == kHalf - 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(EMPTY_S + ks / kHalf));
+                }
                 uint32_t a[4][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -424,17 +433,20 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (i < tiles) {
-                    const float f0 = m->far[i * 16 + g], f1 = m->far[i * 16 + g + 8];
+                    const float f[2] = {m->far[i * 16 + g], m->far[i * 16 + g + 8]};
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const float f = c < 2 ? f0 : f1;
-                            acc[i][t][c] = f == 0.f ? 0.f : f * acc[i][t][c];
-                        }
+                        for (int c = 0; c < 4; ++c) acc[i][t][c] *= f[c >> 1];
+                    if (__any_sync(0xffffffffu, f[0] == 0.f || f[1] == 0.f)) {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) acc[i][t][c] = f[c >> 1] == 0.f ? 0.f : acc[i][t][c];
+                    }
                 }
             // P V: 16 nodes j at a time
-            if (!wait(FULL_V + s, par) || !wait(FULL_P + s, par)) return;
+            if (!wait(FULL_P + s, par)) return;
             // (of a tile of v, three pieces of 64 channels with the 128-byte swizzle; channels 2 g, 2 g + 1 of the warp's 16)
             const uint32_t sV = base + kOffV + (uint32_t)s * kNodeV + (uint32_t)(warp / 4) * 2048 + (uint32_t)(g & 3) * 4;
             const uint32_t cV = (uint32_t)(warp & 3) * 2 + (uint32_t)(g >> 2);
@@ -477,11 +489,12 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
                         }
                 }
             }
-            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + ((size_t)m->first * p.H + u % (uint32_t)p.H) * kDv + warp * 16 + 4 * q4;
+            const size_t step = (size_t)p.H * kDv;
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + ((size_t)m->first * p.H + u % (uint32_t)p.H) * kDv + warp * 16 + 4 * q4 + (size_t)g * step;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
+                for (int r = 0; r < 2; ++r, o += 8 * step) {
                     const int x = i * 16 + g + 8 * r;
                     if (x >= M) continue;
                     if (dirty) {
@@ -503,7 +516,7 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
                                 }
                         }
                     }
-                    *reinterpret_cast<uint2 *>(o + (size_t)x * p.H * kDv) =
+                    *reinterpret_cast<uint2 *>(o) =
                         make_uint2(pack_bf16x2(p.scale * acc[i][0][2 * r], p.scale * acc[i][1][2 * r]),
                                    pack_bf16x2(p.scale * acc[i][0][2 * r + 1], p.scale * acc[i][1][2 * r + 1]));
                 }
