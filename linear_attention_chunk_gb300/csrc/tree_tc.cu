@@ -281,7 +281,8 @@ __device__ __forceinline__ void scorer(unsigned char *sm, uint32_t base, const W
         const Meta *m = reinterpret_cast<const Meta *>(sm + kOffMeta) + meta;
         const int tiles = (m->nodes + 15) / 16;
         const float factor = m->factor;
-        const uint32_t sQ = base + kOffQ + (uint32_t)s * kNodeQ, sK = base + kOffK + (uint32_t)s * kNodeQ;
+        const uint32_t bQ = base + kOffQ + (uint32_t)s * kNodeQ, bK = base + kOffK + (uint32_t)s * kNodeQ;
+        const uint32_t sQ[2] = {at_q(bQ, a_row, a_col), at_q(bQ, a_row, 16 + a_col)}, sK[2] = {at_q(bK, b_row, b_col), at_q(bK, b_row, 16 + b_col)};
         for (int x = warp; x < tiles * (tiles + 1) / 2; x += kScorers) {
             const int ti = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, tj = x - ti * (ti + 1) / 2;
             float c[2][4] = {};
@@ -290,8 +291,9 @@ __device__ __forceinline__ void scorer(unsigned char *sm, uint32_t base, const W
                 uint32_t a[3][4], b[3][4];
 #pragma unroll
                 for (int ks = 0; ks < 3; ++ks) {
-                    ldmatrix4(a[ks], at_q(sQ, ti * 16 + a_row, (half + ks) * 16 + a_col));
-                    ldmatrix4(b[ks], at_q(sK, tj * 16 + b_row, (half + ks) * 16 + b_col));
+                    const uint32_t piece = (uint32_t)((half + ks) >> 1) * 1024;
+                    ldmatrix4(a[ks], sQ[(half + ks) & 1] + (uint32_t)ti * kTileQ + piece);
+                    ldmatrix4(b[ks], sK[(half + ks) & 1] + (uint32_t)tj * kTileQ + piece);
                 }
 #pragma unroll
                 for (int ks = 0; ks < 3; ++ks) {
@@ -380,7 +382,8 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
         const Meta *m = reinterpret_cast<const Meta *>(sm + kOffMeta) + meta;
         const int M = m->nodes, tiles = (M + 15) / 16;
         if (M > 0) {
-            const uint32_t sQ = base + kOffQ + (uint32_t)s * kNodeQ;
+            // q's fragments of even and odd steps: all else of their addresses is constant
+            const uint32_t sQ[2] = {at_q(base + kOffQ + (uint32_t)s * kNodeQ, a_row, a_col), at_q(base + kOffQ + (uint32_t)s * kNodeQ, a_row, 16 + a_col)};
             float acc[4][2][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -415,7 +418,7 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
                 uint32_t a[4][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (i < tiles) ldmatrix4(a[i], at_q(sQ, i * 16 + a_row, ks * 16 + a_col));
+                    if (i < tiles) ldmatrix4(a[i], sQ[ks & 1] + (uint32_t)i * kTileQ + (uint32_t)(ks >> 1) * 1024);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (i < tiles) {
@@ -448,9 +451,9 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
             // P V: 16 nodes j at a time
             if (!wait(FULL_P + s, par)) return;
             // (of a tile of v, three pieces of 64 channels with the 128-byte swizzle; channels 2 g, 2 g + 1 of the warp's 16)
-            const uint32_t sV = base + kOffV + (uint32_t)s * kNodeV + (uint32_t)(warp / 4) * 2048 + (uint32_t)(g & 3) * 4;
-            const uint32_t cV = (uint32_t)(warp & 3) * 2 + (uint32_t)(g >> 2);
-            const uint32_t sPh = base + kOffPh + (uint32_t)s * kNodes * kPitchP, sPl = base + kOffPl + (uint32_t)s * kNodes * kPitchP;
+            const uint32_t bV = base + kOffV + (uint32_t)s * kNodeV + (uint32_t)(warp / 4) * 2048 + (uint32_t)(g & 3) * 4, cV = (uint32_t)(warp & 3) * 2 + (uint32_t)(g >> 2);
+            const uint32_t sV[2] = {bV + (uint32_t)(2 * q4) * 128 + ((cV ^ (uint32_t)(2 * q4)) << 4), bV + (uint32_t)(2 * q4 + 1) * 128 + ((cV ^ (uint32_t)(2 * q4 + 1)) << 4)};
+            const uint32_t sP = base + kOffPh + ((uint32_t)s * kNodes + a_row) * kPitchP + a_col * 2;
             bool dirty = false;
 #pragma unroll
             for (int js = 0; js < 4; ++js) {
@@ -458,9 +461,9 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
                 uint32_t x[4], odd = 0;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const uint32_t j = (uint32_t)(2 * q4 + (r & 1) + (r >> 1) * 8);
-                    x[r] = lds1(sV + (uint32_t)js * kTileV + j * 128 + ((cV ^ (j & 7u)) << 4));
-                    if (js * 16 + (int)j >= M) x[r] = 0;             // (rows of another tree)
+                    const int j = 2 * q4 + (r & 1) + (r >> 1) * 8;
+                    x[r] = lds1(sV[r & 1] + (uint32_t)js * kTileV + (uint32_t)(r >> 1) * 1024);
+                    if (js * 16 + j >= M) x[r] = 0;             // (rows of another tree)
                     odd |= mul_bf16x2(x[r], 0) & 0x7fff7fffu;        // not 0: an element that is not finite
                 }
                 // One that is not finite would reach every node by way of 0 x inf: it is left out here and added on its paths below.
@@ -480,7 +483,7 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
                     uint32_t a[4][4];
 #pragma unroll
                     for (int i = js; i < 4; ++i)
-                        if (i < tiles) ldmatrix4(a[i], (part ? sPl : sPh) + (i * 16 + a_row) * kPitchP + (js * 16 + a_col) * 2);
+                        if (i < tiles) ldmatrix4(a[i], sP + (uint32_t)part * (kOffPl - kOffPh) + (uint32_t)i * 16 * kPitchP + (uint32_t)js * 32);
 #pragma unroll
                     for (int i = js; i < 4; ++i)
                         if (i < tiles) {
