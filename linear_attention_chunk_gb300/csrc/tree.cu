@@ -92,38 +92,15 @@ template <typename T> __global__ void __launch_bounds__(kThreads) tree_fwd_kerne
 }
 
 // ----------------------------------------------------------------- commit
-constexpr int kCommit = 192;   // threads; at 96 x 192 the layout of the decode step: four columns of every fourth row
+constexpr int kCommit = 256;
 
-// The window's new rows for four channels: the last four inputs of the path,
-// before them what the window held.
-template <typename T> __device__ void commit_window(const TreeParams &p, const Tree &t, int last, const int *par, int c) {
-    if (c >= p.D) return;
-    float *win = p.win + (size_t)t.slot * ssm::kTaps * p.D + c;
-    int at[ssm::kTaps], len = 0;
-    for (int j = last; j >= 0 && len < ssm::kTaps; j = par[j]) at[len++] = j;
-    float4 row[ssm::kTaps];
-#pragma unroll
-    for (int r = 0; r < ssm::kTaps; ++r) {
-        const int back = ssm::kTaps - 1 - r;
-        if (back < len) {
-            const T *x = static_cast<const T *>(p.x) + (size_t)(t.first + at[back]) * p.ldx + c;
-            row[r] = make_float4(Elem<T>::load(x), Elem<T>::load(x + 1), Elem<T>::load(x + 2), Elem<T>::load(x + 3));
-        } else {
-            row[r] = *reinterpret_cast<const float4 *>(win + (size_t)(r + len) * p.D);
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < ssm::kTaps; ++r) *reinterpret_cast<float4 *>(win + (size_t)r * p.D) = row[r];
-}
-
-// One CTA per (sequence, head), and behind a sequence's heads its window's
-// channels, 768 a CTA. k0: 96 x 192.
-template <typename T, bool k0> __global__ void __launch_bounds__(kCommit) tree_commit_kernel(const TreeParams p, int per) {
+// Any head sizes: one CTA per (sequence, head). fp32's validation mode; pages of 96 x 192 go through tree_commit.cu.
+template <typename T> __global__ void __launch_bounds__(kCommit) tree_commit_any_kernel(const TreeParams p) {
     extern __shared__ float4 smem4[];
     __shared__ int par[kNodes], way[kNodes], s_len;
     __shared__ float s_w[kNodes], gate[kNodes], s_far;
     float *kt = reinterpret_cast<float *>(smem4);          // [path node][dk], decayed
-    const int n = blockIdx.x / per, h = blockIdx.x % per, tid = threadIdx.x;
+    const int n = blockIdx.x / p.H, h = blockIdx.x % p.H, tid = threadIdx.x;
     const int last = p.last[n];
     const Tree t = open_tree(p, n, par);
     if (t.nodes < 0 || last < -1 || last >= t.nodes) {
@@ -131,19 +108,7 @@ template <typename T, bool k0> __global__ void __launch_bounds__(kCommit) tree_c
         return;
     }
     if (last < 0) return;
-    if (h >= p.H) {
-        commit_window<T>(p, t, last, par, ((h - p.H) * kCommit + tid) * 4);
-        return;
-    }
-    const int dk = k0 ? 96 : p.dk, dv = k0 ? 192 : p.dv;
-    float *S = p.pool + (t.slot * p.H + h) * ((size_t)dk * dv);
-    constexpr int kCols = 48, kRows = 24;
-    const int cg = tid % kCols, rg = tid / kCols;
-    float4 s[k0 ? kRows : 1];
-    if constexpr (k0) {
-#pragma unroll
-        for (int m = 0; m < kRows; ++m) s[m] = __ldcs(reinterpret_cast<const float4 *>(S) + (rg + 4 * m) * kCols + cg);
-    }
+    const int dk = p.dk, dv = p.dv;
     if (p.g && tid < t.nodes) gate[tid] = p.g[(size_t)(t.first + tid) * p.H + h];
     __syncthreads();
     if (tid == 0) {
@@ -162,33 +127,13 @@ template <typename T, bool k0> __global__ void __launch_bounds__(kCommit) tree_c
         kt[e] = s_w[j] * Elem<T>::load(static_cast<const T *>(p.k) + (size_t)(t.first + way[j]) * p.ldk + (size_t)h * dk + r);
     }
     __syncthreads();
+    float *S = p.pool + (t.slot * p.H + h) * ((size_t)dk * dv);
     const T *v = static_cast<const T *>(p.v) + (size_t)t.first * p.ldv + (size_t)h * dv;
-    if constexpr (k0) {
-#pragma unroll
-        for (int m = 0; m < kRows; ++m)
-            s[m] = far == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                              : make_float4(far * s[m].x, far * s[m].y, far * s[m].z, far * s[m].w);
-        for (int j = 0; j < len; ++j) {
-            const T *vj = v + (size_t)way[j] * p.ldv + 4 * cg;
-            const float a = Elem<T>::load(vj), b = Elem<T>::load(vj + 1), c = Elem<T>::load(vj + 2), d = Elem<T>::load(vj + 3);
-#pragma unroll
-            for (int m = 0; m < kRows; ++m) {
-                const float kr = kt[j * 96 + rg + 4 * m];
-                s[m].x = fmaf(kr, a, s[m].x);
-                s[m].y = fmaf(kr, b, s[m].y);
-                s[m].z = fmaf(kr, c, s[m].z);
-                s[m].w = fmaf(kr, d, s[m].w);
-            }
-        }
-#pragma unroll
-        for (int m = 0; m < kRows; ++m) __stcs(reinterpret_cast<float4 *>(S) + (rg + 4 * m) * kCols + cg, s[m]);
-    } else {
-        for (int e = tid; e < dk * dv; e += kCommit) {
-            const int r = e / dv, c = e % dv;
-            float x = far == 0.f ? 0.f : far * S[e];
-            for (int j = 0; j < len; ++j) x = fmaf(kt[j * dk + r], Elem<T>::load(v + (size_t)way[j] * p.ldv + c), x);
-            S[e] = x;
-        }
+    for (int e = tid; e < dk * dv; e += kCommit) {
+        const int r = e / dv, c = e % dv;
+        float x = far == 0.f ? 0.f : far * S[e];
+        for (int j = 0; j < len; ++j) x = fmaf(kt[j * dk + r], Elem<T>::load(v + (size_t)way[j] * p.ldv + c), x);
+        S[e] = x;
     }
 }
 
@@ -245,11 +190,9 @@ template <typename T> cudaError_t fwd_any(const TreeParams &p, cudaStream_t s, i
     return cudaGetLastError();
 }
 
-template <typename T> cudaError_t commit(const TreeParams &p, cudaStream_t s, int *launches) {
-    const int per = p.H + (p.x ? (p.D + 4 * kCommit - 1) / (4 * kCommit) : 0);
+template <typename T> cudaError_t commit_any(const TreeParams &p, cudaStream_t s, int *launches) {
     const int bytes = kNodes * p.dk * (int)sizeof(float);   // at most 32 KB
-    auto *kern = p.dk == 96 && p.dv == 192 ? tree_commit_kernel<T, true> : tree_commit_kernel<T, false>;
-    kern<<<(unsigned)((size_t)p.nseq * per), kCommit, bytes, s>>>(p, per);
+    tree_commit_any_kernel<T><<<(unsigned)((size_t)p.nseq * p.H), kCommit, bytes, s>>>(p);
     if (launches) ++*launches;
     return cudaGetLastError();
 }
@@ -268,7 +211,10 @@ cudaError_t launch_tree_fwd(const TreeParams &p, bool bf16, cudaStream_t s, int 
     return bf16 ? fwd_any<__nv_bfloat16>(p, s, launches) : fwd_any<float>(p, s, launches);
 }
 cudaError_t launch_tree_commit(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {
-    return bf16 ? commit<__nv_bfloat16>(p, s, launches) : commit<float>(p, s, launches);
+    const cudaError_t e = p.x ? launch_tree_windows(p, bf16, s, launches) : cudaSuccess;
+    if (e != cudaSuccess || p.H == 0) return e;
+    if (p.dk == 96 && p.dv == 192) return launch_tree_pages(p, bf16, s, launches);
+    return bf16 ? commit_any<__nv_bfloat16>(p, s, launches) : commit_any<float>(p, s, launches);
 }
 cudaError_t launch_conv_tree(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {
     return bf16 ? conv<__nv_bfloat16>(p, s, launches) : conv<float>(p, s, launches);
