@@ -34,29 +34,54 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
 }
-// Two sums over the CTA; `s` is not written again before the CTA's next barrier but one.
-__device__ __forceinline__ float2 block_sums(float a, float b, float2 *s) {
+// Sums over the CTA, each thread adding the warps' in order (a second tree of
+// shuffles costs more); `s` is not written again before the CTA's next barrier
+// but one.
+__device__ __forceinline__ float2 block_sums(float a, float b, float4 *s) {   // (two warps' sums an element)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, nw = blockDim.x / 32;
-    a = warp_sum(a);
-    b = warp_sum(b);
-    if (nw > 1) {
-        if (lane == 0) s[warp] = make_float2(a, b);
-        __syncthreads();
-        const float2 r = lane < nw ? s[lane] : make_float2(0.f, 0.f);
-        a = warp_sum(r.x);
-        b = warp_sum(r.y);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, off);
+        b += __shfl_xor_sync(0xffffffffu, b, off);
+    }
+    if (nw == 1) return make_float2(a, b);
+    if (lane == 0) reinterpret_cast<float2 *>(s)[warp] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.f;
+    for (int i = 0; i < nw / 2; ++i) {
+        const float4 u = s[i];
+        a += u.x;
+        b += u.y;
+        a += u.z;
+        b += u.w;
+    }
+    if (nw & 1) {
+        a += s[nw / 2].x;
+        b += s[nw / 2].y;
     }
     return make_float2(a, b);
 }
-__device__ __forceinline__ float block_sum(float a, float *s) {
+__device__ __forceinline__ float block_sum(float a, float4 *s) {   // (four warps' sums an element)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, nw = blockDim.x / 32;
     a = warp_sum(a);
-    if (nw > 1) {
-        if (lane == 0) s[warp] = a;
-        __syncthreads();
-        a = warp_sum(lane < nw ? s[lane] : 0.f);
+    if (nw == 1) return a;
+    if (lane == 0) reinterpret_cast<float *>(s)[warp] = a;
+    __syncthreads();
+    a = 0.f;
+    for (int i = 0; i < nw / 4; ++i) {
+        const float4 u = s[i];
+        a += u.x;
+        a += u.y;
+        a += u.z;
+        a += u.w;
     }
+    for (int i = nw & ~3; i < nw; ++i) a += reinterpret_cast<const float *>(s)[i];
     return a;
+}
+// sum / D with inv = 1 / D: one correction, without which a constant row's mean is off by a step.
+__device__ __forceinline__ float mean_of(float sum, float D, float inv) {
+    const float q = sum * inv;
+    return fmaf(fmaf(-q, D, sum), inv, q);
 }
 
 // kIn rows of one array each (x, res; s, dy, ds) in a ring of kStages; a thread copies and reads its own vectors.
@@ -84,7 +109,7 @@ constexpr int kFwdRows = 2, kFwdThreads = 768;   // rows in the forward's ring, 
 
 template <typename T, int VPT> __global__ void __launch_bounds__(kMost) layernorm_fwd_kernel(const LayerNormParams p) {
     extern __shared__ __align__(16) uint4 smem[];
-    __shared__ float s_a[32], s_b[32];
+    __shared__ float4 s_a[4], s_b[4];
     const Ring<T, VPT, 2> ring{smem};
     const int tid = threadIdx.x;
     auto issue = [&](long row, int stage) {
@@ -109,7 +134,7 @@ template <typename T, int VPT> __global__ void __launch_bounds__(kMost) layernor
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[i][j] = 1.f;
     }
-    const float D = (float)p.D;    // (sums are divided by it: times 1/D, a constant row's mean would be off by a step)
+    const float D = (float)p.D, inv = 1.f / D;
     int stage = 0;
     for (; row < p.rows; row += gridDim.x) {
         copies_wait<kFwdRows - 2>();
@@ -128,7 +153,7 @@ template <typename T, int VPT> __global__ void __launch_bounds__(kMost) layernor
         }
         issue(row + (long)(kFwdRows - 1) * gridDim.x, stage == 0 ? kFwdRows - 1 : stage - 1);   // the row before's stage
         stage = stage == kFwdRows - 1 ? 0 : stage + 1;
-        const float mean = block_sum(sum, s_a) / D;
+        const float mean = mean_of(block_sum(sum, s_a), D, inv);
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -140,7 +165,7 @@ template <typename T, int VPT> __global__ void __launch_bounds__(kMost) layernor
                 ss = fmaf(v[i][j], v[i][j], ss);
             }
         }
-        const float r = rsqrtf(block_sum(ss, s_b) / D + p.eps);
+        const float r = rsqrtf(block_sum(ss, s_b) * inv + p.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (i * (int)blockDim.x + tid) * 8;
@@ -158,7 +183,7 @@ template <typename T, int VPT> constexpr int ring_rows() { return sizeof(T) == 4
 template <typename T, int VPT> __global__ void __launch_bounds__(kMost) layernorm_bwd_kernel(const LayerNormParams p) {
     constexpr int kStages = ring_rows<T, VPT>();
     extern __shared__ __align__(16) uint4 smem[];
-    __shared__ float2 s_a[32], s_b[32];
+    __shared__ float4 s_a[8], s_b[8];
     const Ring<T, VPT, 3> ring{smem};
     ssm::let_next_start();
     const int tid = threadIdx.x;
@@ -182,7 +207,7 @@ template <typename T, int VPT> __global__ void __launch_bounds__(kMost) layernor
             dw[i][j] = db[i][j] = 0.f;
         }
     }
-    const float D = (float)p.D;
+    const float D = (float)p.D, inv = 1.f / D;
     int stage = 0;
     long row = blockIdx.x;
 #pragma unroll
@@ -208,7 +233,7 @@ template <typename T, int VPT> __global__ void __launch_bounds__(kMost) layernor
         issue(row + (long)(kStages - 1) * gridDim.x, stage == 0 ? kStages - 1 : stage - 1);   // the row before's stage
         stage = stage == kStages - 1 ? 0 : stage + 1;
         const float2 first = block_sums(sx, sg, s_a);
-        const float mean = first.x / D, mg = first.y / D;
+        const float mean = mean_of(first.x, D, inv), mg = first.y * inv;
         float ss = 0.f, sc = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -223,8 +248,8 @@ template <typename T, int VPT> __global__ void __launch_bounds__(kMost) layernor
             }
         }
         const float2 second = block_sums(ss, sc, s_b);
-        const float r = rsqrtf(second.x / D + p.eps);
-        const float k = r * r * (second.y / D);      // xn mean(g xn) = c k
+        const float r = rsqrtf(second.x * inv + p.eps);
+        const float k = r * r * (second.y * inv);      // xn mean(g xn) = c k
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (i * (int)blockDim.x + tid) * 8;

@@ -138,45 +138,81 @@ template <typename T> __global__ void __launch_bounds__(kCommit) tree_commit_any
 }
 
 // ------------------------------------------------------------- convolution
+// A CTA takes the channels of one block of one tree: its rows of x and the
+// window's last three arrive in shared memory by asynchronous copies, all in
+// flight at once, and each is read up to four times from there (as a node and
+// as an ancestor). HBM-bound: x and y once.
 constexpr int kConv = 128;   // threads, eight channels each
+template <typename T> constexpr int conv_lanes() { return sizeof(T) == 2 ? 32 : 16; }   // of a row: 256 channels at bf16, 128 at fp32
 
 template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(const TreeParams p, int per) {
+    constexpr int kLanes = conv_lanes<T>(), kRows = kConv / kLanes, H = sizeof(T) / 2;
+    extern __shared__ uint4 smem_conv[];                      // [nodes][pieces of 16 bytes][lanes]
+    __shared__ __align__(16) float4 wins[3][2][kLanes];       // the window's rows 1 .. 3
     __shared__ int par[kNodes];
-    const int n = blockIdx.x / per, tid = threadIdx.x, c = ((int)(blockIdx.x % per) * kConv + tid) * 8;
-    const Tree t = open_tree(p, n, par);
-    if (t.nodes < 0 && tid == 0) atomicOr(p.status, kDevBadState);
-    if (t.nodes <= 0 || c >= p.D) return;
-    const bool whole = c + 8 <= p.D;
-    const T *x = static_cast<const T *>(p.x) + (size_t)t.first * p.ldx + c;
-    const float *win = p.win + (size_t)t.slot * ssm::kTaps * p.D + c;
-    T *y = static_cast<T *>(p.y) + (size_t)t.first * p.D + c;
-    float w[8][4], b[8];
-    ssm::param8(p.b, c, whole, b);
+    const int n = blockIdx.x / per, lane = threadIdx.x % kLanes, first_row = threadIdx.x / kLanes;
+    const int c = ((int)(blockIdx.x % per) * kLanes + lane) * 8;
+    const bool on = c < p.D, whole = c + 8 <= p.D;
+    // what open_tree checks, before the copies that do not depend on the parents
+    const int lo = p.cu[n], hi = p.cu[n + 1], slot = p.slots ? p.slots[n] : n;
+    const bool fits = lo >= 0 && hi >= lo && hi <= p.total_T && hi - lo <= kNodes && slot >= 0 && slot < p.n_slots;
+    const T *x = static_cast<const T *>(p.x) + c;
+    if (fits) {
+        for (int i = first_row; i < hi - lo; i += kRows)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float4 a = c + j < p.D ? __ldg(reinterpret_cast<const float4 *>(p.w) + c + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-        w[j][0] = a.x; w[j][1] = a.y; w[j][2] = a.z; w[j][3] = a.w;
+            for (int h = 0; h < H; ++h)
+                ssm::copy_async<16>(&smem_conv[(i * H + h) * kLanes + lane], on ? x + (size_t)(lo + i) * p.ldx + 4 * h : x - c, on && (h == 0 || whole));
+        for (int r = first_row; r < 6 && hi > lo; r += kRows) {
+            const float *w = p.win + ((size_t)slot * ssm::kTaps + 1 + r / 2) * p.D + c + 4 * (r % 2);
+            ssm::copy_async<16>(&wins[r / 2][r % 2][lane], on && (r % 2 == 0 || whole) ? w : p.win, on && (r % 2 == 0 || whole));
+        }
     }
-    for (int i = 0; i < t.nodes; ++i) {
-        float acc[8];
+    ssm::copies_commit();
+    ssm::f2 w[4][4], b[4];                                    // taps of channel pairs
+    ssm::param8(on ? p.b : nullptr, c, whole, b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = b[j];
-        int a = i;                                        // a node, or -1 - r: r rows before the window's last
+    for (int j = 0; j < 4; ++j) {
+        const float4 u = c + 2 * j < p.D ? __ldg(reinterpret_cast<const float4 *>(p.w) + c + 2 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 v = c + 2 * j < p.D ? __ldg(reinterpret_cast<const float4 *>(p.w) + c + 2 * j + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        w[0][j] = ssm::f2_pack(u.x, v.x);
+        w[1][j] = ssm::f2_pack(u.y, v.y);
+        w[2][j] = ssm::f2_pack(u.z, v.z);
+        w[3][j] = ssm::f2_pack(u.w, v.w);
+    }
+    const Tree t = open_tree(p, n, par);
+    if (t.nodes < 0 && threadIdx.x == 0) atomicOr(p.status, kDevBadState);
+    ssm::copies_wait<0>();
+    if (t.nodes <= 0) return;
+    __syncthreads();
+    if (!on) return;
+    T *y = static_cast<T *>(p.y) + (size_t)t.first * p.D + c;
+    for (int i = first_row; i < t.nodes; i += kRows) {
+        ssm::f2 acc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = b[j];
+        int a = i;                                            // a node, or -1 - r: r rows before the window's last
 #pragma unroll
         for (int tap = 3; tap >= 0; --tap) {
-            float u[8];
+            ssm::f2 u[4];
             if (a >= 0) {
-                ssm::raw_unpack(ssm::raw_load(x + (size_t)a * p.ldx, whole), u);
+                ssm::Raw8<T> raw;
+#pragma unroll
+                for (int h = 0; h < H; ++h) raw.w[h] = smem_conv[(a * H + h) * kLanes + lane];
+                ssm::raw_unpack(raw, u);
                 a = par[a];
             } else {
-                ssm::param8(win + (size_t)(4 + a) * p.D, 0, whole, u);
+                const float4 e = wins[3 + a][0][lane], f = wins[3 + a][1][lane];
+                u[0] = ssm::f2_pack(e.x, e.y);
+                u[1] = ssm::f2_pack(e.z, e.w);
+                u[2] = ssm::f2_pack(f.x, f.y);
+                u[3] = ssm::f2_pack(f.z, f.w);
                 --a;
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = fmaf(w[j][tap], u[j], acc[j]);
+            for (int j = 0; j < 4; ++j) acc[j] = ssm::fma2(w[tap][j], u[j], acc[j]);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = ssm::silu(acc[j]);
+        for (int j = 0; j < 4; ++j) acc[j] = ssm::silu2(acc[j]);
         ssm::store8(y + (size_t)i * p.D, acc, whole);
     }
 }
@@ -198,8 +234,9 @@ template <typename T> cudaError_t commit_any(const TreeParams &p, cudaStream_t s
 }
 
 template <typename T> cudaError_t conv(const TreeParams &p, cudaStream_t s, int *launches) {
-    const int per = (p.D + 8 * kConv - 1) / (8 * kConv);
-    conv_tree_kernel<T><<<(unsigned)((size_t)p.nseq * per), kConv, 0, s>>>(p, per);
+    constexpr int kLanes = conv_lanes<T>();
+    const int per = (p.D + 8 * kLanes - 1) / (8 * kLanes), bytes = kNodes * kLanes * 8 * (int)sizeof(T);   // 32 KB
+    conv_tree_kernel<T><<<(unsigned)((size_t)p.nseq * per), kConv, bytes, s>>>(p, per);
     if (launches) ++*launches;
     return cudaGetLastError();
 }
