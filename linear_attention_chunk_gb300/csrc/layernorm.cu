@@ -23,29 +23,42 @@ using ssm::Raw8;
 using ssm::copies_commit;
 using ssm::copies_wait;
 using ssm::copy_async;
+using ssm::add2;
+using ssm::both;
+using ssm::f2;
+using ssm::f2_pack;
+using ssm::f2_split;
+using ssm::fma2;
+using ssm::mul2;
 using ssm::param8;
 using ssm::raw_unpack;
 using ssm::store8;
 
-constexpr int kMost = 512;      // threads of a CTA, two vectors a thread: D <= 8192
+constexpr int kMost = 512, kBwdThreads = 512;   // threads of a CTA, two vectors each: D <= 8192; the backward's on an SM
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
 }
-// Sums over the CTA, each thread adding the warps' in order (a second tree of
-// shuffles costs more); `s` is not written again before the CTA's next barrier
-// but one.
+__device__ __forceinline__ float pair_sum(f2 v) {
+    const float2 u = f2_split(v);
+    return u.x + u.y;
+}
+// Sums over threads that share a row, each adding the warps' in order; `s` is
+// not written again before their next barrier but one. Of two sums, lanes 0 .. 15 take
+// on one after the first exchange, 16 .. 31 the other: six exchanges for ten.
 __device__ __forceinline__ float2 block_sums(float a, float b, float4 *s) {   // (two warps' sums an element)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, nw = blockDim.x / 32;
+    const bool upper = lane & 16;
+    float v = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, off);
-        b += __shfl_xor_sync(0xffffffffu, b, off);
+    for (int off = 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (nw == 1) {
+        const float w = __shfl_xor_sync(0xffffffffu, v, 16);
+        return upper ? make_float2(w, v) : make_float2(v, w);
     }
-    if (nw == 1) return make_float2(a, b);
-    if (lane == 0) reinterpret_cast<float2 *>(s)[warp] = make_float2(a, b);
+    if ((lane & 15) == 0) reinterpret_cast<float *>(s)[2 * warp + (lane >> 4)] = v;
     __syncthreads();
     a = b = 0.f;
     for (int i = 0; i < nw / 2; ++i) {
@@ -84,194 +97,213 @@ __device__ __forceinline__ float mean_of(float sum, float D, float inv) {
     return fmaf(fmaf(-q, D, sum), inv, q);
 }
 
-// kIn rows of one array each (x, res; s, dy, ds) in a ring of kStages; a thread copies and reads its own vectors.
+// Rows of kIn arrays in a ring of kStages; a thread copies and reads its own
+// vectors. `at` advances by the copied rows' distance.
 template <typename T, int VPT, int kIn> struct Ring {
     static constexpr int H = sizeof(T) / 2, kRow = kIn * VPT * H;   // 16-byte pieces of a thread and row
-    uint4 *at;
-    __device__ __forceinline__ void issue(int stage, int k, int i, const void *src, long row, bool in, int D) const {
-        const int c = (i * (int)blockDim.x + (int)threadIdx.x) * 8;
+    uint4 *base;
+    __device__ __forceinline__ uint4 *piece(int stage, int k, int i, int h) const {
+        return base + (stage * kRow + (i * kIn + k) * H + h) * (int)blockDim.x + (int)threadIdx.x;
+    }
+    __device__ __forceinline__ void issue(int stage, int k, const T *row, bool in, int D) const {
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-            const bool on = in && c + 4 * h < D;      // (a piece holds 8 / H channels)
-            copy_async<16>(at + ((size_t)stage * kRow + (i * kIn + k) * H + h) * blockDim.x + threadIdx.x,
-                           static_cast<const T *>(src) + (on ? (size_t)row * D + c + 4 * h : 0), on);
-        }
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int c = (i * (int)blockDim.x + (int)threadIdx.x) * 8 + 4 * h;   // (a piece holds 8 / H channels)
+                copy_async<16>(piece(stage, k, i, h), row + c, in && c < D);
+            }
     }
     __device__ __forceinline__ Raw8<T> held(int stage, int k, int i) const {
         Raw8<T> r;
 #pragma unroll
-        for (int h = 0; h < H; ++h) r.w[h] = at[((size_t)stage * kRow + (i * kIn + k) * H + h) * blockDim.x + threadIdx.x];
+        for (int h = 0; h < H; ++h) r.w[h] = *piece(stage, k, i, h);
         return r;
     }
 };
+// A row's mean for the channels of a vector that exist, 0 for the others (which hold zeros), in halves.
+__device__ __forceinline__ void minus_mean(f2 (&v)[4], float mean, bool on, bool whole) {
+    const f2 lo = both(on ? -mean : 0.f), hi = both(whole ? -mean : 0.f);
+    v[0] = add2(v[0], lo);
+    v[1] = add2(v[1], lo);
+    v[2] = add2(v[2], hi);
+    v[3] = add2(v[3], hi);
+}
 
-constexpr int kFwdRows = 2, kFwdThreads = 768;   // rows in the forward's ring, its threads on an SM
+// Rows in the forward's ring, its threads on an SM (16384 x 2048 with the residual, 2 rows at 640, 768, 896, 1,024
+// threads: 57, 44.6, 52, 48.6 us; 3 rows at 768: 49.7).
+constexpr int kFwdRows = 2, kFwdThreads = 768;
 
-template <typename T, int VPT> __global__ void __launch_bounds__(kMost) layernorm_fwd_kernel(const LayerNormParams p) {
+// kCta: the most threads it is launched with.
+template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta, kFwdThreads / kCta) layernorm_fwd_kernel(const LayerNormParams p) {
     extern __shared__ __align__(16) uint4 smem[];
     __shared__ float4 s_a[4], s_b[4];
     const Ring<T, VPT, 2> ring{smem};
     const int tid = threadIdx.x;
-    auto issue = [&](long row, int stage) {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            ring.issue(stage, 0, i, p.x, row, row < p.rows, p.D);
-            if (p.res) ring.issue(stage, 1, i, p.res, row, row < p.rows, p.D);
-        }
+    const size_t hop = (size_t)gridDim.x * p.D;
+    long next = blockIdx.x;                             // the row copied next, and where it lies
+    const T *x = static_cast<const T *>(p.x) + (size_t)next * p.D, *res = static_cast<const T *>(p.res) + (p.res ? (size_t)next * p.D : 0);
+    auto issue = [&](int stage) {
+        const bool in = next < p.rows;
+        ring.issue(stage, 0, x, in, p.D);
+        if (p.res) ring.issue(stage, 1, res, in, p.D);
         copies_commit();
+        next += gridDim.x;
+        x += hop;
+        res += p.res ? hop : 0;
     };
-    long row = blockIdx.x;
 #pragma unroll
-    for (int k = 0; k < kFwdRows - 1; ++k) issue(row + (long)k * gridDim.x, k);
-    float w[VPT][8], b[VPT][8];
+    for (int k = 0; k < kFwdRows - 1; ++k) issue(k);
+    f2 w[VPT][4], b[VPT][4];
+    bool on[VPT], whole[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (i * (int)blockDim.x + tid) * 8;
-        const bool on = c < p.D, whole = c + 8 <= p.D;
-        param8(p.w && on ? p.w : nullptr, c, whole, w[i]);
-        param8(p.b && on ? p.b : nullptr, c, whole, b[i]);
+        on[i] = c < p.D;
+        whole[i] = c + 8 <= p.D;
+        param8(p.w && on[i] ? p.w : nullptr, c, whole[i], w[i]);
+        param8(p.b && on[i] ? p.b : nullptr, c, whole[i], b[i]);
         if (!p.w)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[i][j] = 1.f;
+            for (int j = 0; j < 4; ++j) w[i][j] = both(1.f);
     }
     const float D = (float)p.D, inv = 1.f / D;
     int stage = 0;
-    for (; row < p.rows; row += gridDim.x) {
+    size_t at = (size_t)blockIdx.x * p.D + tid * 8;     // of this row, the thread's first vector
+    for (long row = blockIdx.x; row < p.rows; row += gridDim.x, at += hop) {
         copies_wait<kFwdRows - 2>();
-        float v[VPT][8], sum = 0.f;
+        f2 v[VPT][4], sum = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             raw_unpack(ring.held(stage, 0, i), v[i]);
             if (p.res) {
-                float r[8];
+                f2 r[4];
                 raw_unpack(ring.held(stage, 1, i), r);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+                for (int j = 0; j < 4; ++j) v[i][j] = add2(v[i][j], r[j]);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum += v[i][j];
+            for (int j = 0; j < 4; ++j) sum = add2(sum, v[i][j]);
         }
-        issue(row + (long)(kFwdRows - 1) * gridDim.x, stage == 0 ? kFwdRows - 1 : stage - 1);   // the row before's stage
+        issue(stage == 0 ? kFwdRows - 1 : stage - 1);   // into the row before's stage
         stage = stage == kFwdRows - 1 ? 0 : stage + 1;
-        const float mean = mean_of(block_sum(sum, s_a), D, inv);
-        float ss = 0.f;
+        const float mean = mean_of(block_sum(pair_sum(sum), s_a), D, inv);
+        f2 ss = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (i * (int)blockDim.x + tid) * 8;
-            if (p.s_out && c < p.D) store8(static_cast<T *>(p.s_out) + (size_t)row * p.D + c, v[i], c + 8 <= p.D);
+            if (p.s_out && on[i]) store8(static_cast<T *>(p.s_out) + at + (size_t)i * blockDim.x * 8, v[i], whole[i]);
+            minus_mean(v[i], mean, on[i], whole[i]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[i][j] = c + j < p.D ? v[i][j] - mean : 0.f;
-                ss = fmaf(v[i][j], v[i][j], ss);
-            }
+            for (int j = 0; j < 4; ++j) ss = fma2(v[i][j], v[i][j], ss);
         }
-        const float r = rsqrtf(block_sum(ss, s_b) * inv + p.eps);
+        const f2 r = both(rsqrtf(block_sum(pair_sum(ss), s_b) * inv + p.eps));
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (i * (int)blockDim.x + tid) * 8;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * r, w[i][j], b[i][j]);
-            if (c < p.D) store8(static_cast<T *>(p.y) + (size_t)row * p.D + c, v[i], c + 8 <= p.D);
+            for (int j = 0; j < 4; ++j) v[i][j] = fma2(mul2(v[i][j], r), w[i][j], b[i][j]);
+            if (on[i]) store8(static_cast<T *>(p.y) + at + (size_t)i * blockDim.x * 8, v[i], whole[i]);
         }
     }
 }
 
-// Rows in the backward's ring; two where three would not fit (fp32, D > 4096: 98 KB a row).
+// Rows in the backward's ring (2, 3, 5 at 16384 x 2048: 56, 53, 71 us); two where three would not fit (fp32, 512 threads: 98 KB a row).
 template <typename T, int VPT> constexpr int ring_rows() { return sizeof(T) == 4 && VPT == 2 ? 2 : 3; }
 
-// p.x: s; rows blockIdx.x, + gridDim.x, ...; partial dw and db of the CTA at p.part.
-template <typename T, int VPT> __global__ void __launch_bounds__(kMost) layernorm_bwd_kernel(const LayerNormParams p) {
+// p.x: s; rows blockIdx.x, + gridDim.x, ...; partial dw and db of the CTA at
+// p.part. (Of 53 us at 16384 x 2048 the second launch takes 6. Clusters of two
+// CTAs that add their sums up first: 52; of four: 68, fewer of them fit.)
+template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta, kBwdThreads / kCta) layernorm_bwd_kernel(const LayerNormParams p) {
     constexpr int kStages = ring_rows<T, VPT>();
     extern __shared__ __align__(16) uint4 smem[];
     __shared__ float4 s_a[8], s_b[8];
     const Ring<T, VPT, 3> ring{smem};
     ssm::let_next_start();
     const int tid = threadIdx.x;
-    auto issue = [&](long row, int stage) {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            ring.issue(stage, 0, i, p.x, row, row < p.rows, p.D);
-            ring.issue(stage, 1, i, p.dy, row, row < p.rows, p.D);
-            ring.issue(stage, 2, i, p.ds ? p.ds : p.x, row, row < p.rows && p.ds, p.D);
-        }
+    const size_t hop = (size_t)gridDim.x * p.D;
+    long next = blockIdx.x;                             // the row copied next, and where it lies
+    size_t ahead = (size_t)next * p.D;
+    auto issue = [&](int stage) {
+        const bool in = next < p.rows;
+        ring.issue(stage, 0, static_cast<const T *>(p.x) + ahead, in, p.D);
+        ring.issue(stage, 1, static_cast<const T *>(p.dy) + ahead, in, p.D);
+        ring.issue(stage, 2, static_cast<const T *>(p.ds ? p.ds : p.x) + ahead, in && p.ds, p.D);
         copies_commit();
+        next += gridDim.x;
+        ahead += hop;
     };
-    float w[VPT][8], dw[VPT][8], db[VPT][8];
+    f2 w[VPT][4], dw[VPT][4], db[VPT][4];
+    bool on[VPT], whole[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (i * (int)blockDim.x + tid) * 8;
-        param8(p.w && c < p.D ? p.w : nullptr, c, c + 8 <= p.D, w[i]);
+        on[i] = c < p.D;
+        whole[i] = c + 8 <= p.D;
+        param8(p.w && on[i] ? p.w : nullptr, c, whole[i], w[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (!p.w) w[i][j] = 1.f;
-            dw[i][j] = db[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) {
+            if (!p.w) w[i][j] = both(1.f);
+            dw[i][j] = db[i][j] = both(0.f);
         }
     }
     const float D = (float)p.D, inv = 1.f / D;
     int stage = 0;
-    long row = blockIdx.x;
 #pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) issue(row + (long)k * gridDim.x, k);
-    for (; row < p.rows; row += gridDim.x) {
+    for (int k = 0; k < kStages - 1; ++k) issue(k);
+    size_t at = (size_t)blockIdx.x * p.D + tid * 8;     // of this row, the thread's first vector
+    for (long row = blockIdx.x; row < p.rows; row += gridDim.x, at += hop) {
         copies_wait<kStages - 2>();
-        float x[VPT][8];
-        Raw8<T> cy[VPT], cs[VPT];
-        float sx = 0.f, sg = 0.f;
+        f2 x[VPT][4], g[VPT][4], sx = both(0.f), sg = both(0.f);
+        Raw8<T> cs[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            cy[i] = ring.held(stage, 1, i);
-            cs[i] = ring.held(stage, 2, i);
-            float g[8];
             raw_unpack(ring.held(stage, 0, i), x[i]);
-            raw_unpack(cy[i], g);
+            raw_unpack(ring.held(stage, 1, i), g[i]);
+            cs[i] = ring.held(stage, 2, i);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                sx += x[i][j];
-                sg = fmaf(g[j], w[i][j], sg);
+            for (int j = 0; j < 4; ++j) {
+                sx = add2(sx, x[i][j]);
+                sg = fma2(g[i][j], w[i][j], sg);
             }
         }
-        issue(row + (long)(kStages - 1) * gridDim.x, stage == 0 ? kStages - 1 : stage - 1);   // the row before's stage
+        issue(stage == 0 ? kStages - 1 : stage - 1);    // into the row before's stage
         stage = stage == kStages - 1 ? 0 : stage + 1;
-        const float2 first = block_sums(sx, sg, s_a);
-        const float mean = mean_of(first.x, D, inv), mg = first.y * inv;
-        float ss = 0.f, sc = 0.f;
+        const float2 sums = block_sums(pair_sum(sx), pair_sum(sg), s_a);
+        const float mean = mean_of(sums.x, D, inv);
+        f2 ss = both(0.f), sc = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (i * (int)blockDim.x + tid) * 8;
-            float g[8];
-            raw_unpack(cy[i], g);
+            minus_mean(x[i], mean, on[i], whole[i]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[i][j] = c + j < p.D ? x[i][j] - mean : 0.f;
-                ss = fmaf(x[i][j], x[i][j], ss);
-                sc = fmaf(g[j] * w[i][j], x[i][j], sc);
+            for (int j = 0; j < 4; ++j) {
+                db[i][j] = add2(db[i][j], g[i][j]);
+                ss = fma2(x[i][j], x[i][j], ss);
+                sc = fma2(mul2(g[i][j], w[i][j]), x[i][j], sc);
             }
         }
-        const float2 second = block_sums(ss, sc, s_b);
-        const float r = rsqrtf(second.x * inv + p.eps);
-        const float k = r * r * (second.y * inv);      // xn mean(g xn) = c k
+        const float2 squares = block_sums(pair_sum(ss), pair_sum(sc), s_b);
+        const float r = rsqrtf(squares.x * inv + p.eps);
+        // dx = ds + r (g w - mean(g w)) - c k, with xn mean(g w xn) r = c k
+        const f2 r2 = both(r), k2 = both(-r * (r * (r * (squares.y * inv)))), m2 = both(-sums.y * inv);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (i * (int)blockDim.x + tid) * 8;
-            float g[8], s[8];
-            raw_unpack(cy[i], g);
+            f2 s[4];
             raw_unpack(cs[i], s);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                dw[i][j] = fmaf(g[j], x[i][j] * r, dw[i][j]);
-                db[i][j] += g[j];
-                s[j] = fmaf(r, fmaf(-k, x[i][j], fmaf(g[j], w[i][j], -mg)), s[j]);
+            for (int j = 0; j < 4; ++j) {
+                dw[i][j] = fma2(g[i][j], mul2(x[i][j], r2), dw[i][j]);
+                s[j] = fma2(r2, fma2(g[i][j], w[i][j], m2), fma2(k2, x[i][j], s[j]));
             }
-            if (c < p.D) store8(static_cast<T *>(p.dx) + (size_t)row * p.D + c, s, c + 8 <= p.D);
+            if (on[i]) store8(static_cast<T *>(p.dx) + at + (size_t)i * blockDim.x * 8, s, whole[i]);
         }
     }
     if (!p.part) return;
+    float *part = p.part + (size_t)blockIdx.x * 2 * p.D;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (i * (int)blockDim.x + tid) * 8;
-        if (c >= p.D) continue;
-        store8(p.part + (size_t)blockIdx.x * 2 * p.D + c, dw[i], c + 8 <= p.D);
-        store8(p.part + (size_t)blockIdx.x * 2 * p.D + p.D + c, db[i], c + 8 <= p.D);
+        if (!on[i]) continue;
+        store8(part + c, dw[i], whole[i]);
+        store8(part + p.D + c, db[i], whole[i]);
     }
 }
 
@@ -291,7 +323,8 @@ template <typename T> cudaError_t fwd(const LayerNormParams &p, cudaStream_t s, 
     const int th = round32((vecs + vpt - 1) / vpt);
     const long held = (long)(kFwdThreads / th > 16 ? 16 : kFwdThreads / th) * device_sm_count();
     const int bytes = kFwdRows * 2 * vpt * th * 8 * (int)sizeof(T);
-    auto *kern = vpt == 1 ? layernorm_fwd_kernel<T, 1> : layernorm_fwd_kernel<T, 2>;
+    auto *kern = th <= 256 ? (vpt == 1 ? layernorm_fwd_kernel<T, 1, 256> : layernorm_fwd_kernel<T, 2, 256>)
+                           : (vpt == 1 ? layernorm_fwd_kernel<T, 1, 512> : layernorm_fwd_kernel<T, 2, 512>);
     cudaError_t e = allow_smem(kern, bytes);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)(p.rows < held ? p.rows : held), th, bytes, s>>>(p);
@@ -299,15 +332,16 @@ template <typename T> cudaError_t fwd(const LayerNormParams &p, cudaStream_t s, 
     return cudaGetLastError();
 }
 
-// The backward's shape by D alone: one vector a thread up to 4,096 channels.
-int bwd_vpt(int vecs) { return vecs > kMost ? 2 : 1; }
-int bwd_threads(int vecs) { return round32((vecs + bwd_vpt(vecs) - 1) / bwd_vpt(vecs)); }
+// The backward's shape, by D alone: two vectors a thread from 264 channels on (one, at 16384 x 2048: 59 us for 53).
+int bwd_vpt(int D) { return D > 256 ? 2 : 1; }
+int bwd_threads(int D) { return round32(((D + 7) / 8 + bwd_vpt(D) - 1) / bwd_vpt(D)); }
 
 template <typename T> cudaError_t bwd(const LayerNormParams &p, cudaStream_t s, int *launches) {
-    const int vecs = (p.D + 7) / 8, vpt = bwd_vpt(vecs), th = bwd_threads(vecs);
+    const int vpt = bwd_vpt(p.D), th = bwd_threads(p.D);
     const unsigned grid = (unsigned)layernorm_bwd_grid(p.rows, p.D);
     const int bytes = (vpt == 1 ? ring_rows<T, 1>() : ring_rows<T, 2>()) * 3 * vpt * th * 8 * (int)sizeof(T);
-    auto *kern = vpt == 1 ? layernorm_bwd_kernel<T, 1> : layernorm_bwd_kernel<T, 2>;
+    auto *kern = vpt == 1 ? layernorm_bwd_kernel<T, 1, 128> : th <= 128 ? layernorm_bwd_kernel<T, 2, 128>
+               : th <= 256 ? layernorm_bwd_kernel<T, 2, 256> : layernorm_bwd_kernel<T, 2, 512>;
     cudaError_t e = allow_smem(kern, bytes);
     if (e != cudaSuccess) return e;
     kern<<<grid, th, bytes, s>>>(p);
@@ -322,11 +356,10 @@ template <typename T> cudaError_t bwd(const LayerNormParams &p, cudaStream_t s, 
 
 }  // namespace
 
-// CTAs of the backward: 768 threads an SM, each CTA walking its share of the rows.
+// CTAs of the backward, each walking its share of the rows.
 long layernorm_bwd_grid(long rows, int D) {
-    const int th = bwd_threads((D + 7) / 8);
-    const long per_sm = 768 / th > 8 ? 8 : 768 / th;
-    const long most = per_sm * device_sm_count();
+    const int th = bwd_threads(D);
+    const long per_sm = kBwdThreads / th > 8 ? 8 : kBwdThreads / th, most = per_sm * device_sm_count();
     return rows < most ? rows : most;
 }
 

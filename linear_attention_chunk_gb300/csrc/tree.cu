@@ -141,7 +141,9 @@ template <typename T> __global__ void __launch_bounds__(kCommit) tree_commit_any
 // A CTA takes the channels of one block of one tree: its rows of x and the
 // window's last three arrive in shared memory by asynchronous copies, all in
 // flight at once, and each is read up to four times from there (as a node and
-// as an ancestor). HBM-bound: x and y once.
+// as an ancestor). HBM-bound: x and y once. CTAs of the channels stay for
+// several trees where there are more trees than fit at a time: the taps of a
+// thread's channels, 128 strided bytes, cost as much as ten nodes' rows.
 constexpr int kConv = 128;   // threads, eight channels each
 template <typename T> constexpr int conv_lanes() { return sizeof(T) == 2 ? 32 : 16; }   // of a row: 256 channels at bf16, 128 at fp32
 
@@ -150,70 +152,80 @@ template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(
     extern __shared__ uint4 smem_conv[];                      // [nodes][pieces of 16 bytes][lanes]
     __shared__ __align__(16) float4 wins[3][2][kLanes];       // the window's rows 1 .. 3
     __shared__ int par[kNodes];
-    const int n = blockIdx.x / per, lane = threadIdx.x % kLanes, first_row = threadIdx.x / kLanes;
+    const int lane = threadIdx.x % kLanes, first_row = threadIdx.x / kLanes;
     const int c = ((int)(blockIdx.x % per) * kLanes + lane) * 8;
     const bool on = c < p.D, whole = c + 8 <= p.D;
-    // what open_tree checks, before the copies that do not depend on the parents
-    const int lo = p.cu[n], hi = p.cu[n + 1], slot = p.slots ? p.slots[n] : n;
-    const bool fits = lo >= 0 && hi >= lo && hi <= p.total_T && hi - lo <= kNodes && slot >= 0 && slot < p.n_slots;
-    const T *x = static_cast<const T *>(p.x) + c;
-    if (fits) {
-        for (int i = first_row; i < hi - lo; i += kRows)
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-                ssm::copy_async<16>(&smem_conv[(i * H + h) * kLanes + lane], on ? x + (size_t)(lo + i) * p.ldx + 4 * h : x - c, on && (h == 0 || whole));
-        for (int r = first_row; r < 6 && hi > lo; r += kRows) {
-            const float *w = p.win + ((size_t)slot * ssm::kTaps + 1 + r / 2) * p.D + c + 4 * (r % 2);
-            ssm::copy_async<16>(&wins[r / 2][r % 2][lane], on && (r % 2 == 0 || whole) ? w : p.win, on && (r % 2 == 0 || whole));
-        }
+    // the taps by way of shared memory: coalesced in, and out again a channel's 16 bytes after 144 bytes a lane
+    for (int i = threadIdx.x; i < kLanes * 8; i += kConv) {
+        const int ch = (int)(blockIdx.x % per) * kLanes * 8 + i;
+        if (ch < p.D) smem_conv[i + i / 8] = __ldg(reinterpret_cast<const uint4 *>(p.w) + ch);
     }
-    ssm::copies_commit();
+    __syncthreads();
     ssm::f2 w[4][4], b[4];                                    // taps of channel pairs
     ssm::param8(on ? p.b : nullptr, c, whole, b);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float4 u = c + 2 * j < p.D ? __ldg(reinterpret_cast<const float4 *>(p.w) + c + 2 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 v = c + 2 * j < p.D ? __ldg(reinterpret_cast<const float4 *>(p.w) + c + 2 * j + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool in = c + 2 * j < p.D;
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 u = in ? reinterpret_cast<const float4 *>(smem_conv)[lane * 9 + 2 * j] : zero;
+        const float4 v = in ? reinterpret_cast<const float4 *>(smem_conv)[lane * 9 + 2 * j + 1] : zero;
         w[0][j] = ssm::f2_pack(u.x, v.x);
         w[1][j] = ssm::f2_pack(u.y, v.y);
         w[2][j] = ssm::f2_pack(u.z, v.z);
         w[3][j] = ssm::f2_pack(u.w, v.w);
     }
-    const Tree t = open_tree(p, n, par);
-    if (t.nodes < 0 && threadIdx.x == 0) atomicOr(p.status, kDevBadState);
-    ssm::copies_wait<0>();
-    if (t.nodes <= 0) return;
-    __syncthreads();
-    if (!on) return;
-    T *y = static_cast<T *>(p.y) + (size_t)t.first * p.D + c;
-    for (int i = first_row; i < t.nodes; i += kRows) {
-        ssm::f2 acc[4];
+    const T *x = static_cast<const T *>(p.x) + (on ? c : 0);
+    for (int n = blockIdx.x / per; n < p.nseq; n += (int)(gridDim.x / per)) {
+        __syncthreads();                                      // the taps, or the tree before, have been read
+        // what open_tree checks, before the copies that do not depend on the parents
+        const int lo = p.cu[n], hi = p.cu[n + 1], slot = p.slots ? p.slots[n] : n;
+        const bool fits = lo >= 0 && hi >= lo && hi <= p.total_T && hi - lo <= kNodes && slot >= 0 && slot < p.n_slots;
+        if (fits) {
+            for (int i = first_row; i < hi - lo; i += kRows)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = b[j];
-        int a = i;                                            // a node, or -1 - r: r rows before the window's last
+                for (int h = 0; h < H; ++h)
+                    ssm::copy_async<16>(&smem_conv[(i * H + h) * kLanes + lane], x + (size_t)(lo + i) * p.ldx + 4 * h, on && (h == 0 || whole));
+            for (int r = first_row; r < 6 && hi > lo; r += kRows) {
+                const bool in = on && (r % 2 == 0 || whole);
+                ssm::copy_async<16>(&wins[r / 2][r % 2][lane], in ? p.win + ((size_t)slot * ssm::kTaps + 1 + r / 2) * p.D + c + 4 * (r % 2) : p.win, in);
+            }
+        }
+        ssm::copies_commit();
+        const Tree t = open_tree(p, n, par);
+        if (t.nodes < 0 && threadIdx.x == 0) atomicOr(p.status, kDevBadState);
+        ssm::copies_wait<0>();
+        __syncthreads();
+        if (!on) continue;
+        T *y = static_cast<T *>(p.y) + (size_t)t.first * p.D + c;
+        for (int i = first_row; i < t.nodes; i += kRows) {
+            ssm::f2 acc[4];
 #pragma unroll
-        for (int tap = 3; tap >= 0; --tap) {
-            ssm::f2 u[4];
-            if (a >= 0) {
-                ssm::Raw8<T> raw;
+            for (int j = 0; j < 4; ++j) acc[j] = b[j];
+            int a = i;                                        // a node, or -1 - r: r rows before the window's last
 #pragma unroll
-                for (int h = 0; h < H; ++h) raw.w[h] = smem_conv[(a * H + h) * kLanes + lane];
-                ssm::raw_unpack(raw, u);
-                a = par[a];
-            } else {
-                const float4 e = wins[3 + a][0][lane], f = wins[3 + a][1][lane];
-                u[0] = ssm::f2_pack(e.x, e.y);
-                u[1] = ssm::f2_pack(e.z, e.w);
-                u[2] = ssm::f2_pack(f.x, f.y);
-                u[3] = ssm::f2_pack(f.z, f.w);
-                --a;
+            for (int tap = 3; tap >= 0; --tap) {
+                ssm::f2 u[4];
+                if (a >= 0) {
+                    ssm::Raw8<T> raw;
+#pragma unroll
+                    for (int h = 0; h < H; ++h) raw.w[h] = smem_conv[(a * H + h) * kLanes + lane];
+                    ssm::raw_unpack(raw, u);
+                    a = par[a];
+                } else {
+                    const float4 e = wins[3 + a][0][lane], f = wins[3 + a][1][lane];
+                    u[0] = ssm::f2_pack(e.x, e.y);
+                    u[1] = ssm::f2_pack(e.z, e.w);
+                    u[2] = ssm::f2_pack(f.x, f.y);
+                    u[3] = ssm::f2_pack(f.z, f.w);
+                    --a;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[j] = ssm::fma2(w[tap][j], u[j], acc[j]);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[j] = ssm::fma2(w[tap][j], u[j], acc[j]);
+            for (int j = 0; j < 4; ++j) acc[j] = ssm::silu2(acc[j]);
+            ssm::store8(y + (size_t)i * p.D, acc, whole);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = ssm::silu2(acc[j]);
-        ssm::store8(y + (size_t)i * p.D, acc, whole);
     }
 }
 
@@ -236,7 +248,9 @@ template <typename T> cudaError_t commit_any(const TreeParams &p, cudaStream_t s
 template <typename T> cudaError_t conv(const TreeParams &p, cudaStream_t s, int *launches) {
     constexpr int kLanes = conv_lanes<T>();
     const int per = (p.D + 8 * kLanes - 1) / (8 * kLanes), bytes = kNodes * kLanes * 8 * (int)sizeof(T);   // 32 KB
-    conv_tree_kernel<T><<<(unsigned)((size_t)p.nseq * per), kConv, bytes, s>>>(p, per);
+    const long held = 6L * device_sm_count() / per;   // six CTAs an SM by shared memory
+    const long trees = held < 1 ? 1 : held < p.nseq ? held : p.nseq;
+    conv_tree_kernel<T><<<(unsigned)(trees * per), kConv, bytes, s>>>(p, per);
     if (launches) ++*launches;
     return cudaGetLastError();
 }
