@@ -554,7 +554,7 @@ size_t gla_rmsnorm_bwd_workspace_size(int64_t rows, int D, gla_dtype dtype);
  * gla_conv1d_tree: gla_conv1d_fwd along each node's path: y [total_T, D] of
  *   every node from x [total_T, D] (rows ld_x apart) of the node and its last
  *   three ancestors, behind the root those of the window, which stays as it is.
- * Each call is one launch, a commit with windows two.
+ * Each call is one launch.
  */
 #define GLA_TREE_MAX_NODES 64
 gla_status gla_tree_fwd(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,

@@ -979,10 +979,12 @@ def _heads(c, t, shape, name):
 
 def _tree_args(c, T, cu_nodes, parents, slots):
     """The trees of a call: addresses of the offsets, parents and slots, and the number of sequences."""
-    if cu_nodes.dim() != 1 or cu_nodes.numel() < 1:
+    shape = cu_nodes.shape
+    if len(shape) != 1 or shape[0] < 1:
         raise GlaError(GLA_ERR_INVALID_ARG, "argument", "cu_nodes must hold one offset more than there are sequences")
-    nseq = cu_nodes.numel() - 1
-    return c.i32(cu_nodes, (nseq + 1,), "cu_nodes"), c.i32(parents, (T,), "parents"), c.i32(slots, (nseq,), "slots"), nseq
+    i32, whole, nseq = c.torch.int32, c.whole, shape[0] - 1
+    return (whole(cu_nodes, shape, "cu_nodes", i32), whole(parents, (T,), "parents", i32),
+            whole(slots, (nseq,), "slots", i32), nseq)
 
 
 def _tree_fwd(name, q, k, v, decay, gated, cu_nodes, parents, state_pool, slots, scale, o, stream):
@@ -1076,14 +1078,16 @@ class _PagesCall(_Call):
         if not pools:
             raise GlaError(GLA_ERR_INVALID_ARG, "argument", "no pools")
         super().__init__(pools[0], stream, element=False)
-        n = pools[0].shape[0] if pools[0].dim() else 0
-        for t in pools:
-            if t.get_device() != self.index or not t.is_contiguous() or t.dim() < 1 or t.shape[0] != n:
+        index, n, k = self.index, (pools[0].shape or (0,))[0], len(pools)
+        where, size = (_vp * k)(), (_ll * k)()
+        for i, t in enumerate(pools):
+            shape = t.shape
+            if not shape or shape[0] != n or t.get_device() != index or not t.is_contiguous():
                 raise GlaError(GLA_ERR_INVALID_ARG, "argument",
                                "pools must be contiguous, on one device and of as many pages each")
-        k = len(pools)
-        size = [t.numel() // n * t.element_size() if n else 4 for t in pools]
-        self.pools = ((_vp * k)(*[t.data_ptr() for t in pools]), (_ll * k)(*size), k if n else 0, n)
+            where[i] = t.data_ptr()
+            size[i] = t.nbytes // n if n else 4
+        self.pools = (where, size, k if n else 0, n)
 
 
 def gla_pages_copy(pools, src, dst, *, stream=None):

@@ -214,8 +214,7 @@ cudaError_t launch_tree_fwd(const TreeParams &p, bool bf16, cudaStream_t s, int 
 bool tree_fwd_tc_fits(const TreeParams &p);
 cudaError_t launch_tree_fwd_tc(const TreeParams &p, cudaStream_t s, int *launches);
 cudaError_t launch_tree_commit(const TreeParams &p, bool bf16, cudaStream_t s, int *launches);
-// The commit's parts (tree_commit.cu): the windows, then the pages of 96 x 192.
-cudaError_t launch_tree_windows(const TreeParams &p, bool bf16, cudaStream_t s, int *launches);
+// The commit of pages of 96 x 192, with the windows (tree_commit.cu).
 cudaError_t launch_tree_pages(const TreeParams &p, bool bf16, cudaStream_t s, int *launches);
 cudaError_t launch_conv_tree(const TreeParams &p, bool bf16, cudaStream_t s, int *launches);
 

@@ -94,12 +94,19 @@ template <typename T> __global__ void __launch_bounds__(kThreads) tree_fwd_kerne
 // ----------------------------------------------------------------- commit
 constexpr int kCommit = 256;
 
-// Any head sizes: one CTA per (sequence, head). fp32's validation mode; pages of 96 x 192 go through tree_commit.cu.
+// Any head sizes: one CTA per (sequence, head), behind them the windows', a
+// warp a piece. fp32's validation mode; pages of 96 x 192 go through tree_commit.cu.
 template <typename T> __global__ void __launch_bounds__(kCommit) tree_commit_any_kernel(const TreeParams p) {
     extern __shared__ float4 smem4[];
     __shared__ int par[kNodes], way[kNodes], s_len;
     __shared__ float s_w[kNodes], gate[kNodes], s_far;
     float *kt = reinterpret_cast<float *>(smem4);          // [path node][dk], decayed
+    const unsigned pages = (unsigned)p.nseq * (unsigned)p.H;
+    if (blockIdx.x >= pages) {
+        const long piece = (long)(blockIdx.x - pages) * (kCommit / 32) + threadIdx.x / 32;
+        if (piece < window_pieces(p)) commit_window<T>(p, piece);
+        return;
+    }
     const int n = blockIdx.x / p.H, h = blockIdx.x % p.H, tid = threadIdx.x;
     const int last = p.last[n];
     const Tree t = open_tree(p, n, par);
@@ -152,6 +159,7 @@ template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(
     extern __shared__ uint4 smem_conv[];                      // [nodes][pieces of 16 bytes][lanes]
     __shared__ __align__(16) float4 wins[3][2][kLanes];       // the window's rows 1 .. 3
     __shared__ int par[kNodes];
+    __shared__ char4 up[kNodes];                              // a node's last three ancestors: nodes, or -1 - r: r rows before the window's last
     const int lane = threadIdx.x % kLanes, first_row = threadIdx.x / kLanes;
     const int c = ((int)(blockIdx.x % per) * kLanes + lane) * 8;
     const bool on = c < p.D, whole = c + 8 <= p.D;
@@ -193,38 +201,43 @@ template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(
         ssm::copies_commit();
         const Tree t = open_tree(p, n, par);
         if (t.nodes < 0 && threadIdx.x == 0) atomicOr(p.status, kDevBadState);
+        if ((int)threadIdx.x < t.nodes) {
+            int a[4] = {(int)threadIdx.x};
+#pragma unroll
+            for (int k = 1; k < 4; ++k) a[k] = a[k - 1] >= 0 ? par[a[k - 1]] : a[k - 1] - 1;
+            up[threadIdx.x] = make_char4((signed char)a[1], (signed char)a[2], (signed char)a[3], 0);
+        }
         ssm::copies_wait<0>();
         __syncthreads();
         if (!on) continue;
-        T *y = static_cast<T *>(p.y) + (size_t)t.first * p.D + c;
-        for (int i = first_row; i < t.nodes; i += kRows) {
-            ssm::f2 acc[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[j] = b[j];
-            int a = i;                                        // a node, or -1 - r: r rows before the window's last
-#pragma unroll
-            for (int tap = 3; tap >= 0; --tap) {
+        T *y = static_cast<T *>(p.y) + (size_t)(t.first + first_row) * p.D + c;
+        for (int i = first_row; i < t.nodes; i += kRows, y += (size_t)kRows * p.D) {
+            const auto tap = [&](int a, const ssm::f2 (&wt)[4], ssm::f2 (&acc)[4]) {
                 ssm::f2 u[4];
                 if (a >= 0) {
                     ssm::Raw8<T> raw;
 #pragma unroll
                     for (int h = 0; h < H; ++h) raw.w[h] = smem_conv[(a * H + h) * kLanes + lane];
                     ssm::raw_unpack(raw, u);
-                    a = par[a];
                 } else {
                     const float4 e = wins[3 + a][0][lane], f = wins[3 + a][1][lane];
                     u[0] = ssm::f2_pack(e.x, e.y);
                     u[1] = ssm::f2_pack(e.z, e.w);
                     u[2] = ssm::f2_pack(f.x, f.y);
                     u[3] = ssm::f2_pack(f.z, f.w);
-                    --a;
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[j] = ssm::fma2(w[tap][j], u[j], acc[j]);
-            }
+                for (int j = 0; j < 4; ++j) acc[j] = ssm::fma2(wt[j], u[j], acc[j]);
+            };
+            const char4 a = up[i];
+            ssm::f2 acc[4] = {b[0], b[1], b[2], b[3]};
+            tap(i, w[3], acc);
+            tap((signed char)a.x, w[2], acc);
+            tap((signed char)a.y, w[1], acc);
+            tap((signed char)a.z, w[0], acc);
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[j] = ssm::silu2(acc[j]);
-            ssm::store8(y + (size_t)i * p.D, acc, whole);
+            ssm::store8(y, acc, whole);
         }
     }
 }
@@ -240,7 +253,8 @@ template <typename T> cudaError_t fwd_any(const TreeParams &p, cudaStream_t s, i
 
 template <typename T> cudaError_t commit_any(const TreeParams &p, cudaStream_t s, int *launches) {
     const int bytes = kNodes * p.dk * (int)sizeof(float);   // at most 32 KB
-    tree_commit_any_kernel<T><<<(unsigned)((size_t)p.nseq * p.H), kCommit, bytes, s>>>(p);
+    const long blocks = (long)p.nseq * p.H + (window_pieces(p) + kCommit / 32 - 1) / (kCommit / 32);
+    tree_commit_any_kernel<T><<<(unsigned)blocks, kCommit, bytes, s>>>(p);
     if (launches) ++*launches;
     return cudaGetLastError();
 }
@@ -262,9 +276,7 @@ cudaError_t launch_tree_fwd(const TreeParams &p, bool bf16, cudaStream_t s, int 
     return bf16 ? fwd_any<__nv_bfloat16>(p, s, launches) : fwd_any<float>(p, s, launches);
 }
 cudaError_t launch_tree_commit(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {
-    const cudaError_t e = p.x ? launch_tree_windows(p, bf16, s, launches) : cudaSuccess;
-    if (e != cudaSuccess || p.H == 0) return e;
-    if (p.dk == 96 && p.dv == 192) return launch_tree_pages(p, bf16, s, launches);
+    if (p.dk == 96 && p.dv == 192 && p.H > 0) return launch_tree_pages(p, bf16, s, launches);
     return bf16 ? commit_any<__nv_bfloat16>(p, s, launches) : commit_any<float>(p, s, launches);
 }
 cudaError_t launch_conv_tree(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {

@@ -15,11 +15,12 @@
 //                walk, the decays, and the path's tokens as fp32 W_j k_j and v_j,
 //                eight a piece. (One such warp, whose unit waits for two loads in
 //                turn, held the rest up: 583 us.)
+//   warps 18, 19 the windows, beside the pages' copies (in a launch of their
+//                own before this one: 26 us more).
 // (A CTA for each page, its path found while nothing was in flight: 853 us at
 // 1,280 sequences, H = 16, where this one takes MEASURED.)
 // Sums in fp32, in the path's order from the accepted node to the state.
 #include "ptx.cuh"
-#include "ssm_common.cuh"
 #include "tree_common.cuh"
 
 namespace gla {
@@ -29,7 +30,7 @@ using namespace ptx;
 using tree::kNodes;
 
 constexpr int kDk = 96, kDv = 192, kRows = kDk / 2, kGroup = 6, kCompute = 2 * kGroup;
-constexpr int kMetas = 4, kThreads = (kCompute + 2 + kMetas) * 32, kPiece = 8, kOwn = 12;   // kMetas: planners, each with a plan and a piece; kOwn: a thread's rows
+constexpr int kMetas = 4, kWindows = 2, kThreads = (kCompute + 2 + kMetas + kWindows) * 32, kPiece = 8, kOwn = 12;   // kMetas: planners, each with a plan and a piece; kOwn: a thread's rows
 constexpr uint32_t kHalf = kRows * kDv * 4, kTokens = kPiece * (kDk + kDv) * 4;
 constexpr uint32_t kOffPiece = 4 * kHalf, kOffMeta = kOffPiece + kMetas * kTokens;
 
@@ -212,7 +213,10 @@ template <typename T, bool kGate> __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     __syncthreads();
-    if (warp >= kCompute + 2) {
+    if (warp >= kCompute + 2 + kMetas) {
+        const long pieces = tree::window_pieces(p);
+        for (long i = (long)blockIdx.x * kWindows + warp - (kCompute + 2 + kMetas); i < pieces; i += (long)gridDim.x * kWindows) tree::commit_window<T>(p, i);
+    } else if (warp >= kCompute + 2) {
         planner<T, kGate>(p, sm, base, ctl, units, warp - kCompute - 2);
     } else if (warp >= kCompute) {
         if (lane == 0) copies(p, sm, base, ctl, units, warp - kCompute);
@@ -269,80 +273,22 @@ template <typename T, bool kGate> __global__ void __launch_bounds__(kThreads, 1)
             ++done;
         }
     }
-    if (p.x) ssm::wait_for_previous();   // the windows' launch before this one: whoever waits for this waits for both
-}
-
-// The windows: four channels a thread.
-constexpr int kWindow = 192;
-template <typename T> __global__ void __launch_bounds__(kWindow) tree_window_kernel(const TreeParams p, int per) {
-    __shared__ int par[kNodes];
-    ssm::let_next_start();
-    const int n = blockIdx.x / per, c = ((int)(blockIdx.x % per) * kWindow + (int)threadIdx.x) * 4, last = p.last[n];
-    const tree::Tree t = tree::open_tree(p, n, par);
-    if (t.nodes < 0 || last < -1 || last >= t.nodes) {
-        if (threadIdx.x == 0) atomicOr(p.status, kDevBadState);
-        return;
-    }
-    if (last < 0 || c >= p.D) return;
-    float *win = p.win + (size_t)t.slot * ssm::kTaps * p.D + c;
-    int at[ssm::kTaps], len = 0;     // the path's last four inputs, the newest first
-#pragma unroll
-    for (int k = 0, j = last; k < ssm::kTaps; ++k) {
-        at[k] = j;
-        if (j >= 0) {
-            ++len;
-            j = par[j];
-        }
-    }
-    float4 row[ssm::kTaps];
-#pragma unroll
-    for (int r = 0; r < ssm::kTaps; ++r) {
-        const int back = ssm::kTaps - 1 - r;
-        if (back < len) {
-            const T *x = static_cast<const T *>(p.x) + (size_t)(t.first + at[back]) * p.ldx + c;
-            if constexpr (sizeof(T) == 2) {
-                const uint2 v = *reinterpret_cast<const uint2 *>(x);
-                const float2 a = unpack_bf16x2(v.x), b = unpack_bf16x2(v.y);
-                row[r] = make_float4(a.x, a.y, b.x, b.y);
-            } else {
-                row[r] = *reinterpret_cast<const float4 *>(x);
-            }
-        } else {                      // before them what the window held
-            row[r] = *reinterpret_cast<const float4 *>(win + (size_t)(r + len) * p.D);
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < ssm::kTaps; ++r) *reinterpret_cast<float4 *>(win + (size_t)r * p.D) = row[r];
-}
-
-template <typename T> cudaError_t windows(const TreeParams &p, cudaStream_t s, int *launches) {
-    const int per = (p.D + 4 * kWindow - 1) / (4 * kWindow);
-    tree_window_kernel<T><<<(unsigned)((size_t)p.nseq * per), kWindow, 0, s>>>(p, per);
-    if (launches) ++*launches;
-    return cudaGetLastError();
 }
 
 template <typename T> cudaError_t pages(const TreeParams &p, cudaStream_t s, int *launches) {
     auto *kern = p.g ? tree_commit_kernel<T, true> : tree_commit_kernel<T, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
-    const long units = (long)p.nseq * p.H, most = device_sm_count();
-    const unsigned grid = (unsigned)(units < most ? units : most);
-    if (p.x) {   // beside the windows' launch, which has nothing to do with the pages
-        e = ssm::launch_behind(kern, dim3(grid), kThreads, (int)kSmem, s, p);
-    } else {
-        kern<<<grid, kThreads, kSmem, s>>>(p);
-        e = cudaGetLastError();
-    }
-    if (e == cudaSuccess && launches) ++*launches;
-    return e;
+    const long units = (long)p.nseq * p.H, pieces = (tree::window_pieces(p) + kWindows - 1) / kWindows, most = device_sm_count();
+    const long want = units > pieces ? units : pieces;
+    const unsigned grid = (unsigned)(want < most ? want : most);
+    kern<<<grid, kThreads, kSmem, s>>>(p);
+    if (launches) ++*launches;
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_tree_windows(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {
-    return bf16 ? windows<__nv_bfloat16>(p, s, launches) : windows<float>(p, s, launches);
-}
 cudaError_t launch_tree_pages(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {
     return bf16 ? pages<__nv_bfloat16>(p, s, launches) : pages<float>(p, s, launches);
 }

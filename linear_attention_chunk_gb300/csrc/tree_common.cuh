@@ -4,6 +4,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "ssm_common.cuh"
 
 namespace gla {
 namespace tree {
@@ -55,6 +56,59 @@ __device__ __forceinline__ unsigned long long walk(int i, const int *par, const 
     }
     far = w;
     return seen;
+}
+
+// The windows of a commit, in pieces of 128 channels of a sequence, a warp each
+// (four channels a lane): the last four inputs of the accepted path, before them
+// what the window held.
+__host__ __device__ __forceinline__ long window_pieces(const TreeParams &p) { return p.x ? (long)p.nseq * ((p.D + 127) / 128) : 0; }
+
+template <typename T> __device__ __forceinline__ void commit_window(const TreeParams &p, long piece) {
+    const int lane = threadIdx.x % 32, per = (p.D + 127) / 128, n = (int)(piece / per), c = (int)(piece % per) * 128 + lane * 4;
+    const int a = __ldg(p.cu + n), b = __ldg(p.cu + n + 1), slot = p.slots ? __ldg(p.slots + n) : n, last = __ldg(p.last + n);
+    bool bad = a < 0 || b < a || b > p.total_T || b - a > kNodes || slot < 0 || slot >= p.n_slots || last < -1 || last >= b - a;
+    int par[2] = {-1, -1};   // of nodes lane and lane + 32
+    if (!bad)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = lane + 32 * e;
+            if (i < b - a) par[e] = __ldg(p.parents + a + i);
+            bad |= par[e] < -1 || (par[e] >= i && i < b - a);
+        }
+    if (__any_sync(0xffffffffu, bad)) {
+        if (lane == 0) atomicOr(p.status, kDevBadState);
+        return;
+    }
+    if (last < 0) return;
+    int at[ssm::kTaps], len = 0;   // the newest first
+#pragma unroll
+    for (int k = 0, j = last; k < ssm::kTaps; ++k) {
+        at[k] = j;
+        len += j >= 0;
+        const int lo = __shfl_sync(0xffffffffu, par[0], j & 31), hi = __shfl_sync(0xffffffffu, par[1], j & 31);
+        if (j >= 0) j = j < 32 ? lo : hi;
+    }
+    if (c >= p.D) return;
+    float *win = p.win + (size_t)slot * ssm::kTaps * p.D + c;
+    float4 row[ssm::kTaps];
+#pragma unroll
+    for (int r = 0; r < ssm::kTaps; ++r) {
+        const int back = ssm::kTaps - 1 - r;
+        if (back < len) {
+            const T *x = static_cast<const T *>(p.x) + (size_t)(a + at[back]) * p.ldx + c;
+            if constexpr (sizeof(T) == 2) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(x);
+                const float2 u = unpack_bf16x2(v.x), w = unpack_bf16x2(v.y);
+                row[r] = make_float4(u.x, u.y, w.x, w.y);
+            } else {
+                row[r] = *reinterpret_cast<const float4 *>(x);
+            }
+        } else {
+            row[r] = *reinterpret_cast<const float4 *>(win + (size_t)(r + len) * p.D);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < ssm::kTaps; ++r) *reinterpret_cast<float4 *>(win + (size_t)r * p.D) = row[r];
 }
 
 }  // namespace tree
