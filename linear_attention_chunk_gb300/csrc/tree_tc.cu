@@ -492,15 +492,13 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
                         }
                 }
             }
-            const size_t step = (size_t)p.H * kDv;
-            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + ((size_t)m->first * p.H + u % (uint32_t)p.H) * kDv + warp * 16 + 4 * q4 + (size_t)g * step;
+            if (dirty) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int r = 0; r < 2; ++r, o += 8 * step) {
-                    const int x = i * 16 + g + 8 * r;
-                    if (x >= M) continue;
-                    if (dirty) {
+                for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+                    for (int r = 0; r < 2; ++r) {
+                        const int x = i * 16 + g + 8 * r;
+                        if (x >= M) continue;
                         const __nv_bfloat16 *ph = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPh + (uint32_t)(s * kNodes + x) * kPitchP);
                         const __nv_bfloat16 *pl = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPl + (uint32_t)(s * kNodes + x) * kPitchP);
                         for (unsigned long long path = m->path[x]; path; path &= path - 1) {
@@ -515,10 +513,19 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
                                     const float y = __bfloat162float(v[2 * e + t]);
-                                    if (!isfinite(y) && w != 0.f) acc[i][t][2 * r + e] += w * y;
+                                    if (!isfinite(y) && w != 0.f) acc[i][t][e] += r ? 0.f : w * y, acc[i][t][2 + e] += r ? w * y : 0.f;
                                 }
                         }
                     }
+            }
+            const size_t step = (size_t)p.H * kDv;
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + ((size_t)m->first * p.H + u % (uint32_t)p.H) * kDv + warp * 16 + 4 * q4 + (size_t)g * step;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 2; ++r, o += 8 * step) {
+                    const int x = i * 16 + g + 8 * r;
+                    if (x >= M) continue;
                     *reinterpret_cast<uint2 *>(o) =
                         make_uint2(pack_bf16x2(p.scale * acc[i][0][2 * r], p.scale * acc[i][1][2 * r]),
                                    pack_bf16x2(p.scale * acc[i][0][2 * r + 1], p.scale * acc[i][1][2 * r + 1]));
