@@ -334,6 +334,171 @@ __device__ __forceinline__ void scorer(unsigned char *sm, uint32_t base, const W
     }
 }
 
+// A consumer warp's share of a unit of 1 .. 16 kTiles nodes: 16 channels of its rows. Code of its own for each
+// number of tiles: without branches, and no longer than it needs to be (a unit runs through it once, so that
+// instructions not met cost as much as some that are). False: a wait has given up.
+struct Unit {
+    unsigned char *sm;
+    uint32_t base, x0, x1;   // this thread's entries of a stage
+    const Meta *m;
+    int s, done, warp;
+    uint32_t par;
+    size_t row;              // the first node's row of o and of this head
+};
+template <int kTiles> __device__ __forceinline__ bool readout(const TreeParams &p, const Unit &unit, const WaitCtl &ctl) {
+    const int lane = threadIdx.x % 32, g = lane / 4, q4 = lane % 4;   // a fragment's row (or column), its pair of columns (or rows)
+    const uint32_t a_row = lane % 16, a_col = lane / 16 * 8, base = unit.base, x0 = unit.x0, x1 = unit.x1, par = unit.par;
+    const int s = unit.s, done = unit.done, warp = unit.warp, M = unit.m->nodes;
+    const Meta *m = unit.m;
+    unsigned char *sm = unit.sm;
+    auto bar = [&](int i) { return base + kOffBars + 8u * (uint32_t)i; };
+    auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, ctl)); };
+    // q's fragments of even and odd steps: all else of their addresses is constant
+    const uint32_t sQ[2] = {at_q(base + kOffQ + (uint32_t)s * kNodeQ, a_row, a_col), at_q(base + kOffQ + (uint32_t)s * kNodeQ, a_row, 16 + a_col)};
+    float acc[kTiles][2][4];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[i][t][c] = 0.f;
+    const auto entries = [&](int ks, float2 (&y)[4]) {
+        const uint32_t st = (uint32_t)ks * kStage;
+        y[0] = lds2f(x0 + st);
+        y[1] = lds2f(x1 + st);
+        y[2] = lds2f(x0 + st + 1024);
+        y[3] = lds2f(x1 + st + 1024);
+    };
+    if (!wait(FULL_S, (uint32_t)done & 1u)) return false;
+    float2 y[2][4];   // a step's and the next one's
+    entries(0, y[0]);
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks) {
+        if (ks == kHalf - 1 && !wait(FULL_S + 1, (uint32_t)done & 1u)) return false;
+        if (ks < kSteps - 1) entries(ks + 1, y[(ks + 1) & 1]);
+        const float2(&now)[4] = y[ks & 1];
+        uint32_t hi[2][2], lo[2][2];
+        split(now[0].x, now[1].x, hi[0][0], lo[0][0]);
+        split(now[0].y, now[1].y, hi[1][0], lo[1][0]);
+        split(now[2].x, now[3].x, hi[0][1], lo[0][1]);
+        split(now[2].y, now[3].y, hi[1][1], lo[1][1]);
+        if (ks % kHalf == kHalf - 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(EMPTY_S + ks / kHalf));
+        }
+        uint32_t a[kTiles][4];
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+            ldmatrix4(a[i], sQ[ks & 1] + (uint32_t)i * kTileQ + (uint32_t)(ks >> 1) * 1024);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+            mma16816(acc[i][0], a[i], hi[0][0], hi[0][1]);
+            mma16816(acc[i][1], a[i], hi[1][0], hi[1][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+            mma16816(acc[i][0], a[i], lo[0][0], lo[0][1]);
+            mma16816(acc[i][1], a[i], lo[1][0], lo[1][1]);
+        }
+    }
+    // the state's decay: 0 clears it, whatever it holds
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+        const float f[2] = {m->far[i * 16 + g], m->far[i * 16 + g + 8]};
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[i][t][c] *= f[c >> 1];
+        if (__any_sync(0xffffffffu, f[0] == 0.f || f[1] == 0.f)) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[i][t][c] = f[c >> 1] == 0.f ? 0.f : acc[i][t][c];
+        }
+    }
+    // P V: 16 nodes j at a time
+    if (!wait(FULL_P + s, par)) return false;
+    // (of a tile of v, three pieces of 64 channels with the 128-byte swizzle; channels 2 g, 2 g + 1 of the warp's 16)
+    const uint32_t bV = base + kOffV + (uint32_t)s * kNodeV + (uint32_t)(warp / 4) * 2048 + (uint32_t)(g & 3) * 4, cV = (uint32_t)(warp & 3) * 2 + (uint32_t)(g >> 2);
+    const uint32_t sV[2] = {bV + (uint32_t)(2 * q4) * 128 + ((cV ^ (uint32_t)(2 * q4)) << 4), bV + (uint32_t)(2 * q4 + 1) * 128 + ((cV ^ (uint32_t)(2 * q4 + 1)) << 4)};
+    const uint32_t sP = base + kOffPh + ((uint32_t)s * kNodes + a_row) * kPitchP + a_col * 2;
+    bool dirty = false;
+#pragma unroll
+    for (int js = 0; js < kTiles; ++js) {
+        uint32_t x[4], odd = 0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int j = 2 * q4 + (r & 1) + (r >> 1) * 8;
+            x[r] = lds1(sV[r & 1] + (uint32_t)js * kTileV + (uint32_t)(r >> 1) * 1024);
+            if (js * 16 + j >= M) x[r] = 0;             // (rows of another tree)
+            odd |= mul_bf16x2(x[r], 0) & 0x7fff7fffu;        // not 0: an element that is not finite
+        }
+        // One that is not finite would reach every node by way of 0 x inf: it is left out here and added on its paths below.
+        if (__any_sync(0xffffffffu, odd != 0)) {
+            dirty = true;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = finite2(x[r]);
+        }
+        uint32_t b[2][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            b[0][r] = __byte_perm(x[2 * r], x[2 * r + 1], 0x5410);
+            b[1][r] = __byte_perm(x[2 * r], x[2 * r + 1], 0x7632);
+        }
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            uint32_t a[kTiles][4];
+#pragma unroll
+            for (int i = js; i < kTiles; ++i)
+                ldmatrix4(a[i], sP + (uint32_t)part * (kOffPl - kOffPh) + (uint32_t)i * 16 * kPitchP + (uint32_t)js * 32);
+#pragma unroll
+            for (int i = js; i < kTiles; ++i) {
+                mma16816(acc[i][0], a[i], b[0][0], b[0][1]);
+                mma16816(acc[i][1], a[i], b[1][0], b[1][1]);
+            }
+        }
+    }
+    if (dirty) {
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll 1
+            for (int r = 0; r < 2; ++r) {
+                const int x = i * 16 + g + 8 * r;
+                if (x >= M) continue;
+                const __nv_bfloat16 *ph = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPh + (uint32_t)(s * kNodes + x) * kPitchP);
+                const __nv_bfloat16 *pl = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPl + (uint32_t)(s * kNodes + x) * kPitchP);
+                for (unsigned long long path = m->path[x]; path; path &= path - 1) {
+                    const int j = __ffsll((long long)path) - 1;
+                    const float w = __bfloat162float(ph[j]) + __bfloat162float(pl[j]);
+                    // channels 4 q4 .. 4 q4 + 3 of the warp's 16
+                    const uint32_t piece = kOffV + (uint32_t)s * kNodeV + (uint32_t)(j >> 4) * kTileV + (uint32_t)(warp / 4) * 2048 + (uint32_t)(j & 15) * 128;
+                    const uint32_t c16 = ((uint32_t)(warp & 3) * 2 + (uint32_t)(q4 >> 1)) ^ (uint32_t)(j & 7);
+                    const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(sm + piece + c16 * 16 + (uint32_t)(q4 & 1) * 8);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float y = __bfloat162float(v[2 * e + t]);
+                            if (!isfinite(y) && w != 0.f) acc[i][t][e] += r ? 0.f : w * y, acc[i][t][2 + e] += r ? w * y : 0.f;
+                        }
+                }
+            }
+    }
+    const size_t step = (size_t)p.H * kDv;
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + unit.row * kDv + warp * 16 + 4 * q4 + (size_t)g * step;
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r, o += 8 * step) {
+            const int x = i * 16 + g + 8 * r;
+            if (x >= M) continue;
+            *reinterpret_cast<uint2 *>(o) =
+                make_uint2(pack_bf16x2(p.scale * acc[i][0][2 * r], p.scale * acc[i][1][2 * r]),
+                           pack_bf16x2(p.scale * acc[i][0][2 * r + 1], p.scale * acc[i][1][2 * r + 1]));
+        }
+    return true;
+}
+
 template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -368,7 +533,6 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
         return;
     }
     const int g = lane / 4, q4 = lane % 4;   // a fragment's row (or column), its pair of columns (or rows)
-    const uint32_t a_row = lane % 16, a_col = lane / 16 * 8;
     // This thread's entries of a stage: channels 2 g, 2 g + 1 of the warp's 16, rows 2 q4, 2 q4 + 1 and eight below those
     const uint32_t box = base + (uint32_t)(warp / 2) * kBox + (uint32_t)(g & 1) * 8, chunk = (uint32_t)(warp & 1) * 4 + (uint32_t)(g >> 1);
     const uint32_t x0 = box + (uint32_t)(2 * q4) * 128 + ((chunk ^ (uint32_t)(2 * q4)) << 4);
@@ -380,156 +544,10 @@ template <bool kGate> __global__ void __launch_bounds__(kThreads, 1) tree_fwd_tc
         const uint32_t par = (uint32_t)(it >> 1) & 1u;
         if (!wait(FULL_N + s, par)) return;   // (and with it the plan, which the copies' warp has waited for)
         const Meta *m = reinterpret_cast<const Meta *>(sm + kOffMeta) + meta;
-        const int M = m->nodes, tiles = (M + 15) / 16;
+        const int M = m->nodes;
         if (M > 0) {
-            // q's fragments of even and odd steps: all else of their addresses is constant
-            const uint32_t sQ[2] = {at_q(base + kOffQ + (uint32_t)s * kNodeQ, a_row, a_col), at_q(base + kOffQ + (uint32_t)s * kNodeQ, a_row, 16 + a_col)};
-            float acc[4][2][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[i][t][c] = 0.f;
-            const auto entries = [&](int ks, float2 (&y)[4]) {
-                const uint32_t st = (uint32_t)ks * kStage;
-                y[0] = lds2f(x0 + st);
-                y[1] = lds2f(x1 + st);
-                y[2] = lds2f(x0 + st + 1024);
-                y[3] = lds2f(x1 + st + 1024);
-            };
-            if (!wait(FULL_S, (uint32_t)done & 1u)) return;
-            float2 y[2][4];   // a step's and the next one's
-            entries(0, y[0]);
-#pragma unroll
-            for (int ks = 0; ks < kSteps; ++ks) {
-                if (ks == kHalf - 1 && !wait(FULL_S + 1, (uint32_t)done & 1u)) return;
-                if (ks < kSteps - 1) entries(ks + 1, y[(ks + 1) & 1]);
-                const float2(&now)[4] = y[ks & 1];
-                uint32_t hi[2][2], lo[2][2];
-                split(now[0].x, now[1].x, hi[0][0], lo[0][0]);
-                split(now[0].y, now[1].y, hi[1][0], lo[1][0]);
-                split(now[2].x, now[3].x, hi[0][1], lo[0][1]);
-                split(now[2].y, now[3].y, hi[1][1], lo[1][1]);
-                if (ks % kHalf == kHalf - 1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(EMPTY_S + ks / kHalf));
-                }
-                uint32_t a[4][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < tiles) ldmatrix4(a[i], sQ[ks & 1] + (uint32_t)i * kTileQ + (uint32_t)(ks >> 1) * 1024);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < tiles) {
-                        mma16816(acc[i][0], a[i], hi[0][0], hi[0][1]);
-                        mma16816(acc[i][1], a[i], hi[1][0], hi[1][1]);
-                    }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < tiles) {
-                        mma16816(acc[i][0], a[i], lo[0][0], lo[0][1]);
-                        mma16816(acc[i][1], a[i], lo[1][0], lo[1][1]);
-                    }
-            }
-            // the state's decay: 0 clears it, whatever it holds
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < tiles) {
-                    const float f[2] = {m->far[i * 16 + g], m->far[i * 16 + g + 8]};
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[i][t][c] *= f[c >> 1];
-                    if (__any_sync(0xffffffffu, f[0] == 0.f || f[1] == 0.f)) {
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) acc[i][t][c] = f[c >> 1] == 0.f ? 0.f : acc[i][t][c];
-                    }
-                }
-            // P V: 16 nodes j at a time
-            if (!wait(FULL_P + s, par)) return;
-            // (of a tile of v, three pieces of 64 channels with the 128-byte swizzle; channels 2 g, 2 g + 1 of the warp's 16)
-            const uint32_t bV = base + kOffV + (uint32_t)s * kNodeV + (uint32_t)(warp / 4) * 2048 + (uint32_t)(g & 3) * 4, cV = (uint32_t)(warp & 3) * 2 + (uint32_t)(g >> 2);
-            const uint32_t sV[2] = {bV + (uint32_t)(2 * q4) * 128 + ((cV ^ (uint32_t)(2 * q4)) << 4), bV + (uint32_t)(2 * q4 + 1) * 128 + ((cV ^ (uint32_t)(2 * q4 + 1)) << 4)};
-            const uint32_t sP = base + kOffPh + ((uint32_t)s * kNodes + a_row) * kPitchP + a_col * 2;
-            bool dirty = false;
-#pragma unroll
-            for (int js = 0; js < 4; ++js) {
-                if (js >= tiles) break;
-                uint32_t x[4], odd = 0;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = 2 * q4 + (r & 1) + (r >> 1) * 8;
-                    x[r] = lds1(sV[r & 1] + (uint32_t)js * kTileV + (uint32_t)(r >> 1) * 1024);
-                    if (js * 16 + j >= M) x[r] = 0;             // (rows of another tree)
-                    odd |= mul_bf16x2(x[r], 0) & 0x7fff7fffu;        // not 0: an element that is not finite
-                }
-                // One that is not finite would reach every node by way of 0 x inf: it is left out here and added on its paths below.
-                if (__any_sync(0xffffffffu, odd != 0)) {
-                    dirty = true;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) x[r] = finite2(x[r]);
-                }
-                uint32_t b[2][2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    b[0][r] = __byte_perm(x[2 * r], x[2 * r + 1], 0x5410);
-                    b[1][r] = __byte_perm(x[2 * r], x[2 * r + 1], 0x7632);
-                }
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    uint32_t a[4][4];
-#pragma unroll
-                    for (int i = js; i < 4; ++i)
-                        if (i < tiles) ldmatrix4(a[i], sP + (uint32_t)part * (kOffPl - kOffPh) + (uint32_t)i * 16 * kPitchP + (uint32_t)js * 32);
-#pragma unroll
-                    for (int i = js; i < 4; ++i)
-                        if (i < tiles) {
-                            mma16816(acc[i][0], a[i], b[0][0], b[0][1]);
-                            mma16816(acc[i][1], a[i], b[1][0], b[1][1]);
-                        }
-                }
-            }
-            if (dirty) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll 1
-                    for (int r = 0; r < 2; ++r) {
-                        const int x = i * 16 + g + 8 * r;
-                        if (x >= M) continue;
-                        const __nv_bfloat16 *ph = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPh + (uint32_t)(s * kNodes + x) * kPitchP);
-                        const __nv_bfloat16 *pl = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPl + (uint32_t)(s * kNodes + x) * kPitchP);
-                        for (unsigned long long path = m->path[x]; path; path &= path - 1) {
-                            const int j = __ffsll((long long)path) - 1;
-                            const float w = __bfloat162float(ph[j]) + __bfloat162float(pl[j]);
-                            // channels 4 q4 .. 4 q4 + 3 of the warp's 16
-                            const uint32_t piece = kOffV + (uint32_t)s * kNodeV + (uint32_t)(j >> 4) * kTileV + (uint32_t)(warp / 4) * 2048 + (uint32_t)(j & 15) * 128;
-                            const uint32_t c16 = ((uint32_t)(warp & 3) * 2 + (uint32_t)(q4 >> 1)) ^ (uint32_t)(j & 7);
-                            const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(sm + piece + c16 * 16 + (uint32_t)(q4 & 1) * 8);
-#pragma unroll
-                            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const float y = __bfloat162float(v[2 * e + t]);
-                                    if (!isfinite(y) && w != 0.f) acc[i][t][e] += r ? 0.f : w * y, acc[i][t][2 + e] += r ? w * y : 0.f;
-                                }
-                        }
-                    }
-            }
-            const size_t step = (size_t)p.H * kDv;
-            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + ((size_t)m->first * p.H + u % (uint32_t)p.H) * kDv + warp * 16 + 4 * q4 + (size_t)g * step;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int r = 0; r < 2; ++r, o += 8 * step) {
-                    const int x = i * 16 + g + 8 * r;
-                    if (x >= M) continue;
-                    *reinterpret_cast<uint2 *>(o) =
-                        make_uint2(pack_bf16x2(p.scale * acc[i][0][2 * r], p.scale * acc[i][1][2 * r]),
-                                   pack_bf16x2(p.scale * acc[i][0][2 * r + 1], p.scale * acc[i][1][2 * r + 1]));
-                }
+            const Unit unit{sm, base, x0, x1, m, s, done, warp, par, (size_t)m->first * p.H + u % (uint32_t)p.H};
+            if (!(M <= 16 ? readout<1>(p, unit, ctl) : M <= 32 ? readout<2>(p, unit, ctl) : M <= 48 ? readout<3>(p, unit, ctl) : readout<4>(p, unit, ctl))) return;
             ++done;
         }
         __syncwarp();
