@@ -594,7 +594,8 @@ gla_status gla_conv1d_tree(const void *x, int64_t ld_x, const float *w, const fl
  *   use, those at L and above move into the free ones below L, the lowest into
  *   the lowest and so on; the pages that they leave keep their contents. map
  *   [n_slots] gets each page's new number (-1: not in use), count [1] gets L.
- *   Two launches; workspace: at least gla_pages_compact_workspace_size() bytes.
+ *   workspace: at least gla_pages_compact_workspace_size() bytes (0 up to 4,096
+ *   pages: one launch; above, two).
  */
 #define GLA_PAGES_MAX_POOLS 128
 gla_status gla_pages_copy(void *const *pools, const int64_t *page_bytes, int n_pools, int n_slots, const int *src,

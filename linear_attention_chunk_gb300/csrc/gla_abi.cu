@@ -1179,7 +1179,7 @@ gla_status gla_pages_clear(void *const *pools, const int64_t *page_bytes, int n_
 }
 
 size_t gla_pages_compact_workspace_size(int n_slots) {
-    return n_slots < 0 ? 0 : (size_t)(2 * ((long)n_slots / 2 + 1) + 1) * sizeof(int);
+    return n_slots < 0 || !pages_plan_listed(n_slots) ? 0 : (size_t)(2 * ((long)n_slots / 2 + 1) + 1) * sizeof(int);
 }
 
 gla_status gla_pages_compact(void *const *pools, const int64_t *page_bytes, int n_pools, int n_slots,
@@ -1195,10 +1195,12 @@ gla_status gla_pages_compact(void *const *pools, const int64_t *page_bytes, int 
         if (!live) return fail(GLA_ERR_INVALID_ARG, "live is NULL");
         REQUIRE_INTS(map, "map");
     }
-    REQUIRE_INTS(workspace, "workspace");
     const size_t need = gla_pages_compact_workspace_size(n_slots);
-    if (workspace_bytes < need)
-        return fail(GLA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+    if (need > 0) {
+        REQUIRE_INTS(workspace, "workspace");
+        if (workspace_bytes < need)
+            return fail(GLA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+    }
     p.live = live, p.map = map, p.count = count, p.moves = static_cast<int *>(workspace);
     if ((st = status_word(&p.status)) != GLA_OK) return st;
     int launches = 0;

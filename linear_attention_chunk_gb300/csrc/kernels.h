@@ -227,10 +227,11 @@ struct PageParams {
     const int *src, *dst;        // src NULL: clear
     const unsigned char *live;   // compact: [n_slots]
     int *map, *count;            // compact: [n_slots], [1]
-    int *moves;                  // compact's workspace: sources, then targets, then their number
+    int *moves;                  // compact's workspace, of many pages: sources, then targets, then their number
     unsigned int *status;
 };
 cudaError_t launch_pages_move(const PageParams &p, cudaStream_t s, int *launches);
+bool pages_plan_listed(int n_slots);   // whether a compaction of so many pages lists its moves in the workspace
 cudaError_t launch_pages_compact(PageParams &p, cudaStream_t s, int *launches);
 
 // Residual addition, layer norm and its gradients (layernorm.cu).

@@ -136,6 +136,34 @@ template <typename T> __global__ void __launch_bounds__(kCommit) tree_commit_any
     __syncthreads();
     float *S = p.pool + (t.slot * p.H + h) * ((size_t)dk * dv);
     const T *v = static_cast<const T *>(p.v) + (size_t)t.first * p.ldv + (size_t)h * dv;
+    if (dv % 4 == 0) {   // four columns of four rows a thread at a time
+        const int cols = dv / 4, c = tid % cols * 4, step = kCommit / cols;
+        for (int r0 = tid / cols; r0 < dk && tid < step * cols; r0 += 4 * step) {
+            float4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (r0 + i * step < dk) {
+                    const float4 y = *reinterpret_cast<const float4 *>(S + (size_t)(r0 + i * step) * dv + c);
+                    x[i] = far == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(far * y.x, far * y.y, far * y.z, far * y.w);
+                }
+            for (int j = 0; j < len; ++j) {
+                const T *w = v + (size_t)way[j] * p.ldv + c;
+                const float4 u = make_float4(Elem<T>::load(w), Elem<T>::load(w + 1), Elem<T>::load(w + 2), Elem<T>::load(w + 3));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float k = r0 + i * step < dk ? kt[j * dk + r0 + i * step] : 0.f;
+                    x[i].x = fmaf(k, u.x, x[i].x);
+                    x[i].y = fmaf(k, u.y, x[i].y);
+                    x[i].z = fmaf(k, u.z, x[i].z);
+                    x[i].w = fmaf(k, u.w, x[i].w);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (r0 + i * step < dk) *reinterpret_cast<float4 *>(S + (size_t)(r0 + i * step) * dv + c) = x[i];
+        }
+        return;
+    }
     for (int e = tid; e < dk * dv; e += kCommit) {
         const int r = e / dv, c = e % dv;
         float x = far == 0.f ? 0.f : far * S[e];

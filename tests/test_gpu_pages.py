@@ -109,7 +109,7 @@ def plan(live):
     return to, count
 
 
-@pytest.mark.parametrize("n", [1, 2, 7, 64, 1023, 1024, 1025, 5000])
+@pytest.mark.parametrize("n", [1, 2, 7, 64, 255, 256, 257, 1024, 1025, 4095, 4096, 4097, 5000])
 @pytest.mark.parametrize("share", [0.0, 0.05, 0.5, 0.95, 1.0])
 def test_compact(gla, n, share):
     rng = random.Random(n * 10 + int(share * 100))
@@ -131,9 +131,10 @@ def test_compact(gla, n, share):
     assert again.tolist() == [i if i < count else -1 for i in range(n)] and k.tolist() == [count] and same(wide, want)
 
 
-def test_captured_with_a_mask_that_changes(gla):
-    n = 50
-    ps, live = pools(n)[:2], torch.zeros(n, dtype=torch.bool, device="cuda")
+@pytest.mark.parametrize("n", [50, 4100])
+def test_captured_with_a_mask_that_changes(gla, n):
+    ps = pools(n)[:2] if n < 100 else [torch.arange(n * 8, dtype=torch.int32, device="cuda").view(n, 8)]
+    live = torch.zeros(n, dtype=torch.bool, device="cuda")
     ws = torch.empty(gla.gla_pages_compact_workspace_size(n), dtype=torch.uint8, device="cuda")
     gla.gla_pages_compact(ps, live, workspace=ws)
     torch.cuda.synchronize()
@@ -195,7 +196,8 @@ def test_refusals(gla):
               lambda: gla.gla_pages_copy(p, one.cpu(), one), lambda: gla.gla_pages_clear(p, one.view(1, 1)),
               lambda: gla.gla_pages_copy(torch.zeros(4, 3, dtype=torch.bfloat16, device="cuda"), one, one),
               lambda: gla.gla_pages_compact(p, live[:3]), lambda: gla.gla_pages_compact(p, live.int()),
-              lambda: gla.gla_pages_compact(p, live, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))):
+              lambda: gla.gla_pages_compact(torch.zeros(4097, 4, device="cuda"), torch.ones(4097, dtype=torch.bool, device="cuda"),
+                                            workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(gla.GlaError):
             f()
     none = torch.zeros(0, 8, device="cuda")

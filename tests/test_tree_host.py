@@ -87,10 +87,10 @@ def test_pages(L):
     def compact(ns=4, live=FAKE, to=FAKE, count=FAKE, ws=FAKE, size=1 << 20):
         return L.gla_pages_compact(*arrays((FAKE,), (64,)), 1, ns, live, to, count, ws, size, None)
 
-    assert compact(live=None) == BAD and compact(to=None) == BAD and compact(count=None) == BAD and compact(ws=None) == BAD
-    assert compact(size=8) == WS and compact(ns=-1) == BAD and compact(to=FAKE + 1) == BAD
-    assert L.gla_pages_compact_workspace_size(-1) == 0
-    assert L.gla_pages_compact_workspace_size(1000) >= 4 * 1001
+    assert compact(live=None) == BAD and compact(to=None) == BAD and compact(count=None) == BAD and compact(ns=-1) == BAD
+    assert compact(to=FAKE + 1) == BAD and compact(ns=5000, ws=None) == BAD and compact(ns=5000, size=8) == WS
+    assert [L.gla_pages_compact_workspace_size(n) for n in (-1, 0, 4096)] == [0, 0, 0]
+    assert L.gla_pages_compact_workspace_size(5000) >= 4 * 5001
     assert L.gla_pages_compact_workspace_size(2 ** 31 - 1) >= 4 * (2 ** 31 - 1)
 
 
