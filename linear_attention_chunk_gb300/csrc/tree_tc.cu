@@ -21,9 +21,11 @@
 //                copy may hold rows of the next one), a stage of S as it comes free;
 //   warps 12-15  P of the unit ahead, 16 x 16 tiles below the diagonal;
 //   warps 0-11   16 channels each: Q S step by step, the decay, P V, the rows out.
-// (Two CTAs of six consumer warps that did all of it in turn, P between CTA
-// barriers and one warp a slice of S: 112 us where this one takes MEASURED at
-// 256 trees of up to 32 nodes, H = 16, and 101 at 128 of 48 to 64.)
+// 256 trees of up to 32 nodes, H = 16: 65 us, 0.86 of the measured copy rate;
+// 128 of 48 to 64, gated: 59, 0.71, where the products' 3,600 clocks a unit and
+// their latencies show. (Two CTAs of six consumer warps that did all of it in
+// turn, P between CTA barriers: 112 and 101. Two groups of consumers a unit
+// each, 32 channels a warp: 149 and 90. Three halves of S held: 101 and 71.)
 //
 // Accumulator columns: of the two 8-column tiles of a warp, column n of tile t
 // is channel 2 n + t. A thread's entries of S are then 8-byte loads (the
