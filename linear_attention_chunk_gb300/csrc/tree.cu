@@ -176,9 +176,13 @@ template <typename T> __global__ void __launch_bounds__(kCommit) tree_commit_any
 // A CTA takes the channels of one block of one tree: its rows of x and the
 // window's last three arrive in shared memory by asynchronous copies, all in
 // flight at once, and each is read up to four times from there (as a node and
-// as an ancestor). HBM-bound: x and y once. CTAs of the channels stay for
-// several trees where there are more trees than fit at a time: the taps of a
-// thread's channels, 128 strided bytes, cost as much as ten nodes' rows.
+// as an ancestor): 47 us at 256 trees of 16 to 64 nodes, D = 4096, 0.56 of the
+// copy rate, instructions (unpacking, two special functions an element) on the
+// rest; rows straight from global memory 93. The next tree's rows under way
+// while one is worked on, and code without branches on the window's taps, both
+// measured the same 47. CTAs of the channels stay for several trees where there
+// are more trees than fit at a time: the taps of a thread's channels, 128
+// strided bytes, cost as much as ten nodes' rows.
 constexpr int kConv = 128;   // threads, eight channels each
 template <typename T> constexpr int conv_lanes() { return sizeof(T) == 2 ? 32 : 16; }   // of a row: 256 channels at bf16, 128 at fp32
 
