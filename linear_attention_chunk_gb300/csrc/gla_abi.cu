@@ -1034,6 +1034,8 @@ static gla_status tree_common(const void *q, int64_t ld_q, const void *k, int64_
     if ((st = check_heads(v, ld_v, H, dv, dtype, "v")) != GLA_OK) return st;
     REQUIRE_PTR(o, "o");
     if (o == q || o == k || o == v || o == state_pool) return fail(GLA_ERR_INVALID_ARG, "o may not alias an input");
+    if (dtype == GLA_BF16 && (long double)n_slots * H * dk > 2147483647.0L)   // the copies' row numbers are ints
+        return fail(GLA_ERR_UNSUPPORTED, "a pool of %d slots with %d heads is too large", n_slots, H);
     if ((st = status_word(&p.status)) != GLA_OK) return st;
     int launches = 0;
     const cudaError_t e = launch_tree_fwd(p, dtype == GLA_BF16, static_cast<cudaStream_t>(stream), &launches);

@@ -210,8 +210,7 @@ struct TreeParams {
     unsigned int *status;
 };
 cudaError_t launch_tree_fwd(const TreeParams &p, bool bf16, cudaStream_t s, int *launches);
-// bf16, dk = 96, dv = 192 on the tensor cores (tree_tc.cu); `fits`: the pool's rows are within its copies' reach.
-bool tree_fwd_tc_fits(const TreeParams &p);
+// bf16, dk = 96, dv = 192 on the tensor cores (tree_tc.cu); the pool has at most 2^31 - 1 rows of dv.
 cudaError_t launch_tree_fwd_tc(const TreeParams &p, cudaStream_t s, int *launches);
 cudaError_t launch_tree_commit(const TreeParams &p, bool bf16, cudaStream_t s, int *launches);
 // The commit of pages of 96 x 192, with the windows (tree_commit.cu).

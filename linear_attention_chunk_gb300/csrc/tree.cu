@@ -25,9 +25,9 @@ constexpr int kThreads = 256, kBlock = 16;   // threads of a CTA; nodes a thread
 
 __host__ __device__ constexpr int round4(int v) { return (v + 3) / 4 * 4; }
 
-// Any head sizes and element type: one CTA per (sequence, head), a thread a
-// state column. fp32's validation mode.
-template <typename T> __global__ void __launch_bounds__(kThreads) tree_fwd_kernel(const TreeParams p) {
+// Any head sizes, fp32 (the validation mode): one CTA per (sequence, head), a
+// thread a state column.
+__global__ void __launch_bounds__(kThreads) tree_fwd_kernel(const TreeParams p) {
     extern __shared__ float4 smem4[];
     __shared__ int par[kNodes];
     __shared__ unsigned long long path[kNodes];
@@ -40,13 +40,13 @@ template <typename T> __global__ void __launch_bounds__(kThreads) tree_fwd_kerne
     }
     const int M = t.nodes, dk = p.dk, dv = p.dv, ldq = round4(dk);
     float *qs = reinterpret_cast<float *>(smem4), *ks = qs + kNodes * ldq, *P = ks + kNodes * ldq;
-    const T *q = static_cast<const T *>(p.q) + (size_t)t.first * p.ldq + (size_t)h * dk;
-    const T *k = static_cast<const T *>(p.k) + (size_t)t.first * p.ldk + (size_t)h * dk;
-    const T *v = static_cast<const T *>(p.v) + (size_t)t.first * p.ldv + (size_t)h * dv;
+    const float *q = static_cast<const float *>(p.q) + (size_t)t.first * p.ldq + (size_t)h * dk;
+    const float *k = static_cast<const float *>(p.k) + (size_t)t.first * p.ldk + (size_t)h * dk;
+    const float *v = static_cast<const float *>(p.v) + (size_t)t.first * p.ldv + (size_t)h * dv;
     for (int e = tid; e < M * ldq; e += kThreads) {
         const int i = e / ldq, c = e % ldq;
-        qs[e] = c < dk ? Elem<T>::load(q + (size_t)i * p.ldq + c) : 0.f;
-        ks[e] = c < dk ? Elem<T>::load(k + (size_t)i * p.ldk + c) : 0.f;
+        qs[e] = c < dk ? q[(size_t)i * p.ldq + c] : 0.f;
+        ks[e] = c < dk ? k[(size_t)i * p.ldk + c] : 0.f;
     }
     const float l2 = p.g ? 0.f : log2_of_decay(p.log_lambda[h]);
     if (p.g && tid < M) gate[tid] = p.g[(size_t)(t.first + tid) * p.H + h];
@@ -65,7 +65,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) tree_fwd_kerne
     const int c = tid % lanes, grp = tid / lanes;
     if (grp >= groups || c >= dv) return;
     const float *S = p.pool + (t.slot * p.H + h) * ((size_t)dk * dv) + c;
-    T *o = static_cast<T *>(p.o) + ((size_t)t.first * p.H + h) * dv + c;
+    float *o = static_cast<float *>(p.o) + ((size_t)t.first * p.H + h) * dv + c;
     for (int nb = grp * kBlock; nb < M; nb += groups * kBlock) {
         float acc[kBlock] = {};
         for (int r = 0; r < dk; r += 4) {
@@ -84,9 +84,9 @@ template <typename T> __global__ void __launch_bounds__(kThreads) tree_fwd_kerne
             float sum = far[nb + i] == 0.f ? 0.f : far[nb + i] * acc[i];
             for (unsigned long long m = path[nb + i]; m; m &= m - 1) {
                 const int j = __ffsll((long long)m) - 1;
-                sum = fmaf(P[(nb + i) * kNodes + j], Elem<T>::load(v + (size_t)j * p.ldv + c), sum);
+                sum = fmaf(P[(nb + i) * kNodes + j], __ldg(v + (size_t)j * p.ldv + c), sum);
             }
-            Elem<T>::store(o + (size_t)(nb + i) * p.H * dv, p.scale * sum);
+            o[(size_t)(nb + i) * p.H * dv] = p.scale * sum;
         }
     }
 }
@@ -274,11 +274,11 @@ template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(
     }
 }
 
-template <typename T> cudaError_t fwd_any(const TreeParams &p, cudaStream_t s, int *launches) {
+cudaError_t fwd_any(const TreeParams &p, cudaStream_t s, int *launches) {
     const int bytes = (2 * kNodes * round4(p.dk) + kNodes * kNodes) * (int)sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(tree_fwd_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaFuncSetAttribute(tree_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    tree_fwd_kernel<T><<<(unsigned)((size_t)p.nseq * p.H), kThreads, bytes, s>>>(p);
+    tree_fwd_kernel<<<(unsigned)((size_t)p.nseq * p.H), kThreads, bytes, s>>>(p);
     if (launches) ++*launches;
     return cudaGetLastError();
 }
@@ -304,8 +304,7 @@ template <typename T> cudaError_t conv(const TreeParams &p, cudaStream_t s, int 
 }  // namespace
 
 cudaError_t launch_tree_fwd(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {
-    if (bf16 && tree_fwd_tc_fits(p)) return launch_tree_fwd_tc(p, s, launches);
-    return bf16 ? fwd_any<__nv_bfloat16>(p, s, launches) : fwd_any<float>(p, s, launches);
+    return bf16 ? launch_tree_fwd_tc(p, s, launches) : fwd_any(p, s, launches);
 }
 cudaError_t launch_tree_commit(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {
     if (p.dk == 96 && p.dv == 192 && p.H > 0) return launch_tree_pages(p, bf16, s, launches);

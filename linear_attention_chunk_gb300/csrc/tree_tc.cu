@@ -571,16 +571,12 @@ bool make_map(CUtensorMap *m, CUtensorMapDataType type, const void *at, cuuint64
 
 }  // namespace
 
-bool tree_fwd_tc_fits(const TreeParams &p) {
-    return p.dk == kDk && p.dv == kDv && p.n_slots > 0 && (long)p.n_slots * p.H * kDk <= 0x7fffffffL;   // TMA coordinates are ints
-}
-
 cudaError_t launch_tree_fwd_tc(const TreeParams &p, cudaStream_t s, int *launches) {
     if (!encode_tiled_fn()) return cudaErrorNotSupported;
     Maps maps;
     const cuuint64_t T = (cuuint64_t)p.total_T, H = (cuuint64_t)p.H;
     const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    if (!make_map(&maps.s, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.pool, 32, (cuuint64_t)p.n_slots * H * kDk, kDv * 4, 6, 128, 32, 16, 6, CU_TENSOR_MAP_SWIZZLE_128B) ||
+    if (!make_map(&maps.s, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.pool, 32, (p.n_slots > 0 ? (cuuint64_t)p.n_slots : 1) * H * kDk, kDv * 4, 6, 128, 32, 16, 6, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map(&maps.q, bf16, p.q, 32, T, (cuuint64_t)p.ldq * 2, 3 * H, 64, 32, 16, 3, CU_TENSOR_MAP_SWIZZLE_64B) ||
         !make_map(&maps.k, bf16, p.k, 32, T, (cuuint64_t)p.ldk * 2, 3 * H, 64, 32, 16, 3, CU_TENSOR_MAP_SWIZZLE_64B) ||
         !make_map(&maps.v, bf16, p.v, 64, T, (cuuint64_t)p.ldv * 2, 3 * H, 128, 64, 16, 3, CU_TENSOR_MAP_SWIZZLE_128B))

@@ -34,6 +34,7 @@ def test_tree_forward(L, name):
     assert st(slots=None, ns=1) == BAD and st(ns=-1) == BAD and st(nseq=-1) == BAD and st(T=-1) == BAD and st(H=-1) == BAD
     assert st(lq=191) == BAD and st(lk=196) == BAD and st(lv=100) == BAD and st(cu=FAKE + 2) == BAD and st(par=FAKE + 1) == BAD
     assert st(dk=64, lq=128, lk=128) == NOT and st(dt=1, dk=129) == NOT and st(dt=1, dv=257) == NOT and st(dt=3) == BAD
+    assert st(ns=1 << 24, H=2) == NOT                              # rows of pages past an int
     assert st(dk=0) == BAD and st(o=FAKE) == BAD and st(nseq=1 << 20, ns=1 << 20, H=1 << 12) == BAD
     assert st(nseq=0, q=None, cu=None, o=None) == OK and st(H=0, q=None) == OK and st(T=0, q=None, o=None, par=None) == OK
 
