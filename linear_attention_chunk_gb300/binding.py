@@ -925,17 +925,65 @@ def gla_rmsnorm_bwd(s, w, dy, ds=None, eps=1e-6, *, dx=None, dw=None, want_dw=Tr
     return dx, dw
 
 
+class _Quick:
+    """One call's device and stream, for operators whose small calls cost the
+    host more than the GPU: on the current device and its current stream next
+    to nothing is set up, for any other a _Call does the work."""
+
+    __slots__ = ("torch", "index", "device", "call")
+
+    def __init__(self, x, stream, element=True):
+        torch = self.torch = _torch()
+        index = self.index = x.get_device()
+        self.device = x.device
+        here = stream is None and index >= 0 and index == torch._C._cuda_getDevice()
+        self.call = None if here else _Call(x, stream, element)
+
+    def empty(self, shape, dtype):
+        if self.call is None:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        return self.call.empty(shape, dtype)
+
+    def run(self, name, *args):
+        if self.call is not None:
+            return self.call.run(name, *args)
+        f = _entry.get(name)
+        if f is None:
+            f = _entry[name] = getattr(lib(), name)
+        st = f(*args, self.torch._C._cuda_getCurrentRawStream(self.index))
+        if st != GLA_OK:
+            _raise_on(st, name)
+
+
+def _at(t, dtype, shape, index, name):
+    """Address of a contiguous tensor of this type, shape and device (None passes)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    if t.get_device() != index:
+        raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} is on {t.device}, not on the call's device {index}")
+    if t.dtype != dtype:
+        raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise GlaError(GLA_ERR_INVALID_ARG, "argument", f"{name} must be contiguous")
+
+
 def gla_layernorm(x, w=None, b=None, res=None, eps=1e-6, *, y=None, s=None, stream=None):
     """Residual addition and layer norm over the last dimension: x, res [..., D],
     w, b [D] fp32 or None. Returns (y, s): s = x + res (may be given as res, in
     place), or None without res; y = w (s - mean(s)) / sqrt(var(s) + eps) + b."""
     rows, D = _norm_rows(x)
-    c = _Call(x, stream)
-    y = c.empty(x.shape) if y is None else y
+    c = _Quick(x, stream)
+    index, dtype, shape, f32 = c.index, x.dtype, x.shape, c.torch.float32
+    if y is None:
+        y = c.empty(shape, dtype)
     if s is None and res is not None:
-        s = c.empty(x.shape)
-    c.run("gla_layernorm_fwd", c.whole(x, x.shape, "x"), c.whole(res, x.shape, "res"), c.f32(w, (D,), "w"),
-          c.f32(b, (D,), "b"), float(eps), rows, D, c.code, c.whole(s, x.shape, "s"), c.whole(y, x.shape, "y"))
+        s = c.empty(shape, dtype)
+    c.run("gla_layernorm_fwd", _at(x, dtype, shape, index, "x"), _at(res, dtype, shape, index, "res"),
+          _at(w, f32, (D,), index, "w"), _at(b, f32, (D,), index, "b"), eps, rows, D, _dtype_code(x),
+          _at(s, dtype, shape, index, "s"), _at(y, dtype, shape, index, "y"))
     return y, s
 
 
@@ -950,56 +998,80 @@ def gla_layernorm_bwd(s, w, dy, ds=None, eps=1e-6, *, dx=None, dw=None, db=None,
     dx is x's and res's alike, dw and db [D] fp32 (None with want_dw=False,
     want_db=False)."""
     rows, D = _norm_rows(s)
-    c = _Call(s, stream)
-    args = (c.whole(s, s.shape, "s"), c.f32(w, (D,), "w"), c.whole(dy, s.shape, "dy"), c.whole(ds, s.shape, "ds"))
-    dx = c.empty(s.shape) if dx is None else dx
+    c = _Quick(s, stream)
+    index, dtype, shape, f32, code = c.index, s.dtype, s.shape, c.torch.float32, _dtype_code(s)
+    args = (_at(s, dtype, shape, index, "s"), _at(w, f32, (D,), index, "w"), _at(dy, dtype, shape, index, "dy"),
+            _at(ds, dtype, shape, index, "ds"))
+    if dx is None:
+        dx = c.empty(shape, dtype)
     if dw is None and want_dw:
-        dw = c.empty((D,), c.torch.float32)
+        dw = c.empty((D,), f32)
     if db is None and want_db:
-        db = c.empty((D,), c.torch.float32)
+        db = c.empty((D,), f32)
     size = None if dw is None and db is None else gla_layernorm_bwd_workspace_size
-    c.run("gla_layernorm_bwd", *args, float(eps), rows, D, c.code, c.whole(dx, s.shape, "dx"), c.f32(dw, (D,), "dw"),
-          c.f32(db, (D,), "db"), *c.scratch(workspace, size, rows, D))
+    if c.call is None and workspace is None and size is not None:
+        need = size(rows, D, code)
+        workspace = c.empty((need,), c.torch.uint8)
+        scratch = workspace.data_ptr(), need
+    else:
+        scratch = (c.call or _Call(s, None)).scratch(workspace, size, rows, D)
+    c.run("gla_layernorm_bwd", *args, eps, rows, D, code, _at(dx, dtype, shape, index, "dx"),
+          _at(dw, f32, (D,), index, "dw"), _at(db, f32, (D,), index, "db"), *scratch)
     return dx, dw, db
 
 
-def _heads(c, t, shape, name):
+def _heads(t, dtype, shape, index, name):
     """Address and row step of [T, H, d] token rows an equal distance apart,
     each with contiguous heads (a column range of a wider tensor passes)."""
-    if t.dtype is c.dtype and t.shape == shape and t.get_device() == c.index and t.is_contiguous():
-        return t.data_ptr(), shape[1] * shape[2]
-    c._refuse(t, shape, c.dtype, name)
-    T, H, d = shape
-    step = t.stride(0) if T > 1 else H * d
-    if t.numel() and (d > 1 and t.stride(2) != 1 or H > 1 and t.stride(1) != d or step < H * d):
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        T, H, d = shape
+        if t.is_contiguous():
+            return t.data_ptr(), H * d
+        step = t.stride(0) if T > 1 else H * d
+        if not (d > 1 and t.stride(2) != 1 or H > 1 and t.stride(1) != d or step < H * d):
+            return t.data_ptr(), step
         raise GlaError(GLA_ERR_INVALID_ARG, "argument",
                        f"{name} must have contiguous heads and token rows an equal distance apart")
-    return t.data_ptr(), step
+    return _at(t, dtype, shape, index, name), shape[1] * shape[2]
 
 
-def _tree_args(c, T, cu_nodes, parents, slots):
-    """The trees of a call: addresses of the offsets, parents and slots, and the number of sequences."""
+def _rows(t, dtype, shape, index, name):
+    """Address and row step of [T, D] rows an equal distance apart with contiguous columns (None passes)."""
+    if t is None:
+        return None, 0
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        T, D = shape
+        if t.is_contiguous():
+            return t.data_ptr(), D
+        step = t.stride(0) if T > 1 else D
+        if not (D > 1 and t.stride(1) != 1 or step < D):
+            return t.data_ptr(), step
+        raise GlaError(GLA_ERR_INVALID_ARG, "argument",
+                       f"{name} must have contiguous columns and token rows an equal distance apart")
+    return _at(t, dtype, shape, index, name), shape[1]
+
+
+def _offsets(cu_nodes):
     shape = cu_nodes.shape
     if len(shape) != 1 or shape[0] < 1:
         raise GlaError(GLA_ERR_INVALID_ARG, "argument", "cu_nodes must hold one offset more than there are sequences")
-    i32, whole, nseq = c.torch.int32, c.whole, shape[0] - 1
-    return (whole(cu_nodes, shape, "cu_nodes", i32), whole(parents, (T,), "parents", i32),
-            whole(slots, (nseq,), "slots", i32), nseq)
+    return shape
 
 
 def _tree_fwd(name, q, k, v, decay, gated, cu_nodes, parents, state_pool, slots, scale, o, stream):
     T, H, dk = _lead(q, 3, "q")
     dv = _lead(v, 3, "v")[2]
-    c = _Call(q, stream)
-    if scale is None:
-        scale = 1.0 / math.sqrt(dk)
-    cu, par, sl, nseq = _tree_args(c, T, cu_nodes, parents, slots)
-    n_slots = _lead(state_pool, 4, "state_pool")[0]
-    args = (*_heads(c, q, (T, H, dk), "q"), *_heads(c, k, (T, H, dk), "k"), *_heads(c, v, (T, H, dv), "v"),
-            c.f32(decay, (T, H) if gated else (H,), "g" if gated else "log_lambda"), float(scale), cu, par, sl,
-            c.f32(state_pool, (n_slots, H, dk, dv), "state_pool"), n_slots, nseq, T, H, dk, dv, c.code)
-    o = c.empty((T, H, dv)) if o is None else o
-    c.run(name, *args, c.whole(o, (T, H, dv), "o"))
+    c = _Quick(q, stream)
+    index, dtype, i32, f32, cu = c.index, q.dtype, c.torch.int32, c.torch.float32, _offsets(cu_nodes)
+    narrow, wide, nseq, n_slots = (T, H, dk), (T, H, dv), cu[0] - 1, _lead(state_pool, 4, "state_pool")[0]
+    args = (*_heads(q, dtype, narrow, index, "q"), *_heads(k, dtype, narrow, index, "k"),
+            *_heads(v, dtype, wide, index, "v"), _at(decay, f32, (T, H) if gated else (H,), index, "g" if gated else "log_lambda"),
+            (dk or 1) ** -0.5 if scale is None else scale, _at(cu_nodes, i32, cu, index, "cu_nodes"),
+            _at(parents, i32, (T,), index, "parents"), _at(slots, i32, (nseq,), index, "slots"),
+            _at(state_pool, f32, (n_slots, H, dk, dv), index, "state_pool"), n_slots, nseq, T, H, dk, dv, _dtype_code(q))
+    if o is None:
+        o = c.empty(wide, dtype)
+    c.run(name, *args, _at(o, dtype, wide, index, "o"))
     return o
 
 
@@ -1023,14 +1095,15 @@ def gla_tree_fwd_gated(q, k, v, g, cu_nodes, parents, state_pool, slots=None, sc
 def _tree_commit(name, k, v, decay, gated, cu_nodes, parents, last, state_pool, slots, x, win_pool, stream):
     T, H, dk = _lead(k, 3, "k")
     dv = _lead(v, 3, "v")[2]
-    c = _Call(k, stream)
-    cu, par, sl, nseq = _tree_args(c, T, cu_nodes, parents, slots)
-    n_slots = _lead(state_pool, 4, "state_pool")[0]
-    D = 0 if x is None else _lead(x, 2, "x")[1]
-    c.run(name, *_heads(c, k, (T, H, dk), "k"), *_heads(c, v, (T, H, dv), "v"),
-          c.f32(decay, (T, H) if gated else (H,), "g" if gated else "log_lambda"), cu, par,
-          c.i32(last, (nseq,), "last"), sl, c.f32(state_pool, (n_slots, H, dk, dv), "state_pool"),
-          *c.rows(x, (T, D), "x"), c.f32(win_pool, (n_slots, 4, D), "win_pool"), n_slots, nseq, T, H, dk, dv, D, c.code)
+    c = _Quick(k, stream)
+    index, dtype, i32, f32, cu = c.index, k.dtype, c.torch.int32, c.torch.float32, _offsets(cu_nodes)
+    nseq, n_slots, D = cu[0] - 1, _lead(state_pool, 4, "state_pool")[0], 0 if x is None else _lead(x, 2, "x")[1]
+    c.run(name, *_heads(k, dtype, (T, H, dk), index, "k"), *_heads(v, dtype, (T, H, dv), index, "v"),
+          _at(decay, f32, (T, H) if gated else (H,), index, "g" if gated else "log_lambda"),
+          _at(cu_nodes, i32, cu, index, "cu_nodes"), _at(parents, i32, (T,), index, "parents"),
+          _at(last, i32, (nseq,), index, "last"), _at(slots, i32, (nseq,), index, "slots"),
+          _at(state_pool, f32, (n_slots, H, dk, dv), index, "state_pool"), *_rows(x, dtype, (T, D), index, "x"),
+          _at(win_pool, f32, (n_slots, 4, D), index, "win_pool"), n_slots, nseq, T, H, dk, dv, D, _dtype_code(k))
     return state_pool
 
 
@@ -1056,25 +1129,27 @@ def gla_conv1d_tree(x, w, b, cu_nodes, parents, win_pool, slots=None, *, y=None,
     """The causal Conv1d with SiLU along each path of the trees of gla_tree_fwd:
     x [T,D], w [D,4], b [D] or None; behind a tree's root the inputs of
     win_pool [n_slots,4,D] fp32 at slots[n], which stays as it is. Returns y [T,D]."""
-    T, D = _lead(x, 2, "x")
-    c = _Call(x, stream)
-    cu, par, sl, nseq = _tree_args(c, T, cu_nodes, parents, slots)
-    n_slots = _lead(win_pool, 3, "win_pool")[0]
-    args = (*c.rows(x, (T, D), "x"), c.f32(w, (D, 4), "w"), c.f32(b, (D,), "b"), cu, par, sl,
-            c.f32(win_pool, (n_slots, 4, D), "win_pool"), n_slots, nseq, T, D, c.code)
-    y = c.empty((T, D)) if y is None else y
-    c.run("gla_conv1d_tree", *args, c.whole(y, (T, D), "y"))
+    T, D = wide = _lead(x, 2, "x")
+    c = _Quick(x, stream)
+    index, dtype, i32, f32, cu = c.index, x.dtype, c.torch.int32, c.torch.float32, _offsets(cu_nodes)
+    nseq, n_slots = cu[0] - 1, _lead(win_pool, 3, "win_pool")[0]
+    args = (*_rows(x, dtype, wide, index, "x"), _at(w, f32, (D, 4), index, "w"), _at(b, f32, (D,), index, "b"),
+            _at(cu_nodes, i32, cu, index, "cu_nodes"), _at(parents, i32, (T,), index, "parents"),
+            _at(slots, i32, (nseq,), index, "slots"), _at(win_pool, f32, (n_slots, 4, D), index, "win_pool"), n_slots,
+            nseq, T, D, _dtype_code(x))
+    if y is None:
+        y = c.empty(wide, dtype)
+    c.run("gla_conv1d_tree", *args, _at(y, dtype, wide, index, "y"))
     return y
 
 
-class _PagesCall(_Call):
+class _PagesCall(_Quick):
     """A call over pools of any element type, one or a sequence of [n_slots, ...] tensors."""
 
     __slots__ = ("pools",)
 
     def __init__(self, pools, stream):
-        torch = _torch()
-        pools = [pools] if isinstance(pools, torch.Tensor) else list(pools)
+        pools = [pools] if isinstance(pools, _torch().Tensor) else list(pools)
         if not pools:
             raise GlaError(GLA_ERR_INVALID_ARG, "argument", "no pools")
         super().__init__(pools[0], stream, element=False)
@@ -1096,19 +1171,19 @@ def gla_pages_copy(pools, src, dst, *, stream=None):
     tensors), in every pool. A source may have several targets (one prompt
     continued several times); targets are distinct and no other pair's source."""
     c = _PagesCall(pools, stream)
-    n = _lead(src, 1, "src")[0]
-    c.run("gla_pages_copy", *c.pools, c.i32(src, (n,), "src"), c.i32(dst, (n,), "dst"), n)
+    n, i32 = _lead(src, 1, "src"), c.torch.int32
+    c.run("gla_pages_copy", *c.pools, _at(src, i32, n, c.index, "src"), _at(dst, i32, n, c.index, "dst"), n[0])
 
 
 def gla_pages_clear(pools, slots, *, stream=None):
     """Fills the pages `slots` (int32 CUDA tensor) of the pools with zeros, as a
     new sequence needs them; pools as gla_pages_copy."""
     c = _PagesCall(pools, stream)
-    n = _lead(slots, 1, "slots")[0]
-    c.run("gla_pages_clear", *c.pools, c.i32(slots, (n,), "slots"), n)
+    n = _lead(slots, 1, "slots")
+    c.run("gla_pages_clear", *c.pools, _at(slots, c.torch.int32, n, c.index, "slots"), n[0])
 
 
-def gla_pages_compact_workspace_size(n_slots, dtype=None) -> int:
+def gla_pages_compact_workspace_size(n_slots) -> int:
     return int(lib().gla_pages_compact_workspace_size(n_slots))
 
 
@@ -1119,13 +1194,21 @@ def gla_pages_compact(pools, live, *, map=None, count=None, workspace=None, stre
     [n_slots] int32: each page's new number, -1 where not in use; count [1]
     int32: L), on the device."""
     c = _PagesCall(pools, stream)
-    n = c.pools[3]
-    i32 = c.torch.int32
-    kind = c.torch.bool if live.dtype == c.torch.bool else c.torch.uint8
-    map = c.empty((n,), i32) if map is None else map
-    count = c.empty((1,), i32) if count is None else count
-    c.run("gla_pages_compact", *c.pools, c.whole(live, (n,), "live", kind), c.i32(map, (n,), "map"),
-          c.i32(count, (1,), "count"), *c.scratch(workspace, gla_pages_compact_workspace_size, n))
+    n, index, i32, u8 = c.pools[3], c.index, c.torch.int32, c.torch.uint8
+    kind = c.torch.bool if live.dtype == c.torch.bool else u8
+    if map is None:
+        map = c.empty((n,), i32)
+    if count is None:
+        count = c.empty((1,), i32)
+    if workspace is None:
+        need = gla_pages_compact_workspace_size(n)
+        if need > 0:
+            workspace = c.empty((need,), u8)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise GlaError(GLA_ERR_INVALID_ARG, "argument", "the workspace must be contiguous and on the call's device")
+    scratch = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    c.run("gla_pages_compact", *c.pools, _at(live, kind, (n,), index, "live"), _at(map, i32, (n,), index, "map"),
+          _at(count, i32, (1,), index, "count"), *scratch)
     return map, count
 
 
