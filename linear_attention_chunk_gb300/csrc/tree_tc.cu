@@ -99,9 +99,10 @@ __device__ __forceinline__ uint32_t lds1(uint32_t at) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
     return v;
 }
-// Two numbers as their bf16 halves: x = hi + lo up to 2^-17.
+// Two numbers as their bf16 halves: x = hi + lo up to 2^-17. hi is finite unless x is NaN: of an infinite x (and one that
+// bf16 would round to it) it is the largest number, so that lo is what is left and not inf - inf.
 __device__ __forceinline__ void split(float x0, float x1, uint32_t &hi, uint32_t &lo) {
-    hi = pack_bf16x2(x0, x1);
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x1), "f"(x0));
     lo = pack_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
 }
 // Zero where an element is not finite.
@@ -347,6 +348,30 @@ struct Unit {
     uint32_t par;
     size_t row;              // the first node's row of o and of this head
 };
+// What the elements of v that are not finite give node x, channels 4 q4 .. 4 q4 + 3 of the warp's 16. (Not inline: it is rarely
+// called, and its instructions would stand in the readout's way.)
+__device__ __noinline__ float4 not_finite(const unsigned char *sm, const Meta *m, int s, int x) {
+    const int q4 = threadIdx.x % 4, warp = threadIdx.x / 32;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (x >= m->nodes) return sum;
+    const __nv_bfloat16 *ph = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPh + (uint32_t)(s * kNodes + x) * kPitchP);
+    const __nv_bfloat16 *pl = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPl + (uint32_t)(s * kNodes + x) * kPitchP);
+    for (unsigned long long path = m->path[x]; path; path &= path - 1) {
+        const int j = __ffsll((long long)path) - 1;
+        const float2 si = m->sum[x], sj = m->sum[j];
+        if (exp2f(((si.x - sj.x) + (si.y - sj.y)) * m->factor) == 0.f) continue;   // (cleared on the way)
+        const float w = __bfloat162float(ph[j]) + __bfloat162float(pl[j]);
+        const uint32_t piece = kOffV + (uint32_t)s * kNodeV + (uint32_t)(j >> 4) * kTileV + (uint32_t)(warp / 4) * 2048 + (uint32_t)(j & 15) * 128;
+        const uint32_t c16 = ((uint32_t)(warp & 3) * 2 + (uint32_t)(q4 >> 1)) ^ (uint32_t)(j & 7);
+        const uint2 v = *reinterpret_cast<const uint2 *>(sm + piece + c16 * 16 + (uint32_t)(q4 & 1) * 8);
+        const float2 a = unpack_bf16x2(v.x), b = unpack_bf16x2(v.y);
+        if (!isfinite(a.x)) sum.x += w * a.x;
+        if (!isfinite(a.y)) sum.y += w * a.y;
+        if (!isfinite(b.x)) sum.z += w * b.x;
+        if (!isfinite(b.y)) sum.w += w * b.y;
+    }
+    return sum;
+}
 template <int kTiles> __device__ __forceinline__ bool readout(const TreeParams &p, const Unit &unit, const WaitCtl &ctl) {
     const int lane = threadIdx.x % 32, g = lane / 4, q4 = lane % 4;   // a fragment's row (or column), its pair of columns (or rows)
     const uint32_t a_row = lane % 16, a_col = lane / 16 * 8, base = unit.base, x0 = unit.x0, x1 = unit.x1, par = unit.par;
@@ -460,32 +485,17 @@ template <int kTiles> __device__ __forceinline__ bool readout(const TreeParams &
             }
         }
     }
-    if (dirty) {
+    if (dirty)
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
-#pragma unroll 1
+#pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int x = i * 16 + g + 8 * r;
-                if (x >= M) continue;
-                const __nv_bfloat16 *ph = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPh + (uint32_t)(s * kNodes + x) * kPitchP);
-                const __nv_bfloat16 *pl = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPl + (uint32_t)(s * kNodes + x) * kPitchP);
-                for (unsigned long long path = m->path[x]; path; path &= path - 1) {
-                    const int j = __ffsll((long long)path) - 1;
-                    const float w = __bfloat162float(ph[j]) + __bfloat162float(pl[j]);
-                    // channels 4 q4 .. 4 q4 + 3 of the warp's 16
-                    const uint32_t piece = kOffV + (uint32_t)s * kNodeV + (uint32_t)(j >> 4) * kTileV + (uint32_t)(warp / 4) * 2048 + (uint32_t)(j & 15) * 128;
-                    const uint32_t c16 = ((uint32_t)(warp & 3) * 2 + (uint32_t)(q4 >> 1)) ^ (uint32_t)(j & 7);
-                    const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(sm + piece + c16 * 16 + (uint32_t)(q4 & 1) * 8);
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float y = __bfloat162float(v[2 * e + t]);
-                            if (!isfinite(y) && w != 0.f) acc[i][t][e] += r ? 0.f : w * y, acc[i][t][2 + e] += r ? w * y : 0.f;
-                        }
-                }
+                const float4 e = not_finite(sm, m, s, i * 16 + g + 8 * r);
+                acc[i][0][2 * r] += e.x;
+                acc[i][1][2 * r] += e.y;
+                acc[i][0][2 * r + 1] += e.z;
+                acc[i][1][2 * r + 1] += e.w;
             }
-    }
     const size_t step = (size_t)p.H * kDv;
     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + unit.row * kDv + warp * 16 + 4 * q4 + (size_t)g * step;
 #pragma unroll

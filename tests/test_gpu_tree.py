@@ -183,6 +183,40 @@ def test_a_page_that_is_not_finite_stays_in_its_channel(gla, dtype):
     assert not torch.isfinite(o[:40, 1][:, [50, 70]].float()).any()
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_infinities_of_a_page_keep_their_sign(gla, dtype):
+    """One infinity a channel: it reaches every node with the sign that q gives it. Numbers next to fp32's largest stay numbers."""
+    c = Case(dtype, [40, 16], 2, 96, 192, seed=9)
+    c.q = torch.where(c.q == 0, torch.ones_like(c.q), c.q)
+    c.pool[c.slots[0], 1, 3, 50] = INF
+    c.pool[c.slots[0], 1, 9, 70] = -INF
+    o = c.fwd(gla)
+    gla.gla_check()
+    up = c.q[:40, 1] > 0
+    assert torch.equal(o[:40, 1, 50] == INF, up[:, 3]) and torch.equal(o[:40, 1, 50] == -INF, ~up[:, 3])
+    assert torch.equal(o[:40, 1, 70] == -INF, up[:, 9]) and torch.equal(o[:40, 1, 70] == INF, ~up[:, 9])
+    c.q *= 2.0 ** -20
+    c.pool[c.slots[0], :, 5, ::3] = 3.4e38      # (bf16's largest is 3.3895e38)
+    c.pool[c.slots[0], 1, 3, 50] = c.pool[c.slots[0], 1, 9, 70] = 3.402823e38
+    ref, tol = c.fwd_ref()
+    near(c.fwd(gla)[: c.T], ref[: c.T], tol[: c.T])
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_zero_times_infinity_is_not_hidden(gla, dtype):
+    """A node's score of 0 with an infinite v on its path gives NaN; cut off by a decay of 0, nothing."""
+    c = Case(dtype, [40, 16], 2, 96, 192, shape="chain", gated=True, seed=10)
+    c.v[5, 1, 20] = INF
+    c.q[8, 1] = 0
+    c.log[20, 1] = -INF
+    o = c.fwd(gla)[: c.T].float()
+    gla.gla_check()
+    assert o[8, 1, 20].isnan() and not o[8, 1, :20].any() and not o[8, 1, 21:].any()
+    assert not o[5:20, 1, 20].isfinite().any()
+    o[5:20, 1, 20] = 0
+    assert o.isfinite().all()
+
+
 def test_column_ranges_of_a_projection(gla):
     c = Case(BF, [17, 64, 3], 3, 96, 192, seed=10)
     want = c.fwd(gla)
