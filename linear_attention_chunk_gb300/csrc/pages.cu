@@ -6,8 +6,9 @@
 // The pages are cut into chunks of 32 KB, taken in turn by resident CTAs; a
 // thread's loads of a chunk are all in flight before its stores (a ring of
 // bulk copies through shared memory, one thread an SM, measured the same: 140
-// us for 0.87 GB moved, 0.92 of the measured copy rate). Chunk by chunk, the pairs of one chunk side by side: several copies of one page read
-// it from L2 after the first.
+// us for 0.87 GB moved, 0.92 of the measured copy rate). Chunk by chunk, the
+// pairs of one chunk side by side: several copies of one page read it from L2
+// after the first.
 //
 // Compaction: with L pages in use, those at or above L move into the free ones
 // below it, in ascending order both. Ranks come from ballots. Of pools of up to

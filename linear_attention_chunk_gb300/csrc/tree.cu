@@ -176,13 +176,17 @@ template <typename T> __global__ void __launch_bounds__(kCommit) tree_commit_any
 // A CTA takes the channels of one block of one tree: its rows of x and the
 // window's last three arrive in shared memory by asynchronous copies, all in
 // flight at once, and each is read up to four times from there (as a node and
-// as an ancestor): 47 us at 256 trees of 16 to 64 nodes, D = 4096, 0.56 of the
-// copy rate, instructions (unpacking, two special functions an element) on the
-// rest; rows straight from global memory 93. The next tree's rows under way
-// while one is worked on, and code without branches on the window's taps, both
-// measured the same 47. CTAs of the channels stay for several trees where there
-// are more trees than fit at a time: the taps of a thread's channels, 128
-// strided bytes, cost as much as ten nodes' rows.
+// as an ancestor): 42 us at 256 trees of 16 to 64 nodes, D = 4096, 0.63 of the
+// copy rate; rows straight from global memory 93. A CTA's copies and its
+// arithmetic take turns: the copies and the output alone take 29 us, the taps
+// (unpacking, and a branch for each while they had one: 3 us more) 8, SiLU 4.
+// Measured at the same 41 to 44: the next tree's rows under way while one is
+// worked on, four channels a thread and 1.5 to twice the warps, blocks of half
+// the channels, the window's part summed ahead.
+// CTAs of the channels stay for several trees: the taps of a thread's channels,
+// 128 strided bytes, cost as much as ten nodes' rows. Three times as many as
+// fit at a time, so that trees of different sizes even out (1, 2, 3, 4, 6
+// times, all at once: 43.1, 43.9, 40.1, 41.2, 42.2, 44 us on the device).
 constexpr int kConv = 128;   // threads, eight channels each
 template <typename T> constexpr int conv_lanes() { return sizeof(T) == 2 ? 32 : 16; }   // of a row: 256 channels at bf16, 128 at fp32
 
@@ -191,7 +195,7 @@ template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(
     extern __shared__ uint4 smem_conv[];                      // [nodes][pieces of 16 bytes][lanes]
     __shared__ __align__(16) float4 wins[3][2][kLanes];       // the window's rows 1 .. 3
     __shared__ int par[kNodes];
-    __shared__ char4 up[kNodes];                              // a node's last three ancestors: nodes, or -1 - r: r rows before the window's last
+    __shared__ int4 up[kNodes];   // a node's last three ancestors: where their rows start in smem_conv, or -1 - r: r rows before the window's last; w: all are nodes
     const int lane = threadIdx.x % kLanes, first_row = threadIdx.x / kLanes;
     const int c = ((int)(blockIdx.x % per) * kLanes + lane) * 8;
     const bool on = c < p.D, whole = c + 8 <= p.D;
@@ -237,36 +241,54 @@ template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(
             int a[4] = {(int)threadIdx.x};
 #pragma unroll
             for (int k = 1; k < 4; ++k) a[k] = a[k - 1] >= 0 ? par[a[k - 1]] : a[k - 1] - 1;
-            up[threadIdx.x] = make_char4((signed char)a[1], (signed char)a[2], (signed char)a[3], 0);
+#pragma unroll
+            for (int k = 1; k < 4; ++k) a[k] *= a[k] >= 0 ? H * kLanes : 1;
+            up[threadIdx.x] = make_int4(a[1], a[2], a[3], a[3] >= 0);
         }
         ssm::copies_wait<0>();
         __syncthreads();
         if (!on) continue;
         T *y = static_cast<T *>(p.y) + (size_t)(t.first + first_row) * p.D + c;
         for (int i = first_row; i < t.nodes; i += kRows, y += (size_t)kRows * p.D) {
-            const auto tap = [&](int a, const ssm::f2 (&wt)[4], ssm::f2 (&acc)[4]) {
-                ssm::f2 u[4];
-                if (a >= 0) {
-                    ssm::Raw8<T> raw;
-#pragma unroll
-                    for (int h = 0; h < H; ++h) raw.w[h] = smem_conv[(a * H + h) * kLanes + lane];
-                    ssm::raw_unpack(raw, u);
-                } else {
-                    const float4 e = wins[3 + a][0][lane], f = wins[3 + a][1][lane];
-                    u[0] = ssm::f2_pack(e.x, e.y);
-                    u[1] = ssm::f2_pack(e.z, e.w);
-                    u[2] = ssm::f2_pack(f.x, f.y);
-                    u[3] = ssm::f2_pack(f.z, f.w);
-                }
+            ssm::f2 acc[4] = {b[0], b[1], b[2], b[3]};
+            const auto add = [&](const ssm::f2 (&u)[4], const ssm::f2 (&wt)[4]) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[j] = ssm::fma2(wt[j], u[j], acc[j]);
             };
-            const char4 a = up[i];
-            ssm::f2 acc[4] = {b[0], b[1], b[2], b[3]};
-            tap(i, w[3], acc);
-            tap((signed char)a.x, w[2], acc);
-            tap((signed char)a.y, w[1], acc);
-            tap((signed char)a.z, w[0], acc);
+            const auto row = [&](int at) {
+                ssm::Raw8<T> raw;
+#pragma unroll
+                for (int h = 0; h < H; ++h) raw.w[h] = smem_conv[at + h * kLanes + lane];
+                return raw;
+            };
+            const auto node = [&](const ssm::Raw8<T> &raw, const ssm::f2 (&wt)[4]) {
+                ssm::f2 u[4];
+                ssm::raw_unpack(raw, u);
+                add(u, wt);
+            };
+            const int4 a = up[i];
+            const ssm::Raw8<T> own = row(i * H * kLanes);
+            if (a.w) {   // without a branch for each
+                const ssm::Raw8<T> r1 = row(a.x), r2 = row(a.y), r3 = row(a.z);
+                node(own, w[3]);
+                node(r1, w[2]);
+                node(r2, w[1]);
+                node(r3, w[0]);
+            } else {
+                node(own, w[3]);
+                const auto tap = [&](int at, const ssm::f2 (&wt)[4]) {
+                    if (at >= 0) {
+                        node(row(at), wt);
+                        return;
+                    }
+                    const float4 e = wins[3 + at][0][lane], f = wins[3 + at][1][lane];
+                    const ssm::f2 u[4] = {ssm::f2_pack(e.x, e.y), ssm::f2_pack(e.z, e.w), ssm::f2_pack(f.x, f.y), ssm::f2_pack(f.z, f.w)};
+                    add(u, wt);
+                };
+                tap(a.x, w[2]);
+                tap(a.y, w[1]);
+                tap(a.z, w[0]);
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[j] = ssm::silu2(acc[j]);
             ssm::store8(y, acc, whole);
@@ -294,7 +316,7 @@ template <typename T> cudaError_t commit_any(const TreeParams &p, cudaStream_t s
 template <typename T> cudaError_t conv(const TreeParams &p, cudaStream_t s, int *launches) {
     constexpr int kLanes = conv_lanes<T>();
     const int per = (p.D + 8 * kLanes - 1) / (8 * kLanes), bytes = kNodes * kLanes * 8 * (int)sizeof(T);   // 32 KB
-    const long held = 6L * device_sm_count() / per;   // six CTAs an SM by shared memory
+    const long held = 18L * device_sm_count() / per;   // thrice the six CTAs an SM that shared memory holds
     const long trees = held < 1 ? 1 : held < p.nseq ? held : p.nseq;
     conv_tree_kernel<T><<<(unsigned)(trees * per), kConv, bytes, s>>>(p, per);
     if (launches) ++*launches;

@@ -5,7 +5,7 @@
 // bytes fp32), so the call is bound by HBM: the pages, q, k, v and o once.
 //
 // S goes from HBM to the tensor cores by way of shared memory and registers
-// alone: a ring of six TMA stages of 16 rows (128-byte swizzle), whose entries
+// alone: six TMA stages of 16 rows (128-byte swizzle), whose entries
 // the consumer warps split into two bf16 halves (hi + lo, 2^-17 of the entry:
 // drafted tokens get the values that the decode step's fp32 arithmetic gives,
 // to a few 2^-17) and multiply Q by both. A stage has too few products a byte
@@ -18,7 +18,7 @@
 //                parents and decays, the paths as bit masks and running sums by
 //                pointer doubling;
 //   warp 16      TMA, a unit ahead: 16 rows of q, k or v a copy (a tree's last
-//                copy may hold rows of the next one), a stage of S as it comes free;
+//                copy may hold rows of the next one), half of S as it comes free;
 //   warps 12-15  P of the unit ahead, 16 x 16 tiles below the diagonal;
 //   warps 0-11   16 channels each: Q S step by step, the decay, P V, the rows out.
 // 256 trees of up to 32 nodes, H = 16: 65 us, 0.86 of the measured copy rate;
