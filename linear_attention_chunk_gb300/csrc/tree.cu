@@ -176,7 +176,7 @@ template <typename T> __global__ void __launch_bounds__(kCommit) tree_commit_any
 // A CTA takes the channels of one block of one tree: its rows of x and the
 // window's last three arrive in shared memory by asynchronous copies, all in
 // flight at once, and each is read up to four times from there (as a node and
-// as an ancestor): 42 us at 256 trees of 16 to 64 nodes, D = 4096, 0.63 of the
+// as an ancestor): 43 us at 256 trees of 16 to 64 nodes, D = 4096, 0.62 of the
 // copy rate; rows straight from global memory 93. A CTA's copies and its
 // arithmetic take turns: the copies and the output alone take 29 us, the taps
 // (unpacking, and a branch for each while they had one: 3 us more) 8, SiLU 4.

@@ -25,7 +25,8 @@
 // 128 of 48 to 64, gated: 59, 0.71, where the products' 3,600 clocks a unit and
 // their latencies show. (Two CTAs of six consumer warps that did all of it in
 // turn, P between CTA barriers: 112 and 101. Two groups of consumers a unit
-// each, 32 channels a warp: 85 and 80. Three halves of S held: 101 and 71.)
+// each, 32 channels a warp: 85 and 80. Three halves of S held, k in one buffer:
+// 71 and 63 on the device where these take 62 and 56: the consumers set the pace.)
 //
 // Accumulator columns: of the two 8-column tiles of a warp, column n of tile t
 // is channel 2 n + t. A thread's entries of S are then 8-byte loads (the

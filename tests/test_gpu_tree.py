@@ -339,6 +339,24 @@ def test_convolution(gla, dtype, D, shape):
         assert (y[c.T:] == 7).all() and torch.equal(c.win, win)
 
 
+@pytest.mark.parametrize("dtype,D,N", [(BF, 2056, 300), (FP, 1028, 700), (BF, 20008, 90), (FP, 20004, 50)])
+def test_convolution_of_many(gla, dtype, D, N):
+    """More trees than CTAs a block of channels, and more blocks than SMs; a bad tree among them is skipped alone."""
+    c = Case(dtype, [(11 * n) % 23 for n in range(N)], 1, 96 if dtype == BF else 4, 192 if dtype == BF else 4, seed=41, D=D)
+    ref, tol = plain.conv_tree(c.x.double().cpu(), c.w.double().cpu(), c.b.double().cpu(), c.cu, c.parents, c.slots, c.win.double().cpu())
+    near(gla.gla_conv1d_tree(c.x, c.w, c.b, *c.tree_args(), c.win, ints(c.slots))[: c.T], ref[: c.T], tol[: c.T], "y")
+    gla.gla_check()
+    a, b = c.cu[7], c.cu[8]                  # 8 nodes
+    c.parents[a + 3] = 3
+    y = torch.full((c.x.shape[0], D), 7.0, dtype=dtype, device="cuda")
+    gla.gla_conv1d_tree(c.x, c.w, c.b, *c.tree_args(), c.win, ints(c.slots), y=y)
+    with pytest.raises(gla.GlaError):
+        gla.gla_check()
+    assert (y[a:b] == 7).all() and b - a == 8
+    near(y[:a], ref[:a], tol[:a], "y")
+    near(y[b: c.T], ref[b: c.T], tol[b: c.T], "y")
+
+
 @pytest.mark.parametrize("sizes", [[12, 5], [64, 64]], ids=str)
 def test_same_as_steps_along_every_path(gla, sizes):
     """A tree's outputs are those of the serving step run along each path from a copy of the page, up to both kernels' errors."""
