@@ -30,9 +30,7 @@ using ssm::f2_pack;
 using ssm::f2_split;
 using ssm::fma2;
 using ssm::mul2;
-using ssm::param8;
 using ssm::raw_unpack;
-using ssm::store8;
 
 constexpr int kMost = 512, kBwdThreads = 512;   // threads of a CTA, two vectors each: D <= 8192; the backward's on an SM
 
@@ -97,6 +95,37 @@ __device__ __forceinline__ float mean_of(float sum, float D, float inv) {
     return fmaf(fmaf(-q, D, sum), inv, q);
 }
 
+// A thread's vectors are of eight channels, i = 0, 1: at bf16 eight neighbours;
+// at fp32 two groups of four, neighbours' groups side by side, so that every
+// load and store of a warp is whole sectors (eight neighbours a thread, half
+// of each sector a store: FP32_BEFORE).
+template <typename T> __device__ __forceinline__ int upper_half() { return sizeof(T) == 2 ? 4 : 4 * (int)blockDim.x; }   // from the lower half's channels
+template <typename T> __device__ __forceinline__ int channel(int i) {
+    return sizeof(T) == 2 ? (i * (int)blockDim.x + (int)threadIdx.x) * 8 : (i * 2 * (int)blockDim.x + (int)threadIdx.x) * 4;
+}
+// A vector's halves that exist: `on` the lower, `whole` the upper.
+template <typename T> __device__ __forceinline__ void load_params(const float *p, int c, bool on, bool whole, float otherwise, f2 (&v)[4]) {
+    const float4 none = make_float4(otherwise, otherwise, otherwise, otherwise);
+    const float4 a = p && on ? __ldg(reinterpret_cast<const float4 *>(p + c)) : none;
+    const float4 b = p && whole ? __ldg(reinterpret_cast<const float4 *>(p + c + upper_half<T>())) : none;
+    v[0] = f2_pack(a.x, a.y);
+    v[1] = f2_pack(a.z, a.w);
+    v[2] = f2_pack(b.x, b.y);
+    v[3] = f2_pack(b.z, b.w);
+}
+template <typename T> __device__ __forceinline__ void store_floats(float *p, const f2 (&v)[4], bool on, bool whole) {
+    const float2 a = f2_split(v[0]), b = f2_split(v[1]), c = f2_split(v[2]), d = f2_split(v[3]);
+    if (on) *reinterpret_cast<float4 *>(p) = make_float4(a.x, a.y, b.x, b.y);
+    if (whole) *reinterpret_cast<float4 *>(p + upper_half<T>()) = make_float4(c.x, c.y, d.x, d.y);
+}
+template <typename T> __device__ __forceinline__ void store(T *p, const f2 (&v)[4], bool on, bool whole) {
+    if constexpr (sizeof(T) == 2) {
+        if (on) ssm::store8(p, v, whole);
+    } else {
+        store_floats<T>(p, v, on, whole);
+    }
+}
+
 // Rows of kIn arrays in a ring of kStages; a thread copies and reads its own
 // vectors. `at` advances by the copied rows' distance.
 template <typename T, int VPT, int kIn> struct Ring {
@@ -110,7 +139,7 @@ template <typename T, int VPT, int kIn> struct Ring {
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                const int c = (i * (int)blockDim.x + (int)threadIdx.x) * 8 + 4 * h;   // (a piece holds 8 / H channels)
+                const int c = channel<T>(i) + h * upper_half<T>();   // (a piece holds 8 / H channels)
                 copy_async<16>(piece(stage, k, i, h), row + c, in && c < D);
             }
     }
@@ -139,7 +168,6 @@ template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta,
     extern __shared__ __align__(16) uint4 smem[];
     __shared__ float4 s_a[4], s_b[4];
     const Ring<T, VPT, 2> ring{smem};
-    const int tid = threadIdx.x;
     const size_t hop = (size_t)gridDim.x * p.D;
     long next = blockIdx.x;                             // the row copied next, and where it lies
     const T *x = static_cast<const T *>(p.x) + (size_t)next * p.D, *res = static_cast<const T *>(p.res) + (p.res ? (size_t)next * p.D : 0);
@@ -158,18 +186,15 @@ template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta,
     bool on[VPT], whole[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = (i * (int)blockDim.x + tid) * 8;
+        const int c = channel<T>(i);
         on[i] = c < p.D;
-        whole[i] = c + 8 <= p.D;
-        param8(p.w && on[i] ? p.w : nullptr, c, whole[i], w[i]);
-        param8(p.b && on[i] ? p.b : nullptr, c, whole[i], b[i]);
-        if (!p.w)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[i][j] = both(1.f);
+        whole[i] = c + upper_half<T>() < p.D;
+        load_params<T>(p.w, c, on[i], whole[i], p.w ? 0.f : 1.f, w[i]);
+        load_params<T>(p.b, c, on[i], whole[i], 0.f, b[i]);
     }
     const float D = (float)p.D, inv = 1.f / D;
     int stage = 0;
-    size_t at = (size_t)blockIdx.x * p.D + tid * 8;     // of this row, the thread's first vector
+    size_t at = (size_t)blockIdx.x * p.D;               // of this row
     for (long row = blockIdx.x; row < p.rows; row += gridDim.x, at += hop) {
         copies_wait<kFwdRows - 2>();
         f2 v[VPT][4], sum = both(0.f);
@@ -191,7 +216,7 @@ template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta,
         f2 ss = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            if (p.s_out && on[i]) store8(static_cast<T *>(p.s_out) + at + (size_t)i * blockDim.x * 8, v[i], whole[i]);
+            if (p.s_out) store<T>(static_cast<T *>(p.s_out) + at + channel<T>(i), v[i], on[i], whole[i]);
             minus_mean(v[i], mean, on[i], whole[i]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) ss = fma2(v[i][j], v[i][j], ss);
@@ -201,7 +226,7 @@ template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta,
         for (int i = 0; i < VPT; ++i) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[i][j] = fma2(mul2(v[i][j], r), w[i][j], b[i][j]);
-            if (on[i]) store8(static_cast<T *>(p.y) + at + (size_t)i * blockDim.x * 8, v[i], whole[i]);
+            store<T>(static_cast<T *>(p.y) + at + channel<T>(i), v[i], on[i], whole[i]);
         }
     }
 }
@@ -218,7 +243,6 @@ template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta,
     __shared__ float4 s_a[8], s_b[8];
     const Ring<T, VPT, 3> ring{smem};
     ssm::let_next_start();
-    const int tid = threadIdx.x;
     const size_t hop = (size_t)gridDim.x * p.D;
     long next = blockIdx.x;                             // the row copied next, and where it lies
     size_t ahead = (size_t)next * p.D;
@@ -235,21 +259,18 @@ template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta,
     bool on[VPT], whole[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = (i * (int)blockDim.x + tid) * 8;
+        const int c = channel<T>(i);
         on[i] = c < p.D;
-        whole[i] = c + 8 <= p.D;
-        param8(p.w && on[i] ? p.w : nullptr, c, whole[i], w[i]);
+        whole[i] = c + upper_half<T>() < p.D;
+        load_params<T>(p.w, c, on[i], whole[i], p.w ? 0.f : 1.f, w[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (!p.w) w[i][j] = both(1.f);
-            dw[i][j] = db[i][j] = both(0.f);
-        }
+        for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = both(0.f);
     }
     const float D = (float)p.D, inv = 1.f / D;
     int stage = 0;
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) issue(k);
-    size_t at = (size_t)blockIdx.x * p.D + tid * 8;     // of this row, the thread's first vector
+    size_t at = (size_t)blockIdx.x * p.D;               // of this row
     for (long row = blockIdx.x; row < p.rows; row += gridDim.x, at += hop) {
         copies_wait<kStages - 2>();
         f2 x[VPT][4], g[VPT][4], sx = both(0.f), sg = both(0.f);
@@ -293,17 +314,15 @@ template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta,
                 dw[i][j] = fma2(g[i][j], mul2(x[i][j], r2), dw[i][j]);
                 s[j] = fma2(r2, fma2(g[i][j], w[i][j], m2), fma2(k2, x[i][j], s[j]));
             }
-            if (on[i]) store8(static_cast<T *>(p.dx) + at + (size_t)i * blockDim.x * 8, s, whole[i]);
+            store<T>(static_cast<T *>(p.dx) + at + channel<T>(i), s, on[i], whole[i]);
         }
     }
     if (!p.part) return;
     float *part = p.part + (size_t)blockIdx.x * 2 * p.D;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = (i * (int)blockDim.x + tid) * 8;
-        if (!on[i]) continue;
-        store8(part + c, dw[i], whole[i]);
-        store8(part + p.D + c, db[i], whole[i]);
+        store_floats<T>(part + channel<T>(i), dw[i], on[i], whole[i]);
+        store_floats<T>(part + p.D + channel<T>(i), db[i], on[i], whole[i]);
     }
 }
 
@@ -323,8 +342,9 @@ template <typename T> cudaError_t fwd(const LayerNormParams &p, cudaStream_t s, 
     const int th = round32((vecs + vpt - 1) / vpt);
     const long held = (long)(kFwdThreads / th > 16 ? 16 : kFwdThreads / th) * device_sm_count();
     const int bytes = kFwdRows * 2 * vpt * th * 8 * (int)sizeof(T);
-    auto *kern = th <= 256 ? (vpt == 1 ? layernorm_fwd_kernel<T, 1, 256> : layernorm_fwd_kernel<T, 2, 256>)
-                           : (vpt == 1 ? layernorm_fwd_kernel<T, 1, 512> : layernorm_fwd_kernel<T, 2, 512>);
+    auto *kern = th <= 256   ? (vpt == 1 ? layernorm_fwd_kernel<T, 1, 256> : layernorm_fwd_kernel<T, 2, 256>)
+                 : th <= 384 ? (vpt == 1 ? layernorm_fwd_kernel<T, 1, 384> : layernorm_fwd_kernel<T, 2, 384>)
+                             : (vpt == 1 ? layernorm_fwd_kernel<T, 1, 512> : layernorm_fwd_kernel<T, 2, 512>);
     cudaError_t e = allow_smem(kern, bytes);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)(p.rows < held ? p.rows : held), th, bytes, s>>>(p);
