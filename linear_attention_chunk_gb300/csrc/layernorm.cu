@@ -98,7 +98,8 @@ __device__ __forceinline__ float mean_of(float sum, float D, float inv) {
 // A thread's vectors are of eight channels, i = 0, 1: at bf16 eight neighbours;
 // at fp32 two groups of four, neighbours' groups side by side, so that every
 // load and store of a warp is whole sectors (eight neighbours a thread, half
-// of each sector a store: FP32_BEFORE).
+// of each sector a store: forward 47 us for 33 at 3,972 x 2,832 fp32 with the
+// residual, gradients 57 for 42).
 template <typename T> __device__ __forceinline__ int upper_half() { return sizeof(T) == 2 ? 4 : 4 * (int)blockDim.x; }   // from the lower half's channels
 template <typename T> __device__ __forceinline__ int channel(int i) {
     return sizeof(T) == 2 ? (i * (int)blockDim.x + (int)threadIdx.x) * 8 : (i * 2 * (int)blockDim.x + (int)threadIdx.x) * 4;
@@ -159,14 +160,17 @@ __device__ __forceinline__ void minus_mean(f2 (&v)[4], float mean, bool on, bool
     v[3] = add2(v[3], hi);
 }
 
-// Rows in the forward's ring, its threads on an SM (16384 x 2048 with the residual, 2 rows at 640, 768, 896, 1,024
-// threads: 57, 44.6, 52, 48.6 us; 3 rows at 768: 49.7).
-constexpr int kFwdRows = 2, kFwdThreads = 768;
+// Threads of the forward on an SM, rows in its ring (16384 x 2048 with the residual, 2 rows at 640, 768, 896, 1,024
+// threads: 57, 44.6, 52, 48.6 us; 3 rows at 768: 49.7). Rows of one vector a thread have fewer bytes in flight: three
+// (87,890 x 256 bf16: 35.4 us with two rows, 31.9 with three, 33.4 with four).
+constexpr int kFwdThreads = 768;
+template <int VPT> constexpr int fwd_rows() { return VPT == 1 ? 3 : 2; }
 
 // kCta: the most threads it is launched with.
 template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta, kFwdThreads / kCta) layernorm_fwd_kernel(const LayerNormParams p) {
     extern __shared__ __align__(16) uint4 smem[];
     __shared__ float4 s_a[4], s_b[4];
+    constexpr int kRows = fwd_rows<VPT>();
     const Ring<T, VPT, 2> ring{smem};
     const size_t hop = (size_t)gridDim.x * p.D;
     long next = blockIdx.x;                             // the row copied next, and where it lies
@@ -181,7 +185,7 @@ template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta,
         res += p.res ? hop : 0;
     };
 #pragma unroll
-    for (int k = 0; k < kFwdRows - 1; ++k) issue(k);
+    for (int k = 0; k < kRows - 1; ++k) issue(k);
     f2 w[VPT][4], b[VPT][4];
     bool on[VPT], whole[VPT];
 #pragma unroll
@@ -196,7 +200,7 @@ template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta,
     int stage = 0;
     size_t at = (size_t)blockIdx.x * p.D;               // of this row
     for (long row = blockIdx.x; row < p.rows; row += gridDim.x, at += hop) {
-        copies_wait<kFwdRows - 2>();
+        copies_wait<kRows - 2>();
         f2 v[VPT][4], sum = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -210,8 +214,8 @@ template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta,
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum = add2(sum, v[i][j]);
         }
-        issue(stage == 0 ? kFwdRows - 1 : stage - 1);   // into the row before's stage
-        stage = stage == kFwdRows - 1 ? 0 : stage + 1;
+        issue(stage == 0 ? kRows - 1 : stage - 1);   // into the row before's stage
+        stage = stage == kRows - 1 ? 0 : stage + 1;
         const float mean = mean_of(block_sum(pair_sum(sum), s_a), D, inv);
         f2 ss = both(0.f);
 #pragma unroll
@@ -340,8 +344,8 @@ template <typename T> cudaError_t fwd(const LayerNormParams &p, cudaStream_t s, 
     // row has half the warps to exchange with.
     const int vpt = vecs > kMost || (p.rows > 2L * device_sm_count() && vecs > 32) ? 2 : 1;
     const int th = round32((vecs + vpt - 1) / vpt);
-    const long held = (long)(kFwdThreads / th > 16 ? 16 : kFwdThreads / th) * device_sm_count();
-    const int bytes = kFwdRows * 2 * vpt * th * 8 * (int)sizeof(T);
+    const long held = (long)(kFwdThreads / th > 24 ? 24 : kFwdThreads / th) * device_sm_count();
+    const int bytes = (vpt == 1 ? fwd_rows<1>() : fwd_rows<2>()) * 2 * vpt * th * 8 * (int)sizeof(T);
     auto *kern = th <= 256   ? (vpt == 1 ? layernorm_fwd_kernel<T, 1, 256> : layernorm_fwd_kernel<T, 2, 256>)
                  : th <= 384 ? (vpt == 1 ? layernorm_fwd_kernel<T, 1, 384> : layernorm_fwd_kernel<T, 2, 384>)
                              : (vpt == 1 ? layernorm_fwd_kernel<T, 1, 512> : layernorm_fwd_kernel<T, 2, 512>);
@@ -379,7 +383,7 @@ template <typename T> cudaError_t bwd(const LayerNormParams &p, cudaStream_t s, 
 // CTAs of the backward, each walking its share of the rows.
 long layernorm_bwd_grid(long rows, int D) {
     const int th = bwd_threads(D);
-    const long per_sm = kBwdThreads / th > 8 ? 8 : kBwdThreads / th, most = per_sm * device_sm_count();
+    const long per_sm = kBwdThreads / th > 16 ? 16 : kBwdThreads / th, most = per_sm * device_sm_count();
     return rows < most ? rows : most;
 }
 

@@ -24,6 +24,8 @@ using namespace tree;
 constexpr int kThreads = 256, kBlock = 16;   // threads of a CTA; nodes a thread sums at once
 
 __host__ __device__ constexpr int round4(int v) { return (v + 3) / 4 * 4; }
+// A row of q or k in shared memory: an odd number of 16-byte pieces, so that neighbours' rows start in different banks.
+__host__ __device__ constexpr int padded(int v) { return ((v + 3) / 4 | 1) * 4; }
 
 // Any head sizes, fp32 (the validation mode): one CTA per (sequence, head), a
 // thread a state column.
@@ -38,7 +40,7 @@ __global__ void __launch_bounds__(kThreads) tree_fwd_kernel(const TreeParams p) 
         if (t.nodes < 0 && tid == 0) atomicOr(p.status, kDevBadState);
         return;
     }
-    const int M = t.nodes, dk = p.dk, dv = p.dv, ldq = round4(dk);
+    const int M = t.nodes, dk = p.dk, dv = p.dv, ldq = padded(dk);
     float *qs = reinterpret_cast<float *>(smem4), *ks = qs + kNodes * ldq, *P = ks + kNodes * ldq;
     const float *q = static_cast<const float *>(p.q) + (size_t)t.first * p.ldq + (size_t)h * dk;
     const float *k = static_cast<const float *>(p.k) + (size_t)t.first * p.ldk + (size_t)h * dk;
@@ -57,7 +59,10 @@ __global__ void __launch_bounds__(kThreads) tree_fwd_kernel(const TreeParams p) 
         const int i = e / M, j = e % M;
         if (!(path[i] >> j & 1)) continue;
         float dot = 0.f;
-        for (int c = 0; c < dk; ++c) dot = fmaf(qs[i * ldq + c], ks[j * ldq + c], dot);
+        for (int c = 0; c < dk; c += 4) {   // (zeros behind the last channel)
+            const float4 a = *reinterpret_cast<const float4 *>(qs + i * ldq + c), b = *reinterpret_cast<const float4 *>(ks + j * ldq + c);
+            dot = fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, dot))));
+        }
         P[i * kNodes + j] *= dot;
     }
     __syncthreads();
@@ -297,7 +302,7 @@ template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(
 }
 
 cudaError_t fwd_any(const TreeParams &p, cudaStream_t s, int *launches) {
-    const int bytes = (2 * kNodes * round4(p.dk) + kNodes * kNodes) * (int)sizeof(float);
+    const int bytes = (2 * kNodes * padded(p.dk) + kNodes * kNodes) * (int)sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(tree_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     tree_fwd_kernel<<<(unsigned)((size_t)p.nseq * p.H), kThreads, bytes, s>>>(p);
