@@ -202,22 +202,27 @@ template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(
     __shared__ int par[kNodes];
     __shared__ int4 up[kNodes];   // a node's last three ancestors: where their rows start in smem_conv, or -1 - r: r rows before the window's last; w: all are nodes
     const int lane = threadIdx.x % kLanes, first_row = threadIdx.x / kLanes;
-    const int c = ((int)(blockIdx.x % per) * kLanes + lane) * 8;
-    const bool on = c < p.D, whole = c + 8 <= p.D;
+    // a thread's channels: eight neighbours at bf16; two groups of four at fp32, so that a warp's stores are whole sectors
+    // (128 trees of 16 to 64 nodes, D = 4096, fp32: 34.5 us; eight neighbours 47)
+    const int first = (int)(blockIdx.x % per) * kLanes * 8, c = first + lane * (8 / H), half = H == 1 ? 4 : kLanes * 4;
+    const bool on = c < p.D, whole = c + half < p.D;
     // the taps by way of shared memory: coalesced in, and out again a channel's 16 bytes after 144 bytes a lane
     for (int i = threadIdx.x; i < kLanes * 8; i += kConv) {
-        const int ch = (int)(blockIdx.x % per) * kLanes * 8 + i;
-        if (ch < p.D) smem_conv[i + i / 8] = __ldg(reinterpret_cast<const uint4 *>(p.w) + ch);
+        if (first + i < p.D) smem_conv[i + i / 8] = __ldg(reinterpret_cast<const uint4 *>(p.w) + first + i);
     }
     __syncthreads();
     ssm::f2 w[4][4], b[4];                                    // taps of channel pairs
-    ssm::param8(on ? p.b : nullptr, c, whole, b);
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 b_lo = p.b && on ? __ldg(reinterpret_cast<const float4 *>(p.b + c)) : zero;
+    const float4 b_hi = p.b && whole ? __ldg(reinterpret_cast<const float4 *>(p.b + c + half)) : zero;
+    b[0] = ssm::f2_pack(b_lo.x, b_lo.y), b[1] = ssm::f2_pack(b_lo.z, b_lo.w);
+    b[2] = ssm::f2_pack(b_hi.x, b_hi.y), b[3] = ssm::f2_pack(b_hi.z, b_hi.w);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const bool in = c + 2 * j < p.D;
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 u = in ? reinterpret_cast<const float4 *>(smem_conv)[lane * 9 + 2 * j] : zero;
-        const float4 v = in ? reinterpret_cast<const float4 *>(smem_conv)[lane * 9 + 2 * j + 1] : zero;
+        const int ch = c - first + 2 * j + (j < 2 ? 0 : half - 4);   // (an even one and the next: no multiple of 8 between)
+        const bool in = first + ch < p.D;
+        const float4 u = in ? reinterpret_cast<const float4 *>(smem_conv)[ch + ch / 8] : zero;
+        const float4 v = in ? reinterpret_cast<const float4 *>(smem_conv)[ch + ch / 8 + 1] : zero;
         w[0][j] = ssm::f2_pack(u.x, v.x);
         w[1][j] = ssm::f2_pack(u.y, v.y);
         w[2][j] = ssm::f2_pack(u.z, v.z);
@@ -233,10 +238,10 @@ template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(
             for (int i = first_row; i < hi - lo; i += kRows)
 #pragma unroll
                 for (int h = 0; h < H; ++h)
-                    ssm::copy_async<16>(&smem_conv[(i * H + h) * kLanes + lane], x + (size_t)(lo + i) * p.ldx + 4 * h, on && (h == 0 || whole));
+                    ssm::copy_async<16>(&smem_conv[(i * H + h) * kLanes + lane], x + (size_t)(lo + i) * p.ldx + h * half, h == 0 ? on : whole);
             for (int r = first_row; r < 6 && hi > lo; r += kRows) {
-                const bool in = on && (r % 2 == 0 || whole);
-                ssm::copy_async<16>(&wins[r / 2][r % 2][lane], in ? p.win + ((size_t)slot * ssm::kTaps + 1 + r / 2) * p.D + c + 4 * (r % 2) : p.win, in);
+                const bool in = r % 2 == 0 ? on : whole;
+                ssm::copy_async<16>(&wins[r / 2][r % 2][lane], in ? p.win + ((size_t)slot * ssm::kTaps + 1 + r / 2) * p.D + c + half * (r % 2) : p.win, in);
             }
         }
         ssm::copies_commit();
@@ -296,7 +301,13 @@ template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[j] = ssm::silu2(acc[j]);
-            ssm::store8(y, acc, whole);
+            if constexpr (H == 1) {
+                ssm::store8(y, acc, whole);
+            } else {
+                const float2 a0 = ssm::f2_split(acc[0]), a1 = ssm::f2_split(acc[1]), a2 = ssm::f2_split(acc[2]), a3 = ssm::f2_split(acc[3]);
+                *reinterpret_cast<float4 *>(y) = make_float4(a0.x, a0.y, a1.x, a1.y);
+                if (whole) *reinterpret_cast<float4 *>(y + half) = make_float4(a2.x, a2.y, a3.x, a3.y);
+            }
         }
     }
 }
