@@ -21,15 +21,76 @@ namespace {
 
 using namespace tree;
 
-constexpr int kThreads = 256, kBlock = 16;   // threads of a CTA; nodes a thread sums at once
+constexpr int kThreads = 256;
 
 __host__ __device__ constexpr int round4(int v) { return (v + 3) / 4 * 4; }
 // A row of q or k in shared memory: an odd number of 16-byte pieces, so that neighbours' rows start in different banks.
 __host__ __device__ constexpr int padded(int v) { return ((v + 3) / 4 | 1) * 4; }
 
+// A thread's sums over the state and the path: kBlock nodes at a time, two columns `lanes` apart.
+struct Sums {
+    const float *qs, *P, *far, *S, *v;
+    const unsigned long long *path;
+    float *o;
+    int M, ldq, dk, dv, lanes;
+    size_t ldv, ldo;
+    float scale;
+    bool second;   // the second column exists
+};
+template <int kBlock> __device__ __forceinline__ void sum_nodes(const Sums &a, int grp, int groups) {
+    for (int nb = grp * kBlock; nb < a.M; nb += groups * kBlock) {
+        float acc[kBlock][2] = {};
+        for (int r = 0; r < a.dk; r += 4) {
+            float s[4][2];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                s[u][0] = r + u < a.dk ? __ldg(a.S + (size_t)(r + u) * a.dv) : 0.f;
+                s[u][1] = r + u < a.dk && a.second ? __ldg(a.S + (size_t)(r + u) * a.dv + a.lanes) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kBlock; ++i) {
+                const float4 q = *reinterpret_cast<const float4 *>(a.qs + (nb + i) * a.ldq + r);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) acc[i][x] = fmaf(q.x, s[0][x], fmaf(q.y, s[1][x], fmaf(q.z, s[2][x], fmaf(q.w, s[3][x], acc[i][x]))));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBlock; ++i) {
+            if (nb + i >= a.M) break;
+            const float far = a.far[nb + i];
+            float y0 = far == 0.f ? 0.f : far * acc[i][0], y1 = far == 0.f ? 0.f : far * acc[i][1];
+            for (unsigned long long m = a.path[nb + i]; m;) {   // four of the path's nodes at a time, their loads in flight together
+                float w[4], v0[4], v1[4];
+                bool in[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    in[u] = m != 0;
+                    const int j = in[u] ? __ffsll((long long)m) - 1 : 0;
+                    m &= m - 1;
+                    w[u] = in[u] ? a.P[(nb + i) * kNodes + j] : 0.f;
+                    v0[u] = in[u] ? __ldg(a.v + (size_t)j * a.ldv) : 0.f;
+                    v1[u] = in[u] && a.second ? __ldg(a.v + (size_t)j * a.ldv + a.lanes) : 0.f;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    y0 = fmaf(w[u], v0[u], y0);
+                    y1 = fmaf(w[u], v1[u], y1);
+                }
+            }
+            a.o[(size_t)(nb + i) * a.ldo] = a.scale * y0;
+            if (a.second) a.o[(size_t)(nb + i) * a.ldo + a.lanes] = a.scale * y1;
+        }
+    }
+}
+
 // Any head sizes, fp32 (the validation mode): one CTA per (sequence, head), a
-// thread a state column.
-__global__ void __launch_bounds__(kThreads) tree_fwd_kernel(const TreeParams p) {
+// thread two state columns of as few nodes at a time (16, 8, 4: a load of q
+// serves both columns, one of S all nodes) as keep the threads in work. 60 trees
+// of 29 to 59 nodes, H = 16: 78 us at heads of 49 x 69, 406 at 128 x 256; 256
+// trees of 1 to 32 at 96 x 192 368 (one column a thread, the path's nodes one by
+// one: 98, 577, 476). Shared memory holds two or three such CTAs an SM, whose
+// loads it waits for.
+__global__ void __launch_bounds__(kThreads, 3) tree_fwd_kernel(const TreeParams p) {
     extern __shared__ float4 smem4[];
     __shared__ int par[kNodes];
     __shared__ unsigned long long path[kNodes];
@@ -66,34 +127,14 @@ __global__ void __launch_bounds__(kThreads) tree_fwd_kernel(const TreeParams p) 
         P[i * kNodes + j] *= dot;
     }
     __syncthreads();
-    const int lanes = (dv + 31) / 32 * 32, groups = kThreads / lanes;
-    const int c = tid % lanes, grp = tid / lanes;
-    if (grp >= groups || c >= dv) return;
-    const float *S = p.pool + (t.slot * p.H + h) * ((size_t)dk * dv) + c;
-    float *o = static_cast<float *>(p.o) + ((size_t)t.first * p.H + h) * dv + c;
-    for (int nb = grp * kBlock; nb < M; nb += groups * kBlock) {
-        float acc[kBlock] = {};
-        for (int r = 0; r < dk; r += 4) {
-            float s[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) s[u] = r + u < dk ? __ldg(S + (size_t)(r + u) * dv) : 0.f;
-#pragma unroll
-            for (int i = 0; i < kBlock; ++i) {
-                const float4 a = *reinterpret_cast<const float4 *>(qs + (nb + i) * ldq + r);
-                acc[i] = fmaf(a.x, s[0], fmaf(a.y, s[1], fmaf(a.z, s[2], fmaf(a.w, s[3], acc[i]))));
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kBlock; ++i) {
-            if (nb + i >= M) break;
-            float sum = far[nb + i] == 0.f ? 0.f : far[nb + i] * acc[i];
-            for (unsigned long long m = path[nb + i]; m; m &= m - 1) {
-                const int j = __ffsll((long long)m) - 1;
-                sum = fmaf(P[(nb + i) * kNodes + j], __ldg(v + (size_t)j * p.ldv + c), sum);
-            }
-            o[(size_t)(nb + i) * p.H * dv] = p.scale * sum;
-        }
-    }
+    const int lanes = (dv + 1) / 2, groups = kThreads / lanes, c = tid % lanes, grp = tid / lanes;
+    if (grp >= groups) return;
+    const Sums a{qs, P, far, p.pool + (t.slot * p.H + h) * ((size_t)dk * dv) + c, v + c, path,
+                 static_cast<float *>(p.o) + ((size_t)t.first * p.H + h) * dv + c, M, ldq, dk, dv, lanes, (size_t)p.ldv, (size_t)p.H * dv,
+                 p.scale, c + lanes < dv};
+    if (M <= 4 * groups) sum_nodes<4>(a, grp, groups);
+    else if (M <= 8 * groups) sum_nodes<8>(a, grp, groups);
+    else sum_nodes<16>(a, grp, groups);
 }
 
 // ----------------------------------------------------------------- commit
