@@ -1128,8 +1128,9 @@ gla_status gla_conv1d_tree(const void *x, int64_t ld_x, const float *w, const fl
                            int total_T, int D, gla_dtype dtype, void *y, void *stream) {
     t_err[0] = 0;
     t_launches = 0;
-    gla_status st = check_conv_shape(nseq, total_T, D, dtype);
+    gla_status st = check_conv_shape(1, total_T, D, dtype);   // (the trees are packed: total_T rows in all)
     if (st != GLA_OK) return st;
+    if (nseq < 0) return fail(GLA_ERR_INVALID_ARG, "negative nseq=%d", nseq);
     OPTIONAL_PTR(b, "b");
     if (nseq == 0) return GLA_OK;
     TreeParams p{};
