@@ -60,10 +60,12 @@ template <int kCta> __device__ __forceinline__ int rank_of(bool flag, int &all, 
     return before + __popc(m & ((1u << lane) - 1));
 }
 
-// The moves: sources, targets; returns how many. `live` gets the number of pages in use.
+// The moves: sources, targets; returns how many. `live` gets the number of pages in use. Page numbers are unsigned
+// here and in write_map: of up to 2^31 - 1 pages, the last step of a thread goes past an int.
 template <int kCta> __device__ __forceinline__ int make_plan(const PageParams &p, int *srcs, int *dsts, int *s, int &live) {
     live = 0;
-    for (int i = threadIdx.x; i < p.n_slots; i += kCta) live += p.live[i] != 0;
+    const unsigned slots = (unsigned)p.n_slots;
+    for (unsigned i = threadIdx.x; i < slots; i += kCta) live += p.live[i] != 0;
     live = __reduce_add_sync(0xffffffffu, live);
     if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = live;
     __syncthreads();
@@ -71,24 +73,24 @@ template <int kCta> __device__ __forceinline__ int make_plan(const PageParams &p
     for (int w = 0; w < kCta / 32; ++w) live += s[w];
     __syncthreads();
     int holes = 0, far = 0;
-    for (int base = 0; base < p.n_slots; base += kCta) {
-        const int i = base + threadIdx.x;
-        const bool in = i < p.n_slots, on = in && p.live[i] != 0;
-        const bool hole = in && !on && i < live, moves = on && i >= live;
+    for (unsigned base = 0; base < slots; base += kCta) {
+        const unsigned i = base + threadIdx.x;
+        const bool in = i < slots, on = in && p.live[i] != 0;
+        const bool hole = in && !on && i < (unsigned)live, moves = on && i >= (unsigned)live;
         int n;
         const int a = holes + rank_of<kCta>(hole, n, s);
         holes += n;
         const int b = far + rank_of<kCta>(moves, n, s);
         far += n;
-        if (hole) dsts[a] = i;
-        if (moves) srcs[b] = i;
+        if (hole) dsts[a] = (int)i;
+        if (moves) srcs[b] = (int)i;
     }
     __syncthreads();
     return holes;
 }
 // The pages' new numbers, and how many are in use.
 __device__ __forceinline__ void write_map(const PageParams &p, const int *srcs, const int *dsts, int moves, int live) {
-    for (int i = threadIdx.x; i < p.n_slots; i += blockDim.x) p.map[i] = p.live[i] ? i : -1;
+    for (unsigned i = threadIdx.x; i < (unsigned)p.n_slots; i += blockDim.x) p.map[i] = p.live[i] ? (int)i : -1;
     if (threadIdx.x == 0) *p.count = live;
     __syncthreads();
     for (int j = threadIdx.x; j < moves; j += blockDim.x) p.map[srcs[j]] = dsts[j];
@@ -104,7 +106,7 @@ template <Pairs kFrom> __global__ void __launch_bounds__(kThreads) pages_kernel(
     int pairs = p.n;
     if constexpr (kFrom == kListed) {
         ssm::wait_for_previous();
-        pairs = __ldcg(p.moves + 2 * half);
+        pairs = __ldcg(p.moves + 2L * half);
         srcs = p.moves;
         dsts = p.moves + half;
     } else if constexpr (kFrom == kOwn) {
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(kPlan) plan_kernel(const PageParams p) {
     const int half = p.n_slots / 2 + 1;
     int *srcs = p.moves, *dsts = p.moves + half, live;
     const int moves = make_plan<kPlan>(p, srcs, dsts, s, live);
-    if (threadIdx.x == 0) p.moves[2 * half] = moves;
+    if (threadIdx.x == 0) p.moves[2L * half] = moves;
     write_map(p, srcs, dsts, moves, live);
 }
 

@@ -245,11 +245,12 @@ template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(
     const int lane = threadIdx.x % kLanes, first_row = threadIdx.x / kLanes;
     // a thread's channels: eight neighbours at bf16; two groups of four at fp32, so that a warp's stores are whole sectors
     // (128 trees of 16 to 64 nodes, D = 4096, fp32: 34.5 us; eight neighbours 47)
-    const int first = (int)(blockIdx.x % per) * kLanes * 8, c = first + lane * (8 / H), half = H == 1 ? 4 : kLanes * 4;
-    const bool on = c < p.D, whole = c + half < p.D;
+    // (unsigned: the lanes of the last block go past D, which may be next to 2^31)
+    const unsigned first = blockIdx.x % per * (kLanes * 8), c = first + lane * (8 / H), half = H == 1 ? 4 : kLanes * 4, D = (unsigned)p.D;
+    const bool on = c < D, whole = c + half < D;
     // the taps by way of shared memory: coalesced in, and out again a channel's 16 bytes after 144 bytes a lane
-    for (int i = threadIdx.x; i < kLanes * 8; i += kConv) {
-        if (first + i < p.D) smem_conv[i + i / 8] = __ldg(reinterpret_cast<const uint4 *>(p.w) + first + i);
+    for (unsigned i = threadIdx.x; i < kLanes * 8; i += kConv) {
+        if (first + i < D) smem_conv[i + i / 8] = __ldg(reinterpret_cast<const uint4 *>(p.w) + first + i);
     }
     __syncthreads();
     ssm::f2 w[4][4], b[4];                                    // taps of channel pairs
@@ -260,8 +261,8 @@ template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(
     b[2] = ssm::f2_pack(b_hi.x, b_hi.y), b[3] = ssm::f2_pack(b_hi.z, b_hi.w);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int ch = c - first + 2 * j + (j < 2 ? 0 : half - 4);   // (an even one and the next: no multiple of 8 between)
-        const bool in = first + ch < p.D;
+        const unsigned ch = c - first + 2 * j + (j < 2 ? 0 : half - 4);   // (an even one and the next: no multiple of 8 between)
+        const bool in = first + ch < D;
         const float4 u = in ? reinterpret_cast<const float4 *>(smem_conv)[ch + ch / 8] : zero;
         const float4 v = in ? reinterpret_cast<const float4 *>(smem_conv)[ch + ch / 8 + 1] : zero;
         w[0][j] = ssm::f2_pack(u.x, v.x);
@@ -372,7 +373,7 @@ template <typename T> cudaError_t commit_any(const TreeParams &p, cudaStream_t s
 
 template <typename T> cudaError_t conv(const TreeParams &p, cudaStream_t s, int *launches) {
     constexpr int kLanes = conv_lanes<T>();
-    const int per = (p.D + 8 * kLanes - 1) / (8 * kLanes), bytes = kNodes * kLanes * 8 * (int)sizeof(T);   // 32 KB
+    const int per = (int)((p.D + 8L * kLanes - 1) / (8 * kLanes)), bytes = kNodes * kLanes * 8 * (int)sizeof(T);   // 32 KB
     const long held = 18L * device_sm_count() / per;   // thrice the six CTAs an SM that shared memory holds
     const long trees = held < 1 ? 1 : held < p.nseq ? held : p.nseq;
     conv_tree_kernel<T><<<(unsigned)(trees * per), kConv, bytes, s>>>(p, per);

@@ -61,10 +61,11 @@ __device__ __forceinline__ unsigned long long walk(int i, const int *par, const 
 // The windows of a commit, in pieces of 128 channels of a sequence, a warp each
 // (four channels a lane): the last four inputs of the accepted path, before them
 // what the window held.
-__host__ __device__ __forceinline__ long window_pieces(const TreeParams &p) { return p.x ? (long)p.nseq * ((p.D + 127) / 128) : 0; }
+__host__ __device__ __forceinline__ long window_pieces(const TreeParams &p) { return p.x ? p.nseq * ((p.D + 127L) / 128) : 0; }
 
 template <typename T> __device__ __forceinline__ void commit_window(const TreeParams &p, long piece) {
-    const int lane = threadIdx.x % 32, per = (p.D + 127) / 128, n = (int)(piece / per), c = (int)(piece % per) * 128 + lane * 4;
+    const int lane = threadIdx.x % 32, per = (int)((p.D + 127L) / 128), n = (int)(piece / per);
+    const unsigned c = (unsigned)(piece % per) * 128 + lane * 4;   // (unsigned: the last lanes go past D, which may be next to 2^31)
     const int a = __ldg(p.cu + n), b = __ldg(p.cu + n + 1), slot = p.slots ? __ldg(p.slots + n) : n, last = __ldg(p.last + n);
     bool bad = a < 0 || b < a || b > p.total_T || b - a > kNodes || slot < 0 || slot >= p.n_slots || last < -1 || last >= b - a;
     int par[2] = {-1, -1};   // of nodes lane and lane + 32
@@ -88,7 +89,7 @@ template <typename T> __device__ __forceinline__ void commit_window(const TreePa
         const int lo = __shfl_sync(0xffffffffu, par[0], j & 31), hi = __shfl_sync(0xffffffffu, par[1], j & 31);
         if (j >= 0) j = j < 32 ? lo : hi;
     }
-    if (c >= p.D) return;
+    if (c >= (unsigned)p.D) return;
     float *win = p.win + (size_t)slot * ssm::kTaps * p.D + c;
     float4 row[ssm::kTaps];
 #pragma unroll
