@@ -349,29 +349,57 @@ struct Unit {
     uint32_t par;
     size_t row;              // the first node's row of o and of this head
 };
-// What the elements of v that are not finite give node x, channels 4 q4 .. 4 q4 + 3 of the warp's 16. (Not inline: it is rarely
-// called, and its instructions would stand in the readout's way.)
-__device__ __noinline__ float4 not_finite(const unsigned char *sm, const Meta *m, int s, int x) {
+// This thread's outputs again (every eighth node from g on, channels 4 q4 .. 4 q4 + 3 of the warp's 16, `o` and `S` their
+// columns in the outputs and the page), where a node's q, a score on its path or a v there is not finite (of a v, in its
+// channel): term by term in fp32. The halves of S and P make NaN of such terms where fp32 makes an infinity (inf hi + inf lo is inf - inf where the
+// halves' signs differ, and inf 0 where one is 0), and a v that is not finite was left out. (Not inline: it is rarely called,
+// and its instructions would stand in the readout's way.)
+__device__ __noinline__ void term_by_term(const unsigned char *sm, const Meta *m, int s, const float *S, __nv_bfloat16 *o, size_t step, float scale) {
     const int q4 = threadIdx.x % 4, warp = threadIdx.x / 32;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (x >= m->nodes) return sum;
-    const __nv_bfloat16 *ph = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPh + (uint32_t)(s * kNodes + x) * kPitchP);
-    const __nv_bfloat16 *pl = reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPl + (uint32_t)(s * kNodes + x) * kPitchP);
-    for (unsigned long long path = m->path[x]; path; path &= path - 1) {
-        const int j = __ffsll((long long)path) - 1;
-        const float2 si = m->sum[x], sj = m->sum[j];
-        if (exp2f(((si.x - sj.x) + (si.y - sj.y)) * m->factor) == 0.f) continue;   // (cleared on the way)
-        const float w = __bfloat162float(ph[j]) + __bfloat162float(pl[j]);
-        const uint32_t piece = kOffV + (uint32_t)s * kNodeV + (uint32_t)(j >> 4) * kTileV + (uint32_t)(warp / 4) * 2048 + (uint32_t)(j & 15) * 128;
-        const uint32_t c16 = ((uint32_t)(warp & 3) * 2 + (uint32_t)(q4 >> 1)) ^ (uint32_t)(j & 7);
-        const uint2 v = *reinterpret_cast<const uint2 *>(sm + piece + c16 * 16 + (uint32_t)(q4 & 1) * 8);
-        const float2 a = unpack_bf16x2(v.x), b = unpack_bf16x2(v.y);
-        if (!isfinite(a.x)) sum.x += w * a.x;
-        if (!isfinite(a.y)) sum.y += w * a.y;
-        if (!isfinite(b.x)) sum.z += w * b.x;
-        if (!isfinite(b.y)) sum.w += w * b.y;
+    for (int x = threadIdx.x % 32 / 4; x < m->nodes; x += 8) {
+        const unsigned char *q = sm + kOffQ + (uint32_t)s * kNodeQ;
+        const auto pair = [&](int r) { return *reinterpret_cast<const uint32_t *>(q + at_q(0, (uint32_t)x, (uint32_t)r & ~7u) + (uint32_t)(r & 7) * 2); };
+        uint32_t odd = 0;   // the channels to form again, one bit each
+        for (int r = 0; r < kDk; r += 2) odd |= finite2(pair(r)) != pair(r) ? 15u : 0u;
+        const uint32_t row = (uint32_t)(s * kNodes + x) * kPitchP;
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        for (unsigned long long path = m->path[x]; path; path &= path - 1) {
+            const int j = __ffsll((long long)path) - 1;
+            const float2 si = m->sum[x], sj = m->sum[j];
+            if (j != x && exp2f(((si.x - sj.x) + (si.y - sj.y)) * m->factor) == 0.f) continue;   // (cleared on the way)
+            const float w = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPh + row + (uint32_t)j * 2)) +
+                            __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(sm + kOffPl + row + (uint32_t)j * 2));
+            const uint32_t piece = kOffV + (uint32_t)s * kNodeV + (uint32_t)(j >> 4) * kTileV + (uint32_t)(warp / 4) * 2048 + (uint32_t)(j & 15) * 128;
+            const uint32_t c16 = ((uint32_t)(warp & 3) * 2 + (uint32_t)(q4 >> 1)) ^ (uint32_t)(j & 7);
+            const uint2 v = *reinterpret_cast<const uint2 *>(sm + piece + c16 * 16 + (uint32_t)(q4 & 1) * 8);
+            const float2 a = unpack_bf16x2(v.x), b = unpack_bf16x2(v.y);
+            const float u[4] = {a.x, a.y, b.x, b.y};
+            odd |= isfinite(w) ? 0u : 15u;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                odd |= isfinite(u[c]) ? 0u : 1u << c;
+                y[c] = fmaf(w, u[c], y[c]);
+            }
+        }
+        if (!odd) continue;
+        const float far = m->far[x];
+        if (far != 0.f) {
+            float z[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int r = 0; r < kDk; ++r) {
+                const float u = __uint_as_float(r & 1 ? pair(r - 1) & 0xffff0000u : pair(r) << 16);
+                const float4 a = __ldg(reinterpret_cast<const float4 *>(S + (size_t)r * kDv));
+                z[0] = fmaf(u, a.x, z[0]);
+                z[1] = fmaf(u, a.y, z[1]);
+                z[2] = fmaf(u, a.z, z[2]);
+                z[3] = fmaf(u, a.w, z[3]);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) y[c] = fmaf(far, z[c], y[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (odd >> c & 1) o[(size_t)x * step + c] = __float2bfloat16_rn(scale * y[c]);
     }
-    return sum;
 }
 template <int kTiles> __device__ __forceinline__ bool readout(const TreeParams &p, const Unit &unit, const WaitCtl &ctl) {
     const int lane = threadIdx.x % 32, g = lane / 4, q4 = lane % 4;   // a fragment's row (or column), its pair of columns (or rows)
@@ -461,7 +489,7 @@ template <int kTiles> __device__ __forceinline__ bool readout(const TreeParams &
             if (js * 16 + j >= M) x[r] = 0;             // (rows of another tree)
             odd |= mul_bf16x2(x[r], 0) & 0x7fff7fffu;        // not 0: an element that is not finite
         }
-        // One that is not finite would reach every node by way of 0 x inf: it is left out here and added on its paths below.
+        // One that is not finite would reach every node by way of 0 x inf: it is left out here, its paths' nodes come again below.
         if (__any_sync(0xffffffffu, odd != 0)) {
             dirty = true;
 #pragma unroll
@@ -486,29 +514,21 @@ template <int kTiles> __device__ __forceinline__ bool readout(const TreeParams &
             }
         }
     }
-    if (dirty)
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float4 e = not_finite(sm, m, s, i * 16 + g + 8 * r);
-                acc[i][0][2 * r] += e.x;
-                acc[i][1][2 * r] += e.y;
-                acc[i][0][2 * r + 1] += e.z;
-                acc[i][1][2 * r + 1] += e.w;
-            }
     const size_t step = (size_t)p.H * kDv;
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + unit.row * kDv + warp * 16 + 4 * q4 + (size_t)g * step;
+    __nv_bfloat16 *const first = static_cast<__nv_bfloat16 *>(p.o) + unit.row * kDv + warp * 16 + 4 * q4, *o = first + (size_t)g * step;
+    float zero = dirty ? 1.f : 0.f;   // NaN where a result is not finite
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r, o += 8 * step) {
             const int x = i * 16 + g + 8 * r;
             if (x >= M) continue;
-            *reinterpret_cast<uint2 *>(o) =
-                make_uint2(pack_bf16x2(p.scale * acc[i][0][2 * r], p.scale * acc[i][1][2 * r]),
-                           pack_bf16x2(p.scale * acc[i][0][2 * r + 1], p.scale * acc[i][1][2 * r + 1]));
+            const float y[4] = {acc[i][0][2 * r], acc[i][1][2 * r], acc[i][0][2 * r + 1], acc[i][1][2 * r + 1]};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) zero = fmaf(y[c], 0.f, zero);
+            *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16x2(p.scale * y[0], p.scale * y[1]), pack_bf16x2(p.scale * y[2], p.scale * y[3]));
         }
+    if (__any_sync(0xffffffffu, zero != 0.f)) term_by_term(sm, m, s, p.pool + (size_t)m->row * kDv + warp * 16 + 4 * q4, first, step, p.scale);
     return true;
 }
 
