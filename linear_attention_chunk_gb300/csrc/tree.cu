@@ -111,10 +111,10 @@ __global__ void __launch_bounds__(kThreads, 3) tree_fwd_kernel(const TreeParams 
         qs[e] = c < dk ? q[(size_t)i * p.ldq + c] : 0.f;
         ks[e] = c < dk ? k[(size_t)i * p.ldk + c] : 0.f;
     }
-    const float l2 = p.g ? 0.f : log2_of_decay(p.log_lambda[h]);
+    const float fixed = p.g ? 0.f : p.log_lambda[h];
     if (p.g && tid < M) gate[tid] = p.g[(size_t)(t.first + tid) * p.H + h];
     __syncthreads();
-    if (tid < M) path[tid] = walk(tid, par, p.g ? gate : nullptr, l2, far[tid], [&](int j, float w) { P[tid * kNodes + j] = w; });
+    if (tid < M) path[tid] = walk(tid, par, p.g ? gate : nullptr, fixed, far[tid], [&](int j, float w) { P[tid * kNodes + j] = w; });
     __syncthreads();
     for (int e = tid; e < M * M; e += kThreads) {
         const int i = e / M, j = e % M;
@@ -166,7 +166,7 @@ template <typename T> __global__ void __launch_bounds__(kCommit) tree_commit_any
     __syncthreads();
     if (tid == 0) {
         int len = 0;
-        walk(last, par, p.g ? gate : nullptr, p.g ? 0.f : log2_of_decay(p.log_lambda[h]), s_far, [&](int j, float w) {
+        walk(last, par, p.g ? gate : nullptr, p.g ? 0.f : p.log_lambda[h], s_far, [&](int j, float w) {
             way[len] = j;
             s_w[len++] = w;
         });

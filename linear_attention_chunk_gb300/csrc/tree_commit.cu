@@ -102,9 +102,10 @@ __device__ __forceinline__ void planner(const TreeParams &p, unsigned char *sm, 
         if (bad && lane == 0) atomicOr(p.status, kDevBadState);
         // The walk: lane k keeps the path's tokens k and k + 32 and the decays behind them.
         int at[2] = {0, 0}, len = 0;
-        float w[2] = {0.f, 0.f}, sum = 0.f, far = 1.f;
+        float w[2] = {0.f, 0.f}, far = 1.f;
         if (!bad && now.last >= 0) {
-            const float l2 = kGate ? 0.f : log2_of_decay(__ldg(p.log_lambda + h));
+            const float fixed = kGate ? 0.f : __ldg(p.log_lambda + h);
+            tree::Decay decay;
             for (int j = now.last; j >= 0 && far != 0.f;) {   // a decay of 0 ends it: what lies before is cleared
                 if ((len & 31) == lane) {
                     at[len >> 5] = j;
@@ -112,12 +113,8 @@ __device__ __forceinline__ void planner(const TreeParams &p, unsigned char *sm, 
                 }
                 ++len;
                 const int up = j < 32 ? __shfl_sync(0xffffffffu, now.par[0], j) : __shfl_sync(0xffffffffu, now.par[1], j - 32);
-                if (kGate) {
-                    sum += j < 32 ? __shfl_sync(0xffffffffu, now.gate[0], j) : __shfl_sync(0xffffffffu, now.gate[1], j - 32);
-                    far = expf(sum);
-                } else {
-                    far = decay_pow(l2, len);
-                }
+                if (kGate) far = decay.then(j < 32 ? __shfl_sync(0xffffffffu, now.gate[0], j) : __shfl_sync(0xffffffffu, now.gate[1], j - 32));
+                else far = decay.of(len, fixed);
                 j = up;
             }
         } else {

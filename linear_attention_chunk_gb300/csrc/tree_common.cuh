@@ -31,27 +31,47 @@ __device__ __forceinline__ Tree open_tree(const TreeParams &p, int n, int *par) 
     return t;
 }
 
+// The decay of a run of nodes from their log-decays: the sum in a high and a
+// low part (in one float, 64 of them would be off by up to 64 half steps of a
+// sum of, say, -10, which is 8 units of 2^-24 each in the decay), so that the
+// decay has little more than the exponential's own error: 4 units, with its
+// last rounding 5. A decay of 0 ends a path; nothing is asked of it behind.
+class Decay {
+    float hi_ = 0.f, lo_ = 0.f;
+    __device__ __forceinline__ float value() const {   // e^(hi + lo)
+        const float w = expf(hi_);
+        return w == 0.f ? 0.f : fmaf(w, lo_, w);       // (of -inf the low part is NaN)
+    }
+
+public:
+    __device__ __forceinline__ float then(float log) {   // one more node
+        const float s = hi_ + log, t = s - hi_;
+        lo_ += (hi_ - (s - t)) + (log - t);
+        hi_ = s;
+        return value();
+    }
+    __device__ __forceinline__ float of(int n, float log) {   // n nodes of the same decay
+        hi_ = (float)n * log;
+        lo_ = fmaf((float)n, log, -hi_);
+        return value();
+    }
+};
+
 // From node i to the state: visit(j, w) for every node j on the path, i first,
 // with w the decay of the nodes behind j; `far` gets that of all of them, the
 // state's. Returns the visited nodes, one bit each. The walk ends where the
 // decay is 0: what lies before it is cleared (far = 0). gate: the nodes' log
-// decays, or NULL for the fixed one, 2^l2.
-// The logarithms are added along the path, so that a product of many decays
-// has no more error than its sum's.
+// decays, or NULL for the fixed one.
 template <typename F>
-__device__ __forceinline__ unsigned long long walk(int i, const int *par, const float *gate, float l2, float &far, F visit) {
+__device__ __forceinline__ unsigned long long walk(int i, const int *par, const float *gate, float fixed, float &far, F visit) {
     unsigned long long seen = 0;
-    float sum = 0.f, w = 1.f;
+    Decay decay;
+    float w = 1.f;
     int steps = 0;
     for (int j = i; j >= 0; j = par[j]) {
         visit(j, w);
         seen |= 1ull << j;
-        if (gate) {
-            sum += gate[j];
-            w = expf(sum);
-        } else {
-            w = decay_pow(l2, ++steps);
-        }
+        w = gate ? decay.then(gate[j]) : decay.of(++steps, fixed);
         if (w == 0.f) break;
     }
     far = w;
