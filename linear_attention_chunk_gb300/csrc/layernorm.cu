@@ -344,7 +344,7 @@ template <typename T> cudaError_t fwd(const LayerNormParams &p, cudaStream_t s, 
     // row has half the warps to exchange with.
     const int vpt = vecs > kMost || (p.rows > 2L * device_sm_count() && vecs > 32) ? 2 : 1;
     const int th = round32((vecs + vpt - 1) / vpt);
-    const long held = (long)(kFwdThreads / th > 24 ? 24 : kFwdThreads / th) * device_sm_count();
+    const long held = (long)(kFwdThreads / th) * device_sm_count();   // (a warp each: 24 CTAs an SM)
     const int bytes = (vpt == 1 ? fwd_rows<1>() : fwd_rows<2>()) * 2 * vpt * th * 8 * (int)sizeof(T);
     auto *kern = th <= 256   ? (vpt == 1 ? layernorm_fwd_kernel<T, 1, 256> : layernorm_fwd_kernel<T, 2, 256>)
                  : th <= 384 ? (vpt == 1 ? layernorm_fwd_kernel<T, 1, 384> : layernorm_fwd_kernel<T, 2, 384>)
@@ -383,7 +383,7 @@ template <typename T> cudaError_t bwd(const LayerNormParams &p, cudaStream_t s, 
 // CTAs of the backward, each walking its share of the rows.
 long layernorm_bwd_grid(long rows, int D) {
     const int th = bwd_threads(D);
-    const long per_sm = kBwdThreads / th > 16 ? 16 : kBwdThreads / th, most = per_sm * device_sm_count();
+    const long most = (long)(kBwdThreads / th) * device_sm_count();   // (a warp each: 16 an SM)
     return rows < most ? rows : most;
 }
 

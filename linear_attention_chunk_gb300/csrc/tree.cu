@@ -23,7 +23,6 @@ using namespace tree;
 
 constexpr int kThreads = 256;
 
-__host__ __device__ constexpr int round4(int v) { return (v + 3) / 4 * 4; }
 // A row of q or k in shared memory: an odd number of 16-byte pieces, so that neighbours' rows start in different banks.
 __host__ __device__ constexpr int padded(int v) { return ((v + 3) / 4 | 1) * 4; }
 
@@ -140,17 +139,24 @@ __global__ void __launch_bounds__(kThreads, 3) tree_fwd_kernel(const TreeParams 
 // ----------------------------------------------------------------- commit
 constexpr int kCommit = 256;
 
-// Any head sizes: one CTA per (sequence, head), behind them the windows', a
-// warp a piece. fp32's validation mode; pages of 96 x 192 go through tree_commit.cu.
-template <typename T> __global__ void __launch_bounds__(kCommit) tree_commit_any_kernel(const TreeParams p) {
+// The windows' pieces from CTA `first` on, a warp each.
+template <typename T> __device__ __forceinline__ void windows_of(const TreeParams &p, unsigned first) {
+    const long piece = (long)(blockIdx.x - first) * (kCommit / 32) + threadIdx.x / 32;
+    if (piece < window_pieces(p)) commit_window<T>(p, piece);
+}
+// No heads: the windows alone.
+template <typename T> __global__ void __launch_bounds__(kCommit) windows_kernel(const TreeParams p) { windows_of<T>(p, 0); }
+
+// Any head sizes, fp32 (the validation mode): one CTA per (sequence, head),
+// behind them the windows'. Pages of 96 x 192, all of bf16's, go through tree_commit.cu.
+__global__ void __launch_bounds__(kCommit) tree_commit_any_kernel(const TreeParams p) {
     extern __shared__ float4 smem4[];
     __shared__ int par[kNodes], way[kNodes], s_len;
     __shared__ float s_w[kNodes], gate[kNodes], s_far;
     float *kt = reinterpret_cast<float *>(smem4);          // [path node][dk], decayed
     const unsigned pages = (unsigned)p.nseq * (unsigned)p.H;
     if (blockIdx.x >= pages) {
-        const long piece = (long)(blockIdx.x - pages) * (kCommit / 32) + threadIdx.x / 32;
-        if (piece < window_pieces(p)) commit_window<T>(p, piece);
+        windows_of<float>(p, pages);
         return;
     }
     const int n = blockIdx.x / p.H, h = blockIdx.x % p.H, tid = threadIdx.x;
@@ -177,11 +183,11 @@ template <typename T> __global__ void __launch_bounds__(kCommit) tree_commit_any
     const float far = s_far;
     for (int e = tid; e < len * dk; e += kCommit) {
         const int j = e / dk, r = e % dk;
-        kt[e] = s_w[j] * Elem<T>::load(static_cast<const T *>(p.k) + (size_t)(t.first + way[j]) * p.ldk + (size_t)h * dk + r);
+        kt[e] = s_w[j] * static_cast<const float *>(p.k)[(size_t)(t.first + way[j]) * p.ldk + (size_t)h * dk + r];
     }
     __syncthreads();
     float *S = p.pool + (t.slot * p.H + h) * ((size_t)dk * dv);
-    const T *v = static_cast<const T *>(p.v) + (size_t)t.first * p.ldv + (size_t)h * dv;
+    const float *v = static_cast<const float *>(p.v) + (size_t)t.first * p.ldv + (size_t)h * dv;
     if (dv % 4 == 0) {   // four columns of four rows a thread at a time
         const int cols = dv / 4, c = tid % cols * 4, step = kCommit / cols;
         for (int r0 = tid / cols; r0 < dk && tid < step * cols; r0 += 4 * step) {
@@ -193,8 +199,8 @@ template <typename T> __global__ void __launch_bounds__(kCommit) tree_commit_any
                     x[i] = far == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(far * y.x, far * y.y, far * y.z, far * y.w);
                 }
             for (int j = 0; j < len; ++j) {
-                const T *w = v + (size_t)way[j] * p.ldv + c;
-                const float4 u = make_float4(Elem<T>::load(w), Elem<T>::load(w + 1), Elem<T>::load(w + 2), Elem<T>::load(w + 3));
+                const float *w = v + (size_t)way[j] * p.ldv + c;   // (4-byte aligned)
+                const float4 u = make_float4(w[0], w[1], w[2], w[3]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float k = r0 + i * step < dk ? kt[j * dk + r0 + i * step] : 0.f;
@@ -213,7 +219,7 @@ template <typename T> __global__ void __launch_bounds__(kCommit) tree_commit_any
     for (int e = tid; e < dk * dv; e += kCommit) {
         const int r = e / dv, c = e % dv;
         float x = far == 0.f ? 0.f : far * S[e];
-        for (int j = 0; j < len; ++j) x = fmaf(kt[j * dk + r], Elem<T>::load(v + (size_t)way[j] * p.ldv + c), x);
+        for (int j = 0; j < len; ++j) x = fmaf(kt[j * dk + r], v[(size_t)way[j] * p.ldv + c], x);
         S[e] = x;
     }
 }
@@ -363,10 +369,18 @@ cudaError_t fwd_any(const TreeParams &p, cudaStream_t s, int *launches) {
     return cudaGetLastError();
 }
 
-template <typename T> cudaError_t commit_any(const TreeParams &p, cudaStream_t s, int *launches) {
+long window_blocks(const TreeParams &p) { return (window_pieces(p) + kCommit / 32 - 1) / (kCommit / 32); }
+
+template <typename T> cudaError_t windows(const TreeParams &p, cudaStream_t s, int *launches) {
+    windows_kernel<T><<<(unsigned)window_blocks(p), kCommit, 0, s>>>(p);
+    if (launches) ++*launches;
+    return cudaGetLastError();
+}
+
+cudaError_t commit_any(const TreeParams &p, cudaStream_t s, int *launches) {
     const int bytes = kNodes * p.dk * (int)sizeof(float);   // at most 32 KB
-    const long blocks = (long)p.nseq * p.H + (window_pieces(p) + kCommit / 32 - 1) / (kCommit / 32);
-    tree_commit_any_kernel<T><<<(unsigned)blocks, kCommit, bytes, s>>>(p);
+    const long blocks = (long)p.nseq * p.H + window_blocks(p);
+    tree_commit_any_kernel<<<(unsigned)blocks, kCommit, bytes, s>>>(p);
     if (launches) ++*launches;
     return cudaGetLastError();
 }
@@ -387,8 +401,8 @@ cudaError_t launch_tree_fwd(const TreeParams &p, bool bf16, cudaStream_t s, int 
     return bf16 ? launch_tree_fwd_tc(p, s, launches) : fwd_any(p, s, launches);
 }
 cudaError_t launch_tree_commit(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {
-    if (p.dk == 96 && p.dv == 192 && p.H > 0) return launch_tree_pages(p, bf16, s, launches);
-    return bf16 ? commit_any<__nv_bfloat16>(p, s, launches) : commit_any<float>(p, s, launches);
+    if (p.H == 0) return bf16 ? windows<__nv_bfloat16>(p, s, launches) : windows<float>(p, s, launches);
+    return p.dk == 96 && p.dv == 192 ? launch_tree_pages(p, bf16, s, launches) : commit_any(p, s, launches);
 }
 cudaError_t launch_conv_tree(const TreeParams &p, bool bf16, cudaStream_t s, int *launches) {
     return bf16 ? conv<__nv_bfloat16>(p, s, launches) : conv<float>(p, s, launches);

@@ -76,3 +76,19 @@ def test_commit_of_many_units_a_cta(gla, dtype, gated, N, shape):
         assert (off <= tol + 1e-36).all(), (n, float((off / (tol + 1e-36)).max()))
     still = [s for s in range(N + 2) if s not in [c.slots[n] for n in kept]]
     assert len(still) > N // 9 and torch.equal(c.pool[still], pool[still]) and torch.equal(c.win.double().cpu(), windows)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF, 8), (BF, 4096), (FP, 516)])
+def test_windows_without_heads(gla, dtype, D):
+    """A layer's windows alone (H = 0), a bad parent among them."""
+    N = 70
+    c = Case(dtype, [(5 * n) % 65 for n in range(N)], 1, 96, 192, seed=5, D=D)
+    empty, log = c.k[:, :0], torch.empty(0, device="cuda")
+    c.parents[c.cu[9] + 2] = 5
+    kept = [last if n != 9 else -1 for n, last in enumerate(c.last)]
+    want = plain.windows(c.x.double().cpu(), c.cu, c.parents, kept, c.slots, c.win.double().cpu())
+    gla.gla_tree_commit(empty, empty.new_empty(empty.shape[0], 0, 192), log, *c.tree_args(), ints(c.last),
+                        torch.empty(N + 2, 0, 96, 192, device="cuda"), ints(c.slots), x=c.x, win_pool=c.win)
+    with pytest.raises(gla.GlaError):
+        gla.gla_check()
+    assert torch.equal(c.win.double().cpu(), want)
