@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kCommit) tree_commit_any_kernel(const TreePara
     const int n = blockIdx.x / p.H, h = blockIdx.x % p.H, tid = threadIdx.x;
     const int last = p.last[n];
     const Tree t = open_tree(p, n, par);
-    if (t.nodes < 0 || last < -1 || last >= t.nodes) {
+    if (t.nodes < 0 || bad_last(last, t.nodes)) {
         if (tid == 0) atomicOr(p.status, kDevBadState);
         return;
     }
@@ -281,8 +281,7 @@ template <typename T> __global__ void __launch_bounds__(kConv) conv_tree_kernel(
         __syncthreads();                                      // the taps, or the tree before, have been read
         // what open_tree checks, before the copies that do not depend on the parents
         const int lo = p.cu[n], hi = p.cu[n + 1], slot = p.slots ? p.slots[n] : n;
-        const bool fits = lo >= 0 && hi >= lo && hi <= p.total_T && hi - lo <= kNodes && slot >= 0 && slot < p.n_slots;
-        if (fits) {
+        if (!bad_entry(p, lo, hi, slot)) {
             for (int i = first_row; i < hi - lo; i += kRows)
 #pragma unroll
                 for (int h = 0; h < H; ++h)

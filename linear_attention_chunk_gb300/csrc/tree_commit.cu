@@ -75,8 +75,7 @@ __device__ __forceinline__ void planner(const TreeParams &p, unsigned char *sm, 
         a.first = r.lo;
         a.slot = r.slot;
         a.last = r.last;
-        const bool bad = r.lo < 0 || r.hi < r.lo || r.hi > p.total_T || r.hi - r.lo > kNodes || r.slot < 0 || r.slot >= p.n_slots;
-        a.count = bad || r.last < -1 || r.last >= r.hi - r.lo ? -1 : r.hi - r.lo;
+        a.count = tree::bad_entry(p, r.lo, r.hi, r.slot) || tree::bad_last(r.last, r.hi - r.lo) ? -1 : r.hi - r.lo;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = lane + 32 * e;
@@ -97,7 +96,7 @@ __device__ __forceinline__ void planner(const TreeParams &p, unsigned char *sm, 
         const int h = (int)(u % H);
         bool bad = now.count < 0;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) bad |= lane + 32 * e < now.count && (now.par[e] < -1 || now.par[e] >= lane + 32 * e);
+        for (int e = 0; e < 2; ++e) bad |= tree::bad_parent(now.par[e], lane + 32 * e);   // (-1 behind the tree)
         bad = __any_sync(0xffffffffu, bad);
         if (bad && lane == 0) atomicOr(p.status, kDevBadState);
         // The walk: lane k keeps the path's tokens k and k + 32 and the decays behind them.

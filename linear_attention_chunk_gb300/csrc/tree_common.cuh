@@ -11,6 +11,13 @@ namespace tree {
 
 constexpr int kNodes = 64;   // the most a tree may have
 
+// What counts as a bad entry: a sequence's offsets lo, hi and slot, and the parent of node i of its tree.
+__device__ __forceinline__ bool bad_entry(const TreeParams &p, int lo, int hi, int slot) {
+    return lo < 0 || hi < lo || hi > p.total_T || hi - lo > kNodes || slot < 0 || slot >= p.n_slots;
+}
+__device__ __forceinline__ bool bad_parent(int parent, int i) { return parent < -1 || parent >= i; }
+__device__ __forceinline__ bool bad_last(int last, int nodes) { return last < -1 || last >= nodes; }
+
 struct Tree {
     int first, nodes;   // its first packed node; nodes -1: a bad entry, the sequence is skipped
     size_t slot;
@@ -21,11 +28,11 @@ struct Tree {
 // its node, so walks end.
 __device__ __forceinline__ Tree open_tree(const TreeParams &p, int n, int *par) {
     const int a = p.cu[n], b = p.cu[n + 1], slot = p.slots ? p.slots[n] : n;
-    int bad = a < 0 || b < a || b > p.total_T || b - a > kNodes || slot < 0 || slot >= p.n_slots;
+    int bad = bad_entry(p, a, b, slot);
     Tree t{a, bad ? 0 : b - a, (size_t)slot};
     for (int i = threadIdx.x; i < t.nodes; i += blockDim.x) {
         par[i] = p.parents[a + i];
-        bad |= par[i] < -1 || par[i] >= i;
+        bad |= bad_parent(par[i], i);
     }
     if (__syncthreads_or(bad)) t.nodes = -1;
     return t;
@@ -87,14 +94,14 @@ template <typename T> __device__ __forceinline__ void commit_window(const TreePa
     const int lane = threadIdx.x % 32, per = (int)((p.D + 127L) / 128), n = (int)(piece / per);
     const unsigned c = (unsigned)(piece % per) * 128 + lane * 4;   // (unsigned: the last lanes go past D, which may be next to 2^31)
     const int a = __ldg(p.cu + n), b = __ldg(p.cu + n + 1), slot = p.slots ? __ldg(p.slots + n) : n, last = __ldg(p.last + n);
-    bool bad = a < 0 || b < a || b > p.total_T || b - a > kNodes || slot < 0 || slot >= p.n_slots || last < -1 || last >= b - a;
+    bool bad = bad_entry(p, a, b, slot) || bad_last(last, b - a);
     int par[2] = {-1, -1};   // of nodes lane and lane + 32
     if (!bad)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = lane + 32 * e;
             if (i < b - a) par[e] = __ldg(p.parents + a + i);
-            bad |= par[e] < -1 || (par[e] >= i && i < b - a);
+            bad |= bad_parent(par[e], i);   // (-1 behind the tree)
         }
     if (__any_sync(0xffffffffu, bad)) {
         if (lane == 0) atomicOr(p.status, kDevBadState);

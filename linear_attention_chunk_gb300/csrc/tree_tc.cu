@@ -147,7 +147,7 @@ __device__ __forceinline__ void planner(const TreeParams &p, unsigned char *sm, 
         Nodes a;
         a.first = r.lo;
         a.slot = r.slot;
-        a.count = r.lo < 0 || r.hi < r.lo || r.hi > p.total_T || r.hi - r.lo > kNodes || r.slot < 0 || r.slot >= p.n_slots ? -1 : r.hi - r.lo;
+        a.count = tree::bad_entry(p, r.lo, r.hi, r.slot) ? -1 : r.hi - r.lo;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = lane + 32 * e;
@@ -167,7 +167,7 @@ __device__ __forceinline__ void planner(const TreeParams &p, unsigned char *sm, 
         const int h = (int)(u % H), s = it % kMetas;
         bool bad = now.count < 0;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) bad |= lane + 32 * e < now.count && (now.par[e] < -1 || now.par[e] >= lane + 32 * e);
+        for (int e = 0; e < 2; ++e) bad |= tree::bad_parent(now.par[e], lane + 32 * e);   // (-1 behind the tree)
         if (__any_sync(0xffffffffu, bad)) {
             now.count = 0;
             if (lane == 0) atomicOr(p.status, kDevBadState);
