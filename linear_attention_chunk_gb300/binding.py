@@ -1162,7 +1162,7 @@ class _PagesCall(_Quick):
                                "pools must be contiguous, on one device and of as many pages each")
             where[i] = t.data_ptr()
             size[i] = t.nbytes // n if n else 4
-        self.pools = (where, size, k if n else 0, n)
+        self.pools = (where, size, k, n)
 
 
 def gla_pages_copy(pools, src, dst, *, stream=None):

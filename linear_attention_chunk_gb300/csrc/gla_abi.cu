@@ -261,7 +261,7 @@ gla_status check_pools(PageParams &p, void *const *pools, const int64_t *page_by
     if (n_pools > 0 && (!pools || !page_bytes)) return fail(GLA_ERR_INVALID_ARG, "pools or page_bytes is NULL");
     long double all = 0;
     for (int i = 0; i < n_pools; ++i) {
-        REQUIRE_PTR(pools[i], "a pool");
+        if (n_slots > 0) REQUIRE_PTR(pools[i], "a pool");   // (without pages there is nothing to point at)
         if (page_bytes[i] <= 0 || page_bytes[i] % 4 != 0)
             return fail(GLA_ERR_UNSUPPORTED, "pages of %lld bytes: a positive multiple of 4 is needed", (long long)page_bytes[i]);
         if (page_bytes[i] > (1ll << 36)) return fail(GLA_ERR_INVALID_ARG, "pages of %lld bytes are too large", (long long)page_bytes[i]);

@@ -58,3 +58,17 @@ def test_compaction_of_the_most_pages(gla):
     for t, odd in ((pool, [5, 1000]), (where, [5, 1000, n - 3, n - 2, n - 1])):
         t[odd] = same[odd]
         assert torch.equal(t, same)
+
+
+def test_page_numbers_of_a_pool_without_pages(gla):
+    """Every number is outside: the call moves nothing and the next check says so."""
+    pools = [torch.empty(0, 4, device="cuda"), torch.empty(0, 3, 5, device="cuda")]
+    for call in (lambda: gla.gla_pages_copy(pools, ints([0]), ints([1])), lambda: gla.gla_pages_clear(pools, ints([0]))):
+        call()
+        with pytest.raises(gla.GlaError) as e:
+            gla.gla_check()
+        assert e.value.status == gla.GLA_ERR_INVALID_ARG
+    where, count = gla.gla_pages_compact(pools, torch.empty(0, dtype=torch.bool, device="cuda"))
+    gla.gla_pages_copy(pools, ints([]), ints([]))
+    gla.gla_check()
+    assert where.numel() == 0 and int(count) == 0

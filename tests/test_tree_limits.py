@@ -36,3 +36,14 @@ def test_convolution_sizes_refused(L):
     assert "too large" in conv(L, 1, (1 << 15) + 1, 1 << 25, y=2 * FAKE)
     assert "nseq*D" in conv(L, 1 << 16, 1 << 16, 1 << 15, y=2 * FAKE)
     assert "negative" in conv(L, -1, 8, 64, y=2 * FAKE) and "negative" in conv(L, 2, -1, 64, y=2 * FAKE)
+
+
+def test_pools_without_pages(L):
+    """They need no address; with pages they do."""
+    import ctypes
+
+    null, size = (ctypes.c_void_p * 2)(None, None), (ctypes.c_int64 * 2)(4, 4)
+    assert "src" in why(L, L.gla_pages_copy(null, size, 2, 0, None, FAKE, 3, None))
+    assert "slots" in why(L, L.gla_pages_clear(null, size, 2, 0, None, 3, None))
+    assert "a pool" in why(L, L.gla_pages_copy(null, size, 2, 1, FAKE, FAKE, 3, None))
+    assert L.gla_pages_copy(null, size, 2, 0, None, None, 0, None) == binding.GLA_OK
