@@ -526,6 +526,13 @@ size_t gla_rmsnorm_bwd_workspace_size(int64_t rows, int D, gla_dtype dtype);
  * gla_decode_step would give along every path, without a copy of the page for
  * each. A decay of 0 (log-decay -inf, or a product that underflows) clears
  * what lies before it.
+ *   No state is formed: o_i = scale (F_i S^T q_i + sum over the path of
+ *   W_ij (q_i . k_j) v_j), F_i and W_ij the decays behind the page and node j. At
+ *   GLA_FP32 all of it is fp32. At GLA_BF16 the entries of the page and the
+ *   numbers W_ij (q_i . k_j) enter the products as two bf16 each, off by up to
+ *   2^-17 of themselves where gla_decode_step keeps 2^-24; sums are fp32, and o
+ *   is rounded to bf16 once (2^-9). Infinities and NaN give what the sum of those
+ *   terms gives in fp32: infinite terms of both signs, or 0 times an infinity, NaN.
  *   Trees are packed one behind another: sequence n's nodes are
  *   [cu_nodes[n], cu_nodes[n+1]) (int32 [nseq + 1] in device memory), parents
  *   [total_T] int32 hold each node's parent counted within its tree, always
@@ -547,7 +554,7 @@ size_t gla_rmsnorm_bwd_workspace_size(int64_t rows, int D, gla_dtype dtype);
  *   they were. o may not overlap an input.
  * gla_tree_commit, gla_tree_commit_gated: last [nseq] int32 in device memory,
  *   the last accepted node of each tree, counted within it (-1: none): the
- *   page becomes S_last, the others stay. With x [total_T, D] and win_pool
+ *   page becomes S_last, in fp32, the others stay. With x [total_T, D] and win_pool
  *   [n_slots, 4, D] fp32 (both or neither) also the Conv1d's window: its last
  *   four inputs, those of the accepted path last. Slots of one call are distinct.
  *   D a multiple of 8 (bf16) or 4 (fp32).

@@ -1082,7 +1082,9 @@ def gla_tree_fwd(q, k, v, log_lambda, cu_nodes, parents, state_pool, slots=None,
     state). q, k [T,H,dk], v [T,H,dv] (column ranges of wider tensors pass),
     state_pool [n_slots,H,dk,dv] fp32, read at slots[n] (int32 CUDA tensor, or
     None for slot n) and left as it is. Returns o [T,H,dv]: what
-    gla_decode_step would give along each node's path."""
+    gla_decode_step would give along each node's path (at bf16 with the page's
+    entries and the decayed scores as two bf16 each, 2^-17 of themselves, before
+    the one rounding of o; fp32 throughout at fp32)."""
     return _tree_fwd("gla_tree_fwd", q, k, v, log_lambda, False, cu_nodes, parents, state_pool, slots, scale, o, stream)
 
 

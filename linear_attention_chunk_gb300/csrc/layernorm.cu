@@ -235,12 +235,15 @@ template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta,
     }
 }
 
-// Rows in the backward's ring (2, 3, 5 at 16384 x 2048: 56, 53, 71 us); two where three would not fit (fp32, 512 threads: 98 KB a row).
+// Rows in the backward's ring (2, 3, 5 at 16384 x 2048 bf16: 50.6, 48.5, 61.6 us on the device). Two at fp32 of two vectors a
+// thread, at every D: three would not fit at 512 threads (98 KB a row). At 384 they would; not measured.
 template <typename T, int VPT> constexpr int ring_rows() { return sizeof(T) == 4 && VPT == 2 ? 2 : 3; }
 
 // p.x: s; rows blockIdx.x, + gridDim.x, ...; partial dw and db of the CTA at
-// p.part. (Of 53 us at 16384 x 2048 the second launch takes 6. Clusters of two
-// CTAs that add their sums up first: 52; of four: 68, fewer of them fit.)
+// p.part. 16384 x 2048 bf16: 48.5 us on the device, 51 a call with other inputs
+// each time; the second launch takes 6 of them. (Measured while it took 53:
+// clusters of two CTAs that add their sums up first, 52; of four, 68, fewer of
+// them fit.)
 template <typename T, int VPT, int kCta> __global__ void __launch_bounds__(kCta, kBwdThreads / kCta) layernorm_bwd_kernel(const LayerNormParams p) {
     constexpr int kStages = ring_rows<T, VPT>();
     extern __shared__ __align__(16) uint4 smem[];
@@ -356,7 +359,7 @@ template <typename T> cudaError_t fwd(const LayerNormParams &p, cudaStream_t s, 
     return cudaGetLastError();
 }
 
-// The backward's shape, by D alone: two vectors a thread from 264 channels on (one, at 16384 x 2048: 59 us for 53).
+// The backward's shape, by D alone: two vectors a thread from 264 channels on (one, at 16384 x 2048: 57 us on the device for 48.5).
 int bwd_vpt(int D) { return D > 256 ? 2 : 1; }
 int bwd_threads(int D) { return round32(((D + 7) / 8 + bwd_vpt(D) - 1) / bwd_vpt(D)); }
 

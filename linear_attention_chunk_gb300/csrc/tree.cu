@@ -85,8 +85,8 @@ template <int kBlock> __device__ __forceinline__ void sum_nodes(const Sums &a, i
 // Any head sizes, fp32 (the validation mode): one CTA per (sequence, head), a
 // thread two state columns of as few nodes at a time (16, 8, 4: a load of q
 // serves both columns, one of S all nodes) as keep the threads in work. 60 trees
-// of 29 to 59 nodes, H = 16: 78 us at heads of 49 x 69, 406 at 128 x 256; 256
-// trees of 1 to 32 at 96 x 192 368 (one column a thread, the path's nodes one by
+// of 29 to 59 nodes, H = 16: 76 us at heads of 49 x 69, 406 at 128 x 256; 256
+// trees of 1 to 32 at 96 x 192 367 (one column a thread, the path's nodes one by
 // one: 98, 577, 476). Shared memory holds two or three such CTAs an SM, whose
 // loads it waits for.
 __global__ void __launch_bounds__(kThreads, 3) tree_fwd_kernel(const TreeParams p) {

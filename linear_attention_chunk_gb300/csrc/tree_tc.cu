@@ -2,16 +2,23 @@
 // F_i the decay of the whole path of node i and W_ij that of its nodes behind j,
 //     O = scale ( diag(F) Q S + (W o Q K^T) V ),
 // W_ij = 0 off the path. Up to 64 nodes share one read of the page S (73,728
-// bytes fp32), so the call is bound by HBM: the pages, q, k, v and o once.
+// bytes fp32): the pages, q, k, v and o cross HBM once, which is what the call
+// cannot do without (56 us for 256 trees of up to 32 nodes, H = 16).
 //
 // S goes from HBM to the tensor cores by way of shared memory and registers
 // alone: six TMA stages of 16 rows (128-byte swizzle), whose entries
-// the consumer warps split into two bf16 halves (hi + lo, 2^-17 of the entry:
-// drafted tokens get the values that the decode step's fp32 arithmetic gives,
-// to a few 2^-17) and multiply Q by both. A stage has too few products a byte
-// to pay for tcgen05's operand layouts (the halves would first go back to
-// shared memory); warp-level products take them from registers. P = W o Q K^T
-// is split likewise.
+// the consumer warps split into two bf16 halves (hi + lo, 16 of an entry's 24
+// bits: off by 2^-17 of it) and multiply Q by both; P = W o Q K^T is split
+// likewise. Drafted tokens so get what the decode step's fp32 arithmetic gives
+// to a few 2^-17 before their one rounding to bf16, which is off by up to 2^-9:
+// against 64 bits both are off by 1.7e-3 of the outputs' norm. Three parts each,
+// all 24 bits, measured: outputs that differ from fp32's by 3.8e-5 of their norm
+// for 9.6e-5 (roundings that fall the other way), the error against 64 bits the
+// same, at 75 us on the device for 62.6 (256 trees of up to 32 nodes) and 78 for
+// 56.9 (128 of 48 to 64, gated).
+// Warp-level products take the halves from registers. tcgen05 has not been
+// tried here: S^T's halves as its A operand would go from registers to tensor
+// memory, not back to shared memory.
 //
 // One CTA an SM, no CTA-wide barrier, every hand-over by mbarrier:
 //   warp 17      the trees, up to four units (sequence, head) ahead: offsets,
@@ -21,9 +28,9 @@
 //                copy may hold rows of the next one), half of S as it comes free;
 //   warps 12-15  P of the unit ahead, 16 x 16 tiles below the diagonal;
 //   warps 0-11   16 channels each: Q S step by step, the decay, P V, the rows out.
-// 256 trees of up to 32 nodes, H = 16: 65 us, 0.86 of the measured copy rate;
-// 128 of 48 to 64, gated: 59, 0.71, where the products' 3,600 clocks a unit and
-// their latencies show. (Two CTAs of six consumer warps that did all of it in
+// 256 trees of up to 32 nodes, H = 16: 65 us a call, 0.86 of the measured copy
+// rate; 128 of 48 to 64, gated: 59, 0.71, where the products' 3,600 clocks a
+// unit and their latencies show. (Two CTAs of six consumer warps that did all of it in
 // turn, P between CTA barriers: 112 and 101. Two groups of consumers a unit
 // each, 32 channels a warp: 85 and 80. Three halves of S held, k in one buffer:
 // 71 and 63 on the device where these take 62 and 56: the consumers set the pace.)
