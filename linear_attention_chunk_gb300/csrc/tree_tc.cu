@@ -14,8 +14,8 @@
 // against 64 bits both are off by 1.7e-3 of the outputs' norm. Three parts each,
 // all 24 bits, measured: outputs that differ from fp32's by 3.8e-5 of their norm
 // for 9.6e-5 (roundings that fall the other way), the error against 64 bits the
-// same, at 75 us on the device for 62.6 (256 trees of up to 32 nodes) and 78 for
-// 56.9 (128 of 48 to 64, gated).
+// same, at 75 us on the device for 62.8 (256 trees of up to 32 nodes) and 78 for
+// 56.8 (128 of 48 to 64, gated).
 // Warp-level products take the halves from registers. tcgen05 has not been
 // tried here: S^T's halves as its A operand would go from registers to tensor
 // memory, not back to shared memory.
@@ -67,6 +67,7 @@ struct Meta {
     float far[kNodes];                 // the state's decay
     float factor;                      // W_ij = 2^(factor (sum_i - sum_j))
     int first, nodes, row;             // row: the first of its page in the pool, as rows of dv
+    int odd;                           // not 0: a score is not finite (as a node's own is where its q is not)
 };
 enum { FULL_S = 0, EMPTY_S = FULL_S + 2, FULL_M = EMPTY_S + 2, FREE_M = FULL_M + kMetas, FULL_N = FREE_M + kMetas, FULL_P = FULL_N + 2, FREE = FULL_P + 2, BARS = FREE + 2 };
 constexpr uint32_t kOffNext = kOffMeta + kMetas * sizeof(Meta), kOffBars = kOffNext + kNodes * 4, kOffAbort = kOffBars + BARS * 8,
@@ -227,6 +228,7 @@ __device__ __forceinline__ void planner(const TreeParams &p, unsigned char *sm, 
             m->factor = factor;
             m->first = now.first;
             m->nodes = M;
+            m->odd = 0;
             m->row = (now.slot * p.H + h) * kDk;
         }
         __syncwarp();
@@ -289,9 +291,10 @@ __device__ __forceinline__ void scorer(unsigned char *sm, uint32_t base, const W
         const int s = it & 1, meta = it % kMetas;
         const uint32_t par = (uint32_t)(it >> 1) & 1u;
         if (!wait(FULL_N + s, par)) return;   // (and with it the plan, which the copies' warp has waited for)
-        const Meta *m = reinterpret_cast<const Meta *>(sm + kOffMeta) + meta;
+        Meta *m = reinterpret_cast<Meta *>(sm + kOffMeta) + meta;
         const int tiles = (m->nodes + 15) / 16;
         const float factor = m->factor;
+        float zero = 0.f;   // NaN where a score is not finite
         const uint32_t bQ = base + kOffQ + (uint32_t)s * kNodeQ, bK = base + kOffK + (uint32_t)s * kNodeQ;
         const uint32_t sQ[2] = {at_q(bQ, a_row, a_col), at_q(bQ, a_row, 16 + a_col)}, sK[2] = {at_q(bK, b_row, b_col), at_q(bK, b_row, 16 + b_col)};
         for (int x = warp; x < tiles * (tiles + 1) / 2; x += kScorers) {
@@ -328,6 +331,7 @@ __device__ __forceinline__ void scorer(unsigned char *sm, uint32_t base, const W
                         // (a fixed decay of 0: a node's own weight is 2^(-inf 0))
                         v[e] = !(path >> (j + e) & 1) || w == 0.f ? 0.f : (i == j + e ? 1.f : w) * c[b][2 * r + e];
                     }
+                    zero = fmaf(v[1], 0.f, fmaf(v[0], 0.f, zero));
                     uint32_t hi, lo;
                     split(v[0], v[1], hi, lo);
                     const uint32_t at = (uint32_t)(s * kNodes + i) * kPitchP + (uint32_t)j * 2;
@@ -336,6 +340,7 @@ __device__ __forceinline__ void scorer(unsigned char *sm, uint32_t base, const W
                 }
             }
         }
+        if (zero != 0.f) m->odd = 1;
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(bar(FULL_P + s));
@@ -357,19 +362,22 @@ struct Unit {
     size_t row;              // the first node's row of o and of this head
 };
 // This thread's outputs again (every eighth node from g on, channels 4 q4 .. 4 q4 + 3 of the warp's 16, `o` and `S` their
-// columns in the outputs and the page), where a node's q, a score on its path or a v there is not finite (of a v, in its
-// channel): term by term in fp32. The halves of S and P make NaN of such terms where fp32 makes an infinity (inf hi + inf lo is inf - inf where the
-// halves' signs differ, and inf 0 where one is 0), and a v that is not finite was left out. (Not inline: it is rarely called,
-// and its instructions would stand in the readout's way.)
+// columns in the outputs and the page), where a score on a node's path is not finite (its own is not where its q is not) or a v
+// there (of a v, in its channel): term by term in fp32. The halves of S and P make NaN of such terms where fp32 makes an
+// infinity (inf hi + inf lo is inf - inf where the halves' signs differ, and inf 0 where one is 0), and a v that is not finite
+// was left out. Not inline, and its outer loops rolled up: it is rarely called, and its length stands in the readout's way
+// (256 trees of up to 32 nodes, on the device: 64.0 us unrolled, 62.8 so). One infinite q among those adds 7 us, NaN in every q 100.
 __device__ __noinline__ void term_by_term(const unsigned char *sm, const Meta *m, int s, const float *S, __nv_bfloat16 *o, size_t step, float scale) {
     const int q4 = threadIdx.x % 4, warp = threadIdx.x / 32;
+#pragma unroll 1
     for (int x = threadIdx.x % 32 / 4; x < m->nodes; x += 8) {
         const unsigned char *q = sm + kOffQ + (uint32_t)s * kNodeQ;
         const auto pair = [&](int r) { return *reinterpret_cast<const uint32_t *>(q + at_q(0, (uint32_t)x, (uint32_t)r & ~7u) + (uint32_t)(r & 7) * 2); };
         uint32_t odd = 0;   // the channels to form again, one bit each
-        for (int r = 0; r < kDk; r += 2) odd |= finite2(pair(r)) != pair(r) ? 15u : 0u;
+        bool nan = false;   // a score is: the products have then given NaN everywhere, which stands
         const uint32_t row = (uint32_t)(s * kNodes + x) * kPitchP;
         float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
         for (unsigned long long path = m->path[x]; path; path &= path - 1) {
             const int j = __ffsll((long long)path) - 1;
             const float2 si = m->sum[x], sj = m->sum[j];
@@ -382,16 +390,21 @@ __device__ __noinline__ void term_by_term(const unsigned char *sm, const Meta *m
             const float2 a = unpack_bf16x2(v.x), b = unpack_bf16x2(v.y);
             const float u[4] = {a.x, a.y, b.x, b.y};
             odd |= isfinite(w) ? 0u : 15u;
+            nan |= w != w;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 odd |= isfinite(u[c]) ? 0u : 1u << c;
                 y[c] = fmaf(w, u[c], y[c]);
             }
         }
-        if (!odd) continue;
+        if (!odd || nan) continue;
         const float far = m->far[x];
-        if (far != 0.f) {
+        bool open = false;   // a channel to form again that the path has not made NaN
+#pragma unroll
+        for (int c = 0; c < 4; ++c) open |= (odd >> c & 1) && y[c] == y[c];
+        if (open && far != 0.f) {
             float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
             for (int r = 0; r < kDk; ++r) {
                 const float u = __uint_as_float(r & 1 ? pair(r - 1) & 0xffff0000u : pair(r) << 16);
                 const float4 a = __ldg(reinterpret_cast<const float4 *>(S + (size_t)r * kDv));
@@ -523,19 +536,17 @@ template <int kTiles> __device__ __forceinline__ bool readout(const TreeParams &
     }
     const size_t step = (size_t)p.H * kDv;
     __nv_bfloat16 *const first = static_cast<__nv_bfloat16 *>(p.o) + unit.row * kDv + warp * 16 + 4 * q4, *o = first + (size_t)g * step;
-    float zero = dirty ? 1.f : 0.f;   // NaN where a result is not finite
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r, o += 8 * step) {
             const int x = i * 16 + g + 8 * r;
             if (x >= M) continue;
-            const float y[4] = {acc[i][0][2 * r], acc[i][1][2 * r], acc[i][0][2 * r + 1], acc[i][1][2 * r + 1]};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) zero = fmaf(y[c], 0.f, zero);
-            *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16x2(p.scale * y[0], p.scale * y[1]), pack_bf16x2(p.scale * y[2], p.scale * y[3]));
+            *reinterpret_cast<uint2 *>(o) =
+                make_uint2(pack_bf16x2(p.scale * acc[i][0][2 * r], p.scale * acc[i][1][2 * r]),
+                           pack_bf16x2(p.scale * acc[i][0][2 * r + 1], p.scale * acc[i][1][2 * r + 1]));
         }
-    if (__any_sync(0xffffffffu, zero != 0.f)) term_by_term(sm, m, s, p.pool + (size_t)m->row * kDv + warp * 16 + 4 * q4, first, step, p.scale);
+    if (dirty || m->odd) term_by_term(sm, m, s, p.pool + (size_t)m->row * kDv + warp * 16 + 4 * q4, first, step, p.scale);
     return true;
 }
 
