@@ -98,3 +98,19 @@ def test_a_decay_of_zero_among_long_paths(gla, dtype):
     c.commit(gla)
     gla.gla_check()
     within(c.pool, ref, tol, "pool")
+
+
+@pytest.mark.parametrize("dtype,dk,dv", PAGES)
+def test_fixed_decays_of_zero_and_one(gla, dtype, dk, dv):
+    """log_lambda -inf keeps a path's last node alone, whatever the page holds; 0 keeps everything; -60 and -104 run out on the way."""
+    c = Case(dtype, [64, 9], 4, dk, dv, shape="chain", seed=6)
+    c.log = torch.tensor([-INF, 0.0, -60.0, -104.0], device="cuda")
+    c.last = [63, 8]
+    ref, tol = committed(c)
+    c.pool[:, 0] = float("nan")
+    used = c.slots[:2]
+    o = c.fwd(gla)[: c.T]
+    c.commit(gla)
+    gla.gla_check()
+    within(c.pool[used], ref[used], tol[used], "pool")
+    assert torch.isfinite(o.float()).all()
